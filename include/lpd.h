@@ -97,6 +97,7 @@ extern "C" {
 /* ---- workspace kinds --------------------------------------------------- */
 #define LPD_KIND_SCORE 0   /* lpd_score and its stages */
 #define LPD_KIND_SHARDED 1 /* lpd_score_sharded */
+#define LPD_KIND_CONTROLLED 2 /* lpd_score_controlled */
 
 /* One side's logits: [n_rows, row_stride] row-major, columns [0, vocab) used. */
 typedef struct {
@@ -172,8 +173,8 @@ typedef struct {
 /* ---- sizing and introspection ----------------------------------------- */
 
 /* Bytes of device workspace that a call of the given kind needs for n_rows
- * rows (vocab and n_shards are used by the sharded kind; pass 0
- * otherwise).  Returns 0 for invalid arguments. */
+ * rows (n_shards is used by the sharded kind, vocab by the sharded and the
+ * controlled kind; pass 0 otherwise).  Returns 0 for invalid arguments. */
 size_t lpd_workspace_size(int32_t kind, int64_t n_rows, int64_t vocab, int32_t n_shards);
 
 /* Fills *info.  Returns LPD_OK, or LPD_ERR_NULL_POINTER. */
@@ -493,6 +494,99 @@ int lpd_score_fused_transformed(const void *hidden_train, const void *hidden_rol
                                 float *out_logp_train, float *out_logp_rollout,
                                 float *out_dlogp, lpd_metrics *out_metrics, void *workspace,
                                 size_t workspace_bytes, void *stream);
+
+/* ---- sampling controls ------------------------------------------------------- */
+
+/* What a request's sampler does to a row of logits before it samples: penalties
+ * for repeated tokens, biases, a grammar mask, and the temperature.  A rollout's
+ * tokens come from the distribution after these, so that is the distribution
+ * that its drift is measured in ("WS2 Cross-Config Logprob Drift Contract",
+ * "Measurement Contract").  For row r and token j, with n_all the occurrences
+ * of j in history[hist_begin[r], hist_end[r]) and n_gen those in
+ * history[hist_split[r], hist_end[r]):
+ *
+ *     x1 = n_all > 0 ? (x > 0 ? x / repetition[r] : x * repetition[r]) : x
+ *     x2 = n_gen > 0 ? x1 - frequency[r] * n_gen - presence[r]         : x1
+ *     x3 = x2 + (the sum of bias[r, e] over the entries e with bias_ids[r, e] == j)
+ *     z  = (bit j of the row's mask is 0) ? -inf : scale[r] * x3
+ *
+ * A NULL array leaves its step out (scale: 1).  Every array is in device memory
+ * and dense but the mask, and holds one entry a row where a row count is given;
+ * the struct itself is a host struct, read during the call.
+ *
+ * history     int32 [n_history], the tokens of all sequences.  The rows' ranges
+ *             may overlap: teacher-forced rows of one sequence share its tokens
+ *             and differ in hist_end.  Ids outside [0, vocab) are skipped.  The
+ *             three offsets are required with it; they are clamped to
+ *             [0, n_history] and to begin <= split <= end, and a range of more
+ *             than 2^30 - 1 tokens counts its last 2^30 - 1.
+ * repetition, frequency, presence, scale   float [n_rows].  A repetition or a
+ *             scale that is not finite and > 0 makes the values it enters NaN.
+ * bias_ids, bias   int32 and float [n_rows, n_bias], n_bias <= LPD_MAX_BIAS.
+ *             Ids outside [0, vocab) are unused entries; an id that occurs
+ *             twice adds both.
+ * mask        uint32 [n_masks, mask_stride], token j at bit j % 32 of word
+ *             j / 32, 1 = allowed; mask_stride >= ceil(vocab / 32) words.
+ * mask_row    int32 [n_rows]: the row's mask, negative: everything allowed,
+ *             n_masks or more: nothing allowed.  NULL: mask r for row r
+ *             (n_masks >= n_rows). */
+#define LPD_MAX_BIAS 1024
+typedef struct {
+    const int32_t *history;
+    int64_t n_history;
+    const int64_t *hist_begin;
+    const int64_t *hist_split;
+    const int64_t *hist_end;
+    const float *repetition;
+    const float *frequency;
+    const float *presence;
+    const float *scale;
+    const int32_t *bias_ids;
+    const float *bias;
+    int64_t n_bias;
+    const uint32_t *mask;
+    int64_t n_masks;
+    int64_t mask_stride;
+    const int32_t *mask_row;
+} lpd_controls;
+
+/* The controlled logits z of every row, for the sampler: out [n_rows,
+ * out_row_stride] of out_dtype, columns [0, vocab) written, each value rounded
+ * once.  Logits in masked places are not looked at: they may be NaN or
+ * infinite.  A row whose mask allows nothing is -inf throughout.  `out` may be
+ * the logits themselves (same pointer, type and stride, else
+ * LPD_ERR_UNSUPPORTED); it may not overlap them otherwise, nor the controls.
+ * controls NULL copies (and converts). */
+int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows, int64_t vocab,
+                       void *out, int32_t out_dtype, int64_t out_row_stride, void *stream);
+
+/* lpd_score under each side's controls (each may be NULL), in one read of each
+ * row; the controlled logits are never written.  Arguments, outputs and status
+ * are those of lpd_score.  A selected token that its side's mask does not
+ * allow, a row whose mask allows nothing and a scale that is not finite and > 0
+ * set LPD_STATUS_NONFINITE, as a non-finite selected logit or log-sum-exp does.
+ * The scale is not rounded into the logits: it enters the exponents and the
+ * final arithmetic in double.
+ * workspace   lpd_workspace_size(LPD_KIND_CONTROLLED, n_rows, vocab, 0) bytes. */
+int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, const lpd_controls *train_controls,
+                         const lpd_controls *rollout_controls, int64_t n_rows, int64_t vocab,
+                         const int32_t *token_ids, const uint8_t *action_mask, double clip_lo, double clip_hi,
+                         float *out_logp_train, float *out_logp_rollout, float *out_dlogp,
+                         lpd_metrics *out_metrics, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of one side's selected-token logprob under its controls with respect
+ * to the raw logits (the form of lpd_logprob_backward):
+ *   out[r, j] = grad_logp[r] * scale[r] * (1[j == token_ids[r]] - p_j) * dx3/dx,
+ * p_j = exp(z_j - lse[r]), lse[r] = z[token_ids[r]] - logp[r]; dx3/dx is
+ * 1 / repetition[r] or repetition[r] (x > 0 or not) for the history's tokens and
+ * 1 for the others; masked places get 0.  The controls themselves get no
+ * gradient.  Arguments, inactive rows and ids outside [0, vocab) as
+ * lpd_logprob_backward; a selected token that is masked gives NaN. out may not
+ * overlap the logits. */
+int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows,
+                                    int64_t vocab, const int32_t *token_ids, const uint8_t *action_mask,
+                                    const float *logp, const float *grad_logp, void *out_dlogits,
+                                    int32_t out_dtype, int64_t out_row_stride, void *stream);
 
 /* ---- attention (out, lse) merge --------------------------------------------- */
 

@@ -33,7 +33,7 @@ LPD_STATUS_NONFINITE = 2
 LPD_STATUS_TIMEOUT = 4
 LPD_FLAG_NO_ACTIVE = 1
 LPD_FLAG_NO_PERCENTILES = 2
-LPD_KIND_SCORE, LPD_KIND_SHARDED = 0, 1
+LPD_KIND_SCORE, LPD_KIND_SHARDED, LPD_KIND_CONTROLLED = 0, 1, 2
 LPD_TOPO_ALLGATHER_PARTIALS_FIXED_MERGE, LPD_TOPO_ALLREDUCE_PARTIALS, LPD_TOPO_ALLGATHER_LOGITS = 0, 1, 2
 TOPOLOGIES = {"allgather_partials_fixed_merge": 0, "allreduce_partials": 1, "allgather_logits": 2}
 
@@ -62,6 +62,15 @@ def transform_struct(ops):
         t.kind[i] = k
         t.param[i] = p
     return t
+
+
+class LpdControls(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("n_history", ctypes.c_int64), ("hist_begin", ctypes.c_void_p),
+                ("hist_split", ctypes.c_void_p), ("hist_end", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("n_bias", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("n_masks", ctypes.c_int64), ("mask_stride", ctypes.c_int64),
+                ("mask_row", ctypes.c_void_p)]
 
 
 class LpdMetrics(ctypes.Structure):
@@ -115,7 +124,9 @@ EXPORTED = ("lpd_workspace_size", "lpd_backend_info", "lpd_strerror", "lpd_score
             "lpd_fused_workspace_size", "lpd_score_fused", "lpd_score_fused_transformed", "lpd_score_transformed",
             "lpd_score_entropy", "lpd_logprob_backward", "lpd_attn_merge", "lpd_attn_merge_order_drift",
             "lpd_topology_workspace_size", "lpd_score_sharded_topology", "lpd_drift_metrics_from_dlogp",
-            "lpd_logp_drift_summary", "lpd_merge_rank_metrics")
+            "lpd_logp_drift_summary", "lpd_merge_rank_metrics", "lpd_controls_apply", "lpd_score_controlled",
+            "lpd_logprob_backward_controlled")
+LPD_MAX_BIAS = 1024
 LPD_NOALLOC_MAX_ROWS = 32768
 LPD_ATTN_MAX_PARTS = 64
 
@@ -182,6 +193,12 @@ def lib() -> ctypes.CDLL:
         L.lpd_merge_rank_metrics.restype = ctypes.c_int
         L.lpd_merge_rank_metrics.argtypes = [P, P, I32, P]
         L.lpd_logp_drift_summary.argtypes = [I64, P, P, P, P, P, P, P]
+        L.lpd_controls_apply.restype = ctypes.c_int
+        L.lpd_controls_apply.argtypes = [P, P, I64, I64, P, I32, I64, P]
+        L.lpd_score_controlled.restype = ctypes.c_int
+        L.lpd_score_controlled.argtypes = [P, P, P, P, I64, I64, P, P, D, D, P, P, P, P, P, SZ, P]
+        L.lpd_logprob_backward_controlled.restype = ctypes.c_int
+        L.lpd_logprob_backward_controlled.argtypes = [P, P, I64, I64, P, P, P, P, P, I32, I64, P]
         _LIB = L
     return _LIB
 
@@ -477,6 +494,162 @@ def lpd_logp_drift_summary(logp_train_a, logp_rollout_a, logp_train_b, logp_roll
     _check(rc, "lpd_logp_drift_summary")
 
 
+@dataclass(frozen=True)
+class Controls:
+    """One side's sampling controls as device tensors (lpd_controls; None leaves
+    a step out).  Row arrays have one entry a logits row: hist_begin, hist_split
+    and hist_end int64 into history int32; repetition, frequency, presence and
+    scale float32; bias_ids int32 and bias float32 [rows, n_bias]; mask int32
+    [n_masks, words] with bit j % 32 of word j / 32 set where token j is
+    allowed; mask_row int32.  The tensors must live as long as this object."""
+    history: object = None
+    hist_begin: object = None
+    hist_split: object = None
+    hist_end: object = None
+    repetition: object = None
+    frequency: object = None
+    presence: object = None
+    scale: object = None
+    bias_ids: object = None
+    bias: object = None
+    mask: object = None
+    mask_row: object = None
+
+    def __post_init__(self):
+        import torch
+
+        kinds = {"history": torch.int32, "hist_begin": torch.int64, "hist_split": torch.int64,
+                 "hist_end": torch.int64, "repetition": torch.float32, "frequency": torch.float32,
+                 "presence": torch.float32, "scale": torch.float32, "bias_ids": torch.int32, "bias": torch.float32,
+                 "mask": torch.int32, "mask_row": torch.int32}
+        rows, device = None, None
+        for name, kind in kinds.items():
+            t = getattr(self, name)
+            if t is None:
+                continue
+            if t.dtype != kind:
+                raise ValueError(f"{name} must be {kind}, got {t.dtype}")
+            if device is not None and t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the other controls on {device}")
+            device = t.device
+            if t.dim() != (2 if name in ("bias_ids", "bias", "mask") else 1):
+                raise ValueError(f"{name} has {t.dim()} dimensions")
+            if name == "mask":
+                if t.shape[1] > 1 and t.stride(1) != 1:
+                    raise ValueError("mask must have contiguous words")
+            elif not t.is_contiguous():
+                raise ValueError(f"{name} must be dense")
+            if name not in ("history", "mask"):
+                if rows is not None and t.shape[0] != rows:
+                    raise ValueError(f"{name} has {t.shape[0]} rows, the other controls {rows}")
+                rows = t.shape[0]
+        if self.history is not None and None in (self.hist_begin, self.hist_split, self.hist_end):
+            raise ValueError("history needs hist_begin, hist_split and hist_end")
+        if (self.bias_ids is None) != (self.bias is None):
+            raise ValueError("bias_ids and bias go together")
+        if self.bias is not None and self.bias.shape != self.bias_ids.shape:
+            raise ValueError("bias and bias_ids must have one shape")
+        m = self.mask
+        n = lambda t: t.shape[0] if t is not None else 0  # noqa: E731
+        struct = LpdControls(_ptr(self.history), n(self.history), _ptr(self.hist_begin), _ptr(self.hist_split),
+                             _ptr(self.hist_end), _ptr(self.repetition), _ptr(self.frequency), _ptr(self.presence),
+                             _ptr(self.scale), _ptr(self.bias_ids), _ptr(self.bias),
+                             self.bias.shape[1] if self.bias is not None else 0, _ptr(m), n(m),
+                             (m.stride(0) if m.shape[0] > 1 else m.shape[1]) if m is not None else 0,
+                             _ptr(self.mask_row))
+        object.__setattr__(self, "_struct", struct)
+        object.__setattr__(self, "_rows", rows)
+        object.__setattr__(self, "_device", device)
+
+
+def _controls(c, logits):
+    """Pointer to the side's lpd_controls (None: no controls) after the checks
+    that only the tensors allow."""
+    if c is None:
+        return None
+    if c._rows is not None and c._rows != logits.shape[0]:
+        raise ValueError(f"controls of {c._rows} rows for {logits.shape[0]} logits rows")
+    if c._device is not None and c._device != logits.device:
+        raise ValueError(f"controls on {c._device}, logits on {logits.device}")
+    return ctypes.byref(c._struct)
+
+
+def _same_rows(n, device, **tensors):
+    for name, (t, kind) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != kind or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a dense {kind} tensor of {n} values on {device}")
+
+
+class _on:
+    """The device of the call's tensors made current, where it is not."""
+
+    def __init__(self, t):
+        import torch
+
+        if not t.is_cuda:
+            raise ValueError("the tensors must be in device memory")
+        self._guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def lpd_controls_apply(logits, controls, out, stream=None) -> None:
+    """The controlled logits of every row into `out` (bf16 or f32; may be `logits`)."""
+    x, o = logits_struct(logits), logits_struct(out)
+    if out.shape != logits.shape or out.device != logits.device:
+        raise ValueError("out must have the logits' shape and device")
+    c = _controls(controls, logits)
+    with _on(logits):
+        rc = lib().lpd_controls_apply(ctypes.byref(x), c, logits.shape[0], logits.shape[1], o.ptr, o.dtype,
+                                      o.row_stride, _stream(stream))
+    _check(rc, "lpd_controls_apply")
+
+
+def lpd_score_controlled(train, rollout, train_controls, rollout_controls, token_ids, action_mask, clip_lo, clip_hi,
+                         out_logp_train, out_logp_rollout, out_dlogp, out_metrics, workspace, stream=None) -> None:
+    import torch
+
+    t, r = logits_struct(train), logits_struct(rollout)
+    if train.shape != rollout.shape or train.device != rollout.device:
+        raise ValueError("train and rollout must have one shape and device")
+    _same_rows(train.shape[0], train.device, token_ids=(token_ids, torch.int32), action_mask=(action_mask, torch.uint8),
+               out_logp_train=(out_logp_train, torch.float32), out_logp_rollout=(out_logp_rollout, torch.float32),
+               out_dlogp=(out_dlogp, torch.float32))
+    ct, cr = _controls(train_controls, train), _controls(rollout_controls, rollout)
+    with _on(train):
+        rc = lib().lpd_score_controlled(ctypes.byref(t), ctypes.byref(r), ct, cr, train.shape[0], train.shape[1],
+                                        _ptr(token_ids), _ptr(action_mask), float(clip_lo), float(clip_hi),
+                                        _ptr(out_logp_train), _ptr(out_logp_rollout), _ptr(out_dlogp),
+                                        _ptr(out_metrics), _ptr(workspace),
+                                        workspace.numel() if workspace is not None else 0, _stream(stream))
+    _check(rc, "lpd_score_controlled")
+
+
+def lpd_logprob_backward_controlled(logits, controls, token_ids, action_mask, logp, grad_logp, out_dlogits,
+                                    stream=None) -> None:
+    import torch
+
+    x, o = logits_struct(logits), logits_struct(out_dlogits)
+    if out_dlogits.shape != logits.shape or out_dlogits.device != logits.device:
+        raise ValueError("out_dlogits must have the logits' shape and device")
+    _same_rows(logits.shape[0], logits.device, token_ids=(token_ids, torch.int32),
+               action_mask=(action_mask, torch.uint8), logp=(logp, torch.float32), grad_logp=(grad_logp, torch.float32))
+    c = _controls(controls, logits)
+    with _on(logits):
+        rc = lib().lpd_logprob_backward_controlled(ctypes.byref(x), c, logits.shape[0], logits.shape[1],
+                                                   _ptr(token_ids), _ptr(action_mask), _ptr(logp), _ptr(grad_logp),
+                                                   o.ptr, o.dtype, o.row_stride, _stream(stream))
+    _check(rc, "lpd_logprob_backward_controlled")
+
+
 # ---- convenience: allocate with torch, call, read back ------------------------
 
 def read_merge_drift(buf) -> dict:
@@ -611,4 +784,28 @@ def score_sharded_topology(train_shards, rollout_shards, v_ranges, token_ids, ac
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     lpd_score_sharded_topology(train_shards, rollout_shards, v_ranges, token_ids, action_mask, clip[0], clip[1],
                                topology, reduce_order, *outs, met, ws, stream)
+    return ScoreResult(*outs, read_metrics(met))
+
+
+def controls_apply(logits, controls, out_dtype=None, stream=None):
+    """The controlled logits in a new tensor (the logits' type unless given)."""
+    import torch
+
+    out = torch.empty(logits.shape, dtype=out_dtype or logits.dtype, device=logits.device)
+    lpd_controls_apply(logits, controls, out, stream)
+    return out
+
+
+def score_controlled(train, rollout, token_ids, action_mask, train_controls=None, rollout_controls=None,
+                     clip=(0.8, 1.2), stream=None) -> ScoreResult:
+    """lpd_score_controlled with torch-allocated outputs and workspace."""
+    import torch
+
+    dev = train.device
+    n = train.shape[0]
+    outs = [torch.empty(n, dtype=torch.float32, device=dev) for _ in range(3)]
+    met = torch.empty(METRICS_BYTES, dtype=torch.uint8, device=dev)
+    ws = torch.empty(lpd_workspace_size(LPD_KIND_CONTROLLED, n, train.shape[1]), dtype=torch.uint8, device=dev)
+    lpd_score_controlled(train, rollout, train_controls, rollout_controls, token_ids, action_mask, clip[0], clip[1],
+                         *outs, met, ws, stream)
     return ScoreResult(*outs, read_metrics(met))

@@ -380,6 +380,76 @@ GatherLayout gather_layout(int64_t n_rows, int64_t vocab, int32_t dt, int32_t dr
     return g;
 }
 
+// Workspace of the controlled scoring path: the common regions (no per-warp
+// states), then one state per active row and chunk, and the selected logits.
+struct ControlledLayout {
+    WsLayout base;
+    size_t part_a, part_b, pick, total;
+};
+
+ControlledLayout controlled_layout(int64_t n_rows, int64_t vocab) {
+    ControlledLayout L{};
+    L.base = ws_layout(n_rows, 0);
+    const size_t parts = static_cast<size_t>(n_rows) * static_cast<size_t>(controls_chunks(vocab));
+    size_t off = L.base.total;
+    L.part_a = off;  off += align256(parts * sizeof(float4));
+    L.part_b = off;  off += align256(parts * sizeof(float));
+    L.pick = off;    off += align256(static_cast<size_t>(n_rows) * sizeof(double2));
+    L.total = off;
+    return L;
+}
+
+bool ptr_aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// A side's controls as the kernels' copy; NULL is none.
+int to_controls(const lpd_controls *c, int64_t n_rows, int64_t vocab, CtlSide *out) {
+    *out = CtlSide{};
+    if (!c) return LPD_OK;
+    if (c->n_history < 0 || c->n_bias < 0 || c->n_masks < 0) return LPD_ERR_BAD_SIZE;
+    if (c->n_bias > LPD_MAX_BIAS) return LPD_ERR_UNSUPPORTED;
+    if (c->history && (!c->hist_begin || !c->hist_split || !c->hist_end) && n_rows > 0) return LPD_ERR_NULL_POINTER;
+    if (c->n_bias > 0 && n_rows > 0 && (!c->bias_ids || !c->bias)) return LPD_ERR_NULL_POINTER;
+    if (c->mask) {
+        if (c->mask_stride < (vocab + 31) / 32) return LPD_ERR_BAD_STRIDE;
+        if (!c->mask_row && c->n_masks < n_rows) return LPD_ERR_BAD_SIZE;
+    }
+    for (const void *p : {static_cast<const void *>(c->history), static_cast<const void *>(c->repetition),
+                          static_cast<const void *>(c->frequency), static_cast<const void *>(c->presence),
+                          static_cast<const void *>(c->scale), static_cast<const void *>(c->bias_ids),
+                          static_cast<const void *>(c->bias), static_cast<const void *>(c->mask),
+                          static_cast<const void *>(c->mask_row)})
+        if (!ptr_aligned(p, 4)) return LPD_ERR_ALIGNMENT;
+    for (const int64_t *p : {c->hist_begin, c->hist_split, c->hist_end})
+        if (!ptr_aligned(p, 8)) return LPD_ERR_ALIGNMENT;
+    out->history = c->history;
+    out->n_history = c->n_history;
+    out->hist_begin = c->hist_begin;
+    out->hist_split = c->hist_split;
+    out->hist_end = c->hist_end;
+    out->counts = c->history && c->n_history > 0 && (c->repetition || c->frequency || c->presence) ? 1 : 0;
+    out->repetition = c->repetition;
+    out->frequency = c->frequency;
+    out->presence = c->presence;
+    out->scale = c->scale;
+    out->bias_ids = c->bias_ids;
+    out->bias = c->bias;
+    out->n_bias = static_cast<int>(c->n_bias);
+    out->mask = c->mask;
+    out->n_masks = c->n_masks;
+    out->mask_stride = c->mask_stride;
+    out->mask_row = c->mask_row;
+    return LPD_OK;
+}
+
+// A [n_rows, vocab] output of the elementwise control forms.
+int check_output(const void *out, int32_t out_dtype, int64_t out_row_stride, int64_t n_rows, int64_t vocab) {
+    if (!out && n_rows > 0) return LPD_ERR_NULL_POINTER;
+    if (!valid_dtype(out_dtype)) return LPD_ERR_BAD_DTYPE;
+    if (out_row_stride < vocab) return LPD_ERR_BAD_STRIDE;
+    if (!elt_aligned(out, out_dtype)) return LPD_ERR_ALIGNMENT;
+    return LPD_OK;
+}
+
 }  // namespace
 }  // namespace lpd
 
@@ -395,8 +465,10 @@ size_t lpd_workspace_size(int32_t kind, int64_t n_rows, int64_t vocab, int32_t n
         case LPD_KIND_SHARDED:
             if (n_shards < 1 || n_shards > kMaxSegments) return 0;
             return ws_layout(n_rows, n_shards).total;
+        case LPD_KIND_CONTROLLED:
+            if (vocab <= 0 || vocab > kMaxVocab) return 0;
+            return controlled_layout(n_rows, vocab).total;
         default:
-            (void)vocab;
             return 0;
     }
 }
@@ -906,6 +978,75 @@ int lpd_score_fused_transformed(const void *hidden_train, const void *hidden_rol
         return rc;
     if ((rc = cuda_status(launch_fused(c, s)))) return rc;
     return run_metrics(n_rows, clip_lo, clip_hi, out_metrics, w, s);
+}
+
+int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows, int64_t vocab,
+                       void *out, int32_t out_dtype, int64_t out_row_stride, void *stream) {
+    int rc = check_rows_vocab(n_rows, vocab);
+    if (rc) return rc;
+    if ((rc = check_logits(logits, n_rows, vocab))) return rc;
+    if ((rc = check_output(out, out_dtype, out_row_stride, n_rows, vocab))) return rc;
+    if (out == logits->ptr && n_rows > 0 &&
+        (out_dtype != logits->dtype || (n_rows > 1 && out_row_stride != logits->row_stride)))
+        return LPD_ERR_UNSUPPORTED;
+    CtlSide c;
+    if ((rc = to_controls(controls, n_rows, vocab, &c))) return rc;
+    return cuda_status(launch_controls_apply(c, logits->ptr, logits->dtype, logits->row_stride, out, out_dtype,
+                                             out_row_stride, n_rows, vocab, static_cast<cudaStream_t>(stream)));
+}
+
+int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, const lpd_controls *train_controls,
+                         const lpd_controls *rollout_controls, int64_t n_rows, int64_t vocab,
+                         const int32_t *token_ids, const uint8_t *action_mask, double clip_lo, double clip_hi,
+                         float *out_logp_train, float *out_logp_rollout, float *out_dlogp,
+                         lpd_metrics *out_metrics, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = validate_pair(train, rollout, n_rows, vocab);
+    if (rc) return rc;
+    if (!out_metrics || ((!token_ids || !action_mask) && n_rows > 0)) return LPD_ERR_NULL_POINTER;
+    if ((rc = check_clip(clip_lo, clip_hi))) return rc;
+    CtlScoreArgs a{};
+    if ((rc = to_controls(train_controls, n_rows, vocab, &a.t))) return rc;
+    if ((rc = to_controls(rollout_controls, n_rows, vocab, &a.r))) return rc;
+    const ControlledLayout L = controlled_layout(n_rows, vocab);
+    if ((rc = check_workspace(workspace, workspace_bytes, L.total))) return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Ws w = carve(workspace, n_rows, 0);
+    char *base = static_cast<char *>(workspace);
+    if ((rc = run_select(n_rows, token_ids, action_mask, out_logp_train, out_logp_rollout, out_dlogp, out_metrics, w,
+                         s)))
+        return rc;
+    a.xt = static_cast<const char *>(train->ptr);
+    a.xr = static_cast<const char *>(rollout->ptr);
+    a.t_stride = train->row_stride * elt_bytes(train->dtype);
+    a.r_stride = rollout->row_stride * elt_bytes(rollout->dtype);
+    a.vocab = vocab;
+    a.hdr = w.hdr;
+    a.rowid = w.rowid;
+    a.part_a = reinterpret_cast<float4 *>(base + L.part_a);
+    a.part_b = reinterpret_cast<float *>(base + L.part_b);
+    a.pick = reinterpret_cast<double2 *>(base + L.pick);
+    if ((rc = cuda_status(launch_controls_score(a, train->dtype, rollout->dtype, n_rows, out_logp_train,
+                                                out_logp_rollout, out_dlogp, w.dval, w.keys, &out_metrics->status,
+                                                s))))
+        return rc;
+    return run_metrics(n_rows, clip_lo, clip_hi, out_metrics, w, s);
+}
+
+int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows,
+                                    int64_t vocab, const int32_t *token_ids, const uint8_t *action_mask,
+                                    const float *logp, const float *grad_logp, void *out_dlogits, int32_t out_dtype,
+                                    int64_t out_row_stride, void *stream) {
+    int rc = check_rows_vocab(n_rows, vocab);
+    if (rc) return rc;
+    if ((rc = check_logits(logits, n_rows, vocab))) return rc;
+    if (n_rows > 0 && (!token_ids || !action_mask || !logp || !grad_logp)) return LPD_ERR_NULL_POINTER;
+    if ((rc = check_output(out_dlogits, out_dtype, out_row_stride, n_rows, vocab))) return rc;
+    if (out_dlogits == logits->ptr && n_rows > 0) return LPD_ERR_UNSUPPORTED;
+    CtlSide c;
+    if ((rc = to_controls(controls, n_rows, vocab, &c))) return rc;
+    return cuda_status(launch_controls_gradient(c, logits->ptr, logits->dtype, logits->row_stride, out_dlogits,
+                                                out_dtype, out_row_stride, n_rows, vocab, token_ids, action_mask, logp,
+                                                grad_logp, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

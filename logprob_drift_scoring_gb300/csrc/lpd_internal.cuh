@@ -232,6 +232,49 @@ cudaError_t launch_backward(const void *x, int x_dtype, int64_t x_stride_elems, 
                             int64_t out_stride_elems, int64_t n_rows, int64_t vocab, const int32_t *ids,
                             const uint8_t *mask, const float *logp, const float *grad, cudaStream_t stream);
 
+// ---------------------------------------------------------------- sampling controls
+// One side's controls as the kernels take them (include/lpd.h, lpd_controls);
+// all zero: no controls.
+struct CtlSide {
+    const int32_t *history;
+    int64_t n_history;
+    const int64_t *hist_begin, *hist_split, *hist_end;
+    int counts;  // a history and at least one penalty
+    const float *repetition, *frequency, *presence, *scale;
+    const int32_t *bias_ids;
+    const float *bias;
+    int n_bias;
+    const uint32_t *mask;
+    int64_t n_masks, mask_stride;
+    const int32_t *mask_row;
+};
+
+struct CtlScoreArgs {
+    CtlSide t, r;
+    const char *xt, *xr;
+    int64_t t_stride, r_stride;  // bytes
+    int64_t vocab;
+    int n_chunks;
+    int same;                    // both sides mark the same tokens: one table
+    const WsHeader *hdr;
+    const int2 *rowid;
+    float4 *part_a;              // [active row][chunk] (mt, st, dd, mr)
+    float *part_b;               // [active row][chunk] sr
+    double2 *pick;               // selected controlled logits, before the scale
+};
+
+int controls_chunks(int64_t vocab);  // units a row of the scoring form
+cudaError_t launch_controls_apply(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
+                                  int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,
+                                  cudaStream_t stream);
+cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
+                                     int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,
+                                     const int32_t *ids, const uint8_t *mask, const float *logp, const float *grad,
+                                     cudaStream_t stream);
+cudaError_t launch_controls_score(const CtlScoreArgs &a, int dtype_t, int dtype_r, int64_t n_rows, float *out_lt,
+                                  float *out_lr, float *out_d, double *dval, uint32_t *keys, uint32_t *status,
+                                  cudaStream_t stream);
+
 // Attention (out, lse) merge: one call of lpd_attn_merge (diag false) or of
 // lpd_attn_merge_order_drift (diag true).  Orders are validated permutations.
 struct AttnMergeCall {

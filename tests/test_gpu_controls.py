@@ -1,0 +1,486 @@
+"""Sampling controls on the GPU (needs a GPU): the controlled logits, the scores
+and the gradients against the float64 definition in controls_ref.py.
+
+Bounds.  Apply: a touched logit is carried as two floats and scaled in one
+multiply-add, an untouched one is one product, so float32 is within two
+roundings (2^-23) of the value, plus 2^-46 of the intermediate terms (at most
+some hundreds here: 1e-10); bf16 adds its half step, 2^-8.  Logprobs: an exponent
+a = (x - m) s log2 e carries three roundings, 3 * 2^-24 |a|, and terms below
+2^-40 do not count, so a term is off by at most 40 * 3 * 2^-24 * ln 2 = 5e-6
+relative, and so is the sum; the special-function unit adds 2^-22 and the sums
+some 2^-24: 1e-5 in all, and the float32 result 2^-24 of itself.  Gradients:
+the same 1e-5 on p, three roundings on the rest.
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests import controls_ref as ref
+from logprob_drift_scoring_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+KINDS = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {"bf16": 2.0 ** -8, "f32": 0.0}
+
+
+def to_device(c):
+    return B.Controls(**{k: torch.from_numpy(np.ascontiguousarray(v)).to(DEV) for k, v in c.items()})
+
+
+def tensor(x, kind, pad=0):
+    t = torch.from_numpy(x.astype(np.float32)).to(DEV).to(KINDS[kind])
+    if pad:
+        wide = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=DEV)
+        wide[:, :t.shape[1]] = t
+        t = wide[:, :t.shape[1]]
+    return t
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def check_apply(c, x, out_kind, out):
+    got, xh = host(out), host(x)
+    for r in range(len(xh)):
+        z, _ = ref.row(c, xh[r], r)
+        inf = np.isneginf(z)
+        assert np.array_equal(np.isneginf(got[r]), inf), r
+        err = np.abs(got[r][~inf] - z[~inf])
+        assert np.all(err <= (2.0 ** -23 + HALF[out_kind]) * np.abs(z[~inf]) + 1e-10), (r, err.max())
+
+
+@pytest.mark.parametrize("vocab,pad", [(1, 0), (5, 3), (31, 0), (33, 7), (1000, 8), (2048, 0), (2049, 0), (8193, 7),
+                                       (20011, 0), (20016, 0)])
+@pytest.mark.parametrize("xk,ok", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+def test_apply(vocab, pad, xk, ok):
+    rng = np.random.default_rng(vocab + pad)
+    rows = 7
+    c = ref.random_controls(rng, rows, vocab, history=70)
+    x = tensor(rng.normal(0, 3, (rows, vocab)), xk, pad)
+    check_apply(c, x, ok, B.controls_apply(x, to_device(c), KINDS[ok]))
+
+
+@pytest.mark.parametrize("rows,vocab,history", [(200, 20008, 300), (3, 50000, 40000), (90, 40007, 900)])
+def test_apply_many_units(rows, vocab, history):
+    """Both chunk widths, several units a block (the table is zero again after each)."""
+    rng = np.random.default_rng(rows)
+    c = ref.random_controls(rng, rows, vocab, history=history, masks=3, bias=40)
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "bf16")
+    check_apply(c, x, "bf16", B.controls_apply(x, to_device(c)))
+
+
+@pytest.mark.parametrize("leave", ["history", "bias", "masks", "scale", "penalties", "all"])
+def test_apply_parts_left_out(leave):
+    rng = np.random.default_rng(3)
+    parts = ("repetition", "frequency", "presence", "scale")
+    kw = {"history": dict(history=None), "bias": dict(bias=0), "masks": dict(masks=0), "scale": dict(parts=parts[:3]),
+          "penalties": dict(parts=("scale",)), "all": dict(history=None, bias=0, masks=0, parts=())}[leave]
+    c = ref.random_controls(rng, 5, 700, **kw)
+    x = tensor(rng.normal(0, 3, (5, 700)), "f32")
+    check_apply(c, x, "f32", B.controls_apply(x, to_device(c)))
+    if leave == "all":
+        assert torch.equal(B.controls_apply(x, None), x)
+        assert torch.equal(B.controls_apply(x, None, torch.bfloat16), x.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("name", ["repetition", "frequency", "presence"])
+def test_apply_one_penalty(name):
+    rng = np.random.default_rng(4)
+    c = ref.random_controls(rng, 6, 900, bias=0, masks=0, parts=(name,))
+    x = tensor(rng.normal(0, 3, (6, 900)), "f32")
+    check_apply(c, x, "f32", B.controls_apply(x, to_device(c)))
+
+
+def test_apply_in_place_and_zero_rows():
+    rng = np.random.default_rng(5)
+    for kind, vocab, pad in (("bf16", 9001, 7), ("f32", 4096, 0)):
+        c = to_device(ref.random_controls(rng, 40, vocab, history=200))
+        x = tensor(rng.normal(0, 3, (40, vocab)), kind, pad)
+        want = B.controls_apply(x, c)
+        B.lpd_controls_apply(x, c, x)
+        assert torch.equal(x, want)
+    empty = torch.empty(0, 16, device=DEV)
+    B.lpd_controls_apply(empty, None, empty)
+
+
+def test_apply_leaves_the_padding():
+    rng = np.random.default_rng(6)
+    for vocab in (100, 8200, 8203):
+        c = to_device(ref.random_controls(rng, 9, vocab))
+        x = tensor(rng.normal(0, 3, (9, vocab)), "bf16", 5)
+        wide = torch.full((10, vocab + 11), 7.0, device=DEV)
+        B.lpd_controls_apply(x, c, wide[:9, :vocab])
+        assert bool((wide[:, vocab:] == 7).all()) and bool((wide[9] == 7).all())
+
+
+def test_ranges_are_clamped():
+    """Offsets outside the history, crossed offsets, a begin that passes 32 bits."""
+    rng = np.random.default_rng(7)
+    c = ref.random_controls(rng, 6, 300, history=20)
+    c["hist_begin"][:] = [-5, 3, 1 << 40, 15, 0, -(1 << 62)]
+    c["hist_split"][:] = [-9, 1, 5, 30, 1 << 50, 0]
+    c["hist_end"][:] = [9, 50, 1 << 41, 4, 21, (1 << 62)]
+    x = tensor(rng.normal(0, 3, (6, 300)), "f32")
+    check_apply(c, x, "f32", B.controls_apply(x, to_device(c)))
+
+
+def test_masks():
+    """Every row its own mask; nothing allowed; a mask row behind the table."""
+    rng = np.random.default_rng(8)
+    c = ref.random_controls(rng, 5, 333, masks=5)
+    c["mask"][2] = 0
+    x = tensor(rng.normal(0, 3, (5, 333)), "f32")
+    for rows in (None, np.array([0, 5, 2, -7, 1 << 30], np.int32)):
+        d = dict(c)
+        if rows is None:
+            del d["mask_row"]
+        else:
+            d["mask_row"] = rows
+        out = B.controls_apply(x, to_device(d))
+        check_apply(d, x, "f32", out)
+        assert bool(torch.isneginf(out[2]).all())
+    # a mask table with rows wider than the vocabulary, set bits behind its end
+    wide = np.full((5, 40), -1, np.int32)
+    d = dict(c, mask=wide)
+    check_apply(d, x, "f32", B.controls_apply(x, to_device(d)))
+
+
+def test_what_masked_places_hold_does_not_matter():
+    rng = np.random.default_rng(9)
+    rows, vocab = 6, 9000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, masks=rows, keep=ids)
+    c["mask_row"] = np.arange(rows, dtype=np.int32)
+    for r in range(rows):
+        c["mask"][r, ids[r] // 32] |= np.int32(np.uint32(1 << (ids[r] % 32)).view(np.int32))
+    x = rng.normal(0, 3, (rows, vocab))
+    dirty = x.copy()
+    for r in range(rows):
+        z, _ = ref.row(c, x[r], r)
+        off = np.flatnonzero(np.isneginf(z))
+        dirty[r, off] = rng.choice([np.nan, np.inf, -np.inf, 3.4e38, -3.4e38], len(off))
+    h = to_device(c)
+    idt, act = torch.from_numpy(ids).to(DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    a, b = tensor(x, "f32"), tensor(dirty, "f32")
+    assert torch.equal(B.controls_apply(a, h), B.controls_apply(b, h))
+    s1, s2 = (B.score_controlled(t, t, idt, act, h, h) for t in (a, b))
+    assert s2.metrics["status"] == 0
+    for k in ("logp_train", "logp_rollout", "dlogp"):
+        assert torch.equal(getattr(s1, k), getattr(s2, k))
+    g = torch.randn(rows, device=DEV)
+    o1, o2 = torch.empty_like(a), torch.empty_like(a)
+    B.lpd_logprob_backward_controlled(a, h, idt, act, s1.logp_train, g, o1)
+    B.lpd_logprob_backward_controlled(b, h, idt, act, s1.logp_train, g, o2)
+    assert torch.equal(o1, o2)
+
+
+def test_extreme_logits():
+    """The type's lowest value as a mask, infinities among touched tokens."""
+    rng = np.random.default_rng(10)
+    c = ref.random_controls(rng, 4, 500, history=400, masks=0)
+    c["repetition"][:] = 2.0
+    for kind in KINDS:
+        x = rng.normal(0, 3, (4, 500))
+        x[:, ::2] = torch.finfo(KINDS[kind]).min
+        x[1, 1::4] = -np.inf
+        t = tensor(x, kind)
+        out = host(B.controls_apply(t, to_device(c), torch.float32))
+        for r in range(4):
+            z, _ = ref.row(c, host(t)[r], r)
+            z = np.where(z < -3.4028235e38, -np.inf, z)
+            ok = np.isclose(out[r], z, rtol=2.0 ** -22, atol=1e-6) | (out[r] == z)
+            assert ok.all(), (kind, r)
+        ids = torch.full((4,), 3, dtype=torch.int32, device=DEV)
+        s = B.score_controlled(t, t, ids, torch.ones(4, dtype=torch.uint8, device=DEV), to_device(c), to_device(c))
+        for r in (0, 2, 3):
+            z, _ = ref.row(c, host(t)[r], r)
+            assert abs(float(s.logp_train[r]) - ref.logp(z, 3)) <= 1e-5 + 2.0 ** -23 * abs(ref.logp(z, 3))
+            assert float(s.dlogp[r]) == 0.0
+
+
+def check_score(ct, cr, x, y, ids, act, res):
+    xh, yh = host(x), host(y)
+    for side, c, v, got in (("t", ct, xh, res.logp_train), ("r", cr, yh, res.logp_rollout)):
+        got = got.double().cpu().numpy()
+        for r in range(len(ids)):
+            if not act[r]:
+                assert got[r] == 0.0
+                continue
+            want = ref.logp(ref.row(c, v[r], r)[0], ids[r])
+            assert abs(got[r] - want) <= 1e-5 + 2.0 ** -23 * abs(want), (side, r, got[r], want)
+    d = res.dlogp.double().cpu().numpy()
+    for r in np.flatnonzero(act):
+        want = ref.logp(ref.row(ct, xh[r], r)[0], ids[r]) - ref.logp(ref.row(cr, yh[r], r)[0], ids[r])
+        assert abs(d[r] - want) <= 2e-5 + 2.0 ** -23 * abs(want)
+    # the metrics are those of the per-token differences (the scorer's own stage, held to the oracle elsewhere)
+    m = B.drift_metrics_from_dlogp(res.dlogp, torch.from_numpy(act).to(DEV))
+    assert res.metrics["n_active"] == m["n_active"] == int(act.sum()) and res.metrics["status"] == 0
+    for k in ("mean_abs_dlogp", "max_abs_dlogp", "p95_abs_dlogp", "ratio0_mean"):
+        assert abs(res.metrics[k] - m[k]) <= 1e-6 * (1 + abs(m[k]))
+
+
+@pytest.mark.parametrize("vocab,pad", [(1, 0), (2, 1), (40, 0), (1000, 3), (8192, 0), (8200, 8), (16385, 7), (30000, 0)])
+@pytest.mark.parametrize("xk,yk", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("sides", ["both", "own", "rollout", "train", "none"])
+def test_score(vocab, pad, xk, yk, sides):
+    if sides != "both" and xk != yk:
+        pytest.skip("the type pairs are covered with one handle")
+    rng = np.random.default_rng(vocab * 7 + pad)
+    rows = 9
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    x = rng.normal(0, 3, (rows, vocab))
+    y = x + rng.normal(0, 2e-3, x.shape)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=60)
+    c["history"][5] = ids[0]
+    other = ref.random_controls(rng, rows, vocab, keep=ids, history=33, bias=2)
+    ct, cr = {"both": (c, c), "own": (c, other), "rollout": ({}, c), "train": (c, {}), "none": ({}, {})}[sides]
+    h = to_device(c)
+    ht, hr = {"both": (h, h), "own": (h, to_device(other)), "rollout": (None, h), "train": (h, None),
+              "none": (None, None)}[sides]
+    act = (rng.random(rows) < 0.8).astype(np.uint8)
+    act[0] = 1
+    xt, yt = tensor(x, xk, pad), tensor(y, yk, pad)
+    res = B.score_controlled(xt, yt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), ht, hr)
+    check_score(ct, cr, xt, yt, ids, act, res)
+
+
+def test_score_differing_bias_over_one_history():
+    """One history, one bias list, other values and penalties a side: one table serves both."""
+    rng = np.random.default_rng(11)
+    rows, vocab = 8, 9000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, history=500, masks=0, bias=20)
+    ids[:4] = c["bias_ids"][:4, 1].clip(0, vocab - 1)
+    d = dict(c, bias=-c["bias"], repetition=c["repetition"][::-1].copy(), scale=c["scale"][::-1].copy())
+    shared = {k: torch.from_numpy(v).to(DEV) for k, v in c.items()}
+    ht = B.Controls(**shared)
+    hr = B.Controls(**{**shared, **{k: torch.from_numpy(d[k]).to(DEV) for k in ("bias", "repetition", "scale")}})
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "bf16")
+    act = np.ones(rows, np.uint8)
+    check_score(c, d, x, x, ids, act, B.score_controlled(x, x, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), ht, hr))
+
+
+def test_score_of_applied_logits():
+    """lpd_score on the float32 controlled logits gives the same logprobs."""
+    rng = np.random.default_rng(12)
+    rows, vocab = 50, 33000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=800)
+    h, idt = to_device(c), torch.from_numpy(ids).to(DEV)
+    act = torch.ones(rows, dtype=torch.uint8, device=DEV)
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "bf16")
+    y = (x.float() + 1e-3 * torch.randn(rows, vocab, device=DEV)).to(torch.bfloat16)
+    a = B.score_controlled(x, y, idt, act, h, h)
+    b = B.score(B.controls_apply(x, h, torch.float32), B.controls_apply(y, h, torch.float32), idt, act)
+    # the applied logits are rounded to float32: 2^-24 of at most 64, twice
+    for k in ("logp_train", "logp_rollout"):
+        assert float((getattr(a, k) - getattr(b, k)).abs().max()) <= 2e-5 + 8e-6
+    n = B.score_controlled(x, y, idt, act)
+    m = B.score(x, y, idt, act)
+    assert float((n.dlogp - m.dlogp).abs().max()) <= 2e-5
+
+
+def test_batch_invariance_and_load_paths():
+    """A row's bits do not depend on its batch, its place, or its alignment."""
+    rng = np.random.default_rng(13)
+    rows, vocab = 30, 20003
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=400, masks=4, bias=9)
+    x = rng.normal(0, 3, (rows, vocab))
+    y = x + rng.normal(0, 2e-3, x.shape)
+
+    def run(at, pad, kind="f32"):
+        d = {k: (v[at] if k not in ("history", "mask") else v) for k, v in c.items()}
+        h = to_device(d)
+        r = B.score_controlled(tensor(x[at], kind, pad), tensor(y[at], kind, pad), torch.from_numpy(ids[at]).to(DEV),
+                               torch.ones(len(at), dtype=torch.uint8, device=DEV), h, h)
+        return [r.logp_train, r.logp_rollout, r.dlogp]
+
+    full = run(np.arange(rows), 0)
+    for at in ([4], [29, 4, 0], list(range(10, 20))):
+        for pad in (0, 1, 5):
+            for a, b in zip(full, run(np.array(at), pad)):
+                assert torch.equal(a[at], b), (at, pad)
+    # bf16 values scored as bf16 and as their float32 copies
+    x = host(tensor(x, "bf16"))
+    y = host(tensor(y, "bf16"))
+    for a, b in zip(run(np.arange(rows), 0, "bf16"), run(np.arange(rows), 3, "f32")):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("what", ["masked_id", "nothing_allowed", "bad_scale", "nan_logit", "oob"])
+def test_score_status(what):
+    rng = np.random.default_rng(14)
+    rows, vocab = 4, 600
+    ids = np.array([1, 2, 3, 4], np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, masks=rows)
+    c["mask_row"] = np.arange(rows, dtype=np.int32)
+    for r in range(rows):
+        c["mask"][r, 0] |= 0x1E
+    x = rng.normal(0, 3, (rows, vocab))
+    if what == "masked_id":
+        c["mask"][1, 0] &= ~4
+    elif what == "nothing_allowed":
+        c["mask"][1] = 0
+    elif what == "bad_scale":
+        c["scale"][1] = 0.0
+    elif what == "nan_logit":
+        x[1, 2] = np.nan
+    else:
+        ids[1] = vocab
+    h, t = to_device(c), tensor(x, "f32")
+    act = torch.ones(rows, dtype=torch.uint8, device=DEV)
+    idt = torch.from_numpy(ids).to(DEV)
+    res = B.score_controlled(t, t, idt, act, h, h)
+    assert res.metrics["status"] == (B.LPD_STATUS_TOKEN_OOB if what == "oob" else B.LPD_STATUS_NONFINITE)
+    for r in (0, 2, 3):
+        want = ref.logp(ref.row(c, host(t)[r], r)[0], ids[r])
+        assert abs(float(res.logp_train[r]) - want) <= 1e-5 + 2.0 ** -23 * abs(want)
+    assert not np.isfinite(float(res.logp_train[1]))
+    out = torch.empty(rows, vocab, device=DEV)
+    B.lpd_logprob_backward_controlled(t, h, idt, act, res.logp_train, torch.ones(rows, device=DEV), out)
+    assert bool(torch.isfinite(out[[0, 2, 3]]).all())
+    if what == "nothing_allowed":
+        assert bool((out[1] == 0).all())
+    else:
+        assert bool(torch.isnan(out[1]).any())
+    # the row counts nowhere when it is inactive
+    act[1] = 0
+    res = B.score_controlled(t, t, idt, act, h, h)
+    assert res.metrics["status"] == 0 and res.metrics["n_active"] == 3
+    none = B.score_controlled(t, t, idt, torch.zeros_like(act), h, h)
+    assert none.metrics["n_active"] == 0 and none.metrics["flags"] == B.LPD_FLAG_NO_ACTIVE
+
+
+@pytest.mark.parametrize("vocab,pad", [(1, 0), (7, 2), (65, 0), (2050, 0), (8192, 0), (20011, 3)])
+@pytest.mark.parametrize("xk,ok", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")])
+def test_gradient(vocab, pad, xk, ok):
+    rng = np.random.default_rng(vocab + 1)
+    rows = 8
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=60)
+    c["history"][7] = ids[1]
+    x = tensor(rng.normal(0, 3, (rows, vocab)), xk, pad)
+    xh = host(x)
+    act = np.ones(rows, np.uint8)
+    act[3] = 0
+    g = rng.normal(0, 1, rows).astype(np.float32)
+    lp = np.array([ref.logp(ref.row(c, xh[r], r)[0], ids[r]) for r in range(rows)]).astype(np.float32)
+    lp[3] = np.nan
+    wide = torch.full((rows, vocab + pad), 5.0, dtype=KINDS[ok], device=DEV)
+    out = wide[:, :vocab]
+    B.lpd_logprob_backward_controlled(x, to_device(c), *(torch.from_numpy(v).to(DEV) for v in (ids, act, lp, g)), out)
+    got = host(out)
+    assert bool((wide[:, vocab:] == 5).all())
+    for r in range(rows):
+        if not act[r]:
+            assert np.all(got[r] == 0)
+            continue
+        z, slope = ref.row(c, xh[r], r)
+        p = np.exp(z - z[ids[r]] + np.float64(lp[r]))
+        hot = np.arange(vocab) == ids[r]
+        want = g[r] * slope * (hot - p)
+        # logp's own rounding is an input: p follows it on both sides
+        tol = np.abs(g[r] * slope) * 1e-5 * p + (2.0 ** -21 + HALF[ok]) * np.abs(want) + 2.0 ** -24 * np.abs(g[r] * slope) * hot
+        assert np.all(np.abs(got[r] - want) <= tol + 1e-38), (r, np.max(np.abs(got[r] - want) - tol))
+
+
+def test_gradient_against_differences():
+    """Central differences of the float64 logprob with respect to single raw logits."""
+    rng = np.random.default_rng(15)
+    rows, vocab, h = 6, 300, 1e-4
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=100)
+    c["history"][:rows] = ids
+    x = rng.normal(0, 3, (rows, vocab)).astype(np.float32)
+    x[np.abs(x) < 1e-3] = 0.5  # the penalty's kink
+    t = tensor(x, "f32")
+    x = host(t)
+    idt, act = torch.from_numpy(ids).to(DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    hc = to_device(c)
+    res = B.score_controlled(t, t, idt, act, hc, hc)
+    out = torch.empty_like(t)
+    B.lpd_logprob_backward_controlled(t, hc, idt, act, res.logp_train, torch.ones(rows, device=DEV), out)
+    got = host(out)
+    for r in range(rows):
+        begin, _, end = ref.clamp_range(c, r)
+        for j in [int(ids[r])] + [int(v) for v in c["history"][begin:end][:4] if 0 <= v < vocab] + rng.integers(0, vocab, 6).tolist():
+            f = []
+            for d in (h, -h):
+                v = x[r].copy()
+                v[j] += d
+                f.append(ref.logp(ref.row(c, v, r)[0], ids[r]))
+            # third derivative at most slope^3 <= 64: h^2 * 64 / 6 = 1e-7; the forward's 1e-5 on p
+            assert abs((f[0] - f[1]) / (2 * h) - got[r, j]) <= 4e-5 + 2.0 ** -20 * abs(got[r, j]), (r, j)
+
+
+def test_long_history_counts():
+    """More occurrences than a small counter holds; a history far longer than a row."""
+    rng = np.random.default_rng(16)
+    n, vocab = 200_000, 700
+    c = {"history": rng.integers(0, 5, n).astype(np.int32), "hist_begin": np.zeros(2, np.int64),
+         "hist_split": np.array([0, 150_000], np.int64), "hist_end": np.array([n, n - 1], np.int64),
+         "frequency": np.array([1e-4, 2e-5], np.float32), "presence": np.array([0.5, 0.0], np.float32),
+         "repetition": np.array([1.1, 1.3], np.float32)}
+    x = tensor(rng.normal(0, 3, (2, vocab)), "f32")
+    check_apply(c, x, "f32", B.controls_apply(x, to_device(c)))
+
+
+def test_streams_graphs_and_determinism():
+    """Two streams with a workspace each; a captured and replayed run on new inputs; the same bits each time."""
+    rng = np.random.default_rng(17)
+    rows, vocab = 60, 40000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    h = to_device(ref.random_controls(rng, rows, vocab, keep=ids, history=3000, masks=6, bias=30))
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "bf16")
+    y = (x.float() + 1e-3).to(torch.bfloat16)
+    idt, act = torch.from_numpy(ids).to(DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    g = torch.randn(rows, device=DEV)
+
+    def buffers():
+        outs = [torch.empty(rows, device=DEV) for _ in range(3)]
+        met = torch.empty(B.METRICS_BYTES, dtype=torch.uint8, device=DEV)
+        ws = torch.empty(B.lpd_workspace_size(B.LPD_KIND_CONTROLLED, rows, vocab), dtype=torch.uint8, device=DEV)
+        return outs, met, ws, torch.empty_like(x), torch.empty_like(x)
+
+    def step(b):
+        outs, met, ws, z, dx = b
+        B.lpd_controls_apply(x, h, z)
+        B.lpd_score_controlled(x, y, h, h, idt, act, 0.8, 1.2, *outs, met, ws)
+        B.lpd_logprob_backward_controlled(x, h, idt, act, outs[0], g, dx)
+
+    def results(b):
+        torch.cuda.synchronize()
+        # as bytes: the flipped ids select masked tokens, whose logprob is not finite
+        return [t.view(torch.uint8).clone() for t in (*b[0], b[1], b[3], b[4])]
+
+    first = buffers()
+    step(first)
+    want = results(first)
+    sets = [buffers(), buffers()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, b in zip(streams, sets):
+            with torch.cuda.stream(s):
+                step(b)
+    for b in sets:
+        for a, w in zip(results(b), want):
+            assert torch.equal(a, w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(first)
+    x.copy_((x.float() * 0.9).to(torch.bfloat16))
+    idt.copy_(idt.flip(0))
+    h.scale.mul_(1.1)
+    h.hist_end.sub_(7)
+    for t in (*first[0], first[1], first[3], first[4]):
+        t.zero_()
+    graph.replay()
+    replayed = results(first)
+    step(sets[0])
+    for a, b in zip(replayed, results(sets[0])):
+        assert torch.equal(a, b)
+    assert not torch.equal(replayed[0], want[0])
