@@ -68,6 +68,8 @@ extern "C" {
 /* ---- element types --------------------------------------------------- */
 #define LPD_BF16 0 /* bfloat16, 2 bytes */
 #define LPD_F32 1  /* IEEE float32, 4 bytes */
+#define LPD_E4M3 2 /* 8-bit float, 4 exponent bits, largest value 448 (block-scaled operands only) */
+#define LPD_E5M2 3 /* 8-bit float, 5 exponent bits, largest value 57344 (block-scaled operands only) */
 
 /* ---- return codes ----------------------------------------------------- */
 #define LPD_OK 0
@@ -587,6 +589,60 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
                                     int64_t vocab, const int32_t *token_ids, const uint8_t *action_mask,
                                     const float *logp, const float *grad_logp, void *out_dlogits,
                                     int32_t out_dtype, int64_t out_row_stride, void *stream);
+
+/* ---- block-scaled 8-bit products ---------------------------------------------- */
+
+/* An operand of the 8-bit matrix product: [rows, k] of 8-bit floats, k innermost,
+ * with one float32 scale for each block of 128 values along k, of one row
+ * (block = 0) or of 128 rows (block = 1).  Element (r, c) stands for
+ *     value(r, c) * scales[(block ? r / 128 : r) * scale_stride + c / 128].
+ * This is how a rollout engine holds its LM head and the hidden rows in front
+ * of it; its rounding is one of the drift sources that the scorer measures
+ * ("[WS2] Framework for ablation experiment", LogProb knobs table, rows 9-10). */
+typedef struct {
+    void *ptr;            /* device, row 0; 16-byte aligned for the product */
+    int32_t dtype;        /* LPD_E4M3 or LPD_E5M2 */
+    int32_t block;        /* 0: 1 x 128 scales, 1: 128 x 128 scales */
+    int64_t row_stride;   /* elements (bytes) between rows, >= k; a multiple of 16 for the product */
+    float *scales;        /* device [rows or ceil(rows / 128), scale_stride] */
+    int64_t scale_stride; /* floats between rows of scales, >= ceil(k / 128) */
+} lpd_block_scaled;
+
+/* Quantises x [rows, cols] (bf16 or f32) into `out`: the same matrix
+ * (transpose 0: out is [rows, cols], blocks along x's columns) or its transpose
+ * (transpose 1: out is [cols, rows], blocks along x's rows, as the gradients'
+ * products take them).  For each block, with top = max(largest |x|, 2^-64) and
+ * most = 448 or 57344:
+ *     pow2 = 0:  scale = top / most,                    value = round(x * (most / top))
+ *     pow2 = 1:  scale = that, up to a power of two,    value = round(x / scale)
+ * (the quotients in float32; round to nearest even, saturating).  A block with
+ * a NaN or an infinity reads as NaN throughout.  Bytes between out's last
+ * column and its row stride are left as they were.  out->ptr, out->scales:
+ * written; the struct itself is read. */
+int lpd_block_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols,
+                       int32_t transpose, int32_t pow2, const lpd_block_scaled *out, void *stream);
+
+/* Bytes of device workspace that lpd_block_matmul needs for these sizes on the
+ * current device (0 for invalid arguments). */
+size_t lpd_block_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* out[m, n] = sum_k A[m, k] B[n, k] over the values that the operands stand for,
+ * in float32 (the 128 products of a block on the tensor cores, the blocks in
+ * ascending order), rounded once to out_dtype (LPD_BF16 or LPD_F32).  With Y =
+ * X W^T the forward product is (X, W), the data gradient (dY, W^T) and the
+ * weight gradient (dY^T, X^T): the transposes come from lpd_block_quantize.
+ * The two operands may differ in type and in scale shape.  k = 0 gives zeros.
+ * workspace   lpd_block_workspace_size(m, n, k) bytes, 256-byte aligned.  Its
+ *             first word receives LPD_STATUS_TIMEOUT if an internal wait gives
+ *             up (never expected; the output then holds NaN) and is not
+ *             touched otherwise.
+ * Where n > 256 * (multiprocessors - 1), or m does not change the number of
+ * 128-row tiles, a row's bits do not depend on the other rows; with fewer
+ * columns the k axis may be split over multiprocessors, by a rule on (m, n, k),
+ * and the parts are added in order.  The same call gives the same bits. */
+int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64_t m, int64_t n, int64_t k,
+                     void *out, int32_t out_dtype, int64_t out_row_stride, void *workspace,
+                     size_t workspace_bytes, void *stream);
 
 /* ---- attention (out, lse) merge --------------------------------------------- */
 

@@ -14,6 +14,7 @@ from . import _build
 
 # ---- constants (mirror include/lpd.h) --------------------------------------
 LPD_BF16, LPD_F32 = 0, 1
+LPD_E4M3, LPD_E5M2 = 2, 3  # block-scaled operands only
 LPD_OK = 0
 LPD_ERR_NULL_POINTER = -1
 LPD_ERR_BAD_SIZE = -2
@@ -73,6 +74,11 @@ class LpdControls(ctypes.Structure):
                 ("mask_row", ctypes.c_void_p)]
 
 
+class LpdBlockScaled(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64)]
+
+
 class LpdMetrics(ctypes.Structure):
     _fields_ = [("n_active", ctypes.c_int64), ("argmax_row", ctypes.c_int64), ("flags", ctypes.c_uint32),
                 ("status", ctypes.c_uint32), ("ratio0_mean", ctypes.c_double), ("clipfrac0", ctypes.c_double),
@@ -125,7 +131,7 @@ EXPORTED = ("lpd_workspace_size", "lpd_backend_info", "lpd_strerror", "lpd_score
             "lpd_score_entropy", "lpd_logprob_backward", "lpd_attn_merge", "lpd_attn_merge_order_drift",
             "lpd_topology_workspace_size", "lpd_score_sharded_topology", "lpd_drift_metrics_from_dlogp",
             "lpd_logp_drift_summary", "lpd_merge_rank_metrics", "lpd_controls_apply", "lpd_score_controlled",
-            "lpd_logprob_backward_controlled")
+            "lpd_logprob_backward_controlled", "lpd_block_quantize", "lpd_block_workspace_size", "lpd_block_matmul")
 LPD_MAX_BIAS = 1024
 LPD_NOALLOC_MAX_ROWS = 32768
 LPD_ATTN_MAX_PARTS = 64
@@ -193,6 +199,12 @@ def lib() -> ctypes.CDLL:
         L.lpd_merge_rank_metrics.restype = ctypes.c_int
         L.lpd_merge_rank_metrics.argtypes = [P, P, I32, P]
         L.lpd_logp_drift_summary.argtypes = [I64, P, P, P, P, P, P, P]
+        L.lpd_block_quantize.restype = ctypes.c_int
+        L.lpd_block_quantize.argtypes = [P, I32, I64, I64, I64, I32, I32, P, P]
+        L.lpd_block_workspace_size.restype = SZ
+        L.lpd_block_workspace_size.argtypes = [I64, I64, I64]
+        L.lpd_block_matmul.restype = ctypes.c_int
+        L.lpd_block_matmul.argtypes = [P, P, I64, I64, I64, P, I32, I64, P, SZ, P]
         L.lpd_controls_apply.restype = ctypes.c_int
         L.lpd_controls_apply.argtypes = [P, P, I64, I64, P, I32, I64, P]
         L.lpd_score_controlled.restype = ctypes.c_int
@@ -650,6 +662,82 @@ def lpd_logprob_backward_controlled(logits, controls, token_ids, action_mask, lo
     _check(rc, "lpd_logprob_backward_controlled")
 
 
+@dataclass(frozen=True)
+class BlockScaled:
+    """An 8-bit operand (lpd_block_scaled): values float8_e4m3fn or float8_e5m2
+    [rows, k] with contiguous rows, scales float32 [rows, ceil(k / 128)], or
+    [ceil(rows / 128), ceil(k / 128)] where `block` is true.  The tensors must
+    live as long as this object."""
+    values: object
+    scales: object
+    block: bool = False
+
+    def __post_init__(self):
+        import torch
+
+        v, s = self.values, self.scales
+        codes = {torch.float8_e4m3fn: LPD_E4M3, torch.float8_e5m2: LPD_E5M2}
+        if v.dtype not in codes:
+            raise ValueError(f"values must be float8_e4m3fn or float8_e5m2, got {v.dtype}")
+        if v.dim() != 2 or (v.numel() and v.shape[1] > 1 and v.stride(1) != 1):
+            raise ValueError("values must be 2-D with contiguous columns")
+        want = (-(-v.shape[0] // 128) if self.block else v.shape[0], -(-v.shape[1] // 128))
+        if s.dtype != torch.float32 or tuple(s.shape) != want or (s.numel() and s.shape[1] > 1 and s.stride(1) != 1):
+            raise ValueError(f"scales must be float32 {list(want)} with contiguous columns, got {s.dtype} {list(s.shape)}")
+        if s.device != v.device:
+            raise ValueError(f"values on {v.device}, scales on {s.device}")
+        # the stride of a single row has no meaning in torch: any legal one serves
+        stride = v.stride(0) if v.shape[0] > 1 else -(-v.shape[1] // 16) * 16
+        object.__setattr__(self, "_struct", LpdBlockScaled(
+            v.data_ptr(), codes[v.dtype], int(bool(self.block)), stride, s.data_ptr(),
+            s.stride(0) if s.shape[0] > 1 else want[1]))
+
+
+def block_empty(rows: int, k: int, dtype, block: bool = False, device="cuda") -> BlockScaled:
+    """An operand of these sizes to quantise into, its rows on 16-byte boundaries
+    as the product needs them."""
+    import torch
+
+    room = torch.empty((rows, -(-k // 16) * 16), dtype=torch.uint8, device=device)
+    scales = torch.empty((-(-rows // 128) if block else rows, -(-k // 128)), dtype=torch.float32, device=device)
+    return BlockScaled(room.view(dtype)[:, :k], scales, block)
+
+
+def lpd_block_quantize(x, out, transpose=False, pow2=False, stream=None) -> None:
+    """x (bf16 or f32, 2-D) into the operand `out`, or its transpose."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be 2-D with contiguous columns")
+    if tuple(out.values.shape) != (tuple(x.shape)[::-1] if transpose else tuple(x.shape)):
+        raise ValueError("out has another shape")
+    if out.values.device != x.device:
+        raise ValueError(f"x on {x.device}, out on {out.values.device}")
+    with _on(x):
+        rc = lib().lpd_block_quantize(_ptr(x), _dtype_code(x), max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1],
+                                      int(bool(transpose)), int(bool(pow2)), ctypes.byref(out._struct),
+                                      _stream(stream))
+    _check(rc, "lpd_block_quantize")
+
+
+def lpd_block_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().lpd_block_workspace_size(m, n, k))
+
+
+def lpd_block_matmul(a, b, out, workspace, stream=None) -> None:
+    """out [m, n] (bf16 or f32) = A [m, k] times B [n, k] transposed."""
+    (m, k), n = a.values.shape, b.values.shape[0]
+    if b.values.shape[1] != k or tuple(out.shape) != (m, n):
+        raise ValueError(f"A {[m, k]}, B {list(b.values.shape)} and out {list(out.shape)} do not fit")
+    if out.dim() != 2 or (n > 1 and out.stride(1) != 1):
+        raise ValueError("out must have contiguous columns")
+    if not a.values.device == b.values.device == out.device == workspace.device:
+        raise ValueError("the operands, out and the workspace must be on one device")
+    with _on(out):
+        rc = lib().lpd_block_matmul(ctypes.byref(a._struct), ctypes.byref(b._struct), m, n, k, _ptr(out),
+                                    _dtype_code(out), max(out.stride(0), n), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(rc, "lpd_block_matmul")
+
+
 # ---- convenience: allocate with torch, call, read back ------------------------
 
 def read_merge_drift(buf) -> dict:
@@ -809,3 +897,25 @@ def score_controlled(train, rollout, token_ids, action_mask, train_controls=None
     lpd_score_controlled(train, rollout, train_controls, rollout_controls, token_ids, action_mask, clip[0], clip[1],
                          *outs, met, ws, stream)
     return ScoreResult(*outs, read_metrics(met))
+
+
+def block_quantize(x, dtype=None, block=False, transpose=False, pow2=False, stream=None) -> BlockScaled:
+    """x as a new 8-bit operand (e4m3 unless given)."""
+    import torch
+
+    rows, k = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
+    out = block_empty(rows, k, dtype or torch.float8_e4m3fn, block, x.device)
+    lpd_block_quantize(x, out, transpose, pow2, stream)
+    return out
+
+
+def block_matmul(a, b, out_dtype=None, stream=None):
+    """The product of two operands in a new tensor (bf16 unless given)."""
+    import torch
+
+    m, n = a.values.shape[0], b.values.shape[0]
+    dev = a.values.device
+    out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+    ws = torch.empty(lpd_block_workspace_size(m, n, a.values.shape[1]), dtype=torch.uint8, device=dev)
+    lpd_block_matmul(a, b, out, ws, stream)
+    return out

@@ -441,6 +441,26 @@ int to_controls(const lpd_controls *c, int64_t n_rows, int64_t vocab, CtlSide *o
     return LPD_OK;
 }
 
+// A block-scaled operand of `rows` rows and k columns as the kernels' copy.
+int to_operand(const lpd_block_scaled *x, int64_t rows, int64_t k, bool product, BlockOperand *out) {
+    if (!x) return LPD_ERR_NULL_POINTER;
+    if (rows > 0 && k > 0 && (!x->ptr || !x->scales)) return LPD_ERR_NULL_POINTER;
+    if (x->dtype != LPD_E4M3 && x->dtype != LPD_E5M2) return LPD_ERR_BAD_DTYPE;
+    if (x->block != 0 && x->block != 1) return LPD_ERR_BAD_SIZE;
+    if (x->row_stride < k || x->scale_stride < (k + 127) / 128) return LPD_ERR_BAD_STRIDE;
+    if (!ptr_aligned(x->scales, 4)) return LPD_ERR_ALIGNMENT;
+    if (product && rows > 0 && k > 0 && (!aligned16(x->ptr) || x->row_stride % 16 != 0)) return LPD_ERR_ALIGNMENT;
+    *out = BlockOperand{x->ptr, x->row_stride, x->dtype == LPD_E5M2, x->block == 1, x->scales, x->scale_stride};
+    return LPD_OK;
+}
+
+int check_product_sizes(int64_t m, int64_t n, int64_t k) {
+    if (m < 0 || n < 0 || k < 0) return LPD_ERR_BAD_SIZE;
+    // TMA coordinates are 32-bit
+    if (m > kMaxRows || n > kMaxRows || k > kMaxRows - 256) return LPD_ERR_UNSUPPORTED;
+    return LPD_OK;
+}
+
 // A [n_rows, vocab] output of the elementwise control forms.
 int check_output(const void *out, int32_t out_dtype, int64_t out_row_stride, int64_t n_rows, int64_t vocab) {
     if (!out && n_rows > 0) return LPD_ERR_NULL_POINTER;
@@ -1047,6 +1067,45 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
     return cuda_status(launch_controls_gradient(c, logits->ptr, logits->dtype, logits->row_stride, out_dlogits,
                                                 out_dtype, out_row_stride, n_rows, vocab, token_ids, action_mask, logp,
                                                 grad_logp, static_cast<cudaStream_t>(stream)));
+}
+
+int lpd_block_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols,
+                       int32_t transpose, int32_t pow2, const lpd_block_scaled *out, void *stream) {
+    if (rows < 0 || cols < 0 || (transpose != 0 && transpose != 1) || (pow2 != 0 && pow2 != 1))
+        return LPD_ERR_BAD_SIZE;
+    if (rows > kMaxRows || cols > kMaxRows || (rows + 127) / 128 * ((cols + 127) / 128) > INT32_MAX)
+        return LPD_ERR_UNSUPPORTED;
+    if (!x && rows > 0 && cols > 0) return LPD_ERR_NULL_POINTER;
+    if (!valid_dtype(x_dtype)) return LPD_ERR_BAD_DTYPE;
+    if (x_row_stride < cols) return LPD_ERR_BAD_STRIDE;
+    if (!elt_aligned(x, x_dtype)) return LPD_ERR_ALIGNMENT;
+    BlockOperand o;
+    const int rc = transpose ? to_operand(out, cols, rows, false, &o) : to_operand(out, rows, cols, false, &o);
+    if (rc) return rc;
+    return cuda_status(launch_block_quantize(x, x_dtype, x_row_stride, rows, cols, o.block, transpose == 1, pow2 == 1,
+                                             o.e5m2, out->ptr, o.row_stride, out->scales, o.scale_stride,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+size_t lpd_block_workspace_size(int64_t m, int64_t n, int64_t k) {
+    return check_product_sizes(m, n, k) ? 0 : block_plan(m, n, k).bytes;
+}
+
+int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64_t m, int64_t n, int64_t k,
+                     void *out, int32_t out_dtype, int64_t out_row_stride, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    int rc = check_product_sizes(m, n, k);
+    if (rc) return rc;
+    BlockOperand x, y;
+    if ((rc = to_operand(a, m, k, true, &x))) return rc;
+    if ((rc = to_operand(b, n, k, true, &y))) return rc;
+    if (!out && m > 0 && n > 0) return LPD_ERR_NULL_POINTER;
+    if (!valid_dtype(out_dtype)) return LPD_ERR_BAD_DTYPE;
+    if (out_row_stride < n) return LPD_ERR_BAD_STRIDE;
+    if (!elt_aligned(out, out_dtype)) return LPD_ERR_ALIGNMENT;
+    if ((rc = check_workspace(workspace, workspace_bytes, block_plan(m, n, k).bytes))) return rc;
+    return cuda_status(launch_block_matmul(x, y, m, n, k, out, out_dtype, out_row_stride, workspace,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,815 @@
+// Block-scaled 8-bit floating point: quantisation and the matrix product.
+//
+// A value of an operand is q * s with q in e4m3 or e5m2 and one fp32 scale s
+// for each 1 x 128 or 128 x 128 block along k ("[WS2] Framework for ablation
+// experiment", LogProb knobs table, rows 9-10: the head GEMM of the rollout
+// engine, whose rounding is a drift source).  The product is
+//   C[m, n] = sum_kb sa[m, kb] sb[n, kb] sum_{k in block kb} A[m, k] B[n, k]:
+// the inner sum of 128 terms runs on the tensor cores (tcgen05.mma
+// kind::f8f6f4, fp32 accumulation in tensor memory), the outer one in fp32
+// registers with one multiply-add per output and block, in ascending kb.
+#include <algorithm>
+#include <cfloat>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "lpd_acc.cuh"
+#include "lpd_internal.cuh"
+
+namespace lpd {
+namespace {
+
+constexpr int kBlk = 128;  // values along k that share one scale
+
+// =============================================================== quantisation
+// A block takes a tile of 128 x 128 input values: 16 lanes a row with 8 values
+// each, two rows a warp and pass, 16 rows a pass, eight passes, all held in
+// registers, so the input is read once and each maximum is known before the
+// first value is rounded.  Transposed output goes through shared memory.
+// Bound: HBM (input bytes + one byte a value).
+constexpr int kQThreads = 256;
+constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a scale is made for
+
+struct QuantArgs {
+    const char *x;
+    int64_t x_stride;  // bytes
+    int64_t rows, cols;
+    uint8_t *out;
+    int64_t out_stride;
+    float *scales;
+    int64_t scale_stride;
+    int n_tiles_c;
+    int vec_in, vec_out;  // 16-byte aligned input rows, 8-byte (plain) or 16-byte (transposed) aligned output rows
+    int pow2;
+};
+
+template <bool kE5>
+__device__ __forceinline__ uint32_t pack4(const float *v, float inv) {
+    constexpr __nv_fp8_interpretation_t kKind = kE5 ? __NV_E5M2 : __NV_E4M3;
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)), __NV_SATFINITE, kKind);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)), __NV_SATFINITE, kKind);
+    return lo | hi << 16;
+}
+
+// scale and the factor onto the 8-bit range from the block's largest magnitude
+// (as bits: NaN above infinity above numbers, so neither is lost)
+template <bool kE5>
+__device__ __forceinline__ void scale_of(uint32_t top_bits, int pow2, float *scale, float *inv) {
+    constexpr float kMost = kE5 ? 57344.f : 448.f;
+    const float raw = __uint_as_float(top_bits);
+    if (!(raw <= FLT_MAX)) {  // a non-finite value: the whole block reads as NaN
+        *scale = raw;
+        *inv = CUDART_NAN_F;
+        return;
+    }
+    const float top = fmaxf(raw, kFloor);
+    const float s = __fdiv_rn(top, kMost);
+    if (pow2) {
+        const uint32_t b = __float_as_uint(s);
+        *scale = __uint_as_float((b + 0x7fffffu) & 0x7f800000u);  // up to the next power of two
+        *inv = __fdiv_rn(1.f, *scale);
+    } else {
+        *scale = s;
+        *inv = __fdiv_rn(kMost, top);
+    }
+}
+
+template <bool kBf16, bool kE5, bool kBlock, bool kTranspose>
+__global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ uint32_t tops[kTranspose && !kBlock ? 8 * kBlk : 8];
+    __shared__ __align__(16) uint8_t turned[kTranspose ? kBlk * (kBlk + 16) : 16];
+    constexpr int kElt = kBf16 ? 2 : 4;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int64_t tile_r = blockIdx.x / a.n_tiles_c, tile_c = blockIdx.x % a.n_tiles_c;
+    const int64_t r0 = tile_r * kBlk, c0 = tile_c * kBlk;
+    const int col = (lane & 15) * 8;
+    const int row_in_pass = warp * 2 + (lane >> 4);
+    // raw words of the thread's 8 passes: 8 values each, outside the tensor 0
+    uint4 raw[8][kBf16 ? 1 : 2];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int64_t r = r0 + p * 16 + row_in_pass, c = c0 + col;
+        const char *src = a.x + r * a.x_stride + c * kElt;
+#pragma unroll
+        for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = make_uint4(0, 0, 0, 0);
+        if (r < a.rows && c < a.cols) {
+            if (a.vec_in && c + 8 <= a.cols) {
+#pragma unroll
+                for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = __ldcs(reinterpret_cast<const uint4 *>(src) + h);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const bool in = c + q < a.cols;
+                    if constexpr (kBf16) {
+                        const uint32_t b = in ? reinterpret_cast<const unsigned short *>(src)[q] : 0u;
+                        if (q & 1) w[q >> 1] |= b << 16;
+                        else w[q >> 1] = b;
+                    } else {
+                        w[q] = in ? reinterpret_cast<const uint32_t *>(src)[q] : 0u;
+                    }
+                }
+                raw[p][0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if constexpr (!kBf16) raw[p][1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+    }
+    auto values = [&](int p, float *v) {
+        if constexpr (kBf16) {
+            const uint32_t ws[4] = {raw[p][0].x, raw[p][0].y, raw[p][0].z, raw[p][0].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[2 * q] = __uint_as_float(ws[q] << 16);
+                v[2 * q + 1] = __uint_as_float(ws[q] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < (kBf16 ? 1 : 2); ++h) {
+                v[4 * h] = __uint_as_float(raw[p][h].x);
+                v[4 * h + 1] = __uint_as_float(raw[p][h].y);
+                v[4 * h + 2] = __uint_as_float(raw[p][h].z);
+                v[4 * h + 3] = __uint_as_float(raw[p][h].w);
+            }
+        }
+    };
+    auto bits = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
+    float inv_col[kTranspose && !kBlock ? 8 : 1], inv_all = 0.f;
+    if constexpr (kBlock) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float v[8];
+            values(p, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) tops[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = max(m, tops[w]);
+        float s;
+        scale_of<kE5>(m, a.pow2, &s, &inv_all);
+        if (t == 0) a.scales[kTranspose ? tile_c * a.scale_stride + tile_r : tile_r * a.scale_stride + tile_c] = s;
+    } else if constexpr (kTranspose) {
+        uint32_t m[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m[q] = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float v[8];
+            values(p, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m[q] = max(m[q], bits(v[q]));
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            m[q] = max(m[q], __shfl_xor_sync(0xffffffffu, m[q], 16));
+            if (lane < 16) tops[warp * kBlk + col + q] = m[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) top = max(top, tops[w * kBlk + col + q]);
+            float s;
+            scale_of<kE5>(top, a.pow2, &s, &inv_col[q]);
+            if (t < 16 && c0 + col + q < a.cols) a.scales[(c0 + col + q) * a.scale_stride + tile_r] = s;
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int row = p * 16 + row_in_pass;
+        const int64_t r = r0 + row, c = c0 + col;
+        float v[8];
+        values(p, v);
+        float inv = inv_all;
+        if constexpr (!kBlock && !kTranspose) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+            float s;
+            scale_of<kE5>(m, a.pow2, &s, &inv);
+            if ((lane & 15) == 0 && r < a.rows) a.scales[r * a.scale_stride + tile_c] = s;
+        }
+        if constexpr (!kBlock && kTranspose) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], inv_col[q]);
+            inv = 1.f;
+        }
+        const uint32_t w0 = pack4<kE5>(v, inv), w1 = pack4<kE5>(v + 4, inv);
+        if constexpr (kTranspose) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                turned[(col + q) * (kBlk + 16) + row] = static_cast<uint8_t>(w0 >> (8 * q));
+                turned[(col + 4 + q) * (kBlk + 16) + row] = static_cast<uint8_t>(w1 >> (8 * q));
+            }
+        } else if (r < a.rows && c < a.cols) {
+            uint8_t *dst = a.out + r * a.out_stride + c;
+            if (a.vec_out && c + 8 <= a.cols) {
+                __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w0, w1));
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c + q < a.cols) dst[q] = static_cast<uint8_t>((q < 4 ? w0 : w1) >> (8 * (q & 3)));
+            }
+        }
+    }
+    if constexpr (kTranspose) {
+        // 128 output rows (input columns) of 128 bytes: 8 lanes a row with 16 bytes each
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int row = p * 32 + (t >> 3), at = (t & 7) * 16;
+            const int64_t orow = c0 + row, oc = r0 + at;
+            if (orow >= a.cols || oc >= a.rows) continue;
+            const uint4 w = *reinterpret_cast<const uint4 *>(&turned[row * (kBlk + 16) + at]);
+            uint8_t *dst = a.out + orow * a.out_stride + oc;
+            if (a.vec_out && oc + 16 <= a.rows) {
+                __stcs(reinterpret_cast<uint4 *>(dst), w);
+            } else {
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (int q = 0; q < 16 && oc + q < a.rows; ++q)
+                    dst[q] = static_cast<uint8_t>(ws[q >> 2] >> (8 * (q & 3)));
+            }
+        }
+    }
+}
+
+// ==================================================================== product
+// One persistent CTA per SM.  Warpgroup 0: warp 0 streams 128-wide k blocks of A (128 rows)
+// and B (256 rows) through a four-stage ring (TMA, 128-byte swizzle), warp 1
+// issues four M=128 N=256 K=32 MMAs a block into one of two accumulators in
+// tensor memory, and eight warps read each accumulator back, scale it and add
+// it to 128 fp32 registers a thread: a row is a lane, a warp takes half of the
+// 256 columns.  Two accumulators let the MMAs of block kb + 1 run under the
+// read-back of block kb; at the full MMA rate a block takes 512 cycles, its
+// read-back 256 (32768 values at 128 lanes) and its multiply-adds 256.
+constexpr int kTM = 128, kTN = 256;
+constexpr int kStages = 4;
+constexpr int kABytes = kTM * kBlk, kBBytes = kTN * kBlk;
+constexpr int kStageBytes = kABytes + kBBytes;  // 48 KB
+constexpr int kEpiWarps = 8;
+constexpr int kMmThreads = (4 + kEpiWarps) * 32;  // a warpgroup for the copies and the MMAs, two for the read-back
+// registers a thread after the split (three warps a sub-partition, launched at
+// 168 each: 40 + 2 * 232 = 3 * 168)
+constexpr int kRegsFront = 40, kRegsEpi = 232;
+constexpr int kOutPitch = 80;                   // bytes a staged output row: 64 and 16 against bank conflicts
+constexpr int kOutBytes = kEpiWarps * 32 * kOutPitch;
+constexpr int kScaleGroup = 4;                  // k blocks whose scales are fetched together
+constexpr int kScaleBytes = 2 * kScaleGroup * kTN * 4;
+constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kScaleBytes;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kRaster = 16;                     // row tiles that share a B tile in L2
+constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+constexpr uint32_t kWaitLimitIters = 1u << 30;
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ unsigned long long globaltimer_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Bounded wait; when it gives up it raises the CTA's abort flag and sets
+// LPD_STATUS_TIMEOUT in the workspace's first word.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
+                                           bool honour_abort = true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 255u) == 0) {
+            if (honour_abort && *abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+        }
+    }
+    *abort_flag = 1;
+    atomicOr(status, LPD_STATUS_TIMEOUT);
+    return false;
+}
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+// K-major tile of 128-byte rows under the 128-byte swizzle (8-row groups of 1024 bytes).
+__device__ __forceinline__ uint64_t smem_desc(const void *tile) {
+    const uint64_t addr = (smem_u32(tile) & 0x3FFFFu) >> 4;
+    return addr | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+struct MmMaps {
+    CUtensorMap a, b;
+};
+
+struct MmArgs {
+    const float *sa, *sb;
+    int64_t sa_stride, sb_stride;
+    int sa_shift, sb_shift;    // 0: a scale a row, 7: a scale for 128 rows
+    int64_t m, n;
+    int kb_total, kb_per_split, n_splits;
+    int n_tm, n_tn;
+    uint32_t idesc;
+    char *out;
+    int64_t out_stride;        // bytes
+    int64_t split_stride;      // bytes between the partial results of two splits
+    int vec_out;               // 16-byte aligned output rows
+    uint32_t *status;
+};
+
+// Work items in raster order: groups of kRaster row tiles over all column
+// tiles, row tiles innermost, then the splits.
+__device__ __forceinline__ void item_coords(int64_t w, const MmArgs &a, int &tm, int &tn, int &split) {
+    const int64_t tiles = static_cast<int64_t>(a.n_tm) * a.n_tn;
+    split = static_cast<int>(w / tiles);
+    const int64_t i = w - split * tiles;
+    const int64_t per_group = static_cast<int64_t>(kRaster) * a.n_tn;
+    const int g = static_cast<int>(i / per_group);
+    const int64_t local = i - g * per_group;
+    const int gm = min(kRaster, a.n_tm - g * kRaster);
+    tn = static_cast<int>(local / gm);
+    tm = g * kRaster + static_cast<int>(local - static_cast<int64_t>(tn) * gm);
+}
+
+// kVecB: B's scales are one a row (1 x 128 blocks), so they differ from column
+// to column of the accumulator; else one for 128 columns.
+template <bool kOutF32, bool kVecB>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    product_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
+    extern __shared__ __align__(1024) char smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scales_full[2], done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    char *const staged = smem + static_cast<size_t>(kStages) * kStageBytes;
+    float *const scales = reinterpret_cast<float *>(staged + kOutBytes);  // [2][kScaleGroup][kTN]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits;
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], kEpiWarps);
+            mbar_init(&scales_full[b], kEpiWarps);
+        }
+        mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFront));
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true;
+                for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                    int tm, tn, split;
+                    item_coords(w, a, tm, tn, split);
+                    const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
+                    for (int kb = split * a.kb_per_split; kb < kb1; ++kb, ++it) {
+                        const uint32_t s = it % kStages, round = it / kStages;
+                        if (round > 0 && !wait_phase(&empty[s], (round - 1) & 1, &abort_flag, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        char *st = smem + static_cast<size_t>(s) * kStageBytes;
+                        mbar_arrive_expect_tx(&full[s], kStageBytes);
+                        tma_load_2d(st, &maps.a, kb * kBlk, tm * kTM, &full[s]);
+                        tma_load_2d(st + kABytes, &maps.b, kb * kBlk, tn * kTN, &full[s]);
+                    }
+                }
+                // every copy issued must land before the CTA exits
+                const uint32_t first = it > static_cast<uint32_t>(kStages) ? it - kStages : 0;
+                for (uint32_t j = first; j < it; ++j)
+                    wait_phase(&full[j % kStages], (j / kStages) & 1, &abort_flag, a.status, false);
+            }
+        } else if (warp == 1) {
+            // ----------------------------------------------------------------- MMA
+            if (lane == 0) {
+                uint32_t it = 0;
+                bool ok = true, issued = false;
+                for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                    int tm, tn, split;
+                    item_coords(w, a, tm, tn, split);
+                    const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        const uint32_t s = it % kStages, round = it / kStages, b = it & 1, use = it >> 1;
+                        if ((use > 0 && !wait_phase(&acc_empty[b], (use - 1) & 1, &abort_flag, a.status)) ||
+                            !wait_phase(&full[s], round & 1, &abort_flag, a.status)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const char *st = smem + static_cast<size_t>(s) * kStageBytes;
+                        const uint64_t da = smem_desc(st), db = smem_desc(st + kABytes);
+#pragma unroll
+                        for (int k = 0; k < kBlk / 32; ++k)  // K = 32 bytes inside the swizzle row
+                            umma_f8(tmem + b * kTN, da + 2 * k, db + 2 * k, a.idesc, k > 0 ? 1u : 0u);
+                        umma_commit(&empty[s]);
+                        umma_commit(&acc_full[b]);
+                        issued = true;
+                    }
+                }
+                if (issued) {
+                    umma_commit(&done);
+                    wait_phase(&done, 0, &abort_flag, a.status, false);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // ------------------------------------------------------------ epilogue
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int et = threadIdx.x - 128;  // 0..255
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kTN / 2);
+        char *const mine = staged + (warp - 4) * 32 * kOutPitch;
+        uint32_t it = 0, group = 0;  // k blocks and scale groups so far
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+            int tm, tn, split;
+            item_coords(w, a, tm, tn, split);
+            const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
+            const int64_t row = static_cast<int64_t>(tm) * kTM + quad * 32 + lane;
+            const int64_t col0 = static_cast<int64_t>(tn) * kTN + half * (kTN / 2);
+            const float *sa = a.sa + (min(row, a.m - 1) >> a.sa_shift) * a.sa_stride;
+            const int64_t sb_row = kVecB ? static_cast<int64_t>(tn) * kTN + et : col0;
+            const float *sb = a.sb + (min(sb_row, a.n - 1) >> a.sb_shift) * a.sb_stride;
+            f2_t acc[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[j] = f2(0.f, 0.f);
+            float ra[kScaleGroup], rb[kScaleGroup];
+#pragma unroll 1
+            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
+                const int g = (kb - kb0) & (kScaleGroup - 1);
+                if (g == 0) {
+#pragma unroll
+                    for (int q = 0; q < kScaleGroup; ++q) {
+                        const int k = min(kb + q, kb1 - 1);
+                        ra[q] = __ldg(sa + k);
+                        rb[q] = __ldg(sb + k);
+                    }
+                    if (kVecB) {
+                        // two buffers: a warp that fills one for group i + 2
+                        // has seen every warp arrive for group i + 1, so every
+                        // warp is done with group i
+                        float *dst = scales + (group & 1) * kScaleGroup * kTN;
+#pragma unroll
+                        for (int q = 0; q < kScaleGroup; ++q) dst[q * kTN + et] = rb[q];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&scales_full[group & 1]);
+                        ok = wait_phase(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
+                        ok = !__any_sync(0xffffffffu, !ok);
+                        if (!ok) break;
+                    }
+                    ++group;
+                }
+                float sav = ra[0], sbv = rb[0];
+#pragma unroll
+                for (int q = 1; q < kScaleGroup; ++q) {
+                    sav = g == q ? ra[q] : sav;
+                    sbv = g == q ? rb[q] : sbv;
+                }
+                const uint32_t b = it & 1;
+                ok = wait_phase(&acc_full[b], (it >> 1) & 1, &abort_flag, a.status);
+                ok = !__any_sync(0xffffffffu, !ok);
+                if (!ok) break;
+                tc_fence_after();
+                const float s = kVecB ? sav : __fmul_rn(sav, sbv);
+                const f2_t s2 = f2(s, s);
+                const float4 *col_scales =
+                    reinterpret_cast<const float4 *>(scales + ((group - 1) & 1) * kScaleGroup * kTN + g * kTN + half * (kTN / 2));
+                uint32_t r[2][16];
+                tmem_ld16_issue(lane_addr + b * kTN, r[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait_ld();
+                    if (c < 7) {
+                        tmem_ld16_issue(lane_addr + b * kTN + (c + 1) * 16, r[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[b]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t *p = &r[c & 1][4 * j];
+                        const f2_t p0 = f2(__uint_as_float(p[0]), __uint_as_float(p[1]));
+                        const f2_t p1 = f2(__uint_as_float(p[2]), __uint_as_float(p[3]));
+                        f2_t &x0 = acc[c * 8 + 2 * j], &x1 = acc[c * 8 + 2 * j + 1];
+                        if (kVecB) {
+                            const float4 v = col_scales[c * 4 + j];
+                            x0 = fma2(p0, mul2(f2(v.x, v.y), s2), x0);
+                            x1 = fma2(p1, mul2(f2(v.z, v.w), s2), x1);
+                        } else {
+                            x0 = fma2(p0, s2, x0);
+                            x1 = fma2(p1, s2, x1);
+                        }
+                    }
+                }
+            }
+            if (!ok) {  // a wait gave up: this tile reads as NaN
+#pragma unroll
+                for (int j = 0; j < 64; ++j) acc[j] = f2(CUDART_NAN_F, CUDART_NAN_F);
+            }
+            // 64-byte pieces of 32 rows through shared memory, so that a store
+            // covers whole sectors of a row
+            char *const out = a.out + split * a.split_stride;
+            const int64_t row0 = static_cast<int64_t>(tm) * kTM + quad * 32;
+            constexpr int kCols = kOutF32 ? 16 : 32;  // columns of a piece
+#pragma unroll
+            for (int p = 0; p < kTN / 2 / kCols; ++p) {
+                uint32_t piece[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                    if (kOutF32) {
+                        const f2_t v = acc[p * 8 + q / 2];
+                        piece[q] = __float_as_uint(q & 1 ? f2_hi(v) : f2_lo(v));
+                    } else {
+                        const f2_t v = acc[p * 16 + q];
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+                        piece[q] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4 *>(mine + lane * kOutPitch + 16 * q) =
+                        make_uint4(piece[4 * q], piece[4 * q + 1], piece[4 * q + 2], piece[4 * q + 3]);
+                __syncwarp();
+                const int64_t c = col0 + p * kCols;
+                if (c >= a.n) break;
+                if (a.vec_out && c + kCols <= a.n) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int rr = q * 8 + (lane >> 2);
+                        if (row0 + rr < a.m)
+                            __stcs(reinterpret_cast<uint4 *>(out + (row0 + rr) * a.out_stride + c * (kOutF32 ? 4 : 2)) + (lane & 3),
+                                   *reinterpret_cast<const uint4 *>(mine + rr * kOutPitch + 16 * (lane & 3)));
+                    }
+                } else {
+                    for (int q = 0; q < kCols; ++q) {
+                        const int rr = kOutF32 ? 2 * q + (lane >> 4) : q;
+                        const int cc = kOutF32 ? lane & 15 : lane;
+                        if (row0 + rr < a.m && c + cc < a.n) {
+                            char *dst = out + (row0 + rr) * a.out_stride + (c + cc) * (kOutF32 ? 4 : 2);
+                            if (kOutF32) *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(mine + rr * kOutPitch + 4 * cc);
+                            else *reinterpret_cast<unsigned short *>(dst) = *reinterpret_cast<const unsigned short *>(mine + rr * kOutPitch + 2 * cc);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// C = the partial results added in split order, rounded once.
+template <bool kOutF32>
+__global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t part_stride, int64_t split_stride,
+                                                   int n_splits, int64_t m, int64_t n, char *out, int64_t out_stride) {
+    const int64_t cells = m * n;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < cells; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = i / n, c = i - r * n;
+        const float *p = part + r * part_stride + c;
+        float s = p[0];
+        for (int k = 1; k < n_splits; ++k) s = __fadd_rn(s, p[k * split_stride]);
+        if (kOutF32) *reinterpret_cast<float *>(out + r * out_stride + 4 * c) = s;
+        else *reinterpret_cast<__nv_bfloat16 *>(out + r * out_stride + 2 * c) = __float2bfloat16_rn(s);
+    }
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::atomic<EncodeTiledFn> cached{nullptr};
+    EncodeTiledFn fn = cached.load(std::memory_order_acquire);
+    if (!fn) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn = reinterpret_cast<EncodeTiledFn>(p);
+        cached.store(fn, std::memory_order_release);
+    }
+    return fn;
+}
+
+// [rows, k] bytes, boxes of 128 x box_rows, 128-byte swizzle; what lies
+// outside [rows, k] reads as 0.
+bool make_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t k, int64_t stride, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlk), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kBf16, bool kE5>
+cudaError_t quantize_typed(const QuantArgs &a, bool block, bool transpose, unsigned grid, cudaStream_t s) {
+    if (block) {
+        if (transpose) quantize_kernel<kBf16, kE5, true, true><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, kE5, true, false><<<grid, kQThreads, 0, s>>>(a);
+    } else {
+        if (transpose) quantize_kernel<kBf16, kE5, false, true><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, kE5, false, false><<<grid, kQThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <bool kOutF32, bool kVecB>
+cudaError_t product_typed(const MmMaps &maps, const MmArgs &a, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = set_smem_once(product_kernel<kOutF32, kVecB>, kMmSmem, configured);
+    if (e != cudaSuccess) return e;
+    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits, sms = device_sm_count();
+    product_kernel<kOutF32, kVecB><<<static_cast<unsigned>(items < sms ? items : sms), kMmThreads, kMmSmem, stream>>>(maps, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// The k axis is split where the output's tiles would leave half of the
+// multiprocessors idle (a data gradient of few tokens: 16 tiles and a thousand
+// k blocks), into parts of at least eight blocks.
+BlockPlan block_plan(int64_t m, int64_t n, int64_t k) {
+    BlockPlan p{};
+    p.n_tm = (m + kTM - 1) / kTM;
+    p.n_tn = (n + kTN - 1) / kTN;
+    p.kb_total = (k + kBlk - 1) / kBlk;
+    const int64_t tiles = p.n_tm * p.n_tn;
+    const int64_t sms = device_sm_count();
+    int64_t want = tiles > 0 ? sms / tiles : 1;
+    want = std::min(want, p.kb_total / 8);
+    p.n_splits = std::max<int64_t>(want, 1);
+    p.kb_per_split = p.n_splits > 1 ? (p.kb_total + p.n_splits - 1) / p.n_splits : p.kb_total;
+    if (p.n_splits > 1) p.n_splits = (p.kb_total + p.kb_per_split - 1) / p.kb_per_split;
+    p.part_stride = (n + 3) / 4 * 4;
+    p.bytes = 256;
+    if (p.n_splits > 1) p.bytes += align256(static_cast<size_t>(p.n_splits) * m * p.part_stride * 4);
+    return p;
+}
+
+cudaError_t launch_block_quantize(const void *x, int x_dtype, int64_t x_stride_elems, int64_t rows, int64_t cols,
+                                  bool block, bool transpose, bool pow2, bool e5m2, void *out, int64_t out_stride,
+                                  float *scales, int64_t scale_stride, cudaStream_t stream) {
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    QuantArgs a{};
+    const bool bf16 = x_dtype == LPD_BF16;
+    a.x = static_cast<const char *>(x);
+    a.x_stride = x_stride_elems * (bf16 ? 2 : 4);
+    a.rows = rows;
+    a.cols = cols;
+    a.out = static_cast<uint8_t *>(out);
+    a.out_stride = out_stride;
+    a.scales = scales;
+    a.scale_stride = scale_stride;
+    a.n_tiles_c = static_cast<int>((cols + kBlk - 1) / kBlk);
+    const uintptr_t unit = transpose ? 16 : 8;
+    a.vec_in = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.x_stride % 16 == 0;
+    a.vec_out = reinterpret_cast<uintptr_t>(out) % unit == 0 && static_cast<uintptr_t>(out_stride) % unit == 0;
+    a.pow2 = pow2 ? 1 : 0;
+    const unsigned grid = static_cast<unsigned>((rows + kBlk - 1) / kBlk * a.n_tiles_c);
+    if (bf16) return e5m2 ? quantize_typed<true, true>(a, block, transpose, grid, stream)
+                          : quantize_typed<true, false>(a, block, transpose, grid, stream);
+    return e5m2 ? quantize_typed<false, true>(a, block, transpose, grid, stream)
+                : quantize_typed<false, false>(a, block, transpose, grid, stream);
+}
+
+cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, int64_t m, int64_t n, int64_t k,
+                                void *out, int out_dtype, int64_t out_stride_elems, void *workspace,
+                                cudaStream_t stream) {
+    const bool f32 = out_dtype == LPD_F32;
+    const int64_t out_stride = out_stride_elems * (f32 ? 4 : 2);
+    if (m == 0 || n == 0) return cudaSuccess;
+    if (k == 0) return cudaMemset2DAsync(out, out_stride, 0, n * (f32 ? 4 : 2), m, stream);
+    const BlockPlan p = block_plan(m, n, k);
+    MmMaps maps;
+    if (!make_map(&maps.a, x.ptr, m, k, x.row_stride, kTM) || !make_map(&maps.b, y.ptr, n, k, y.row_stride, kTN))
+        return cudaErrorInvalidValue;
+    MmArgs a{};
+    a.sa = x.scales;
+    a.sb = y.scales;
+    a.sa_stride = x.scale_stride;
+    a.sb_stride = y.scale_stride;
+    a.sa_shift = x.block ? 7 : 0;
+    a.sb_shift = y.block ? 7 : 0;
+    a.m = m;
+    a.n = n;
+    a.kb_total = static_cast<int>(p.kb_total);
+    a.kb_per_split = static_cast<int>(p.kb_per_split);
+    a.n_splits = static_cast<int>(p.n_splits);
+    a.n_tm = static_cast<int>(p.n_tm);
+    a.n_tn = static_cast<int>(p.n_tn);
+    // kind::f8f6f4: fp32 accumulator (bit 4), A's and B's format (bits 7 and 10: 0 e4m3, 1 e5m2), both K-major
+    a.idesc = (1u << 4) | (static_cast<uint32_t>(x.e5m2) << 7) | (static_cast<uint32_t>(y.e5m2) << 10) |
+              (static_cast<uint32_t>(kTN >> 3) << 17) | (static_cast<uint32_t>(kTM >> 4) << 24);
+    a.status = static_cast<uint32_t *>(workspace);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    const bool split = p.n_splits > 1;
+    a.out = split ? reinterpret_cast<char *>(part) : static_cast<char *>(out);
+    a.out_stride = split ? p.part_stride * 4 : out_stride;
+    a.split_stride = split ? m * p.part_stride * 4 : 0;
+    a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 16 == 0;
+    const bool to_f32 = split || f32;
+    cudaError_t e;
+    if (to_f32) e = y.block ? product_typed<true, false>(maps, a, stream) : product_typed<true, true>(maps, a, stream);
+    else e = y.block ? product_typed<false, false>(maps, a, stream) : product_typed<false, true>(maps, a, stream);
+    if (e != cudaSuccess || !split) return e;
+    const int64_t blocks = std::min<int64_t>((m * n + 255) / 256, static_cast<int64_t>(device_sm_count()) * 16);
+    if (f32)
+        join_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
+                                                                          static_cast<char *>(out), out_stride);
+    else
+        join_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
+                                                                           static_cast<char *>(out), out_stride);
+    return cudaGetLastError();
+}
+
+}  // namespace lpd

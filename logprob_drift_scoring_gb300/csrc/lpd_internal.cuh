@@ -275,6 +275,29 @@ cudaError_t launch_controls_score(const CtlScoreArgs &a, int dtype_t, int dtype_
                                   float *out_lr, float *out_d, double *dval, uint32_t *keys, uint32_t *status,
                                   cudaStream_t stream);
 
+// ---------------------------------------------------------------- block-scaled 8-bit operands
+struct BlockOperand {
+    const void *ptr;
+    int64_t row_stride;
+    bool e5m2, block;      // 128 x 128 scales, else 1 x 128
+    const float *scales;
+    int64_t scale_stride;
+};
+
+// How a product is cut: output tiles, k blocks of 128, splits of the k axis.
+struct BlockPlan {
+    int64_t n_tm, n_tn, kb_total, kb_per_split, n_splits;
+    int64_t part_stride;   // floats a row of a partial result
+    size_t bytes;          // workspace
+};
+BlockPlan block_plan(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_block_quantize(const void *x, int x_dtype, int64_t x_stride_elems, int64_t rows, int64_t cols,
+                                  bool block, bool transpose, bool pow2, bool e5m2, void *out, int64_t out_stride,
+                                  float *scales, int64_t scale_stride, cudaStream_t stream);
+cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, int64_t m, int64_t n, int64_t k,
+                                void *out, int out_dtype, int64_t out_stride_elems, void *workspace,
+                                cudaStream_t stream);
+
 // Attention (out, lse) merge: one call of lpd_attn_merge (diag false) or of
 // lpd_attn_merge_order_drift (diag true).  Orders are validated permutations.
 struct AttnMergeCall {
