@@ -26,24 +26,37 @@ namespace {
 constexpr int kChunk = 8192;       // columns of a unit: one bitmap word a thread
 constexpr int kSmallChunk = 2048;  // of the elementwise forms when few rows leave multiprocessors idle
 
+// Shared memory of a block: `tables` count tables, the list, the bitmaps, and
+// the mask table.
 template <int kCols>
 struct Shared {
+    static constexpr int kWords = kCols / 32;
     uint32_t *table;
+    uint4 *lanes;
     uint16_t *list;
-    uint32_t *touched, *allow_t, *allow_r;
-    static constexpr size_t bytes(int tables, int sides) {
-        return static_cast<size_t>(kCols) * (4 * tables + 2) + (kCols / 32) * 4 * (1 + sides);
+    uint32_t *touched, *allow_t, *allow_r, *skip_t, *skip_r;
+    static constexpr size_t bytes(int tables) {
+        return static_cast<size_t>(kCols) * (4 * tables + 2) + 256 * sizeof(uint4) + kWords * 4 * 5;
     }
-    __device__ Shared(char *p, int tables, int sides) {
+    __device__ Shared(char *p, int tables) {
         table = reinterpret_cast<uint32_t *>(p);
         p += static_cast<size_t>(kCols) * 4 * tables;
+        lanes = reinterpret_cast<uint4 *>(p);
+        p += 256 * sizeof(uint4);
         list = reinterpret_cast<uint16_t *>(p);
         p += kCols * 2;
         touched = reinterpret_cast<uint32_t *>(p);
-        allow_t = touched + kCols / 32;
-        allow_r = sides > 1 ? allow_t + kCols / 32 : allow_t;
+        allow_t = touched + kWords;
+        allow_r = allow_t + kWords;
+        skip_t = allow_r + kWords;
+        skip_r = skip_t + kWords;
+    }
+    __device__ void init(int n_table_words) const {
+        for (int j = threadIdx.x; j < n_table_words; j += kCtlThreads) table[j] = 0;
+        lanes[threadIdx.x] = ctl_lanes(threadIdx.x);
     }
 };
+static_assert(kCtlThreads == 256, "one mask table entry a thread");
 
 // the byte of bits for the eight columns of group g
 __device__ __forceinline__ uint32_t group_bits(const uint32_t *words, int g) {
@@ -56,82 +69,101 @@ struct ApplyArgs {
     char *out;
     int64_t x_stride, out_stride;  // bytes
     int64_t n_rows, vocab;
-    int n_chunks;
+    int n_chunks, per_unit;        // chunks a row, chunks a unit
 };
+
+// Unit u of `n_units` a row: the row, and which of its units.  Consecutive
+// units belong to one row; each row starts at another of its units, because a
+// tokenizer's frequent tokens sit in the first columns: with a grid that is a
+// multiple of n_units, the same blocks would otherwise get every row's first
+// unit (measured: 428 us instead of 131 us on 256 rows of long histories).
+__device__ __forceinline__ void unit_of(int64_t u, int n_units, int64_t &row, int &k) {
+    row = u / n_units;
+    k = static_cast<int>((u - row * n_units + row) % n_units);
+}
 
 template <bool kXBf16, bool kOBf16, bool kVec, int kCols>
 __global__ void __launch_bounds__(kCtlThreads, 4) apply_kernel(const __grid_constant__ ApplyArgs a) {
     extern __shared__ __align__(16) char smem[];
     __shared__ int warp_sum[kCtlWarps];
-    const Shared<kCols> sh(smem, 1, 1);
+    __shared__ CtlRow o;
+    const Shared<kCols> sh(smem, 1);
     constexpr int kGroups = kCols / 8 / kCtlThreads;
     const int t = threadIdx.x;
     const bool marks = a.c.counts || a.c.n_bias > 0;
-    if (marks)
-        for (int j = t; j < kCols; j += kCtlThreads) sh.table[j] = 0;
-    const int64_t units = a.n_rows * a.n_chunks;
+    sh.init(marks ? kCols : 0);
+    if (t < Shared<kCols>::kWords) sh.touched[t] = 0;
+    const int n_units = (a.n_chunks + a.per_unit - 1) / a.per_unit;
+    const int64_t units = a.n_rows * n_units;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t r = u / a.n_chunks;
-        const int64_t c0 = (u - r * a.n_chunks) * kCols;
+        int64_t r;
+        int k;
+        unit_of(u, n_units, r, k);
         const char *xrow = a.x + r * a.x_stride;
         char *orow = a.out + r * a.out_stride;
-        Group8<kXBf16> raw[kGroups];
+        __syncthreads();  // the last unit's row is done with
+        if (t == 0) o = ctl_row(a.c, r);
+        const int ch1 = min(a.n_chunks, (k + 1) * a.per_unit);
+        for (int ch = k * a.per_unit; ch < ch1; ++ch) {
+            const int64_t c0 = static_cast<int64_t>(ch) * kCols;
+            Group8<kXBf16> raw[kGroups];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int64_t j = c0 + 8 * (t + g * kCtlThreads);
-            if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
-        }
-        const CtlRow o = ctl_row(a.c, r);
-        if (t < kCols / 32) {
-            sh.touched[t] = 0;
-            sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
-        }
-        __syncthreads();
-        if (marks) {
-            const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
-            ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, -1, nullptr);
+            for (int g = 0; g < kGroups; ++g) {
+                const int64_t j = c0 + 8 * (t + g * kCtlThreads);
+                if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
+            }
+            __syncthreads();  // the table and the bitmaps are free again
+            int n = 0;
+            if (marks) {
+                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
+                ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, -1, nullptr);
+                __syncthreads();
+            }
+            uint32_t bits = 0;
+            if (t < Shared<kCols>::kWords) {
+                bits = sh.touched[t];
+                sh.touched[t] = 0;
+                sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
+            }
+            if (marks) n = ctl_list(bits, sh.list, warp_sum);
             __syncthreads();
-            const int n = ctl_list(sh.touched, kCols / 32, sh.list, warp_sum);
-            __syncthreads();
+            const float scale = o.scale;
             // the touched tokens' logits replace their table words
             for (int i = t; i < n; i += kCtlThreads) {
                 const int j = sh.list[i];
                 const uint32_t w = sh.table[j];
-                float z = 0.f;
+                float z = -INFINITY;
                 if (sh.allow_t[j >> 5] >> (j & 31) & 1u) {
                     const Two v = ctl_value(ctl_elem<kXBf16>(xrow, c0 + j), w, a.c, o, r, c0 + j, nullptr);
-                    z = __fmaf_rn(v.h, o.scale, __fmul_rn(v.l, o.scale));
+                    z = __fmaf_rn(v.h, scale, __fmul_rn(v.l, scale));
                 }
                 sh.table[j] = __float_as_uint(z);
             }
-            __syncthreads();
-        }
+            if (n && a.x == a.out) __syncthreads();  // in place: read before the stream overwrites
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int gi = t + g * kCtlThreads;
-            const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
-            if (j >= a.vocab) continue;
-            float v[8];
-            ctl_unpack8<kXBf16>(raw[g], v);
+            for (int g = 0; g < kGroups; ++g) {
+                const int gi = t + g * kCtlThreads;
+                const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
+                if (j >= a.vocab) continue;
+                float v[8];
+                ctl_unpack8<kXBf16>(raw[g], v);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], o.scale);
-            const uint32_t allow = group_bits(sh.allow_t, gi), touched = group_bits(sh.touched, gi);
-            if (touched) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (touched >> q & 1u) {
-                        v[q] = __uint_as_float(sh.table[8 * gi + q]);
-                        sh.table[8 * gi + q] = 0;
-                    }
+                for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], scale);
+                Group8<kOBf16> w;
+                ctl_pack8<kOBf16>(v, w);
+                const uint32_t skip = group_bits(sh.allow_t, gi) ^ 0xffu;
+                if (skip) ctl_fill8<kOBf16, 0xff80u>(w, sh.lanes[skip]);  // -inf
+                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
             }
-            if (allow != 0xffu) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (!(allow >> q & 1u)) v[q] = -INFINITY;
+            if (n) {
+                __syncthreads();  // the stream's stores come first
+                for (int i = t; i < n; i += kCtlThreads) {
+                    const int j = sh.list[i];
+                    ctl_store1<kOBf16>(orow, c0 + j, __uint_as_float(sh.table[j]));
+                    sh.table[j] = 0;
+                }
             }
-            ctl_store8<kOBf16, kVec>(orow, j, a.vocab, v);
         }
-        __syncthreads();
     }
 }
 
@@ -141,7 +173,7 @@ struct GradArgs {
     char *out;
     int64_t x_stride, out_stride;  // bytes
     int64_t n_rows, vocab;
-    int n_chunks;
+    int n_chunks, per_unit;
     const int32_t *ids;
     const uint8_t *mask;
     const float *logp, *grad;
@@ -149,140 +181,241 @@ struct GradArgs {
 
 // d(g logp)/dx_j = g scale (1[j = id] - p_j) dx3/dx, p_j = 2^(z_j log2 e - lse
 // log2 e) with lse = z[id] - logp from the forward's own output (as the plain
-// gradient does), its base-2 form kept as two floats.
+// gradient does).  Its base-2 form is kept as two floats; the low one enters as
+// a factor, so the stream spends one multiply-add, one exponential and one
+// product a column.  The selected token is always on the list, so the stream
+// has no one-hot term.
 template <bool kXBf16, bool kOBf16, bool kVec, int kCols>
 __global__ void __launch_bounds__(kCtlThreads, 4) gradient_kernel(const __grid_constant__ GradArgs a) {
     extern __shared__ __align__(16) char smem[];
     __shared__ int warp_sum[kCtlWarps];
     __shared__ uint32_t id_word;
     __shared__ float lse2[2];
-    const Shared<kCols> sh(smem, 1, 1);
+    __shared__ CtlRow o;
+    const Shared<kCols> sh(smem, 1);
     constexpr int kGroups = kCols / 8 / kCtlThreads;
     const int t = threadIdx.x;
     const bool marks = a.c.counts || a.c.n_bias > 0;
-    if (marks)
-        for (int j = t; j < kCols; j += kCtlThreads) sh.table[j] = 0;
-    const int64_t units = a.n_rows * a.n_chunks;
+    sh.init(kCols);
+    if (t < Shared<kCols>::kWords) sh.touched[t] = 0;
+    const int n_units = (a.n_chunks + a.per_unit - 1) / a.per_unit;
+    const int64_t units = a.n_rows * n_units;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t r = u / a.n_chunks;
-        const int64_t c0 = (u - r * a.n_chunks) * kCols;
+        int64_t r;
+        int k;
+        unit_of(u, n_units, r, k);
         const char *xrow = a.x + r * a.x_stride;
         char *orow = a.out + r * a.out_stride;
+        const int ch0 = k * a.per_unit, ch1 = min(a.n_chunks, ch0 + a.per_unit);
         const bool active = a.mask[r] != 0;
         const int64_t id = active ? a.ids[r] : 0;
         if (!(active && id >= 0 && id < a.vocab)) {
             // inactive rows: 0; an active row with an out-of-range id: NaN
             float v[8];
+            Group8<kOBf16> w;
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = active ? CUDART_NAN_F : 0.f;
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int64_t j = c0 + 8 * static_cast<int64_t>(t + g * kCtlThreads);
-                if (j < a.vocab) ctl_store8<kOBf16, kVec>(orow, j, a.vocab, v);
-            }
+            ctl_pack8<kOBf16>(v, w);
+            const int64_t end = min(static_cast<int64_t>(ch1) * kCols, a.vocab);
+            for (int64_t j = static_cast<int64_t>(ch0) * kCols + 8 * t; j < end; j += 8 * kCtlThreads)
+                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
             continue;
         }
-        Group8<kXBf16> raw[kGroups];
+        __syncthreads();  // the last unit's row is done with
+        if (t == 0) o = ctl_row(a.c, r);
+        float gs = a.grad[r], f = 0.f, lh = 0.f, ll = 0.f, gl = 0.f;
+        for (int ch = ch0; ch < ch1; ++ch) {
+            const int64_t c0 = static_cast<int64_t>(ch) * kCols;
+            Group8<kXBf16> raw[kGroups];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int64_t j = c0 + 8 * (t + g * kCtlThreads);
-            if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
-        }
-        const CtlRow o = ctl_row(a.c, r);
-        const float gs = __fmul_rn(a.grad[r], o.scale);
-        if (t < kCols / 32) {
-            sh.touched[t] = 0;
-            sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
-        }
-        if (t == 0) id_word = 0;
-        __syncthreads();
-        const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
-        int n = 0;
-        if (marks) {
-            ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, id, &id_word);
+            for (int g = 0; g < kGroups; ++g) {
+                const int64_t j = c0 + 8 * (t + g * kCtlThreads);
+                if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
+            }
+            if (t == 0) id_word = 0;
+            __syncthreads();  // the table and the bitmaps are free again
+            const bool first = ch == ch0;
+            if (marks) {
+                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
+                ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, first ? id : -1, first ? &id_word : nullptr);
+                __syncthreads();
+            }
+            uint32_t bits = 0;
+            if (t < Shared<kCols>::kWords) {
+                bits = sh.touched[t];
+                sh.touched[t] = 0;
+                sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
+                if ((id - c0) >> 5 == t) bits |= 1u << (id & 31);
+            }
+            const int n = ctl_list(bits, sh.list, warp_sum);
+            if (first && t == kCtlThreads - 1) {
+                const uint32_t word = o.mask ? __ldg(o.mask + id / 32) : 0xffffffffu;
+                double z = -CUDART_INF;
+                if (!o.none && (word >> (id & 31) & 1u)) {
+                    const Two v = ctl_value(ctl_elem<kXBf16>(xrow, id), id_word, a.c, o, r, id, nullptr);
+                    z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
+                }
+                const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
+                lse2[0] = static_cast<float>(l2);
+                lse2[1] = static_cast<float>(l2 - static_cast<double>(lse2[0]));
+            }
             __syncthreads();
-            n = ctl_list(sh.touched, kCols / 32, sh.list, warp_sum);
-        }
-        if (t == 0) {
-            const uint32_t word = o.mask ? __ldg(o.mask + id / 32) : 0xffffffffu;
-            double z = -CUDART_INF;
-            if (!o.none && (word >> (id & 31) & 1u)) {
-                const Two v = ctl_value(ctl_elem<kXBf16>(xrow, id), id_word, a.c, o, r, id, nullptr);
-                z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
+            if (first) {
+                gs = __fmul_rn(gs, o.scale);
+                f = __fmul_rn(o.scale, kLog2e);
+                lh = lse2[0];
+                ll = lse2[1];
+                gl = __fmul_rn(-gs, ex2(-ll));
             }
-            const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
-            lse2[0] = static_cast<float>(l2);
-            lse2[1] = static_cast<float>(l2 - static_cast<double>(lse2[0]));
-        }
-        __syncthreads();
-        const float lh = lse2[0], ll = lse2[1];
-        const float f = __fmul_rn(o.scale, kLog2e);
-        for (int i = t; i < n; i += kCtlThreads) {
-            const int j = sh.list[i];
-            const uint32_t w = sh.table[j];
-            float d = 0.f;
-            if (sh.allow_t[j >> 5] >> (j & 31) & 1u) {
-                float slope;
-                const Two v = ctl_value(ctl_elem<kXBf16>(xrow, c0 + j), w, a.c, o, r, c0 + j, &slope);
-                const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -lh), ll), __fmul_rn(v.l, f)));
-                d = __fmul_rn(__fmul_rn(gs, slope), __fsub_rn(c0 + j == id ? 1.f : 0.f, p));
+            for (int i = t; i < n; i += kCtlThreads) {
+                const int j = sh.list[i];
+                const uint32_t w = sh.table[j];
+                float d = 0.f;
+                if (sh.allow_t[j >> 5] >> (j & 31) & 1u) {
+                    float slope;
+                    const Two v = ctl_value(ctl_elem<kXBf16>(xrow, c0 + j), w, a.c, o, r, c0 + j, &slope);
+                    const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -lh), ll), __fmul_rn(v.l, f)));
+                    d = __fmul_rn(__fmul_rn(gs, slope), __fsub_rn(c0 + j == id ? 1.f : 0.f, p));
+                }
+                sh.table[j] = __float_as_uint(d);
             }
-            sh.table[j] = __float_as_uint(d);
-        }
-        if (n) __syncthreads();
+            const f2_t f2f = f2(f, f), l2f = f2(-lh, -lh), g2f = f2(gl, gl);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int gi = t + g * kCtlThreads;
-            const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
-            if (j >= a.vocab) continue;
-            float v[8];
-            ctl_unpack8<kXBf16>(raw[g], v);
-            const int64_t at = id - j;  // the one-hot column, if it is in this group
+            for (int g = 0; g < kGroups; ++g) {
+                const int gi = t + g * kCtlThreads;
+                const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
+                if (j >= a.vocab) continue;
+                float v[8];
+                ctl_unpack8<kXBf16>(raw[g], v);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float p = ex2(__fsub_rn(__fmaf_rn(v[q], f, -lh), ll));
-                v[q] = __fmul_rn(gs, at == q ? __fsub_rn(1.f, p) : -p);
+                for (int q = 0; q < 4; ++q) {
+                    const f2_t d = mul2(g2f, ex2_2(fma2(f2(v[2 * q], v[2 * q + 1]), f2f, l2f)));
+                    v[2 * q] = f2_lo(d);
+                    v[2 * q + 1] = f2_hi(d);
+                }
+                Group8<kOBf16> w;
+                ctl_pack8<kOBf16>(v, w);
+                const uint32_t skip = group_bits(sh.allow_t, gi) ^ 0xffu;
+                if (skip) ctl_fill8<kOBf16, 0u>(w, sh.lanes[skip]);
+                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
             }
-            const uint32_t allow = group_bits(sh.allow_t, gi), touched = group_bits(sh.touched, gi);
-            if (touched) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (touched >> q & 1u) {
-                        v[q] = __uint_as_float(sh.table[8 * gi + q]);
-                        sh.table[8 * gi + q] = 0;
-                    }
+            if (n) {
+                __syncthreads();  // the stream's stores come first
+                for (int i = t; i < n; i += kCtlThreads) {
+                    const int j = sh.list[i];
+                    ctl_store1<kOBf16>(orow, c0 + j, __uint_as_float(sh.table[j]));
+                    sh.table[j] = 0;
+                }
             }
-            if (allow != 0xffu) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (!(allow >> q & 1u)) v[q] = 0.f;
-            }
-            ctl_store8<kOBf16, kVec>(orow, j, a.vocab, v);
         }
-        __syncthreads();
     }
+}
+
+// ---- scoring: sums of both sides ---------------------------------------------------
+// Two sides that nearly agree (the same scale, |z_t - z_r| small) take one
+// exponential a column: e_t = e_r (1 + q), q = expm1(u) of the small exponent
+// difference u by its Taylor series.  The difference of the two sums, e_r q
+// added up, is then accurate relative to itself, where e_t - e_r of two rounded
+// exponentials carries 2^-22 of the term (1e-5 of a logprob difference of
+// 2e-3), and the special-function unit, which bounds the kernel beside HBM, has
+// half the work.
+constexpr float kNear2 = 0.0625f;   // sum of u^2 over a thread's sixteen columns: |u| <= 1/4
+// A masked column of the stream holds about -1e30 (bf16 0xf149) on both sides:
+// its term is 0 and its u finite.  Rows whose allowed logits are all below
+// kFloorZ leave this path.
+constexpr uint32_t kFillBits = 0xf149u;
+constexpr float kFloorZ = -1e29f;
+
+// expm1(u) / u up to u^5 / 720: the next term is u^6 / 5040 = 5e-8 at 1/4
+__device__ __forceinline__ f2_t expm1_ratio2(f2_t u) {
+    f2_t p = fma2(u, f2(1.f / 720.f, 1.f / 720.f), f2(1.f / 120.f, 1.f / 120.f));
+    p = fma2(u, p, f2(1.f / 24.f, 1.f / 24.f));
+    p = fma2(u, p, f2(1.f / 6.f, 1.f / 6.f));
+    p = fma2(u, p, f2(0.5f, 0.5f));
+    return fma2(u, p, f2(1.f, 1.f));
+}
+
+// References (mt, mr) moved up to (nmt, nmr).
+__device__ __forceinline__ void raise_refs(Acc2 &a, float nmt, float nmr, float lt, float lr) {
+    const float at = __fmul_rn(__fsub_rn(a.mt, nmt), lt), ar = __fmul_rn(__fsub_rn(a.mr, nmr), lr);
+    const float ft = ex2(at), fr = ex2(ar);
+    const float corr = scale_diff(ft, fr, at, ar);
+    a.dd = add2(mul2(a.dd, f2(ft, ft)), mul2(a.sr, f2(corr, corr)));
+    a.st = mul2(a.st, f2(ft, ft));
+    a.sr = mul2(a.sr, f2(fr, fr));
+    a.mt = nmt;
+    a.mr = nmr;
+}
+
+// Sixteen columns of two sides that nearly agree; false where they do not (the
+// state is valid either way).  A NaN fails the comparison of the sum of squares.
+__device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, Acc2 &a, float l, float s) {
+    const float cm = max16(vr);
+    if (!(cm > kFloorZ)) return false;
+    if (cm > a.mr) raise_refs(a, fmaxf(a.mt, cm), cm, l, l);
+    const float dm = __fmul_rn(__fsub_rn(a.mr, a.mt), s);
+    const f2_t s2 = f2(s, s), dm2 = f2(dm, dm), l2 = f2(l, l), m2 = f2(a.mr, a.mr);
+    f2_t u[8], q2 = f2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        u[p] = fma2(sub2(vt[p], vr[p]), s2, dm2);
+        q2 = fma2(u[p], u[p], q2);
+    }
+    if (!(__fadd_rn(f2_lo(q2), f2_hi(q2)) <= kNear2)) return false;
+    f2_t se = f2(0.f, 0.f), sd = f2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const f2_t e = ex2_2(mul2(sub2(vr[p], m2), l2));
+        se = add2(se, e);
+        sd = fma2(mul2(e, u[p]), expm1_ratio2(u[p]), sd);
+    }
+    a.sr = add2(a.sr, se);
+    a.dd = add2(a.dd, sd);
+    a.st = add2(a.st, add2(se, sd));
+    return true;
+}
+
+// Sixteen columns of any two sides, each with an exponential of its own; -inf
+// adds nothing (the floor of the references keeps x - m defined).
+__device__ __forceinline__ void accumulate_far(const f2_t *vt, const f2_t *vr, Acc2 &a, float lt, float lr) {
+    const float ct = max16(vt), cr = max16(vr);
+    if (ct > a.mt || cr > a.mr) raise_refs(a, fmaxf(a.mt, ct), fmaxf(a.mr, cr), lt, lr);
+    const f2_t mt2 = f2(a.mt, a.mt), mr2 = f2(a.mr, a.mr), lt2 = f2(lt, lt), lr2 = f2(lr, lr);
+    f2_t st = f2(0.f, 0.f), sr = st, sd = st;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const f2_t et = ex2_2(mul2(sub2(vt[p], mt2), lt2)), er = ex2_2(mul2(sub2(vr[p], mr2), lr2));
+        st = add2(st, et);
+        sr = add2(sr, er);
+        sd = add2(sd, sub2(et, er));
+    }
+    a.st = add2(a.st, st);
+    a.sr = add2(a.sr, sr);
+    a.dd = add2(a.dd, sd);
 }
 
 // One pair of controlled logits (h + l of each side) into the state; an -inf
 // adds nothing.
-__device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float lt, float lr) {
-    if (xt.h > a.mt || xr.h > a.mr) {
-        const float nmt = fmaxf(a.mt, xt.h), nmr = fmaxf(a.mr, xr.h);
-        const float at = __fmul_rn(__fsub_rn(a.mt, nmt), lt), ar = __fmul_rn(__fsub_rn(a.mr, nmr), lr);
-        const float ft = ex2(at), fr = ex2(ar);
-        const float corr = scale_diff(ft, fr, at, ar);
-        a.dd = add2(mul2(a.dd, f2(ft, ft)), mul2(a.sr, f2(corr, corr)));
-        a.st = mul2(a.st, f2(ft, ft));
-        a.sr = mul2(a.sr, f2(fr, fr));
-        a.mt = nmt;
-        a.mr = nmr;
-    }
-    const float et = ex2(__fmaf_rn(xt.l, lt, __fmul_rn(__fsub_rn(xt.h, a.mt), lt)));
+__device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float lt, float lr, float s, bool same_scale) {
+    if (xt.h > a.mt || xr.h > a.mr) raise_refs(a, fmaxf(a.mt, xt.h), fmaxf(a.mr, xr.h), lt, lr);
     const float er = ex2(__fmaf_rn(xr.l, lr, __fmul_rn(__fsub_rn(xr.h, a.mr), lr)));
-    a.st = add2(a.st, f2(et, 0.f));
+    const float u = __fmul_rn(
+        __fadd_rn(__fsub_rn(__fsub_rn(xt.h, xr.h), __fsub_rn(a.mt, a.mr)), __fsub_rn(xt.l, xr.l)), s);
+    float d;
+    if (same_scale && fabsf(u) <= 0.25f) {
+        d = __fmul_rn(__fmul_rn(er, u), f2_lo(expm1_ratio2(f2(u, u))));
+    } else {
+        const float et = ex2(__fmaf_rn(xt.l, lt, __fmul_rn(__fsub_rn(xt.h, a.mt), lt)));
+        d = __fsub_rn(et, er);
+    }
     a.sr = add2(a.sr, f2(er, 0.f));
-    a.dd = add2(a.dd, f2(__fsub_rn(et, er), 0.f));
+    a.st = add2(a.st, f2(__fadd_rn(er, d), 0.f));
+    a.dd = add2(a.dd, f2(d, 0.f));
 }
+
+// A unit is kSegChunks chunks of a row, its state carried over them; the number
+// is fixed, so a row's arithmetic depends on its columns alone.
+constexpr int kSegChunks = 4;
 
 // kTables: 1 when both sides count in the same history (or one side counts in
 // none), else one table a side.
@@ -292,49 +425,69 @@ __global__ void __launch_bounds__(kCtlThreads, kTables == 1 ? 3 : 2)
     extern __shared__ __align__(16) char smem[];
     __shared__ int warp_sum[kCtlWarps];
     __shared__ float states[5][kCtlWarps];
-    const Shared<kChunk> sh(smem, kTables, 2);
+    __shared__ CtlRow ot, orr;
+    const Shared<kChunk> sh(smem, kTables);
     uint32_t *const table_t = sh.table, *const table_r = sh.table + (kTables - 1) * kChunk;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const bool marks_t = a.t.counts || a.t.n_bias > 0, marks_r = a.r.counts || a.r.n_bias > 0;
     const bool marks = marks_t || marks_r;
-    if (marks)
-        for (int j = t; j < kTables * kChunk; j += kCtlThreads) sh.table[j] = 0;
+    sh.init(marks ? kTables * kChunk : 0);
+    sh.touched[t] = 0;
+    const int n_chunks = static_cast<int>((a.vocab + kChunk - 1) / kChunk);
     const int64_t units = a.hdr->n_active * a.n_chunks;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t i = u / a.n_chunks;
-        const int k = static_cast<int>(u - i * a.n_chunks);
-        const int64_t c0 = static_cast<int64_t>(k) * kChunk;
+        int64_t i;
+        int k;
+        unit_of(u, a.n_chunks, i, k);
         const int2 rid = a.rowid[i];
         const int64_t r = rid.x, id = rid.y;
         const char *trow = a.xt + r * a.t_stride, *rrow = a.xr + r * a.r_stride;
+        const int64_t end = min(static_cast<int64_t>(k + 1) * kSegChunks * kChunk, a.vocab);
         // 16 columns of each side a thread and step: groups t and t + 256 of
-        // the step's 4096 columns; the first step's loads go out before the scan
+        // the step's 4096 columns; each step's loads go out before the step
+        // in front of it is worked on, a chunk's first ones before its scan
         Group8<kTBf16> gt[2];
         Group8<kRBf16> gr[2];
-        auto load = [&](int step) {
+        auto load = [&](int64_t c) {
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int64_t j = c0 + 8 * (t + (2 * step + g) * kCtlThreads);
-                if (j < a.vocab) {
+                const int64_t j = c + 8 * (t + g * kCtlThreads);
+                if (j < end) {
                     ctl_load8<kTBf16, kVec>(trow, j, a.vocab, gt[g]);
                     ctl_load8<kRBf16, kVec>(rrow, j, a.vocab, gr[g]);
                 }
             }
         };
-        load(0);
-        const CtlRow ot = ctl_row(a.t, r), orr = ctl_row(a.r, r);
-        sh.touched[t] = 0;
-        sh.allow_t[t] = ctl_allowed(ot, c0, t, a.vocab);
-        sh.allow_r[t] = ctl_allowed(orr, c0, t, a.vocab);
+        const int ch0 = k * kSegChunks, ch1 = min(n_chunks, ch0 + kSegChunks);
+        load(static_cast<int64_t>(ch0) * kChunk);
+        if (t == 0) ot = ctl_row(a.t, r);
+        if (t == 32) orr = ctl_row(a.r, r);
         __syncthreads();
-        const float lt = __fmul_rn(ot.scale, kLog2e), lr = __fmul_rn(orr.scale, kLog2e);
+        const float s_r = orr.scale;
+        const float lt = __fmul_rn(ot.scale, kLog2e), lr = __fmul_rn(s_r, kLog2e);
+        const bool same_scale = ot.scale == s_r;
         Acc2 acc = acc2_init();
-        if (marks) {
-            const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kChunk), a.vocab - c0));
-            if (marks_t) ctl_mark(a.t, ot, r, c0, len, table_t, sh.touched, -1, nullptr);
-            if (marks_r && !a.same) ctl_mark(a.r, orr, r, c0, len, table_r, sh.touched, -1, nullptr);
-            __syncthreads();
-            const int n = ctl_list(sh.touched, kChunk / 32, sh.list, warp_sum);
+#pragma unroll 1
+        for (int ch = ch0; ch < ch1; ++ch) {
+            const int64_t c0 = static_cast<int64_t>(ch) * kChunk;
+            __syncthreads();  // the table and the bitmaps are free again
+            if (marks) {
+                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kChunk), a.vocab - c0));
+                if (marks_t) ctl_mark(a.t, ot, r, c0, len, table_t, sh.touched, -1, nullptr);
+                if (marks_r && !a.same) ctl_mark(a.r, orr, r, c0, len, table_r, sh.touched, -1, nullptr);
+                __syncthreads();
+            }
+            const uint32_t bits = sh.touched[t];
+            sh.touched[t] = 0;
+            const uint32_t at = ctl_allowed(ot, c0, t, a.vocab), ar = ctl_allowed(orr, c0, t, a.vocab);
+            sh.allow_t[t] = at;
+            sh.allow_r[t] = ar;
+            sh.skip_t[t] = bits | ~at;
+            sh.skip_r[t] = bits | ~ar;
+            if ((id - c0) >> 5 == t && id < a.vocab && !(bits >> (id & 31) & 1u))  // an untouched selected token
+                a.pick[i] = make_double2(at >> (id & 31) & 1u ? static_cast<double>(ctl_elem<kTBf16>(trow, id)) : -CUDART_INF,
+                                         ar >> (id & 31) & 1u ? static_cast<double>(ctl_elem<kRBf16>(rrow, id)) : -CUDART_INF);
+            const int n = marks ? ctl_list(bits, sh.list, warp_sum) : 0;
             __syncthreads();
             for (int q = t; q < n; q += kCtlThreads) {
                 const int j = sh.list[q];
@@ -348,50 +501,45 @@ __global__ void __launch_bounds__(kCtlThreads, kTables == 1 ? 3 : 2)
                     vr = ctl_value(ctl_elem<kRBf16>(rrow, c0 + j), wr, a.r, orr, r, c0 + j, nullptr);
                 table_t[j] = 0;
                 if (kTables > 1) table_r[j] = 0;
-                accumulate_pair(vt, vr, acc, lt, lr);
+                accumulate_pair(vt, vr, acc, lt, lr, s_r, same_scale);
                 if (c0 + j == id)
                     a.pick[i] = make_double2(static_cast<double>(vt.h) + static_cast<double>(vt.l),
                                              static_cast<double>(vr.h) + static_cast<double>(vr.l));
             }
-        }
-        if (t == 0 && id >= c0 && id < c0 + kChunk && id < a.vocab) {
-            const int j = static_cast<int>(id - c0);
-            if (!(sh.touched[j >> 5] >> (j & 31) & 1u))
-                a.pick[i] = make_double2(
-                    sh.allow_t[j >> 5] >> (j & 31) & 1u ? static_cast<double>(ctl_elem<kTBf16>(trow, id)) : -CUDART_INF,
-                    sh.allow_r[j >> 5] >> (j & 31) & 1u ? static_cast<double>(ctl_elem<kRBf16>(rrow, id)) : -CUDART_INF);
-        }
+#pragma unroll 1
+            for (int step = 0; step < kChunk / 16 / kCtlThreads; ++step) {
+                uint32_t st[2], sr[2];
 #pragma unroll
-        for (int step = 0; step < kChunk / 16 / kCtlThreads; ++step) {
-            float vt[16], vr[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                ctl_unpack8<kTBf16>(gt[g], vt + 8 * g);
-                ctl_unpack8<kRBf16>(gr[g], vr + 8 * g);
-            }
-            if (step + 1 < kChunk / 16 / kCtlThreads) load(step + 1);
-            if (c0 + 8 * (t + 2 * step * kCtlThreads) >= a.vocab) continue;
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int gi = t + (2 * step + g) * kCtlThreads;
-                const uint32_t touched = group_bits(sh.touched, gi);
-                const uint32_t st = touched | (group_bits(sh.allow_t, gi) ^ 0xffu);
-                const uint32_t sr = touched | (group_bits(sh.allow_r, gi) ^ 0xffu);
-                if (st | sr) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        vt[8 * g + q] = st >> q & 1u ? -INFINITY : vt[8 * g + q];
-                        vr[8 * g + q] = sr >> q & 1u ? -INFINITY : vr[8 * g + q];
-                    }
+                for (int g = 0; g < 2; ++g) {
+                    const int gi = t + (2 * step + g) * kCtlThreads;
+                    st[g] = group_bits(sh.skip_t, gi);
+                    sr[g] = group_bits(sh.skip_r, gi);
+                    if (st[g]) ctl_fill8<kTBf16, kFillBits>(gt[g], sh.lanes[st[g]]);
+                    if (sr[g]) ctl_fill8<kRBf16, kFillBits>(gr[g], sh.lanes[sr[g]]);
                 }
-            }
-            f2_t pt[8], pr[8];
+                float vt[16], vr[16];
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                pt[p] = f2(vt[2 * p], vt[2 * p + 1]);
-                pr[p] = f2(vr[2 * p], vr[2 * p + 1]);
+                for (int g = 0; g < 2; ++g) {
+                    ctl_unpack8<kTBf16>(gt[g], vt + 8 * g);
+                    ctl_unpack8<kRBf16>(gr[g], vr + 8 * g);
+                }
+                load(c0 + (step + 1) * 16 * kCtlThreads);  // the next chunk's first step behind the last one
+                if ((st[0] & st[1] & sr[0] & sr[1]) == 0xffu) continue;  // nothing allowed
+                f2_t pt[8], pr[8];
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    pt[p] = f2(vt[2 * p], vt[2 * p + 1]);
+                    pr[p] = f2(vr[2 * p], vr[2 * p + 1]);
+                }
+                if (same_scale && accumulate_near(pt, pr, acc, lr, s_r)) continue;
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const uint32_t bt = st[p >> 2] >> (2 * (p & 3)), br = sr[p >> 2] >> (2 * (p & 3));
+                    pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(pt[p]), bt & 2u ? -INFINITY : f2_hi(pt[p]));
+                    pr[p] = f2(br & 1u ? -INFINITY : f2_lo(pr[p]), br & 2u ? -INFINITY : f2_hi(pr[p]));
+                }
+                accumulate_far(pt, pr, acc, lt, lr);
             }
-            accumulate16(pt, pr, acc, lt, lr);
         }
         // the block's state: each warp's in a butterfly, then the eight warps' in another
         const Acc w = warp_reduce_acc<false>(acc2_fold(acc), lt, lr);
@@ -422,11 +570,10 @@ __global__ void __launch_bounds__(kCtlThreads, kTables == 1 ? 3 : 2)
                 a.part_b[i * a.n_chunks + k] = b.sr;
             }
         }
-        __syncthreads();
     }
 }
 
-// One warp per active row: lane l folds chunks l, l + 32, ... in order, the
+// One warp per active row: lane l folds units l, l + 32, ... in order, the
 // warp merges in a fixed butterfly, lane 0 does the row's arithmetic in double
 // (the formulas of the plain scorer, with each side's scale).
 __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_constant__ CtlScoreArgs a, float *out_lt,
@@ -505,7 +652,8 @@ template <bool kXB, bool kOB, bool kVec, int kCols>
 cudaError_t apply_typed(ApplyArgs &a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
     a.n_chunks = static_cast<int>(chunks_of(a.vocab, kCols));
-    return launch_units(apply_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4, Shared<kCols>::bytes(1, 1),
+    a.per_unit = 1;
+    return launch_units(apply_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4, Shared<kCols>::bytes(1),
                         configured, stream);
 }
 
@@ -513,8 +661,9 @@ template <bool kXB, bool kOB, bool kVec, int kCols>
 cudaError_t gradient_typed(GradArgs &a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
     a.n_chunks = static_cast<int>(chunks_of(a.vocab, kCols));
-    return launch_units(gradient_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4,
-                        Shared<kCols>::bytes(1, 1), configured, stream);
+    a.per_unit = 1;
+    return launch_units(gradient_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4, Shared<kCols>::bytes(1),
+                        configured, stream);
 }
 
 template <bool kXB, bool kOB>
@@ -541,14 +690,14 @@ cudaError_t score_typed(const CtlScoreArgs &a, bool vec, int64_t n_rows, cudaStr
     static std::atomic<uint64_t> configured[2];
     const int64_t units = n_rows * a.n_chunks;
     const int per_sm = kTables == 1 ? 3 : 2;
-    const size_t smem = Shared<kChunk>::bytes(kTables, 2);
+    const size_t smem = Shared<kChunk>::bytes(kTables);
     return vec ? launch_units(score_kernel<kTB, kRB, true, kTables>, a, units, per_sm, smem, configured[0], s)
                : launch_units(score_kernel<kTB, kRB, false, kTables>, a, units, per_sm, smem, configured[1], s);
 }
 
 }  // namespace
 
-int controls_chunks(int64_t vocab) { return static_cast<int>(chunks_of(vocab, kChunk)); }
+int controls_chunks(int64_t vocab) { return static_cast<int>(chunks_of(vocab, kChunk * kSegChunks)); }
 
 cudaError_t launch_controls_apply(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
                                   int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,

@@ -11,14 +11,18 @@
 // more than the scale and the mask, and they are few: a thousand of a hundred
 // thousand.  A block therefore takes a chunk of one row, marks the touched
 // columns of the chunk in a bitmap, lists them in column order, and works on
-// the list with all lanes busy (a branch per column in the streaming loop costs
-// a whole warp each time: about 80 instructions a touched token, measured as
-// twice the stream itself at 1000 tokens a row).  The streaming loop sees one
-// bit a column.
+// the list with all lanes busy: a touched token is some 80 instructions, which
+// a branch in the streaming loop would spend for a whole warp each time.  The
+// streaming loop sees one bit a column.
 //
 // The occurrence counts live in a table of one word a column of the chunk.  The
 // table is zero between units: whoever consumes a touched entry zeroes it, so
 // the chunk is cleared once a block and not once a unit.
+//
+// Masked columns are replaced eight at a time: a 4 KB table in shared memory
+// gives the 16-bit lane masks of a byte of bits, and one logical instruction a
+// register does the rest (bit tests and selects were 100 instructions a thread
+// and 16 columns, a third of the scoring kernel's).
 //
 // The list is made from the bitmap by a prefix sum over its words, never in the
 // order of arrival, and the counts are integers, so nothing depends on the
@@ -40,7 +44,8 @@ constexpr uint32_t kBiased = 0x40000000u;  // table: the token has a bias entry
 constexpr uint32_t kCount = 0x3fffffffu;   // table: occurrences in the generated part
 constexpr int64_t kMaxRange = kCount;      // so a row's range is cut to its last 2^30 - 1 tokens
 
-// The controls of one row, read once a unit by every thread.
+// The controls of one row: read once a unit by one thread, kept in shared
+// memory (in registers, two of them spilled a quarter of the scoring kernel's).
 struct CtlRow {
     int64_t begin, split, end;
     float rep, inv_h, inv_l;  // repetition penalty and 1 / rep as a sum of two floats
@@ -103,6 +108,7 @@ __device__ __forceinline__ double bias_sum(const CtlSide &c, int64_t r, int64_t 
     const int32_t *ids = c.bias_ids + r * c.n_bias;
     const float *v = c.bias + r * c.n_bias;
     double s = 0.0;
+#pragma unroll 8
     for (int e = 0; e < c.n_bias; ++e)
         if (ids[e] == token) s += static_cast<double>(v[e]);
     return s;
@@ -152,13 +158,15 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlSide &c, 
 // Marks the chunk's touched columns: table words and bitmap bits.  `id_word`
 // (shared, may be null) collects the word of token `id` over the whole row.
 __device__ __forceinline__ void ctl_mark(const CtlSide &c, const CtlRow &o, int64_t r, int64_t c0, uint32_t len,
-                                         uint32_t *table, uint32_t *touched, int64_t id, uint32_t *id_word) {
+                                         volatile uint32_t *vtable, volatile uint32_t *vtouched, int64_t id, uint32_t *id_word) {
+    uint32_t *const table = const_cast<uint32_t *>(vtable), *const touched = const_cast<uint32_t *>(vtouched);
     auto take = [&](int32_t tok, bool gen) {
         const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
         if (j < len) {
             if (gen) atomicAdd(&table[j], 1u);
-            else atomicOr(&table[j], kSeen);
-            atomicOr(&touched[j >> 5], 1u << (j & 31));
+            else if (!(vtable[j] & kSeen)) atomicOr(&table[j], kSeen);  // (a text's frequent tokens come often)
+            const uint32_t bit = 1u << (j & 31);
+            if (!(vtouched[j >> 5] & bit)) atomicOr(&touched[j >> 5], bit);
         }
         if (id_word && tok == id) {
             if (gen) atomicAdd(id_word, 1u);
@@ -196,12 +204,11 @@ __device__ __forceinline__ uint32_t ctl_allowed(const CtlRow &o, int64_t c0, int
     return left >= 32 ? bits : bits & ((1u << left) - 1u);
 }
 
-// The touched columns in ascending order from the bitmap of `words` words (at
-// most one a thread), and their number.  Holds a __syncthreads on entry's side:
-// every mark must be visible before, the list is visible after the caller's.
-__device__ __forceinline__ int ctl_list(const uint32_t *touched, int words, uint16_t *list, int *warp_sum) {
+// The touched columns in ascending order: thread t holds word t of the bitmap
+// (0 behind the chunk's words).  Returns their number; the list is visible
+// after the caller's next __syncthreads.
+__device__ __forceinline__ int ctl_list(uint32_t bits, uint16_t *list, int *warp_sum) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t bits = static_cast<int>(threadIdx.x) < words ? touched[threadIdx.x] : 0u;
     const int n = __popc(bits);
     int incl = n;
 #pragma unroll
@@ -252,6 +259,26 @@ __device__ __forceinline__ void ctl_load8(const char *row, int64_t j, int64_t vo
         return;
     }
     uint32_t w[kBf16 ? 4 : 8];
+    if constexpr (kBf16) {
+        // inside the row: whole words, shifted by half a word where the row
+        // starts on an odd element
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + 2 * j);
+        if (j > 0 && j + 9 <= vocab) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(at & ~uintptr_t{3});
+            if (at & 2) {
+                uint32_t v[5];
+#pragma unroll
+                for (int q = 0; q < 5; ++q) v[q] = p[q];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = __funnelshift_r(v[q], v[q + 1], 16);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = p[q];
+            }
+            g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            return;
+        }
+    }
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         if constexpr (kBf16) {
@@ -282,32 +309,82 @@ __device__ __forceinline__ void ctl_unpack8(const Group8<kBf16> &g, float *x) {
     }
 }
 
-// Columns [j, j + 8) of an output row, each value rounded once to its type.
-template <bool kBf16, bool kVec>
-__device__ __forceinline__ void ctl_store8(char *row, int64_t j, int64_t vocab, const float *v) {
-    if (kVec && j + 8 <= vocab) {
-        if constexpr (kBf16) {
-            uint32_t w[4];
+// Eight values as the words of an output group, each rounded once to its type.
+template <bool kBf16>
+__device__ __forceinline__ void ctl_pack8(const float *v, Group8<kBf16> &g) {
+    uint32_t w[8];
+    if constexpr (kBf16) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-                w[q] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            __stcs(reinterpret_cast<uint4 *>(row + j * 2), make_uint4(w[0], w[1], w[2], w[3]));
-        } else {
-            float4 *p = reinterpret_cast<float4 *>(row + j * 4);
-            __stcs(p, make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(p + 1, make_float4(v[4], v[5], v[6], v[7]));
+        for (int q = 0; q < 4; ++q) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+            w[q] = *reinterpret_cast<const uint32_t *>(&h);
         }
+        g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[q] = __float_as_uint(v[q]);
+        g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        g.w[kBf16 ? 0 : 1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// Entry b of the mask table: the 16-bit lanes of the columns whose bit is set.
+__device__ __forceinline__ uint4 ctl_lanes(uint32_t b) {
+    auto two = [&](int p) { return (b >> (2 * p) & 1u ? 0xffffu : 0u) | (b >> (2 * p + 1) & 1u ? 0xffff0000u : 0u); };
+    return make_uint4(two(0), two(1), two(2), two(3));
+}
+
+// The group's columns whose bit is set replaced by the 16-bit pattern `fill`
+// (of a float32 column: its upper half; the lower half becomes 0).
+template <bool kBf16, uint32_t kFill>
+__device__ __forceinline__ void ctl_fill8(Group8<kBf16> &g, const uint4 &m) {
+    constexpr uint32_t k2 = kFill | kFill << 16, k1 = kFill << 16;
+    if constexpr (kBf16) {
+        g.w[0].x = (g.w[0].x & ~m.x) | (k2 & m.x);
+        g.w[0].y = (g.w[0].y & ~m.y) | (k2 & m.y);
+        g.w[0].z = (g.w[0].z & ~m.z) | (k2 & m.z);
+        g.w[0].w = (g.w[0].w & ~m.w) | (k2 & m.w);
+    } else {
+        auto put = [&](uint32_t &w, uint32_t lane) { w = (w & ~lane) | (k1 & lane); };
+        constexpr int kHi = kBf16 ? 0 : 1;
+        put(g.w[0].x, __byte_perm(m.x, 0, 0x1010));
+        put(g.w[0].y, __byte_perm(m.x, 0, 0x3232));
+        put(g.w[0].z, __byte_perm(m.y, 0, 0x1010));
+        put(g.w[0].w, __byte_perm(m.y, 0, 0x3232));
+        put(g.w[kHi].x, __byte_perm(m.z, 0, 0x1010));
+        put(g.w[kHi].y, __byte_perm(m.z, 0, 0x3232));
+        put(g.w[kHi].z, __byte_perm(m.w, 0, 0x1010));
+        put(g.w[kHi].w, __byte_perm(m.w, 0, 0x3232));
+    }
+}
+
+// Columns [j, j + 8) of an output row.
+template <bool kBf16, bool kVec>
+__device__ __forceinline__ void ctl_store8(char *row, int64_t j, int64_t vocab, const Group8<kBf16> &g) {
+    constexpr int kHi = kBf16 ? 0 : 1;
+    if (kVec && j + 8 <= vocab) {
+        uint4 *p = reinterpret_cast<uint4 *>(row + j * (kBf16 ? 2 : 4));
+        __stcs(p, g.w[0]);
+        if constexpr (!kBf16) __stcs(p + 1, g.w[kHi]);
         return;
     }
+    const uint32_t w[8] = {g.w[0].x,   g.w[0].y,   g.w[0].z,   g.w[0].w,
+                           g.w[kHi].x, g.w[kHi].y, g.w[kHi].z, g.w[kHi].w};
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         if (j + q < vocab) {
-            if constexpr (kBf16) reinterpret_cast<__nv_bfloat16 *>(row)[j + q] = __float2bfloat16_rn(v[q]);
-            else reinterpret_cast<float *>(row)[j + q] = v[q];
+            if constexpr (kBf16)
+                reinterpret_cast<unsigned short *>(row)[j + q] = static_cast<unsigned short>(w[q >> 1] >> (16 * (q & 1)));
+            else
+                reinterpret_cast<uint32_t *>(row)[j + q] = w[q];
         }
     }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void ctl_store1(char *row, int64_t j, float v) {
+    if constexpr (kBf16) reinterpret_cast<__nv_bfloat16 *>(row)[j] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float *>(row)[j] = v;
 }
 
 }  // namespace lpd

@@ -254,12 +254,12 @@ struct CtlScoreArgs {
     const char *xt, *xr;
     int64_t t_stride, r_stride;  // bytes
     int64_t vocab;
-    int n_chunks;
+    int n_chunks;                // units a row
     int same;                    // both sides mark the same tokens: one table
     const WsHeader *hdr;
     const int2 *rowid;
-    float4 *part_a;              // [active row][chunk] (mt, st, dd, mr)
-    float *part_b;               // [active row][chunk] sr
+    float4 *part_a;              // [active row][unit] (mt, st, dd, mr)
+    float *part_b;               // [active row][unit] sr
     double2 *pick;               // selected controlled logits, before the scale
 };
 
