@@ -381,7 +381,8 @@ GatherLayout gather_layout(int64_t n_rows, int64_t vocab, int32_t dt, int32_t dr
 }
 
 // Workspace of the controlled scoring path: the common regions (no per-warp
-// states), then one state per active row and chunk, and the selected logits.
+// states of the plain pass), then the warp states of each active row, and the
+// selected logits.
 struct ControlledLayout {
     WsLayout base;
     size_t part_a, part_b, pick, total;
@@ -390,7 +391,7 @@ struct ControlledLayout {
 ControlledLayout controlled_layout(int64_t n_rows, int64_t vocab) {
     ControlledLayout L{};
     L.base = ws_layout(n_rows, 0);
-    const size_t parts = static_cast<size_t>(n_rows) * static_cast<size_t>(controls_chunks(vocab));
+    const size_t parts = static_cast<size_t>(n_rows) * static_cast<size_t>(controls_states(vocab));
     size_t off = L.base.total;
     L.part_a = off;  off += align256(parts * sizeof(float4));
     L.part_b = off;  off += align256(parts * sizeof(float));
@@ -1024,7 +1025,7 @@ int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, con
     if (rc) return rc;
     if (!out_metrics || ((!token_ids || !action_mask) && n_rows > 0)) return LPD_ERR_NULL_POINTER;
     if ((rc = check_clip(clip_lo, clip_hi))) return rc;
-    CtlScoreArgs a{};
+    CtlScoreCall a{};
     if ((rc = to_controls(train_controls, n_rows, vocab, &a.t))) return rc;
     if ((rc = to_controls(rollout_controls, n_rows, vocab, &a.r))) return rc;
     const ControlledLayout L = controlled_layout(n_rows, vocab);
@@ -1035,20 +1036,26 @@ int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, con
     if ((rc = run_select(n_rows, token_ids, action_mask, out_logp_train, out_logp_rollout, out_dlogp, out_metrics, w,
                          s)))
         return rc;
-    a.xt = static_cast<const char *>(train->ptr);
-    a.xr = static_cast<const char *>(rollout->ptr);
+    a.xt = train->ptr;
+    a.xr = rollout->ptr;
+    a.dtype_t = train->dtype;
+    a.dtype_r = rollout->dtype;
     a.t_stride = train->row_stride * elt_bytes(train->dtype);
     a.r_stride = rollout->row_stride * elt_bytes(rollout->dtype);
+    a.n_rows = n_rows;
     a.vocab = vocab;
     a.hdr = w.hdr;
     a.rowid = w.rowid;
     a.part_a = reinterpret_cast<float4 *>(base + L.part_a);
     a.part_b = reinterpret_cast<float *>(base + L.part_b);
     a.pick = reinterpret_cast<double2 *>(base + L.pick);
-    if ((rc = cuda_status(launch_controls_score(a, train->dtype, rollout->dtype, n_rows, out_logp_train,
-                                                out_logp_rollout, out_dlogp, w.dval, w.keys, &out_metrics->status,
-                                                s))))
-        return rc;
+    a.out_lt = out_logp_train;
+    a.out_lr = out_logp_rollout;
+    a.out_d = out_dlogp;
+    a.dval = w.dval;
+    a.keys = w.keys;
+    a.status = &out_metrics->status;
+    if ((rc = cuda_status(launch_controls_score(a, s)))) return rc;
     return run_metrics(n_rows, clip_lo, clip_hi, out_metrics, w, s);
 }
 

@@ -1,314 +1,233 @@
 // Sampling controls on logits: penalties for repeated tokens, biases, grammar
-// masks and the request's temperature, in three forms.
-//   apply_kernel     writes the controlled logits (what a sampler reads);
-//   score_kernel     the log-sum-exp of both sides' controlled logits in one
-//                    read of each row, never written to memory;
-//   gradient_kernel  the selected-token logprob's gradient with respect to the
-//                    raw logits.
-// The mathematics of a row and the block's way of working on a chunk of it are
-// described in lpd_controls.cuh.
+// masks and the request's temperature, in three forms of one streaming kernel:
+//   kApply   writes the controlled logits (what a sampler reads);
+//   kScore   the log-sum-exp of both sides' controlled logits in one read of
+//            each row, never written to memory;
+//   kGrad    the selected-token logprob's gradient with respect to the raw
+//            logits.
+// The mathematics of a logit is in lpd_controls.cuh.
 //
 // Method: "WS2 Cross-Config Logprob Drift Contract", "Measurement Contract":
 // the rollout's tokens are scored under the distribution that they were
 // sampled from.
 //
-// Bound: HBM.  Units of (row, 8192 columns) go to persistent blocks of 256
-// threads, three or four a multiprocessor, so that one block's history scan
-// and list run under another's loads; each block issues its unit's first loads
-// before the scan.
+// Bound: HBM.  One persistent block per SM works through units: a row, or a
+// range of its columns where there are few rows:
+//   producer  one thread streams the unit's tiles (of both sides when scoring)
+//             through a shared-memory ring with 1-D bulk copies (TMA,
+//             completion on an mbarrier);
+//   scouts    some warps prepare the next unit while this one streams: the
+//             bitmap of its touched columns, and the touched tokens themselves.
+//             When scoring they add these to sums of their own, and the stream
+//             leaves them out; else they keep the values and store them once
+//             the stream has passed over the unit;
+//   stream    the other warps, 16 columns of each side a thread and tile.
+// A first version gave every block a chunk, then scan, list and stream in turn
+// with barriers between: 24 warps on an SM that mostly waited (39 % of issue
+// slots; 4096 x 151936 rows of bf16 on both sides in 1373 us, and 774 us with
+// nothing to control).
+#include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "lpd_controls.cuh"
 
 namespace lpd {
 namespace {
 
-constexpr int kChunk = 8192;       // columns of a unit: one bitmap word a thread
-constexpr int kSmallChunk = 2048;  // of the elementwise forms when few rows leave multiprocessors idle
+constexpr int kApply = 0, kScore = 1, kGrad = 2;
 
-// Shared memory of a block: `tables` count tables, the list, the bitmaps, and
-// the mask table.
-template <int kCols>
-struct Shared {
-    static constexpr int kWords = kCols / 32;
-    uint32_t *table;
-    uint4 *lanes;
-    uint16_t *list;
-    uint32_t *touched, *allow_t, *allow_r, *skip_t, *skip_r;
-    static constexpr size_t bytes(int tables) {
-        return static_cast<size_t>(kCols) * (4 * tables + 2) + 256 * sizeof(uint4) + kWords * 4 * 5;
-    }
-    __device__ Shared(char *p, int tables) {
-        table = reinterpret_cast<uint32_t *>(p);
-        p += static_cast<size_t>(kCols) * 4 * tables;
-        lanes = reinterpret_cast<uint4 *>(p);
-        p += 256 * sizeof(uint4);
-        list = reinterpret_cast<uint16_t *>(p);
-        p += kCols * 2;
-        touched = reinterpret_cast<uint32_t *>(p);
-        allow_t = touched + kWords;
-        allow_r = allow_t + kWords;
-        skip_t = allow_r + kWords;
-        skip_r = skip_t + kWords;
-    }
-    __device__ void init(int n_table_words) const {
-        for (int j = threadIdx.x; j < n_table_words; j += kCtlThreads) table[j] = 0;
-        lanes[threadIdx.x] = ctl_lanes(threadIdx.x);
-    }
-};
-static_assert(kCtlThreads == 256, "one mask table entry a thread");
+constexpr int kStreamWarps = 16, kScoutWarps = 7;
+constexpr int kTile = 16 * 32 * kStreamWarps;  // columns of a stage
+constexpr int kStreamThreads = kStreamWarps * 32, kScoutThreads = kScoutWarps * 32;
+constexpr int kThreads = kStreamThreads + kScoutThreads + 32;  // the producer's warp last
+// Scoring keeps a state for each warp and segment of 57344 columns, whether one
+// unit takes all segments of a row or each is a unit of its own, so a row's
+// bits do not depend on how many rows there are.
+constexpr int kSegment = 7 * 8192;
+constexpr int kStates = kStreamWarps + kScoutWarps;
+static_assert(kSegment % kTile == 0, "segments of whole tiles");
+constexpr int kMaxWidth = 3 * kSegment;        // columns of a unit: the bitmaps' room
+constexpr int kWords = kMaxWidth / 32;
+constexpr int kLines = kWords / 32;            // lines of 32 bitmap words, one warp's scan each
+// touched tokens at a time (more take several passes over the history)
+constexpr int cap_of(int mode) { return mode == kScore ? 1536 : 4096; }
+constexpr int kKept = 8;                       // history tokens that a scout keeps between its two passes
+constexpr int kStagedBias = 128;               // bias entries kept in shared memory (more stay in global)
+constexpr int kStagePad = 64;                  // a copy starts and ends on 16-byte boundaries around its columns
+static_assert(2 * 8 * kStreamThreads == kTile, "two groups of eight columns a thread and tile");
 
-// the byte of bits for the eight columns of group g
-__device__ __forceinline__ uint32_t group_bits(const uint32_t *words, int g) {
-    return reinterpret_cast<const uint8_t *>(words)[g];
+constexpr unsigned long long kWaitLimitNs = 4000000000ull;
+constexpr uint32_t kWaitLimitIters = 1u << 30;
+
+// ---- barriers and copies (inline PTX) ----------------------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-
-struct ApplyArgs {
-    CtlSide c;
-    const char *x;
-    char *out;
-    int64_t x_stride, out_stride;  // bytes
-    int64_t n_rows, vocab;
-    int n_chunks, per_unit;        // chunks a row, chunks a unit
-};
-
-// Unit u of `n_units` a row: the row, and which of its units.  Consecutive
-// units belong to one row; each row starts at another of its units, because a
-// tokenizer's frequent tokens sit in the first columns: with a grid that is a
-// multiple of n_units, the same blocks would otherwise get every row's first
-// unit (measured: 428 us instead of 131 us on 256 rows of long histories).
-__device__ __forceinline__ void unit_of(int64_t u, int n_units, int64_t &row, int &k) {
-    row = u / n_units;
-    k = static_cast<int>((u - row * n_units + row) % n_units);
+__device__ __forceinline__ unsigned long long globaltimer_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
 }
-
-template <bool kXBf16, bool kOBf16, bool kVec, int kCols>
-__global__ void __launch_bounds__(kCtlThreads, 4) apply_kernel(const __grid_constant__ ApplyArgs a) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ int warp_sum[kCtlWarps];
-    __shared__ CtlRow o;
-    const Shared<kCols> sh(smem, 1);
-    constexpr int kGroups = kCols / 8 / kCtlThreads;
-    const int t = threadIdx.x;
-    const bool marks = a.c.counts || a.c.n_bias > 0;
-    sh.init(marks ? kCols : 0);
-    if (t < Shared<kCols>::kWords) sh.touched[t] = 0;
-    const int n_units = (a.n_chunks + a.per_unit - 1) / a.per_unit;
-    const int64_t units = a.n_rows * n_units;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        int64_t r;
-        int k;
-        unit_of(u, n_units, r, k);
-        const char *xrow = a.x + r * a.x_stride;
-        char *orow = a.out + r * a.out_stride;
-        __syncthreads();  // the last unit's row is done with
-        if (t == 0) o = ctl_row(a.c, r);
-        const int ch1 = min(a.n_chunks, (k + 1) * a.per_unit);
-        for (int ch = k * a.per_unit; ch < ch1; ++ch) {
-            const int64_t c0 = static_cast<int64_t>(ch) * kCols;
-            Group8<kXBf16> raw[kGroups];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int64_t j = c0 + 8 * (t + g * kCtlThreads);
-                if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
-            }
-            __syncthreads();  // the table and the bitmaps are free again
-            int n = 0;
-            if (marks) {
-                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
-                ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, -1, nullptr);
-                __syncthreads();
-            }
-            uint32_t bits = 0;
-            if (t < Shared<kCols>::kWords) {
-                bits = sh.touched[t];
-                sh.touched[t] = 0;
-                sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
-            }
-            if (marks) n = ctl_list(bits, sh.list, warp_sum);
-            __syncthreads();
-            const float scale = o.scale;
-            // the touched tokens' logits replace their table words
-            for (int i = t; i < n; i += kCtlThreads) {
-                const int j = sh.list[i];
-                const uint32_t w = sh.table[j];
-                float z = -INFINITY;
-                if (sh.allow_t[j >> 5] >> (j & 31) & 1u) {
-                    const Two v = ctl_value(ctl_elem<kXBf16>(xrow, c0 + j), w, a.c, o, r, c0 + j, nullptr);
-                    z = __fmaf_rn(v.h, scale, __fmul_rn(v.l, scale));
-                }
-                sh.table[j] = __float_as_uint(z);
-            }
-            if (n && a.x == a.out) __syncthreads();  // in place: read before the stream overwrites
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int gi = t + g * kCtlThreads;
-                const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
-                if (j >= a.vocab) continue;
-                float v[8];
-                ctl_unpack8<kXBf16>(raw[g], v);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], scale);
-                Group8<kOBf16> w;
-                ctl_pack8<kOBf16>(v, w);
-                const uint32_t skip = group_bits(sh.allow_t, gi) ^ 0xffu;
-                if (skip) ctl_fill8<kOBf16, 0xff80u>(w, sh.lanes[skip]);  // -inf
-                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
-            }
-            if (n) {
-                __syncthreads();  // the stream's stores come first
-                for (int i = t; i < n; i += kCtlThreads) {
-                    const int j = sh.list[i];
-                    ctl_store1<kOBf16>(orow, c0 + j, __uint_as_float(sh.table[j]));
-                    sh.table[j] = 0;
-                }
-            }
+__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+// Bounded wait; when it gives up it raises the block's abort flag and, where
+// there is a status word, sets LPD_STATUS_TIMEOUT.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
+                                       bool honour_abort) {
+    const unsigned long long t0 = globaltimer_ns();
+    for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 255u) == 0) {
+            if (honour_abort && *abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
         }
     }
+    *abort_flag = 1;
+    if (status) atomicOr(status, LPD_STATUS_TIMEOUT);
+    return false;
 }
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
+                                           bool honour_abort = true) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status, honour_abort);
+}
+// All scouts reach it or none does: what one of them waits for, they all learn from it.
+__device__ __forceinline__ void scout_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kScoutThreads) : "memory"); }
 
-struct GradArgs {
-    CtlSide c;
-    const char *x;
-    char *out;
-    int64_t x_stride, out_stride;  // bytes
+// ---- arguments ---------------------------------------------------------------------
+// One [rows, vocab] tensor as the stream reads it.
+struct Plane {
+    const char *base;
+    int64_t stride;     // bytes
+    const char *end;    // behind the last row's last column
+};
+
+struct StreamArgs {
+    CtlSide c[2];       // the controls (kScore: train, rollout)
+    Plane in[2];
     int64_t n_rows, vocab;
-    int n_chunks, per_unit;
+    int width, n_units; // columns of a unit (a multiple of 32; kScore: of kSegment), units a row
+    int n_segs;         // kScore: segments a row
+    int same;           // kScore: one count serves both sides
+    uint32_t *status;
+    int n_stages;
+    // kApply, kGrad
+    char *out;
+    int64_t out_stride;  // bytes
+    int late;            // in place: the stream starts once the touched logits have been read
     const int32_t *ids;
     const uint8_t *mask;
     const float *logp, *grad;
+    // kScore
+    const WsHeader *hdr;
+    const int2 *rowid;
+    float4 *part_a;
+    float *part_b;
+    double2 *pick;
 };
 
-// d(g logp)/dx_j = g scale (1[j = id] - p_j) dx3/dx, p_j = 2^(z_j log2 e - lse
-// log2 e) with lse = z[id] - logp from the forward's own output (as the plain
-// gradient does).  Its base-2 form is kept as two floats; the low one enters as
-// a factor, so the stream spends one multiply-add, one exponential and one
-// product a column.  The selected token is always on the list, so the stream
-// has no one-hot term.
-template <bool kXBf16, bool kOBf16, bool kVec, int kCols>
-__global__ void __launch_bounds__(kCtlThreads, 4) gradient_kernel(const __grid_constant__ GradArgs a) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ int warp_sum[kCtlWarps];
-    __shared__ uint32_t id_word;
-    __shared__ float lse2[2];
-    __shared__ CtlRow o;
-    const Shared<kCols> sh(smem, 1);
-    constexpr int kGroups = kCols / 8 / kCtlThreads;
-    const int t = threadIdx.x;
-    const bool marks = a.c.counts || a.c.n_bias > 0;
-    sh.init(kCols);
-    if (t < Shared<kCols>::kWords) sh.touched[t] = 0;
-    const int n_units = (a.n_chunks + a.per_unit - 1) / a.per_unit;
-    const int64_t units = a.n_rows * n_units;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        int64_t r;
-        int k;
-        unit_of(u, n_units, r, k);
-        const char *xrow = a.x + r * a.x_stride;
-        char *orow = a.out + r * a.out_stride;
-        const int ch0 = k * a.per_unit, ch1 = min(a.n_chunks, ch0 + a.per_unit);
-        const bool active = a.mask[r] != 0;
-        const int64_t id = active ? a.ids[r] : 0;
-        if (!(active && id >= 0 && id < a.vocab)) {
-            // inactive rows: 0; an active row with an out-of-range id: NaN
-            float v[8];
-            Group8<kOBf16> w;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = active ? CUDART_NAN_F : 0.f;
-            ctl_pack8<kOBf16>(v, w);
-            const int64_t end = min(static_cast<int64_t>(ch1) * kCols, a.vocab);
-            for (int64_t j = static_cast<int64_t>(ch0) * kCols + 8 * t; j < end; j += 8 * kCtlThreads)
-                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
-            continue;
-        }
-        __syncthreads();  // the last unit's row is done with
-        if (t == 0) o = ctl_row(a.c, r);
-        float gs = a.grad[r], f = 0.f, lh = 0.f, ll = 0.f, gl = 0.f;
-        for (int ch = ch0; ch < ch1; ++ch) {
-            const int64_t c0 = static_cast<int64_t>(ch) * kCols;
-            Group8<kXBf16> raw[kGroups];
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int64_t j = c0 + 8 * (t + g * kCtlThreads);
-                if (j < a.vocab) ctl_load8<kXBf16, kVec>(xrow, j, a.vocab, raw[g]);
-            }
-            if (t == 0) id_word = 0;
-            __syncthreads();  // the table and the bitmaps are free again
-            const bool first = ch == ch0;
-            if (marks) {
-                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kCols), a.vocab - c0));
-                ctl_mark(a.c, o, r, c0, len, sh.table, sh.touched, first ? id : -1, first ? &id_word : nullptr);
-                __syncthreads();
-            }
-            uint32_t bits = 0;
-            if (t < Shared<kCols>::kWords) {
-                bits = sh.touched[t];
-                sh.touched[t] = 0;
-                sh.allow_t[t] = ctl_allowed(o, c0, t, a.vocab);
-                if ((id - c0) >> 5 == t) bits |= 1u << (id & 31);
-            }
-            const int n = ctl_list(bits, sh.list, warp_sum);
-            if (first && t == kCtlThreads - 1) {
-                const uint32_t word = o.mask ? __ldg(o.mask + id / 32) : 0xffffffffu;
-                double z = -CUDART_INF;
-                if (!o.none && (word >> (id & 31) & 1u)) {
-                    const Two v = ctl_value(ctl_elem<kXBf16>(xrow, id), id_word, a.c, o, r, id, nullptr);
-                    z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
-                }
-                const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
-                lse2[0] = static_cast<float>(l2);
-                lse2[1] = static_cast<float>(l2 - static_cast<double>(lse2[0]));
-            }
-            __syncthreads();
-            if (first) {
-                gs = __fmul_rn(gs, o.scale);
-                f = __fmul_rn(o.scale, kLog2e);
-                lh = lse2[0];
-                ll = lse2[1];
-                gl = __fmul_rn(-gs, ex2(-ll));
-            }
-            for (int i = t; i < n; i += kCtlThreads) {
-                const int j = sh.list[i];
-                const uint32_t w = sh.table[j];
-                float d = 0.f;
-                if (sh.allow_t[j >> 5] >> (j & 31) & 1u) {
-                    float slope;
-                    const Two v = ctl_value(ctl_elem<kXBf16>(xrow, c0 + j), w, a.c, o, r, c0 + j, &slope);
-                    const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -lh), ll), __fmul_rn(v.l, f)));
-                    d = __fmul_rn(__fmul_rn(gs, slope), __fsub_rn(c0 + j == id ? 1.f : 0.f, p));
-                }
-                sh.table[j] = __float_as_uint(d);
-            }
-            const f2_t f2f = f2(f, f), l2f = f2(-lh, -lh), g2f = f2(gl, gl);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const int gi = t + g * kCtlThreads;
-                const int64_t j = c0 + 8 * static_cast<int64_t>(gi);
-                if (j >= a.vocab) continue;
-                float v[8];
-                ctl_unpack8<kXBf16>(raw[g], v);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f2_t d = mul2(g2f, ex2_2(fma2(f2(v[2 * q], v[2 * q + 1]), f2f, l2f)));
-                    v[2 * q] = f2_lo(d);
-                    v[2 * q + 1] = f2_hi(d);
-                }
-                Group8<kOBf16> w;
-                ctl_pack8<kOBf16>(v, w);
-                const uint32_t skip = group_bits(sh.allow_t, gi) ^ 0xffu;
-                if (skip) ctl_fill8<kOBf16, 0u>(w, sh.lanes[skip]);
-                ctl_store8<kOBf16, kVec>(orow, j, a.vocab, w);
-            }
-            if (n) {
-                __syncthreads();  // the stream's stores come first
-                for (int i = t; i < n; i += kCtlThreads) {
-                    const int j = sh.list[i];
-                    ctl_store1<kOBf16>(orow, c0 + j, __uint_as_float(sh.table[j]));
-                    sh.table[j] = 0;
-                }
-            }
-        }
+// What the stream needs of a row, written by the scouts.
+struct RowNumbers {
+    float s, l, lt;    // scale (kScore: the rollout's), times log2 e, the train side's
+    int same_scale;
+    float lse2, g;     // kGrad: lse in base 2 (upper part), -grad * scale * 2^(-lower part)
+    const uint8_t *mask[2];  // each side's mask bits, null: everything allowed
+    int none[2];             // nothing allowed
+};
+
+template <int kMode>
+struct Smem {
+    static constexpr int kSides = kMode == kScore ? 2 : 1;
+    static constexpr int kCap = cap_of(kMode);
+    uint64_t full[16], empty[16], ready[2], done[2];
+    CtlRow row[2];
+    RowNumbers num[2];
+    uint32_t id_word;
+    int ok, abort_flag;
+    int total;
+    int line_base[kLines + 1];                  // touched columns in the lines in front
+    float gs, ll;                               // kGrad: grad * scale, the lower part of lse2
+    alignas(16) uint4 lanes[256];
+    uint32_t touched[kSides][kWords];           // kScore: [unit parity], the stream leaves these out
+    uint16_t before[kWords];                    // touched columns in the words in front, of the same line
+    uint32_t word[2][kCap];                     // kScore: a side's count words; else [unit parity], the values
+    uint32_t list[kSides == 2 ? 1 : 2][kCap];   // their columns in the unit
+    int32_t bias_ids[kSides][kStagedBias];      // the row's biases
+    float bias[kSides][kStagedBias];
+};
+template <int kMode>
+constexpr size_t ring_offset() {
+    return (sizeof(Smem<kMode>) + 127) / 128 * 128;
+}
+constexpr size_t kSmemMost = 232448 - 1024;  // what a block may have, less the driver's own
+
+// ---- where a tile's columns are ------------------------------------------------------
+// Bulk copies start and end on 16-byte boundaries: the tile's bytes are widened
+// to them as far as the tensor goes.  Column c of the tile's range sits at byte
+// `lead` + (c - first) * size of the stage; columns [lo, hi) are there, the few
+// others (at the tensor's two ends) come from global memory.
+struct Span {
+    const char *src;
+    uint32_t bytes, at;  // copied bytes, and where in the stage they go
+    uint32_t lead;
+    int64_t lo, hi;
+};
+template <int kElt>
+__device__ __forceinline__ Span span_of(const Plane &p, const char *row, int64_t first, int64_t end) {
+    Span s;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(row + first * kElt), a1 = reinterpret_cast<uintptr_t>(row + end * kElt);
+    const uintptr_t low = a0 & ~uintptr_t{15};
+    uintptr_t b = low, e = (a1 + 15) & ~uintptr_t{15};
+    if (b < reinterpret_cast<uintptr_t>(p.base)) b += 16;
+    if (e > reinterpret_cast<uintptr_t>(p.end)) e -= 16;
+    s.lead = static_cast<uint32_t>(a0 - low);
+    s.src = reinterpret_cast<const char *>(b);
+    s.at = static_cast<uint32_t>(b - low);
+    s.bytes = e > b ? static_cast<uint32_t>(e - b) : 0u;
+    // (element sizes divide 16, so both ends fall between columns)
+    s.lo = b > a0 ? first + static_cast<int64_t>((b - a0) / kElt) : first;
+    s.hi = e < a1 ? end - static_cast<int64_t>((a1 - e) / kElt) : end;
+    return s;
+}
+
+// Unit u: the row (kScore: its place among the active rows) and which of its
+// units.  Each row starts at another of its units: a tokenizer's frequent
+// tokens sit in the first columns, and a grid that is a multiple of n_units
+// would give the same blocks every row's first unit.
+__device__ __forceinline__ void unit_of(int64_t u, int n_units, int64_t &row, int &k) {
+    if (n_units == 1) {
+        row = u;
+        k = 0;
+        return;
     }
+    row = u / n_units;
+    k = static_cast<int>((u - row * n_units + row) % n_units);
 }
 
 // ---- scoring: sums of both sides ---------------------------------------------------
@@ -413,170 +332,617 @@ __device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float l
     a.dd = add2(a.dd, f2(d, 0.f));
 }
 
-// A unit is kSegChunks chunks of a row, its state carried over them; the number
-// is fixed, so a row's arithmetic depends on its columns alone.
-constexpr int kSegChunks = 4;
-
-// kTables: 1 when both sides count in the same history (or one side counts in
-// none), else one table a side.
-template <bool kTBf16, bool kRBf16, bool kVec, int kTables>
-__global__ void __launch_bounds__(kCtlThreads, kTables == 1 ? 3 : 2)
-    score_kernel(const __grid_constant__ CtlScoreArgs a) {
-    extern __shared__ __align__(16) char smem[];
-    __shared__ int warp_sum[kCtlWarps];
-    __shared__ float states[5][kCtlWarps];
-    __shared__ CtlRow ot, orr;
-    const Shared<kChunk> sh(smem, kTables);
-    uint32_t *const table_t = sh.table, *const table_r = sh.table + (kTables - 1) * kChunk;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const bool marks_t = a.t.counts || a.t.n_bias > 0, marks_r = a.r.counts || a.r.n_bias > 0;
-    const bool marks = marks_t || marks_r;
-    sh.init(marks ? kTables * kChunk : 0);
-    sh.touched[t] = 0;
-    const int n_chunks = static_cast<int>((a.vocab + kChunk - 1) / kChunk);
-    const int64_t units = a.hdr->n_active * a.n_chunks;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        int64_t i;
-        int k;
-        unit_of(u, a.n_chunks, i, k);
-        const int2 rid = a.rowid[i];
-        const int64_t r = rid.x, id = rid.y;
-        const char *trow = a.xt + r * a.t_stride, *rrow = a.xr + r * a.r_stride;
-        const int64_t end = min(static_cast<int64_t>(k + 1) * kSegChunks * kChunk, a.vocab);
-        // 16 columns of each side a thread and step: groups t and t + 256 of
-        // the step's 4096 columns; each step's loads go out before the step
-        // in front of it is worked on, a chunk's first ones before its scan
-        Group8<kTBf16> gt[2];
-        Group8<kRBf16> gr[2];
-        auto load = [&](int64_t c) {
+// ---- the scouts --------------------------------------------------------------------
+// The tokens k, k + kScoutThreads, ... of a range, kKept of them in flight;
+// those behind its end as -1 (no token).
+__device__ __forceinline__ void fetch_tokens(const CtlSide &c, int64_t k, int64_t end, int32_t *t) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int64_t j = c + 8 * (t + g * kCtlThreads);
-                if (j < end) {
-                    ctl_load8<kTBf16, kVec>(trow, j, a.vocab, gt[g]);
-                    ctl_load8<kRBf16, kVec>(rrow, j, a.vocab, gr[g]);
-                }
-            }
-        };
-        const int ch0 = k * kSegChunks, ch1 = min(n_chunks, ch0 + kSegChunks);
-        load(static_cast<int64_t>(ch0) * kChunk);
-        if (t == 0) ot = ctl_row(a.t, r);
-        if (t == 32) orr = ctl_row(a.r, r);
-        __syncthreads();
-        const float s_r = orr.scale;
-        const float lt = __fmul_rn(ot.scale, kLog2e), lr = __fmul_rn(s_r, kLog2e);
-        const bool same_scale = ot.scale == s_r;
-        Acc2 acc = acc2_init();
+    for (int u = 0; u < kKept; ++u) {
+        const int64_t at = k + u * kScoutThreads;
+        t[u] = at < end ? __ldg(c.history + at) : -1;
+    }
+}
+// f(token, generated) over the row's range; `kept` holds the first tokens.
+template <class F>
+__device__ __forceinline__ void each_token(const CtlSide &c, const CtlRow &o, int st, const int32_t *kept, F f) {
+    int64_t k = o.begin + st;
+#pragma unroll
+    for (int u = 0; u < kKept; ++u)
+        if (kept[u] >= 0) f(kept[u], k + u * kScoutThreads >= o.split);
 #pragma unroll 1
-        for (int ch = ch0; ch < ch1; ++ch) {
-            const int64_t c0 = static_cast<int64_t>(ch) * kChunk;
-            __syncthreads();  // the table and the bitmaps are free again
-            if (marks) {
-                const uint32_t len = static_cast<uint32_t>(min(static_cast<int64_t>(kChunk), a.vocab - c0));
-                if (marks_t) ctl_mark(a.t, ot, r, c0, len, table_t, sh.touched, -1, nullptr);
-                if (marks_r && !a.same) ctl_mark(a.r, orr, r, c0, len, table_r, sh.touched, -1, nullptr);
-                __syncthreads();
-            }
-            const uint32_t bits = sh.touched[t];
-            sh.touched[t] = 0;
-            const uint32_t at = ctl_allowed(ot, c0, t, a.vocab), ar = ctl_allowed(orr, c0, t, a.vocab);
-            sh.allow_t[t] = at;
-            sh.allow_r[t] = ar;
-            sh.skip_t[t] = bits | ~at;
-            sh.skip_r[t] = bits | ~ar;
-            if ((id - c0) >> 5 == t && id < a.vocab && !(bits >> (id & 31) & 1u))  // an untouched selected token
-                a.pick[i] = make_double2(at >> (id & 31) & 1u ? static_cast<double>(ctl_elem<kTBf16>(trow, id)) : -CUDART_INF,
-                                         ar >> (id & 31) & 1u ? static_cast<double>(ctl_elem<kRBf16>(rrow, id)) : -CUDART_INF);
-            const int n = marks ? ctl_list(bits, sh.list, warp_sum) : 0;
-            __syncthreads();
-            for (int q = t; q < n; q += kCtlThreads) {
-                const int j = sh.list[q];
-                const uint32_t bit = 1u << (j & 31);
-                const uint32_t wt = marks_t ? table_t[j] : 0u;
-                const uint32_t wr = a.same ? wt : marks_r ? table_r[j] : 0u;
-                Two vt{-INFINITY, 0.f}, vr{-INFINITY, 0.f};
-                if (sh.allow_t[j >> 5] & bit)
-                    vt = ctl_value(ctl_elem<kTBf16>(trow, c0 + j), wt, a.t, ot, r, c0 + j, nullptr);
-                if (sh.allow_r[j >> 5] & bit)
-                    vr = ctl_value(ctl_elem<kRBf16>(rrow, c0 + j), wr, a.r, orr, r, c0 + j, nullptr);
-                table_t[j] = 0;
-                if (kTables > 1) table_r[j] = 0;
-                accumulate_pair(vt, vr, acc, lt, lr, s_r, same_scale);
-                if (c0 + j == id)
-                    a.pick[i] = make_double2(static_cast<double>(vt.h) + static_cast<double>(vt.l),
-                                             static_cast<double>(vr.h) + static_cast<double>(vr.l));
-            }
-#pragma unroll 1
-            for (int step = 0; step < kChunk / 16 / kCtlThreads; ++step) {
-                uint32_t st[2], sr[2];
+    for (k += kKept * kScoutThreads; k < o.end; k += kKept * kScoutThreads) {
+        int32_t t[kKept];
+        fetch_tokens(c, k, o.end, t);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int gi = t + (2 * step + g) * kCtlThreads;
-                    st[g] = group_bits(sh.skip_t, gi);
-                    sr[g] = group_bits(sh.skip_r, gi);
-                    if (st[g]) ctl_fill8<kTBf16, kFillBits>(gt[g], sh.lanes[st[g]]);
-                    if (sr[g]) ctl_fill8<kRBf16, kFillBits>(gr[g], sh.lanes[sr[g]]);
-                }
-                float vt[16], vr[16];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    ctl_unpack8<kTBf16>(gt[g], vt + 8 * g);
-                    ctl_unpack8<kRBf16>(gr[g], vr + 8 * g);
-                }
-                load(c0 + (step + 1) * 16 * kCtlThreads);  // the next chunk's first step behind the last one
-                if ((st[0] & st[1] & sr[0] & sr[1]) == 0xffu) continue;  // nothing allowed
-                f2_t pt[8], pr[8];
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    pt[p] = f2(vt[2 * p], vt[2 * p + 1]);
-                    pr[p] = f2(vr[2 * p], vr[2 * p + 1]);
-                }
-                if (same_scale && accumulate_near(pt, pr, acc, lr, s_r)) continue;
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const uint32_t bt = st[p >> 2] >> (2 * (p & 3)), br = sr[p >> 2] >> (2 * (p & 3));
-                    pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(pt[p]), bt & 2u ? -INFINITY : f2_hi(pt[p]));
-                    pr[p] = f2(br & 1u ? -INFINITY : f2_lo(pr[p]), br & 2u ? -INFINITY : f2_hi(pr[p]));
-                }
-                accumulate_far(pt, pr, acc, lt, lr);
-            }
-        }
-        // the block's state: each warp's in a butterfly, then the eight warps' in another
-        const Acc w = warp_reduce_acc<false>(acc2_fold(acc), lt, lr);
-        if (lane == 0) {
-            states[0][warp] = w.mt;
-            states[1][warp] = w.st;
-            states[2][warp] = w.dd;
-            states[3][warp] = w.mr;
-            states[4][warp] = w.sr;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            const int s = lane & (kCtlWarps - 1);
-            Acc b{states[0][s], states[1][s], states[2][s], states[3][s], states[4][s], 0.f, 0.f};
-#pragma unroll
-            for (int off = kCtlWarps / 2; off > 0; off >>= 1) {
-                Acc y;
-                y.mt = __shfl_xor_sync(0xffffffffu, b.mt, off);
-                y.st = __shfl_xor_sync(0xffffffffu, b.st, off);
-                y.dd = __shfl_xor_sync(0xffffffffu, b.dd, off);
-                y.mr = __shfl_xor_sync(0xffffffffu, b.mr, off);
-                y.sr = __shfl_xor_sync(0xffffffffu, b.sr, off);
-                y.ht = y.hr = 0.f;
-                merge_acc<false>(b, y, lt, lr);
-            }
-            if (lane == 0) {
-                a.part_a[i * a.n_chunks + k] = make_float4(b.mt, b.st, b.dd, b.mr);
-                a.part_b[i * a.n_chunks + k] = b.sr;
-            }
-        }
+        for (int u = 0; u < kKept; ++u)
+            if (t[u] >= 0) f(t[u], k + u * kScoutThreads >= o.split);
     }
 }
 
-// One warp per active row: lane l folds units l, l + 32, ... in order, the
+// The element type's name in templates.
+template <bool kBf16>
+constexpr int elt() { return kBf16 ? 2 : 4; }
+
+template <int kMode, bool kXBf16, bool kYBf16, bool kAligned>
+__global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_constant__ StreamArgs a) {
+    // kYBf16: the rollout's logits (kScore) or the output
+    extern __shared__ __align__(128) char smem_raw[];
+    Smem<kMode> &sm = *reinterpret_cast<Smem<kMode> *>(smem_raw);
+    char *const ring = smem_raw + ring_offset<kMode>();
+    constexpr bool kTwo = kMode == kScore;
+    constexpr int kXE = elt<kXBf16>(), kYE = elt<kYBf16>();
+    constexpr int kStageX = kTile * kXE + kStagePad;
+    constexpr int kStage = kStageX + (kTwo ? kTile * kYE + kStagePad : 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n_rows = kTwo ? a.hdr->n_active : a.n_rows;
+    const int64_t units = n_rows * a.n_units;
+
+    if (threadIdx.x == 0) {
+        sm.abort_flag = 0;
+        for (int s = 0; s < a.n_stages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], kStreamWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.ready[b], 1);
+            mbar_init(&sm.done[b], kStreamWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (threadIdx.x < 256) sm.lanes[threadIdx.x] = ctl_lanes(threadIdx.x);
+    __syncthreads();
+
+    // kGrad: a row without a gradient (inactive, or an id out of range) has no
+    // tiles and no scouting; every role decides it alike
+    auto live = [&](int64_t r) -> bool {
+        if (kMode != kGrad) return true;
+        if (a.mask[r] == 0) return false;
+        const int64_t id = a.ids[r];
+        return id >= 0 && id < a.vocab;
+    };
+    // Columns between the start of a unit's first group of eight and the unit:
+    // groups start on 16-byte boundaries of the output row.
+    auto lead_in = [&](int64_t r, int64_t c0) -> int {
+        if (kTwo || kAligned) return 0;
+        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(a.out + r * a.out_stride + c0 * kYE) & 15u) / kYE;
+        return kYBf16 ? at : at & 3;
+    };
+
+    if (warp == kStreamWarps + kScoutWarps) {
+        // ------------------------------------------------------------ producer
+        if (lane != 0) return;
+        uint64_t policy;
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+        uint32_t it = 0;
+        bool ok = true;
+        for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            int64_t i;
+            int k;
+            unit_of(u, a.n_units, i, k);
+            const int64_t r = kTwo ? a.rowid[i].x : i;
+            if (!live(r)) continue;
+            const int64_t c0 = static_cast<int64_t>(k) * a.width, c1 = min(c0 + a.width, a.vocab);
+            for (int64_t tc = c0 - lead_in(r, c0); tc < c1; tc += kTile, ++it) {
+                const uint32_t s = it % a.n_stages, round = it / a.n_stages;
+                if (round > 0 && !wait_phase(&sm.empty[s], (round - 1) & 1, &sm.abort_flag, a.status)) {
+                    ok = false;
+                    break;
+                }
+                char *st = ring + static_cast<size_t>(s) * kStage;
+                const int64_t f = max(tc, c0), e = min(tc + kTile, c1);
+                const Span x = span_of<kXE>(a.in[0], a.in[0].base + r * a.in[0].stride, f, e);
+                if (kTwo) {
+                    const Span y = span_of<kYE>(a.in[1], a.in[1].base + r * a.in[1].stride, f, e);
+                    mbar_arrive_expect_tx(&sm.full[s], x.bytes + y.bytes);
+                    if (x.bytes) bulk_g2s(st + x.at, x.src, x.bytes, &sm.full[s], policy);
+                    if (y.bytes) bulk_g2s(st + kStageX + y.at, y.src, y.bytes, &sm.full[s], policy);
+                } else {
+                    mbar_arrive_expect_tx(&sm.full[s], x.bytes);
+                    if (x.bytes) bulk_g2s(st + x.at, x.src, x.bytes, &sm.full[s], policy);
+                }
+            }
+        }
+        // every copy issued must land before the block's shared memory goes away
+        const uint32_t first = it > static_cast<uint32_t>(a.n_stages) ? it - a.n_stages : 0;
+        for (uint32_t j = first; j < it; ++j)
+            wait_phase(&sm.full[j % a.n_stages], (j / a.n_stages) & 1, &sm.abort_flag, a.status, false);
+        return;
+    }
+
+    if (warp >= kStreamWarps) {
+        // -------------------------------------------------------------- scouts
+        const int st = threadIdx.x - kStreamThreads;
+        constexpr int kCap = Smem<kMode>::kCap;
+        constexpr int kLast = kTwo ? 1 : 0;
+        const bool counts[2] = {a.c[0].counts != 0, kTwo && !a.same && a.c[1].counts != 0};
+        uint32_t n_live = 0;
+        // kApply, kGrad: the unit whose touched values wait for the stream to pass
+        int64_t held_row = -1, held_c0 = 0;
+        int held_n = 0;
+        // one scout waits, all learn how it ended
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+            if (st == 0) sm.ok = wait_phase(bar, parity, &sm.abort_flag, a.status) ? 1 : 0;
+            scout_sync();
+            const bool ok = sm.ok != 0;
+            scout_sync();
+            return ok;
+        };
+        auto store_held = [&](uint32_t unit) -> bool {
+            const uint32_t b = unit & 1;
+            if (!wait_all(&sm.done[b], (unit >> 1) & 1)) return false;
+            if constexpr (!kTwo) {
+                char *orow = a.out + held_row * a.out_stride;
+                for (int i = st; i < held_n; i += kScoutThreads)
+                    ctl_store1<kYBf16>(orow, held_c0 + sm.list[b][i], __uint_as_float(sm.word[b][i]));
+            }
+            held_row = -1;
+            scout_sync();
+            return true;
+        };
+        for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+            int64_t i;
+            int k;
+            unit_of(u, a.n_units, i, k);
+            const int2 rid = kTwo ? a.rowid[i] : make_int2(0, 0);
+            const int64_t r = kTwo ? rid.x : i;
+            if (!live(r)) continue;
+            const int64_t id = kTwo ? static_cast<int64_t>(rid.y) : kMode == kGrad ? static_cast<int64_t>(a.ids[r]) : -1;
+            const uint32_t b = n_live & 1;
+            const int64_t c0 = static_cast<int64_t>(k) * a.width, c1 = min(c0 + a.width, a.vocab);
+            const uint32_t len = static_cast<uint32_t>(c1 - c0);
+            const int words = static_cast<int>((len + 31) / 32);
+            const char *xrow = a.in[0].base + r * a.in[0].stride;
+            const char *yrow = kTwo ? a.in[1].base + r * a.in[1].stride : nullptr;
+            uint32_t *const touched = sm.touched[kTwo ? b : 0];
+            // the bitmap of this parity belongs to the unit before the last;
+            // (store_held has waited for it in the elementwise forms)
+            if (kTwo && n_live >= 2 && !wait_all(&sm.done[b], ((n_live >> 1) - 1) & 1)) return;
+            if (st == 0) {
+                sm.row[0] = ctl_row(a.c[0], r);
+                sm.id_word = 0;
+            }
+            if (kTwo && st == 32) sm.row[1] = ctl_row(a.c[1], r);
+            for (int w = st; w < (words + 31) / 32 * 32; w += kScoutThreads) touched[w] = 0;
+            scout_sync();
+            int32_t kept[2][kKept];
+#pragma unroll
+            for (int side = 0; side <= kLast; ++side) {
+#pragma unroll
+                for (int v = 0; v < kKept; ++v) kept[side][v] = -1;
+                if (counts[side]) fetch_tokens(a.c[side], sm.row[side].begin + st, sm.row[side].end, kept[side]);
+            }
+            // first pass: which columns
+            auto mark = [&](int32_t tok) {
+                const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
+                if (j < len) {
+                    const uint32_t bit = 1u << (j & 31);
+                    volatile uint32_t *w = &touched[j >> 5];
+                    if (!(*w & bit)) atomicOr(&touched[j >> 5], bit);  // (a text's frequent tokens come often)
+                }
+            };
+#pragma unroll
+            for (int side = 0; side <= kLast; ++side) {
+                if (counts[side])
+                    each_token(a.c[side], sm.row[side], st, kept[side], [&](int32_t tok, bool gen) {
+                        mark(tok);
+                        if (kMode == kGrad && tok == id) {
+                            if (gen) atomicAdd(&sm.id_word, 1u);
+                            else atomicOr(&sm.id_word, kSeen);
+                        }
+                    });
+                for (int e = st; e < a.c[side].n_bias; e += kScoutThreads) {
+                    const int32_t tok = __ldg(a.c[side].bias_ids + r * a.c[side].n_bias + e);
+                    if (a.c[side].n_bias <= kStagedBias) {
+                        sm.bias_ids[side][e] = tok;
+                        sm.bias[side][e] = __ldg(a.c[side].bias + r * a.c[side].n_bias + e);
+                    }
+                    mark(tok);
+                    if (kMode == kGrad && tok == id) atomicOr(&sm.id_word, kBiased);
+                }
+            }
+            if (kMode == kGrad && st == 0 && id >= c0 && id < c1)
+                atomicOr(&touched[(id - c0) >> 5], 1u << ((id - c0) & 31));
+            scout_sync();
+            auto value = [&](int side, float x, uint32_t w, int64_t token, float *slope) -> Two {
+                const int n = a.c[side].n_bias;
+                const bool staged = n <= kStagedBias;
+                return ctl_value(x, w, sm.row[side], staged ? sm.bias_ids[side] : a.c[side].bias_ids + r * n,
+                                 staged ? sm.bias[side] : a.c[side].bias + r * n, n, token, slope);
+            };
+            // the row's numbers for the stream
+            if (st == 0) {
+                RowNumbers &num = sm.num[b];
+                const float s = sm.row[kLast].scale;
+                num.s = s;
+                num.l = __fmul_rn(s, kLog2e);
+                if (kTwo) {
+                    num.lt = __fmul_rn(sm.row[0].scale, kLog2e);
+                    num.same_scale = sm.row[0].scale == s ? 1 : 0;
+                }
+#pragma unroll
+                for (int side = 0; side <= kLast; ++side) {
+                    num.mask[side] = reinterpret_cast<const uint8_t *>(sm.row[side].mask);
+                    num.none[side] = sm.row[side].none ? 1 : 0;
+                }
+                if (kMode == kGrad) {
+                    const CtlRow &o = sm.row[0];
+                    double z = -CUDART_INF;
+                    if (ctl_allows(o, id)) {
+                        const Two v = value(0, ctl_elem<kXBf16>(xrow, id), sm.id_word, id, nullptr);
+                        z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
+                    }
+                    const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
+                    const float h = static_cast<float>(l2), gs = __fmul_rn(a.grad[r], o.scale);
+                    sm.ll = static_cast<float>(l2 - static_cast<double>(h));
+                    sm.gs = gs;
+                    num.lse2 = h;
+                    num.g = __fmul_rn(-gs, ex2(-sm.ll));
+                }
+                if (!a.late) mbar_arrive(&sm.ready[b]);
+            }
+            // each word's rank within its line
+            for (int line = kScoutWarps - 1 - (warp - kStreamWarps); 32 * line < words; line += kScoutWarps) {
+                const int w = 32 * line + lane;
+                const int n = __popc(touched[w]);
+                int incl = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                    if (lane >= off) incl += v;
+                }
+                sm.before[w] = static_cast<uint16_t>(incl - n);
+                if (lane == 31) sm.line_base[line] = incl;
+            }
+            scout_sync();
+            if (warp == kStreamWarps) {
+                // the lines' sums become what lies in front of them
+                const int lines = (words + 31) / 32;
+                int sum = 0;
+                for (int l0 = 0; l0 <= lines; l0 += 32) {
+                    const int n = l0 + lane < lines ? sm.line_base[l0 + lane] : 0;
+                    int incl = n;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                        if (lane >= off) incl += v;
+                    }
+                    if (l0 + lane <= lines) sm.line_base[l0 + lane] = sum + incl - n;
+                    sum += __shfl_sync(0xffffffffu, incl, 31);
+                }
+                if (lane == 0) sm.total = sum;
+            }
+            scout_sync();
+            const int total = sm.total;
+            uint32_t *const w0 = kTwo ? sm.word[0] : sm.word[b];
+            uint32_t *const w1 = sm.word[1];
+            uint32_t *const list = kTwo ? sm.list[0] : sm.list[b];
+            // The touched tokens of ranks [base, base + m): their columns, and
+            // in a second pass over the history how often each occurs.
+            auto count = [&](int base, int m) {
+                for (int q = st; q < m; q += kScoutThreads) {
+                    w0[q] = 0;
+                    if (kTwo) w1[q] = 0;
+                }
+                for (int w = st; w < words; w += kScoutThreads) {
+                    uint32_t bits = touched[w];
+                    int at = sm.line_base[w >> 5] + sm.before[w] - base;
+                    for (; bits; bits &= bits - 1, ++at)
+                        if (at >= 0 && at < m) list[at] = static_cast<uint32_t>(32 * w + __ffs(bits) - 1);
+                }
+                scout_sync();
+#pragma unroll
+                for (int side = 0; side <= kLast; ++side) {
+                    uint32_t *const word = side ? w1 : w0;
+                    auto place = [&](int32_t tok) -> int {
+                        const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
+                        if (j >= len) return -1;
+                        const uint32_t bits = touched[j >> 5];
+                        const int p = sm.line_base[j >> 10] + sm.before[j >> 5] + __popc(bits & ((1u << (j & 31)) - 1u)) - base;
+                        return p < m ? p : -1;
+                    };
+                    if (counts[side])
+                        each_token(a.c[side], sm.row[side], st, kept[side], [&](int32_t tok, bool gen) {
+                            const int p = place(tok);
+                            if (p < 0) return;
+                            if (gen) atomicAdd(&word[p], 1u);
+                            else if (!(*static_cast<volatile uint32_t *>(&word[p]) & kSeen)) atomicOr(&word[p], kSeen);
+                        });
+                    if (side == 0 || !a.same) {
+                        const int32_t *ids = a.c[side].n_bias <= kStagedBias ? sm.bias_ids[side]
+                                                                             : a.c[side].bias_ids + r * a.c[side].n_bias;
+                        for (int e = st; e < a.c[side].n_bias; e += kScoutThreads) {
+                            const int p = place(ids[e]);
+                            if (p >= 0) atomicOr(&word[p], kBiased);
+                        }
+                    }
+                }
+                scout_sync();
+            };
+            if constexpr (kTwo) {
+                const float s_r = sm.num[b].s, lt = sm.num[b].lt, lr = sm.num[b].l;
+                const bool same_scale = sm.num[b].same_scale != 0;
+                // an untouched selected token (the stream leaves a touched one to the list below)
+                if (st == 0 && id >= c0 && id < c1 && !(touched[(id - c0) >> 5] >> ((id - c0) & 31) & 1u))
+                    a.pick[i] = make_double2(
+                        ctl_allows(sm.row[0], id) ? static_cast<double>(ctl_elem<kXBf16>(xrow, id)) : -CUDART_INF,
+                        ctl_allows(sm.row[1], id) ? static_cast<double>(ctl_elem<kYBf16>(yrow, id)) : -CUDART_INF);
+                if (total > 0 && total <= kCap) count(0, total);
+                for (int64_t f = c0; f < c1; f += kSegment) {
+                    const int first = sm.line_base[(f - c0) >> 10];
+                    const int end = f + kSegment < c1 ? sm.line_base[(f + kSegment - c0) >> 10] : total;
+                    Acc2 acc = acc2_init();
+                    for (int base = first; base < end; base += kCap) {
+                        const int m = min(kCap, end - base);
+                        if (total > kCap) count(base, m);
+                        const int at = total > kCap ? 0 : base;  // list position of rank `base`
+                        for (int q = st; q < m; q += kScoutThreads) {
+                            const int64_t col = c0 + list[at + q];
+                            const float x0 = ctl_elem<kXBf16>(xrow, col), x1 = ctl_elem<kYBf16>(yrow, col);
+                            const bool in0 = ctl_allows(sm.row[0], col), in1 = ctl_allows(sm.row[1], col);
+                            Two vt{-INFINITY, 0.f}, vr{-INFINITY, 0.f};
+                            if (in0) vt = value(0, x0, w0[at + q], col, nullptr);
+                            if (in1) vr = value(1, x1, a.same ? w0[at + q] : w1[at + q], col, nullptr);
+                            accumulate_pair(vt, vr, acc, lt, lr, s_r, same_scale);
+                            if (col == id)
+                                a.pick[i] = make_double2(static_cast<double>(vt.h) + static_cast<double>(vt.l),
+                                                         static_cast<double>(vr.h) + static_cast<double>(vr.l));
+                        }
+                        if (total > kCap) scout_sync();
+                    }
+                    const Acc w = warp_reduce_acc<false>(acc2_fold(acc), lt, lr);
+                    if (lane == 0) {
+                        const int64_t o = (i * a.n_segs + f / kSegment) * kStates + warp;
+                        a.part_a[o] = make_float4(w.mt, w.st, w.dd, w.mr);
+                        a.part_b[o] = w.sr;
+                    }
+                }
+                scout_sync();
+            } else {
+                const float s = sm.row[0].scale, f = sm.num[b].l;
+                auto result = [&](int q) -> float {
+                    const int64_t col = c0 + list[q];
+                    const float x0 = ctl_elem<kXBf16>(xrow, col);
+                    const bool in0 = ctl_allows(sm.row[0], col);
+                    if (!in0) return kMode == kApply ? -INFINITY : 0.f;
+                    float slope;
+                    const Two v = value(0, x0, w0[q], col, &slope);
+                    if (kMode == kApply) return __fmaf_rn(v.h, s, __fmul_rn(v.l, s));
+                    const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -sm.num[b].lse2), sm.ll), __fmul_rn(v.l, f)));
+                    return __fmul_rn(__fmul_rn(sm.gs, slope), __fsub_rn(col == id ? 1.f : 0.f, p));
+                };
+                const int m = min(kCap, total);
+                if (total > 0) {
+                    count(0, m);
+                    for (int q = st; q < m; q += kScoutThreads) w0[q] = __float_as_uint(result(q));
+                }
+                scout_sync();
+                if (a.late && st == 0) mbar_arrive(&sm.ready[b]);
+                // the last unit's values, now that the stream has this one to go on with
+                if (held_row >= 0 && !store_held(n_live - 1)) return;
+                held_row = r;
+                held_c0 = c0;
+                held_n = m;
+                if (total > kCap) {
+                    // more than kCap (never in place): straight to the output, behind the stream
+                    if (!store_held(n_live)) return;
+                    for (int base = kCap; base < total; base += kCap) {
+                        const int n = min(kCap, total - base);
+                        count(base, n);
+                        for (int q = st; q < n; q += kScoutThreads)
+                            ctl_store1<kYBf16>(a.out + r * a.out_stride, c0 + list[q], result(q));
+                        scout_sync();
+                    }
+                }
+            }
+            ++n_live;
+        }
+        if (!kTwo && held_row >= 0) store_held(n_live - 1);
+        return;
+    }
+
+    // ------------------------------------------------------------------ stream
+    const int t = threadIdx.x;
+    uint32_t it = 0, n_live = 0;
+    bool dead = false;  // a wait gave up: what is left of the output reads as NaN
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        int64_t i;
+        int k;
+        unit_of(u, a.n_units, i, k);
+        const int64_t r = kTwo ? a.rowid[i].x : i;
+        const int64_t c0 = static_cast<int64_t>(k) * a.width, c1 = min(c0 + a.width, a.vocab);
+        char *const orow = kTwo ? nullptr : a.out + r * a.out_stride;
+        auto fill = [&](float value) {
+            float v[8];
+            Group8<kYBf16> w;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = value;
+            ctl_pack8<kYBf16>(v, w);
+            for (int64_t j = c0 - lead_in(r, c0) + 8 * t; j < c1; j += 8 * kStreamThreads) {
+                if (j >= c0 && j + 8 <= c1) ctl_store8<kYBf16>(orow, j, w);
+                else ctl_scatter8<kYBf16>(orow, j, c0, c1, w);
+            }
+        };
+        if (!kTwo && (dead || !live(r))) {
+            // inactive rows: 0; an active row with an out-of-range id: NaN
+            fill(!dead && a.mask[r] == 0 ? 0.f : CUDART_NAN_F);
+            continue;
+        }
+        const uint32_t b = n_live & 1;
+        {
+            const bool ok = wait_phase(&sm.ready[b], (n_live >> 1) & 1, &sm.abort_flag, a.status);
+            if (__any_sync(0xffffffffu, !ok)) {
+                if (kTwo) return;
+                dead = true;
+                fill(CUDART_NAN_F);
+                continue;
+            }
+        }
+        const RowNumbers &num = sm.num[b];
+        const bool same_scale = kTwo && num.same_scale != 0;
+        const float n_s = num.s, n_l = num.l, n_lt = kTwo ? num.lt : 0.f;
+        const float n_lse2 = kMode == kGrad ? num.lse2 : 0.f, n_g = kMode == kGrad ? num.g : 0.f;
+        // The columns that the stream leaves out, eight bits a group: masked
+        // ones, touched ones when scoring, and what lies behind the vocabulary.
+        // The mask's bytes come from global memory, asked for a tile ahead.
+        uint32_t masked[2][Smem<kMode>::kSides];
+        auto ask = [&](int64_t tc) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int64_t j = tc + 8 * (t + g * kStreamThreads);
+#pragma unroll
+                for (int side = 0; side < Smem<kMode>::kSides; ++side) {
+                    uint32_t m = num.none[side] ? 0xffu : 0u;
+                    const uint8_t *bits = num.mask[side];
+                    if (bits && j < c1 && j + 8 > c0) {
+                        if (kTwo || kAligned) {
+                            m = ~static_cast<uint32_t>(__ldg(bits + (j >> 3))) & 0xffu;
+                        } else {
+                            // groups that start between bytes, or in front of the unit
+                            const int64_t last = (a.vocab - 1) >> 3, at = j >> 3;
+                            const uint32_t lo = at >= 0 ? __ldg(bits + at) : 0u;
+                            const uint32_t hi = at + 1 <= last ? __ldg(bits + at + 1) : 0u;
+                            m = ~((lo | hi << 8) >> (j & 7)) & 0xffu;
+                        }
+                    }
+                    masked[g][side] = m;
+                }
+            }
+        };
+        ask(c0 - lead_in(r, c0));
+        const char *const xrow = a.in[0].base + r * a.in[0].stride;
+        const char *const yrow = kTwo ? a.in[1].base + r * a.in[1].stride : nullptr;
+        Acc2 acc = acc2_init();
+#pragma unroll 1
+        for (int64_t tc = c0 - lead_in(r, c0); tc < c1; tc += kTile, ++it) {
+            const uint32_t s = it % a.n_stages;
+            const bool ok = wait_phase(&sm.full[s], (it / a.n_stages) & 1, &sm.abort_flag, a.status);
+            if (__any_sync(0xffffffffu, !ok)) {
+                if (kTwo) return;
+                dead = true;
+                break;
+            }
+            const char *stg = ring + static_cast<size_t>(s) * kStage;
+            Group8<kXBf16> gx[2];
+            Group8<kYBf16> gy[2];
+            bool in[2] = {true, true};
+            if (kAligned && tc + kTile <= c1) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t j = 8 * (t + g * kStreamThreads);
+                    ctl_shared8<kXBf16, true>(stg, j * kXE, gx[g]);
+                    if constexpr (kTwo) ctl_shared8<kYBf16, true>(stg + kStageX, j * kYE, gy[g]);
+                }
+            } else {
+                const int64_t f = max(tc, c0), e = min(tc + kTile, c1);
+                auto fetch = [&](auto &g8, const Plane &plane, const char *row, const char *from, int64_t j, auto kind) {
+                    constexpr bool kB = decltype(kind)::value;
+                    const Span x = span_of<elt<kB>()>(plane, row, f, e);
+                    if (j >= x.lo && j + 8 <= x.hi)
+                        ctl_shared8<kB, kAligned>(from, x.lead + static_cast<uint32_t>(j - f) * elt<kB>(), g8);
+                    else
+                        ctl_gather8<kB>(row, j, f, e, g8);
+                };
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
+                    in[g] = j < e && j + 8 > f;
+                    if (!in[g]) continue;
+                    fetch(gx[g], a.in[0], xrow, stg, j, std::integral_constant<bool, kXBf16>{});
+                    if constexpr (kTwo) fetch(gy[g], a.in[1], yrow, stg + kStageX, j, std::integral_constant<bool, kYBf16>{});
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);  // values are in registers now
+            uint32_t skip[2][Smem<kMode>::kSides];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int side = 0; side < Smem<kMode>::kSides; ++side) skip[g][side] = in[g] ? masked[g][side] : 0xffu;
+            if (tc + kTile < c1) ask(tc + kTile);
+            if constexpr (kTwo) {
+                const int64_t seg_end = min((tc / kSegment + 1) * kSegment, c1);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!in[g]) continue;
+                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
+                    uint32_t more = reinterpret_cast<const uint8_t *>(sm.touched[b])[(j - c0) >> 3];
+                    if (j + 8 > c1) more |= 0xffu << (c1 - j) & 0xffu;
+                    skip[g][0] |= more;
+                    skip[g][1] |= more;
+                }
+                if ((skip[0][0] & skip[0][1] & skip[1][0] & skip[1][1]) != 0xffu) {  // something is allowed
+                    float vt[16], vr[16];
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (skip[g][0]) ctl_fill8<kXBf16, kFillBits>(gx[g], sm.lanes[skip[g][0]]);
+                        if (skip[g][1]) ctl_fill8<kYBf16, kFillBits>(gy[g], sm.lanes[skip[g][1]]);
+                        ctl_unpack8<kXBf16>(gx[g], vt + 8 * g);
+                        ctl_unpack8<kYBf16>(gy[g], vr + 8 * g);
+                    }
+                    f2_t pt[8], pr[8];
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        pt[p] = f2(vt[2 * p], vt[2 * p + 1]);
+                        pr[p] = f2(vr[2 * p], vr[2 * p + 1]);
+                    }
+                    if (!(same_scale && accumulate_near(pt, pr, acc, n_l, n_s))) {
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            const uint32_t bt = skip[p >> 2][0] >> (2 * (p & 3)), br = skip[p >> 2][1] >> (2 * (p & 3));
+                            pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(pt[p]), bt & 2u ? -INFINITY : f2_hi(pt[p]));
+                            pr[p] = f2(br & 1u ? -INFINITY : f2_lo(pr[p]), br & 2u ? -INFINITY : f2_hi(pr[p]));
+                        }
+                        accumulate_far(pt, pr, acc, n_lt, n_l);
+                    }
+                }
+                if (tc + kTile >= seg_end) {
+                    const Acc w = warp_reduce_acc<false>(acc2_fold(acc), n_lt, n_l);
+                    if (lane == 0) {
+                        const int64_t o = (i * a.n_segs + tc / kSegment) * kStates + warp;
+                        a.part_a[o] = make_float4(w.mt, w.st, w.dd, w.mr);
+                        a.part_b[o] = w.sr;
+                    }
+                    acc = acc2_init();
+                }
+            } else {
+                const f2_t f2f = f2(n_l, n_l), l2f = f2(-n_lse2, -n_lse2), g2f = f2(n_g, n_g);
+                const f2_t s2f = f2(n_s, n_s);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    if (!in[g]) continue;
+                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
+                    float v[8];
+                    ctl_unpack8<kXBf16>(gx[g], v);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f2_t z = f2(v[2 * q], v[2 * q + 1]);
+                        const f2_t d = kMode == kApply ? mul2(z, s2f) : mul2(g2f, ex2_2(fma2(z, f2f, l2f)));
+                        v[2 * q] = f2_lo(d);
+                        v[2 * q + 1] = f2_hi(d);
+                    }
+                    Group8<kYBf16> w;
+                    ctl_pack8<kYBf16>(v, w);
+                    constexpr uint32_t kMasked = kMode == kApply ? 0xff80u : 0u;  // -inf, or no gradient
+                    if (skip[g][0]) ctl_fill8<kYBf16, kMasked>(w, sm.lanes[skip[g][0]]);
+                    if (j >= c0 && j + 8 <= c1) ctl_store8<kYBf16>(orow, j, w);
+                    else ctl_scatter8<kYBf16>(orow, j, c0, c1, w);
+                }
+            }
+        }
+        if (!kTwo && dead) {
+            fill(CUDART_NAN_F);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.done[b]);
+        ++n_live;
+    }
+}
+
+// One warp per active row: lane l folds the segments' warp states l, l + 32, ... in order, the
 // warp merges in a fixed butterfly, lane 0 does the row's arithmetic in double
 // (the formulas of the plain scorer, with each side's scale).
-__global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_constant__ CtlScoreArgs a, float *out_lt,
+__global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_constant__ StreamArgs a, float *out_lt,
                                                             float *out_lr, float *out_d, double *dval,
                                                             uint32_t *keys, uint32_t *status) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -584,14 +950,15 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_consta
     if (i >= a.hdr->n_active) return;
     const int2 rid = a.rowid[i];
     const int64_t r = rid.x, id = rid.y;
-    float s_t = a.t.scale ? a.t.scale[r] : 1.f, s_r = a.r.scale ? a.r.scale[r] : 1.f;
+    float s_t = a.c[0].scale ? a.c[0].scale[r] : 1.f, s_r = a.c[1].scale ? a.c[1].scale[r] : 1.f;
     if (!(s_t > 0.f && s_t <= FLT_MAX)) s_t = CUDART_NAN_F;
     if (!(s_r > 0.f && s_r <= FLT_MAX)) s_r = CUDART_NAN_F;
     const float lt = __fmul_rn(s_t, kLog2e), lr = __fmul_rn(s_r, kLog2e);
     Acc acc = acc_init();
-    for (int k = lane; k < a.n_chunks; k += 32) {
-        const float4 p = a.part_a[i * a.n_chunks + k];
-        const Acc o{p.x, p.y, p.z, p.w, a.part_b[i * a.n_chunks + k], 0.f, 0.f};
+    const int n = a.n_segs * kStates;
+    for (int k = lane; k < n; k += 32) {
+        const float4 p = a.part_a[i * n + k];
+        const Acc o{p.x, p.y, p.z, p.w, a.part_b[i * n + k], 0.f, 0.f};
         merge_acc<false>(acc, o, lt, lr);
     }
 #pragma unroll
@@ -630,91 +997,76 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_consta
     if (bad) atomicOr(status, bad);
 }
 
-int64_t chunks_of(int64_t vocab, int cols) { return (vocab + cols - 1) / cols; }
+int score_segments(int64_t vocab) { return static_cast<int>((vocab + kSegment - 1) / kSegment); }
 
-template <class Args, class Kernel>
-cudaError_t launch_units(Kernel *kern, const Args &a, int64_t units, int per_sm, size_t smem,
-                         std::atomic<uint64_t> &configured, cudaStream_t stream) {
+template <int kMode, bool kXB, bool kYB, bool kAligned>
+cudaError_t launch_typed(StreamArgs &a, int64_t rows, cudaStream_t stream) {
+    auto kern = stream_kernel<kMode, kXB, kYB, kAligned>;
+    constexpr size_t stage = (kTile * elt<kXB>() + kStagePad) + (kMode == kScore ? kTile * elt<kYB>() + kStagePad : 0);
+    constexpr size_t room = kSmemMost - ring_offset<kMode>();
+    constexpr int stages = static_cast<int>(room / stage < 16 ? room / stage : 16);
+    static_assert(stages >= 2, "a ring of at least two stages");
+    static std::atomic<uint64_t> configured{0};
+    const size_t smem = ring_offset<kMode>() + stages * stage;
     const cudaError_t e = set_smem_once(kern, smem, configured);
     if (e != cudaSuccess) return e;
-    const int64_t most = static_cast<int64_t>(device_sm_count()) * per_sm;
-    kern<<<static_cast<unsigned>(units < most ? units : most), kCtlThreads, smem, stream>>>(a);
+    a.n_stages = stages;
+    const int64_t units = rows * a.n_units, sms = device_sm_count();
+    kern<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 
-// Chunks of 2048 columns where 8192 would leave multiprocessors without a unit
-// (elementwise forms only: a column's value does not depend on the chunk).
-bool few_units(int64_t n_rows, int64_t vocab) {
-    return n_rows * chunks_of(vocab, kChunk) < 2 * static_cast<int64_t>(device_sm_count());
-}
-
-template <bool kXB, bool kOB, bool kVec, int kCols>
-cudaError_t apply_typed(ApplyArgs &a, cudaStream_t stream) {
-    static std::atomic<uint64_t> configured{0};
-    a.n_chunks = static_cast<int>(chunks_of(a.vocab, kCols));
-    a.per_unit = 1;
-    return launch_units(apply_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4, Shared<kCols>::bytes(1),
-                        configured, stream);
-}
-
-template <bool kXB, bool kOB, bool kVec, int kCols>
-cudaError_t gradient_typed(GradArgs &a, cudaStream_t stream) {
-    static std::atomic<uint64_t> configured{0};
-    a.n_chunks = static_cast<int>(chunks_of(a.vocab, kCols));
-    a.per_unit = 1;
-    return launch_units(gradient_kernel<kXB, kOB, kVec, kCols>, a, a.n_rows * a.n_chunks, 4, Shared<kCols>::bytes(1),
-                        configured, stream);
-}
-
-template <bool kXB, bool kOB>
-cudaError_t apply_path(ApplyArgs &a, bool vec, cudaStream_t s) {
-    if (few_units(a.n_rows, a.vocab))
-        return vec ? apply_typed<kXB, kOB, true, kSmallChunk>(a, s) : apply_typed<kXB, kOB, false, kSmallChunk>(a, s);
-    return vec ? apply_typed<kXB, kOB, true, kChunk>(a, s) : apply_typed<kXB, kOB, false, kChunk>(a, s);
-}
-
-template <bool kXB, bool kOB>
-cudaError_t gradient_path(GradArgs &a, bool vec, cudaStream_t s) {
-    if (few_units(a.n_rows, a.vocab))
-        return vec ? gradient_typed<kXB, kOB, true, kSmallChunk>(a, s)
-                   : gradient_typed<kXB, kOB, false, kSmallChunk>(a, s);
-    return vec ? gradient_typed<kXB, kOB, true, kChunk>(a, s) : gradient_typed<kXB, kOB, false, kChunk>(a, s);
+template <int kMode, bool kAligned>
+cudaError_t launch_kinds(StreamArgs &a, bool xb, bool yb, int64_t rows, cudaStream_t s) {
+    if (xb) return yb ? launch_typed<kMode, true, true, kAligned>(a, rows, s) : launch_typed<kMode, true, false, kAligned>(a, rows, s);
+    return yb ? launch_typed<kMode, false, true, kAligned>(a, rows, s) : launch_typed<kMode, false, false, kAligned>(a, rows, s);
 }
 
 bool aligned_rows(const void *p, int64_t stride_bytes) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
 }
 
-template <bool kTB, bool kRB, int kTables>
-cudaError_t score_typed(const CtlScoreArgs &a, bool vec, int64_t n_rows, cudaStream_t s) {
-    static std::atomic<uint64_t> configured[2];
-    const int64_t units = n_rows * a.n_chunks;
-    const int per_sm = kTables == 1 ? 3 : 2;
-    const size_t smem = Shared<kChunk>::bytes(kTables);
-    return vec ? launch_units(score_kernel<kTB, kRB, true, kTables>, a, units, per_sm, smem, configured[0], s)
-               : launch_units(score_kernel<kTB, kRB, false, kTables>, a, units, per_sm, smem, configured[1], s);
+Plane plane(const void *base, int64_t stride_bytes, int elt_bytes, int64_t rows, int64_t vocab) {
+    const char *b = static_cast<const char *>(base);
+    return Plane{b, stride_bytes, b + (rows - 1) * stride_bytes + vocab * elt_bytes};
+}
+
+// Units of the elementwise forms: as few as the bitmaps allow where there are
+// rows enough for four a block, else more and narrower ones, down to 2048
+// columns (a decode step's one row is cut in 63 units of a 128256-column
+// vocabulary).  In place a unit is no wider than the touched values it can
+// hold, where the history might bring more.  Rows that are not 16-byte aligned
+// start up to seven columns early, which a full last tile could not take.
+void set_units(StreamArgs &a, bool aligned) {
+    const int64_t want = 4 * static_cast<int64_t>(device_sm_count());
+    int64_t most = kMaxWidth - (aligned ? 0 : 32);
+    if (a.late && a.c[0].n_history + a.c[0].n_bias > cap_of(kApply)) most = cap_of(kApply);
+    int64_t n = (a.vocab + most - 1) / most;
+    if (a.n_rows * n < want) n = std::max(n, std::min((want + a.n_rows - 1) / a.n_rows, (a.vocab + 2047) / 2048));
+    a.width = static_cast<int>(((a.vocab + n - 1) / n + 31) / 32 * 32);
+    a.n_units = static_cast<int>((a.vocab + a.width - 1) / a.width);
 }
 
 }  // namespace
 
-int controls_chunks(int64_t vocab) { return static_cast<int>(chunks_of(vocab, kChunk * kSegChunks)); }
+int controls_states(int64_t vocab) { return score_segments(vocab) * kStates; }
 
 cudaError_t launch_controls_apply(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
                                   int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,
                                   cudaStream_t stream) {
     if (n_rows == 0) return cudaSuccess;
     const bool xb = x_dtype == LPD_BF16, ob = out_dtype == LPD_BF16;
-    ApplyArgs a{};
-    a.c = c;
-    a.x = static_cast<const char *>(x);
+    StreamArgs a{};
+    a.c[0] = c;
+    a.in[0] = plane(x, x_stride_elems * (xb ? 2 : 4), xb ? 2 : 4, n_rows, vocab);
     a.out = static_cast<char *>(out);
-    a.x_stride = x_stride_elems * (xb ? 2 : 4);
     a.out_stride = out_stride_elems * (ob ? 2 : 4);
     a.n_rows = n_rows;
     a.vocab = vocab;
-    const bool vec = aligned_rows(x, a.x_stride) && aligned_rows(out, a.out_stride);
-    if (xb) return ob ? apply_path<true, true>(a, vec, stream) : apply_path<true, false>(a, vec, stream);
-    return ob ? apply_path<false, true>(a, vec, stream) : apply_path<false, false>(a, vec, stream);
+    a.late = x == out ? 1 : 0;
+    const bool aligned = aligned_rows(x, a.in[0].stride) && aligned_rows(out, a.out_stride);
+    set_units(a, aligned);
+    return aligned ? launch_kinds<kApply, true>(a, xb, ob, n_rows, stream) : launch_kinds<kApply, false>(a, xb, ob, n_rows, stream);
 }
 
 cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
@@ -723,11 +1075,10 @@ cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtyp
                                      cudaStream_t stream) {
     if (n_rows == 0) return cudaSuccess;
     const bool xb = x_dtype == LPD_BF16, ob = out_dtype == LPD_BF16;
-    GradArgs a{};
-    a.c = c;
-    a.x = static_cast<const char *>(x);
+    StreamArgs a{};
+    a.c[0] = c;
+    a.in[0] = plane(x, x_stride_elems * (xb ? 2 : 4), xb ? 2 : 4, n_rows, vocab);
     a.out = static_cast<char *>(out);
-    a.x_stride = x_stride_elems * (xb ? 2 : 4);
     a.out_stride = out_stride_elems * (ob ? 2 : 4);
     a.n_rows = n_rows;
     a.vocab = vocab;
@@ -735,36 +1086,43 @@ cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtyp
     a.mask = mask;
     a.logp = logp;
     a.grad = grad;
-    const bool vec = aligned_rows(x, a.x_stride) && aligned_rows(out, a.out_stride);
-    if (xb) return ob ? gradient_path<true, true>(a, vec, stream) : gradient_path<true, false>(a, vec, stream);
-    return ob ? gradient_path<false, true>(a, vec, stream) : gradient_path<false, false>(a, vec, stream);
+    const bool aligned = aligned_rows(x, a.in[0].stride) && aligned_rows(out, a.out_stride);
+    set_units(a, aligned);
+    return aligned ? launch_kinds<kGrad, true>(a, xb, ob, n_rows, stream) : launch_kinds<kGrad, false>(a, xb, ob, n_rows, stream);
 }
 
-cudaError_t launch_controls_score(const CtlScoreArgs &args, int dtype_t, int dtype_r, int64_t n_rows, float *out_lt,
-                                  float *out_lr, float *out_d, double *dval, uint32_t *keys, uint32_t *status,
-                                  cudaStream_t stream) {
-    if (n_rows == 0) return cudaSuccess;
-    CtlScoreArgs a = args;
-    a.n_chunks = controls_chunks(a.vocab);
-    const bool vec = aligned_rows(a.xt, a.t_stride) && aligned_rows(a.xr, a.r_stride);
-    const bool tb = dtype_t == LPD_BF16, rb = dtype_r == LPD_BF16;
-    const bool mt = a.t.counts || a.t.n_bias > 0, mr = a.r.counts || a.r.n_bias > 0;
-    // one table serves two sides that mark the same tokens, or one side that marks any
-    a.same = mt && mr && a.t.counts == a.r.counts && a.t.history == a.r.history && a.t.hist_begin == a.r.hist_begin &&
-             a.t.hist_split == a.r.hist_split && a.t.hist_end == a.r.hist_end && a.t.n_history == a.r.n_history &&
-             a.t.bias_ids == a.r.bias_ids && a.t.n_bias == a.r.n_bias;
-    const bool one = a.same || !(mt && mr);
-    cudaError_t e;
-    if (one) {
-        if (tb) e = rb ? score_typed<true, true, 1>(a, vec, n_rows, stream) : score_typed<true, false, 1>(a, vec, n_rows, stream);
-        else e = rb ? score_typed<false, true, 1>(a, vec, n_rows, stream) : score_typed<false, false, 1>(a, vec, n_rows, stream);
-    } else {
-        if (tb) e = rb ? score_typed<true, true, 2>(a, vec, n_rows, stream) : score_typed<true, false, 2>(a, vec, n_rows, stream);
-        else e = rb ? score_typed<false, true, 2>(a, vec, n_rows, stream) : score_typed<false, false, 2>(a, vec, n_rows, stream);
-    }
+cudaError_t launch_controls_score(const CtlScoreCall &call, cudaStream_t stream) {
+    if (call.n_rows == 0) return cudaSuccess;
+    const bool tb = call.dtype_t == LPD_BF16, rb = call.dtype_r == LPD_BF16;
+    StreamArgs a{};
+    a.c[0] = call.t;
+    a.c[1] = call.r;
+    a.in[0] = plane(call.xt, call.t_stride, tb ? 2 : 4, call.n_rows, call.vocab);
+    a.in[1] = plane(call.xr, call.r_stride, rb ? 2 : 4, call.n_rows, call.vocab);
+    a.n_rows = call.n_rows;
+    a.vocab = call.vocab;
+    // rows enough for two a block: whole rows (as far as the bitmaps reach); else a unit a segment
+    a.n_segs = score_segments(call.vocab);
+    a.width = call.n_rows >= 2 * static_cast<int64_t>(device_sm_count()) ? std::min(a.n_segs * kSegment, kMaxWidth) : kSegment;
+    a.n_units = static_cast<int>((call.vocab + a.width - 1) / a.width);
+    a.status = call.status;
+    a.hdr = call.hdr;
+    a.rowid = call.rowid;
+    a.part_a = call.part_a;
+    a.part_b = call.part_b;
+    a.pick = call.pick;
+    // one count serves two sides that mark the same tokens
+    const CtlSide &t = call.t, &r = call.r;
+    a.same = t.counts == r.counts && t.n_bias == r.n_bias && (t.counts || t.n_bias) &&
+             (!t.counts || (t.history == r.history && t.n_history == r.n_history && t.hist_begin == r.hist_begin &&
+                            t.hist_split == r.hist_split && t.hist_end == r.hist_end)) &&
+             (!t.n_bias || t.bias_ids == r.bias_ids);
+    const bool aligned = aligned_rows(call.xt, call.t_stride) && aligned_rows(call.xr, call.r_stride);
+    const cudaError_t e = aligned ? launch_kinds<kScore, true>(a, tb, rb, call.n_rows, stream)
+                                  : launch_kinds<kScore, false>(a, tb, rb, call.n_rows, stream);
     if (e != cudaSuccess) return e;
-    score_finalize_kernel<<<static_cast<unsigned>((n_rows + 7) / 8), 256, 0, stream>>>(a, out_lt, out_lr, out_d, dval,
-                                                                                      keys, status);
+    score_finalize_kernel<<<static_cast<unsigned>((call.n_rows + 7) / 8), 256, 0, stream>>>(
+        a, call.out_lt, call.out_lr, call.out_d, call.dval, call.keys, call.status);
     return cudaGetLastError();
 }
 

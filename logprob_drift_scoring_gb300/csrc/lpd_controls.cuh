@@ -1,5 +1,5 @@
-// Sampling controls on logits: what the three control kernels (apply, score,
-// gradient) share.
+// Sampling controls on logits: the arithmetic of one logit, and the block's way
+// of finding the few that need it.
 //
 // For row r and token j with n_all = occurrences of j in the row's history,
 // n_gen = those in its generated part, the controlled logit is
@@ -9,24 +9,19 @@
 //   z  = allowed(j) ? scale * x3 : -inf
 // Only the tokens of the history and of the bias list ("touched" tokens) need
 // more than the scale and the mask, and they are few: a thousand of a hundred
-// thousand.  A block therefore takes a chunk of one row, marks the touched
-// columns of the chunk in a bitmap, lists them in column order, and works on
-// the list with all lanes busy: a touched token is some 80 instructions, which
-// a branch in the streaming loop would spend for a whole warp each time.  The
-// streaming loop sees one bit a column.
-//
-// The occurrence counts live in a table of one word a column of the chunk.  The
-// table is zero between units: whoever consumes a touched entry zeroes it, so
-// the chunk is cleared once a block and not once a unit.
+// thousand.  Four warps of a block (the scouts) look for them while sixteen
+// others stream the row: they mark the touched columns of the unit in a bitmap,
+// and with the bitmap's prefix sums a token's rank among the touched ones is a
+// look-up and a popcount, so that a second pass over the history counts
+// occurrences in a dense array without collisions or empty slots.  The touched
+// columns come out in ascending order whatever the order of the marks, and the
+// counts are integers, so nothing depends on the order of the shared-memory
+// atomics.  The streaming warps see one bit a column.
 //
 // Masked columns are replaced eight at a time: a 4 KB table in shared memory
 // gives the 16-bit lane masks of a byte of bits, and one logical instruction a
-// register does the rest (bit tests and selects were 100 instructions a thread
-// and 16 columns, a third of the scoring kernel's).
-//
-// The list is made from the bitmap by a prefix sum over its words, never in the
-// order of arrival, and the counts are integers, so nothing depends on the
-// order of the shared-memory atomics.
+// register does the rest (bit tests and selects took a third of the scoring
+// kernel's instructions).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,15 +32,12 @@
 
 namespace lpd {
 
-constexpr int kCtlThreads = 256;
-constexpr int kCtlWarps = kCtlThreads / 32;
-constexpr uint32_t kSeen = 0x80000000u;    // table: the token occurs in the prompt part
-constexpr uint32_t kBiased = 0x40000000u;  // table: the token has a bias entry
-constexpr uint32_t kCount = 0x3fffffffu;   // table: occurrences in the generated part
+constexpr uint32_t kSeen = 0x80000000u;    // count word: the token occurs in the prompt part
+constexpr uint32_t kBiased = 0x40000000u;  // the token has a bias entry
+constexpr uint32_t kCount = 0x3fffffffu;   // occurrences in the generated part
 constexpr int64_t kMaxRange = kCount;      // so a row's range is cut to its last 2^30 - 1 tokens
 
-// The controls of one row: read once a unit by one thread, kept in shared
-// memory (in registers, two of them spilled a quarter of the scoring kernel's).
+// The controls of one row: read once a unit by one thread, kept in shared memory.
 struct CtlRow {
     int64_t begin, split, end;
     float rep, inv_h, inv_l;  // repetition penalty and 1 / rep as a sum of two floats
@@ -104,22 +96,20 @@ __device__ __forceinline__ Two two_add(Two a, float b) {
 
 // Sum of the row's bias entries of one token, in double (at most 1024 terms,
 // so the sum is exact to far below a float's step in any order).
-__device__ __forceinline__ double bias_sum(const CtlSide &c, int64_t r, int64_t token) {
-    const int32_t *ids = c.bias_ids + r * c.n_bias;
-    const float *v = c.bias + r * c.n_bias;
+__device__ __forceinline__ double bias_sum(const int32_t *ids, const float *values, int n, int64_t token) {
     double s = 0.0;
-#pragma unroll 8
-    for (int e = 0; e < c.n_bias; ++e)
-        if (ids[e] == token) s += static_cast<double>(v[e]);
+#pragma unroll 4
+    for (int e = 0; e < n; ++e)
+        if (ids[e] == token) s += static_cast<double>(values[e]);
     return s;
 }
 
-// x3 of a touched, allowed token with table word w.  Two floats, so that the
+// x3 of a touched, allowed token with count word w.  Two floats, so that the
 // logit's rounding (a step of 1e-6 at a logit of 20) stays out of the logprob
 // difference of two sides that nearly agree; `slope` (may be null) receives
 // dx3/dx.
-__device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlSide &c, const CtlRow &o, int64_t r,
-                                         int64_t token, float *slope) {
+__device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, const int32_t *bias_ids,
+                                         const float *bias, int n_bias, int64_t token, float *slope) {
     Two v{x, 0.f};
     float d = 1.f;
     if ((w & ~kBiased) != 0u) {
@@ -142,7 +132,7 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlSide &c, 
         }
     }
     if (w & kBiased) {
-        const double b = bias_sum(c, r, token);
+        const double b = bias_sum(bias_ids, bias, n_bias, token);
         const float bh = static_cast<float>(b);
         v = two_add(v, bh);
         v = two_add(v, static_cast<float>(b - static_cast<double>(bh)));
@@ -154,84 +144,10 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlSide &c, 
     return v;
 }
 
-// ---- the unit: one chunk of one row ----------------------------------------------
-// Marks the chunk's touched columns: table words and bitmap bits.  `id_word`
-// (shared, may be null) collects the word of token `id` over the whole row.
-__device__ __forceinline__ void ctl_mark(const CtlSide &c, const CtlRow &o, int64_t r, int64_t c0, uint32_t len,
-                                         volatile uint32_t *vtable, volatile uint32_t *vtouched, int64_t id, uint32_t *id_word) {
-    uint32_t *const table = const_cast<uint32_t *>(vtable), *const touched = const_cast<uint32_t *>(vtouched);
-    auto take = [&](int32_t tok, bool gen) {
-        const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
-        if (j < len) {
-            if (gen) atomicAdd(&table[j], 1u);
-            else if (!(vtable[j] & kSeen)) atomicOr(&table[j], kSeen);  // (a text's frequent tokens come often)
-            const uint32_t bit = 1u << (j & 31);
-            if (!(vtouched[j >> 5] & bit)) atomicOr(&touched[j >> 5], bit);
-        }
-        if (id_word && tok == id) {
-            if (gen) atomicAdd(id_word, 1u);
-            else atomicOr(id_word, kSeen);
-        }
-    };
-    constexpr int kU = 4;  // independent loads in flight
-    int64_t k = o.begin + threadIdx.x;
-    for (; k + (kU - 1) * kCtlThreads < o.end; k += kU * kCtlThreads) {
-        int32_t t[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) t[u] = __ldg(c.history + k + u * kCtlThreads);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) take(t[u], k + u * kCtlThreads >= o.split);
-    }
-    for (; k < o.end; k += kCtlThreads) take(__ldg(c.history + k), k >= o.split);
-    for (int e = threadIdx.x; e < c.n_bias; e += kCtlThreads) {
-        const int32_t tok = __ldg(c.bias_ids + r * c.n_bias + e);
-        const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
-        if (j < len) {
-            atomicOr(&table[j], kBiased);
-            atomicOr(&touched[j >> 5], 1u << (j & 31));
-        }
-        if (id_word && tok == id) atomicOr(id_word, kBiased);
-    }
-}
-
-// Word w of the row's allowed bits for the chunk at column c0 (a multiple of
-// 32), columns from the vocabulary's end on not allowed.
-__device__ __forceinline__ uint32_t ctl_allowed(const CtlRow &o, int64_t c0, int w, int64_t vocab) {
-    const int64_t first = c0 + 32 * static_cast<int64_t>(w);
-    if (first >= vocab || o.none) return 0u;
-    const uint32_t bits = o.mask ? __ldg(o.mask + first / 32) : 0xffffffffu;
-    const int64_t left = vocab - first;
-    return left >= 32 ? bits : bits & ((1u << left) - 1u);
-}
-
-// The touched columns in ascending order: thread t holds word t of the bitmap
-// (0 behind the chunk's words).  Returns their number; the list is visible
-// after the caller's next __syncthreads.
-__device__ __forceinline__ int ctl_list(uint32_t bits, uint16_t *list, int *warp_sum) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = __popc(bits);
-    int incl = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int base = 0, total = 0;
-#pragma unroll
-    for (int k = 0; k < kCtlWarps; ++k) {
-        const int s = warp_sum[k];
-        base += k < warp ? s : 0;
-        total += s;
-    }
-    int pos = base + incl - n;
-    while (bits) {
-        const int b = __ffs(bits) - 1;
-        bits &= bits - 1;
-        list[pos++] = static_cast<uint16_t>(threadIdx.x * 32 + b);
-    }
-    return total;
+// Whether the row's mask lets a token through.
+__device__ __forceinline__ bool ctl_allows(const CtlRow &o, int64_t token) {
+    if (o.none) return false;
+    return !o.mask || (__ldg(o.mask + token / 32) >> (token & 31) & 1u);
 }
 
 // ---- eight consecutive columns -----------------------------------------------------
@@ -248,49 +164,62 @@ __device__ __forceinline__ float ctl_elem(const char *row, int64_t j) {
         return reinterpret_cast<const float *>(row)[j];
 }
 
-// Columns [j, j + 8) of a row as raw words, columns from `vocab` on as 0.
-// kVec: rows start on 16-byte boundaries.
-template <bool kBf16, bool kVec>
-__device__ __forceinline__ void ctl_load8(const char *row, int64_t j, int64_t vocab, Group8<kBf16> &g) {
-    if (kVec && j + 8 <= vocab) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(row + j * (kBf16 ? 2 : 4));
-        g.w[0] = __ldcs(p);
-        if constexpr (!kBf16) g.w[1] = __ldcs(p + 1);
-        return;
-    }
-    uint32_t w[kBf16 ? 4 : 8];
-    if constexpr (kBf16) {
-        // inside the row: whole words, shifted by half a word where the row
-        // starts on an odd element
-        const uintptr_t at = reinterpret_cast<uintptr_t>(row + 2 * j);
-        if (j > 0 && j + 9 <= vocab) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(at & ~uintptr_t{3});
-            if (at & 2) {
-                uint32_t v[5];
-#pragma unroll
-                for (int q = 0; q < 5; ++q) v[q] = p[q];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = __funnelshift_r(v[q], v[q + 1], 16);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = p[q];
-            }
-            g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            return;
-        }
-    }
+// Columns [j, j + 8) of a row one by one, those outside [first, end) as 0.
+template <bool kBf16>
+__device__ __forceinline__ void ctl_gather8(const char *row, int64_t j, int64_t first, int64_t end, Group8<kBf16> &g) {
+    uint32_t w[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
+        const bool in = j + q >= first && j + q < end;
         if constexpr (kBf16) {
-            const uint32_t b = j + q < vocab ? reinterpret_cast<const unsigned short *>(row)[j + q] : 0u;
+            const uint32_t b = in ? reinterpret_cast<const unsigned short *>(row)[j + q] : 0u;
             if (q & 1) w[q >> 1] |= b << 16;
             else w[q >> 1] = b;
         } else {
-            w[q] = j + q < vocab ? reinterpret_cast<const uint32_t *>(row)[j + q] : 0u;
+            w[q] = in ? reinterpret_cast<const uint32_t *>(row)[j + q] : 0u;
         }
     }
     g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
     if constexpr (!kBf16) g.w[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Eight columns from shared memory at byte offset `at` of a stage.  kAligned:
+// `at` is a multiple of 16.  Otherwise the 16-byte words around them, shifted:
+// by two words, one word, half a word, as the offset's bits say (the same for
+// every thread).
+template <bool kBf16, bool kAligned>
+__device__ __forceinline__ void ctl_shared8(const char *stage, uint32_t at, Group8<kBf16> &g) {
+    constexpr int kHi = kBf16 ? 0 : 1;
+    const uint4 *p = reinterpret_cast<const uint4 *>(stage + (at & ~15u));
+    if constexpr (kAligned) {
+        g.w[0] = p[0];
+        if constexpr (!kBf16) g.w[kHi] = p[1];
+        return;
+    }
+    constexpr int kN = kBf16 ? 4 : 8;  // words wanted
+    uint32_t w[kN + 4];
+#pragma unroll
+    for (int q = 0; q < kN / 4 + 1; ++q) {
+        const uint4 v = p[q];
+        w[4 * q] = v.x;
+        w[4 * q + 1] = v.y;
+        w[4 * q + 2] = v.z;
+        w[4 * q + 3] = v.w;
+    }
+    if (at & 8u) {
+#pragma unroll
+        for (int q = 0; q < kN + 2; ++q) w[q] = w[q + 2];
+    }
+    if (at & 4u) {
+#pragma unroll
+        for (int q = 0; q < kN + 1; ++q) w[q] = w[q + 1];
+    }
+    if (kBf16 && (at & 2u)) {
+#pragma unroll
+        for (int q = 0; q < kN; ++q) w[q] = __funnelshift_r(w[q], w[q + 1], 16);
+    }
+    g.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (!kBf16) g.w[kHi] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 template <bool kBf16>
@@ -358,21 +287,23 @@ __device__ __forceinline__ void ctl_fill8(Group8<kBf16> &g, const uint4 &m) {
     }
 }
 
-// Columns [j, j + 8) of an output row.
-template <bool kBf16, bool kVec>
-__device__ __forceinline__ void ctl_store8(char *row, int64_t j, int64_t vocab, const Group8<kBf16> &g) {
+// Columns [j, j + 8) of an output row on a 16-byte boundary.
+template <bool kBf16>
+__device__ __forceinline__ void ctl_store8(char *row, int64_t j, const Group8<kBf16> &g) {
+    uint4 *p = reinterpret_cast<uint4 *>(row + j * (kBf16 ? 2 : 4));
+    __stcs(p, g.w[0]);
+    if constexpr (!kBf16) __stcs(p + 1, g.w[kBf16 ? 0 : 1]);
+}
+
+// Those of columns [j, j + 8) that lie in [first, end), one by one.
+template <bool kBf16>
+__device__ __forceinline__ void ctl_scatter8(char *row, int64_t j, int64_t first, int64_t end, const Group8<kBf16> &g) {
     constexpr int kHi = kBf16 ? 0 : 1;
-    if (kVec && j + 8 <= vocab) {
-        uint4 *p = reinterpret_cast<uint4 *>(row + j * (kBf16 ? 2 : 4));
-        __stcs(p, g.w[0]);
-        if constexpr (!kBf16) __stcs(p + 1, g.w[kHi]);
-        return;
-    }
     const uint32_t w[8] = {g.w[0].x,   g.w[0].y,   g.w[0].z,   g.w[0].w,
                            g.w[kHi].x, g.w[kHi].y, g.w[kHi].z, g.w[kHi].w};
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        if (j + q < vocab) {
+        if (j + q >= first && j + q < end) {
             if constexpr (kBf16)
                 reinterpret_cast<unsigned short *>(row)[j + q] = static_cast<unsigned short>(w[q >> 1] >> (16 * (q & 1)));
             else

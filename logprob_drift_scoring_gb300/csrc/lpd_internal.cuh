@@ -249,21 +249,24 @@ struct CtlSide {
     const int32_t *mask_row;
 };
 
-struct CtlScoreArgs {
+// One call of lpd_score_controlled behind the row selection.
+struct CtlScoreCall {
     CtlSide t, r;
-    const char *xt, *xr;
+    const void *xt, *xr;
+    int dtype_t, dtype_r;
     int64_t t_stride, r_stride;  // bytes
-    int64_t vocab;
-    int n_chunks;                // units a row
-    int same;                    // both sides mark the same tokens: one table
+    int64_t n_rows, vocab;
     const WsHeader *hdr;
     const int2 *rowid;
-    float4 *part_a;              // [active row][unit] (mt, st, dd, mr)
-    float *part_b;               // [active row][unit] sr
+    float4 *part_a;              // [active row][warp state] (mt, st, dd, mr)
+    float *part_b;               // [active row][warp state] sr
     double2 *pick;               // selected controlled logits, before the scale
+    float *out_lt, *out_lr, *out_d;
+    double *dval;
+    uint32_t *keys, *status;
 };
 
-int controls_chunks(int64_t vocab);  // units a row of the scoring form
+int controls_states(int64_t vocab);  // warp states a row of the scoring form
 cudaError_t launch_controls_apply(const CtlSide &c, const void *x, int x_dtype, int64_t x_stride_elems, void *out,
                                   int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,
                                   cudaStream_t stream);
@@ -271,9 +274,7 @@ cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtyp
                                      int out_dtype, int64_t out_stride_elems, int64_t n_rows, int64_t vocab,
                                      const int32_t *ids, const uint8_t *mask, const float *logp, const float *grad,
                                      cudaStream_t stream);
-cudaError_t launch_controls_score(const CtlScoreArgs &a, int dtype_t, int dtype_r, int64_t n_rows, float *out_lt,
-                                  float *out_lr, float *out_d, double *dval, uint32_t *keys, uint32_t *status,
-                                  cudaStream_t stream);
+cudaError_t launch_controls_score(const CtlScoreCall &c, cudaStream_t stream);
 
 // ---------------------------------------------------------------- block-scaled 8-bit operands
 struct BlockOperand {

@@ -310,6 +310,53 @@ def test_batch_invariance_and_load_paths():
         assert torch.equal(a, b)
 
 
+def test_batch_invariance_over_unit_shapes():
+    """Many rows take whole rows at a time, few rows segments: the same bits.  One row's history has more
+    distinct tokens than the kernel counts at a time."""
+    rng = np.random.default_rng(23)
+    rows, vocab = 330, 130000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=6000, masks=3, bias=5)
+    c["hist_begin"][1], c["hist_split"][1], c["hist_end"][1] = 0, 100, 6001
+    x = torch.randn(rows, vocab, device=DEV, generator=torch.Generator(DEV).manual_seed(5)).mul_(3).to(torch.bfloat16)
+    y = (x.float() + 1e-3).to(torch.bfloat16)
+
+    def run(at):
+        h = to_device({k: (v[at] if k not in ("history", "mask") else v) for k, v in c.items()})
+        r = B.score_controlled(x[at], y[at], torch.from_numpy(ids[at]).to(DEV),
+                               torch.ones(len(at), dtype=torch.uint8, device=DEV), h, h)
+        return [r.logp_train, r.logp_rollout, r.dlogp]
+
+    full = run(np.arange(rows))
+    for at in ([1], [0, 1, 2], list(range(200, 260))):
+        for a, b in zip(full, run(np.array(at))):
+            assert torch.equal(a[at], b), at
+    for r in (0, 1, 77):
+        want = ref.logp(ref.row(c, host(x[r:r + 1])[0], r)[0], ids[r])
+        assert abs(float(full[0][r]) - want) <= 1e-5 + 2.0 ** -23 * abs(want)
+
+
+def test_more_touched_tokens_than_counted_at_a_time():
+    """Elementwise forms with thousands of distinct tokens in a unit, in place too, and a long bias list."""
+    rng = np.random.default_rng(24)
+    rows, vocab = 3, 9000
+    c = ref.random_controls(rng, rows, vocab, history=30000, masks=2, bias=600)
+    c["hist_begin"][:], c["hist_split"][:], c["hist_end"][:] = 0, [5, 20000, 29000], 30001
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "f32")
+    h = to_device(c)
+    out = B.controls_apply(x, h)
+    check_apply(c, x, "f32", out)
+    # enough rows that a unit is a whole row
+    many = 700
+    big = {k: (np.repeat(v, 234, axis=0)[:many] if k not in ("history", "mask") else v) for k, v in c.items()}
+    xs = x.repeat_interleave(234, 0)[:many].contiguous()
+    hb = to_device(big)
+    got = B.controls_apply(xs, hb)
+    assert torch.equal(got, out.repeat_interleave(234, 0)[:many])
+    B.lpd_controls_apply(xs, hb, xs)
+    assert torch.equal(xs, got)
+
+
 @pytest.mark.parametrize("what", ["masked_id", "nothing_allowed", "bad_scale", "nan_logit", "oob"])
 def test_score_status(what):
     rng = np.random.default_rng(14)
