@@ -190,13 +190,14 @@ constexpr size_t kSmemMost = 232448 - 1024;  // what a block may have, less the 
 // ---- where a tile's columns are ------------------------------------------------------
 // Bulk copies start and end on 16-byte boundaries: the tile's bytes are widened
 // to them as far as the tensor goes.  Column c of the tile's range sits at byte
-// `lead` + (c - first) * size of the stage; columns [lo, hi) are there, the few
-// others (at the tensor's two ends) come from global memory.
+// `lead` + (c - first) * size of the stage.  At the tensor's two ends up to
+// seven columns may be missing there; the scouts take a row's first eight
+// columns and its last eight to fifteen always (of a unit's, in the elementwise
+// forms), whether they are missing or not, so that a row's arithmetic does not
+// depend on its place.
 struct Span {
     const char *src;
     uint32_t bytes, at;  // copied bytes, and where in the stage they go
-    uint32_t lead;
-    int64_t lo, hi;
 };
 template <int kElt>
 __device__ __forceinline__ Span span_of(const Plane &p, const char *row, int64_t first, int64_t end) {
@@ -206,14 +207,18 @@ __device__ __forceinline__ Span span_of(const Plane &p, const char *row, int64_t
     uintptr_t b = low, e = (a1 + 15) & ~uintptr_t{15};
     if (b < reinterpret_cast<uintptr_t>(p.base)) b += 16;
     if (e > reinterpret_cast<uintptr_t>(p.end)) e -= 16;
-    s.lead = static_cast<uint32_t>(a0 - low);
     s.src = reinterpret_cast<const char *>(b);
     s.at = static_cast<uint32_t>(b - low);
     s.bytes = e > b ? static_cast<uint32_t>(e - b) : 0u;
-    // (element sizes divide 16, so both ends fall between columns)
-    s.lo = b > a0 ? first + static_cast<int64_t>((b - a0) / kElt) : first;
-    s.hi = e < a1 ? end - static_cast<int64_t>((a1 - e) / kElt) : end;
     return s;
+}
+// The columns of a unit [c0, c1) that are the scouts' for their place: [c0,
+// head) and [tail, c1).
+template <int kMode>
+__device__ __forceinline__ void edges(int64_t c0, int64_t c1, int64_t vocab, int64_t &head, int64_t &tail) {
+    const bool first = kMode != kScore || c0 == 0, last = kMode != kScore || c1 == vocab;
+    head = first ? min(c0 + 8, c1) : c0;
+    tail = last ? max(c1 / 8 * 8 - 8, head) : c1;
 }
 
 // Unit u: the row (kScore: its place among the active rows) and which of its
@@ -231,14 +236,17 @@ __device__ __forceinline__ void unit_of(int64_t u, int n_units, int64_t &row, in
 }
 
 // ---- scoring: sums of both sides ---------------------------------------------------
-// Two sides that nearly agree (the same scale, |z_t - z_r| small) take one
-// exponential a column: e_t = e_r (1 + q), q = expm1(u) of the small exponent
-// difference u by its Taylor series.  The difference of the two sums, e_r q
-// added up, is then accurate relative to itself, where e_t - e_r of two rounded
-// exponentials carries 2^-22 of the term (1e-5 of a logprob difference of
-// 2e-3), and the special-function unit, which bounds the kernel beside HBM, has
-// half the work.
-constexpr float kNear2 = 0.0625f;   // sum of u^2 over a thread's sixteen columns: |u| <= 1/4
+// Two sides that nearly agree (the same scale, u = z_t - z_r small) take one
+// exponential a column, e = exp of the mean of the two exponents:
+//   e_t - e_r = 2 e sinh(u / 2) = e (u + u^3 / 24 + ...)
+//   e_t + e_r = 2 e cosh(u / 2) = e (2 + u^2 / 4 + ...)
+// so four sums over the columns, of e, e u, e u^2 and e u^3, give both sides.
+// Their difference is accurate relative to itself, where e_t - e_r of two
+// rounded exponentials carries 2^-22 of the term (1e-5 of a logprob difference
+// of 2e-3; this form: 1e-7), and the special-function unit has half the work.
+// For |u| <= 1/8 the series' next terms are u^4 / 1920 = 1.3e-7 of the
+// difference and u^4 / 192 = 1.3e-6 of the sum (the same on both sides).
+constexpr float kNear2 = 0.015625f;  // sum of u^2 over a thread's sixteen columns
 // A masked column of the stream holds about -1e30 (bf16 0xf149) on both sides:
 // its term is 0 and its u finite.  Rows whose allowed logits are all below
 // kFloorZ leave this path.
@@ -246,12 +254,12 @@ constexpr uint32_t kFillBits = 0xf149u;
 constexpr float kFloorZ = -1e29f;
 
 // expm1(u) / u up to u^5 / 720: the next term is u^6 / 5040 = 5e-8 at 1/4
-__device__ __forceinline__ f2_t expm1_ratio2(f2_t u) {
-    f2_t p = fma2(u, f2(1.f / 720.f, 1.f / 720.f), f2(1.f / 120.f, 1.f / 120.f));
-    p = fma2(u, p, f2(1.f / 24.f, 1.f / 24.f));
-    p = fma2(u, p, f2(1.f / 6.f, 1.f / 6.f));
-    p = fma2(u, p, f2(0.5f, 0.5f));
-    return fma2(u, p, f2(1.f, 1.f));
+__device__ __forceinline__ float expm1_ratio(float u) {
+    float p = __fmaf_rn(u, 1.f / 720.f, 1.f / 120.f);
+    p = __fmaf_rn(u, p, 1.f / 24.f);
+    p = __fmaf_rn(u, p, 1.f / 6.f);
+    p = __fmaf_rn(u, p, 0.5f);
+    return __fmaf_rn(u, p, 1.f);
 }
 
 // References (mt, mr) moved up to (nmt, nmr).
@@ -267,30 +275,38 @@ __device__ __forceinline__ void raise_refs(Acc2 &a, float nmt, float nmr, float 
 }
 
 // Sixteen columns of two sides that nearly agree; false where they do not (the
-// state is valid either way).  A NaN fails the comparison of the sum of squares.
+// state is valid either way).  A NaN fails the comparison of the sum of
+// squares.  The exponent is one multiply-add: the rounding of m l is the same
+// for both sides.
 __device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, Acc2 &a, float l, float s) {
     const float cm = max16(vr);
     if (!(cm > kFloorZ)) return false;
     if (cm > a.mr) raise_refs(a, fmaxf(a.mt, cm), cm, l, l);
-    const float dm = __fmul_rn(__fsub_rn(a.mr, a.mt), s);
-    const f2_t s2 = f2(s, s), dm2 = f2(dm, dm), l2 = f2(l, l), m2 = f2(a.mr, a.mr);
-    f2_t u[8], q2 = f2(0.f, 0.f);
+    if (a.mt != a.mr) {  // only where some columns in front did not agree
+        if (fabsf(__fsub_rn(a.mt, a.mr)) > 8.f) return false;
+        const float m = fmaxf(a.mt, a.mr);
+        raise_refs(a, m, m, l, l);
+    }
+    const float ml = __fmul_rn(-a.mr, l), h = __fmul_rn(0.5f, l);
+    const f2_t s2 = f2(s, s), ml2 = f2(ml, ml), h2 = f2(h, h);
+    f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        u[p] = fma2(sub2(vt[p], vr[p]), s2, dm2);
-        q2 = fma2(u[p], u[p], q2);
+        const f2_t u = mul2(sub2(vt[p], vr[p]), s2);
+        const f2_t e = ex2_2(fma2(add2(vt[p], vr[p]), h2, ml2));
+        const f2_t v = mul2(u, u), w = mul2(e, u);
+        q = add2(q, v);
+        e0 = add2(e0, e);
+        e1 = add2(e1, w);
+        e2 = fma2(e, v, e2);
+        e3 = fma2(w, v, e3);
     }
-    if (!(__fadd_rn(f2_lo(q2), f2_hi(q2)) <= kNear2)) return false;
-    f2_t se = f2(0.f, 0.f), sd = f2(0.f, 0.f);
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const f2_t e = ex2_2(mul2(sub2(vr[p], m2), l2));
-        se = add2(se, e);
-        sd = fma2(mul2(e, u[p]), expm1_ratio2(u[p]), sd);
-    }
-    a.sr = add2(a.sr, se);
-    a.dd = add2(a.dd, sd);
-    a.st = add2(a.st, add2(se, sd));
+    if (!(__fadd_rn(f2_lo(q), f2_hi(q)) <= kNear2)) return false;
+    const f2_t d = fma2(e3, f2(1.f / 24.f, 1.f / 24.f), e1);       // e_t - e_r
+    const f2_t m = fma2(e2, f2(0.125f, 0.125f), e0);               // their mean
+    a.dd = add2(a.dd, d);
+    a.st = add2(a.st, fma2(d, f2(0.5f, 0.5f), m));
+    a.sr = add2(a.sr, fma2(d, f2(-0.5f, -0.5f), m));
     return true;
 }
 
@@ -322,7 +338,7 @@ __device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float l
         __fadd_rn(__fsub_rn(__fsub_rn(xt.h, xr.h), __fsub_rn(a.mt, a.mr)), __fsub_rn(xt.l, xr.l)), s);
     float d;
     if (same_scale && fabsf(u) <= 0.25f) {
-        d = __fmul_rn(__fmul_rn(er, u), f2_lo(expm1_ratio2(f2(u, u))));
+        d = __fmul_rn(__fmul_rn(er, u), expm1_ratio(u));
     } else {
         const float et = ex2(__fmaf_rn(xt.l, lt, __fmul_rn(__fsub_rn(xt.h, a.mt), lt)));
         d = __fsub_rn(et, er);
@@ -414,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         if (lane != 0) return;
         uint64_t policy;
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-        uint32_t it = 0;
+        int s = 0, issued = 0;
+        uint32_t phase = 1;  // the first turn finds every stage empty
         bool ok = true;
         for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
             int64_t i;
@@ -423,30 +440,43 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
             const int64_t r = kTwo ? a.rowid[i].x : i;
             if (!live(r)) continue;
             const int64_t c0 = static_cast<int64_t>(k) * a.width, c1 = min(c0 + a.width, a.vocab);
-            for (int64_t tc = c0 - lead_in(r, c0); tc < c1; tc += kTile, ++it) {
-                const uint32_t s = it % a.n_stages, round = it / a.n_stages;
-                if (round > 0 && !wait_phase(&sm.empty[s], (round - 1) & 1, &sm.abort_flag, a.status)) {
+            const char *const xrow = a.in[0].base + r * a.in[0].stride;
+            const char *const yrow = kTwo ? a.in[1].base + r * a.in[1].stride : nullptr;
+            for (int64_t tc = c0 - lead_in(r, c0); tc < c1; tc += kTile) {
+                if (!wait_phase(&sm.empty[s], phase, &sm.abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
                 char *st = ring + static_cast<size_t>(s) * kStage;
-                const int64_t f = max(tc, c0), e = min(tc + kTile, c1);
-                const Span x = span_of<kXE>(a.in[0], a.in[0].base + r * a.in[0].stride, f, e);
-                if (kTwo) {
-                    const Span y = span_of<kYE>(a.in[1], a.in[1].base + r * a.in[1].stride, f, e);
+                if (kAligned && tc + kTile <= c1) {
+                    mbar_arrive_expect_tx(&sm.full[s], kTile * (kXE + (kTwo ? kYE : 0)));
+                    bulk_g2s(st, xrow + tc * kXE, kTile * kXE, &sm.full[s], policy);
+                    if (kTwo) bulk_g2s(st + kStageX, yrow + tc * kYE, kTile * kYE, &sm.full[s], policy);
+                } else {
+                    const int64_t f = max(tc, c0), e = min(tc + kTile, c1);
+                    const Span x = span_of<kXE>(a.in[0], xrow, f, e);
+                    Span y{nullptr, 0, 0};
+                    if (kTwo) y = span_of<kYE>(a.in[1], yrow, f, e);
                     mbar_arrive_expect_tx(&sm.full[s], x.bytes + y.bytes);
                     if (x.bytes) bulk_g2s(st + x.at, x.src, x.bytes, &sm.full[s], policy);
                     if (y.bytes) bulk_g2s(st + kStageX + y.at, y.src, y.bytes, &sm.full[s], policy);
-                } else {
-                    mbar_arrive_expect_tx(&sm.full[s], x.bytes);
-                    if (x.bytes) bulk_g2s(st + x.at, x.src, x.bytes, &sm.full[s], policy);
+                }
+                issued = min(issued + 1, a.n_stages);
+                if (++s == a.n_stages) {
+                    s = 0;
+                    phase ^= 1;
                 }
             }
         }
-        // every copy issued must land before the block's shared memory goes away
-        const uint32_t first = it > static_cast<uint32_t>(a.n_stages) ? it - a.n_stages : 0;
-        for (uint32_t j = first; j < it; ++j)
-            wait_phase(&sm.full[j % a.n_stages], (j / a.n_stages) & 1, &sm.abort_flag, a.status, false);
+        // every copy issued must land before the block's shared memory goes
+        // away: the last turn's stages, each in the phase of its last use
+        for (int j = 0; j < issued; ++j) {
+            if (--s < 0) {
+                s = a.n_stages - 1;
+                phase ^= 1;
+            }
+            wait_phase(&sm.full[s], phase ^ 1, &sm.abort_flag, a.status, false);
+        }
         return;
     }
 
@@ -543,6 +573,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
             }
             if (kMode == kGrad && st == 0 && id >= c0 && id < c1)
                 atomicOr(&touched[(id - c0) >> 5], 1u << ((id - c0) & 31));
+            {
+                // the unit's edges; behind the vocabulary up to a group of eight, which the list leaves out
+                int64_t head, tail;
+                edges<kMode>(c0, c1, a.vocab, head, tail);
+                const int n_head = static_cast<int>(head - c0), up = static_cast<int>((len + 7) / 8 * 8);
+                const int at = st < n_head ? st : static_cast<int>(tail - c0) + st - n_head;
+                if (at < up) atomicOr(&touched[at >> 5], 1u << (at & 31));
+            }
             scout_sync();
             auto value = [&](int side, float x, uint32_t w, int64_t token, float *slope) -> Two {
                 const int n = a.c[side].n_bias;
@@ -610,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     if (l0 + lane <= lines) sm.line_base[l0 + lane] = sum + incl - n;
                     sum += __shfl_sync(0xffffffffu, incl, 31);
                 }
-                if (lane == 0) sm.total = sum;
+                if (lane == 0) sm.total = sum - static_cast<int>((8 - len % 8) % 8);
             }
             scout_sync();
             const int total = sm.total;
@@ -743,24 +781,30 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
 
     // ------------------------------------------------------------------ stream
     const int t = threadIdx.x;
-    uint32_t it = 0, n_live = 0;
+    int stage = 0;
+    uint32_t phase = 0, n_live = 0;
     bool dead = false;  // a wait gave up: what is left of the output reads as NaN
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         int64_t i;
         int k;
         unit_of(u, a.n_units, i, k);
-        const int64_t r = kTwo ? a.rowid[i].x : i;
-        const int64_t c0 = static_cast<int64_t>(k) * a.width, c1 = min(c0 + a.width, a.vocab);
-        char *const orow = kTwo ? nullptr : a.out + r * a.out_stride;
+        const int64_t r = kTwo ? 0 : i;
+        const int64_t c0 = static_cast<int64_t>(k) * a.width;
+        const int len = static_cast<int>(min(static_cast<int64_t>(a.width), a.vocab - c0));
+        const int lead = kTwo ? 0 : lead_in(r, c0);
+        char *const orow = kTwo ? nullptr : a.out + r * a.out_stride + c0 * kYE;  // the unit's first column
         auto fill = [&](float value) {
             float v[8];
             Group8<kYBf16> w;
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = value;
             ctl_pack8<kYBf16>(v, w);
-            for (int64_t j = c0 - lead_in(r, c0) + 8 * t; j < c1; j += 8 * kStreamThreads) {
-                if (j >= c0 && j + 8 <= c1) ctl_store8<kYBf16>(orow, j, w);
-                else ctl_scatter8<kYBf16>(orow, j, c0, c1, w);
+            for (int j = 8 * t - lead; j < len; j += 8 * kStreamThreads) {
+                if (j >= 0 && j + 8 <= len) {
+                    ctl_store8<kYBf16>(orow, j, w);
+                } else {
+                    for (int q = max(j, 0); q < min(j + 8, len); ++q) ctl_store1<kYBf16>(orow, q, value);
+                }
             }
         };
         if (!kTwo && (dead || !live(r))) {
@@ -782,127 +826,124 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         const bool same_scale = kTwo && num.same_scale != 0;
         const float n_s = num.s, n_l = num.l, n_lt = kTwo ? num.lt : 0.f;
         const float n_lse2 = kMode == kGrad ? num.lse2 : 0.f, n_g = kMode == kGrad ? num.g : 0.f;
-        // The columns that the stream leaves out, eight bits a group: masked
-        // ones, touched ones when scoring, and what lies behind the vocabulary.
-        // The mask's bytes come from global memory, asked for a tile ahead.
-        uint32_t masked[2][Smem<kMode>::kSides];
-        auto ask = [&](int64_t tc) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int64_t j = tc + 8 * (t + g * kStreamThreads);
-#pragma unroll
-                for (int side = 0; side < Smem<kMode>::kSides; ++side) {
-                    uint32_t m = num.none[side] ? 0xffu : 0u;
-                    const uint8_t *bits = num.mask[side];
-                    if (bits && j < c1 && j + 8 > c0) {
-                        if (kTwo || kAligned) {
-                            m = ~static_cast<uint32_t>(__ldg(bits + (j >> 3))) & 0xffu;
-                        } else {
-                            // groups that start between bytes, or in front of the unit
-                            const int64_t last = (a.vocab - 1) >> 3, at = j >> 3;
-                            const uint32_t lo = at >= 0 ? __ldg(bits + at) : 0u;
-                            const uint32_t hi = at + 1 <= last ? __ldg(bits + at + 1) : 0u;
-                            m = ~((lo | hi << 8) >> (j & 7)) & 0xffu;
-                        }
-                    }
-                    masked[g][side] = m;
-                }
+        // Masked columns, eight bits a group.  The mask's bytes come from global
+        // memory, asked for a tile ahead; `last` keeps them inside the row's.
+        const bool none0 = num.none[0] != 0, none1 = kTwo && num.none[kTwo ? 1 : 0] != 0;
+        const uint8_t *const mask0 = num.mask[0], *const mask1 = kTwo ? num.mask[1] : nullptr;
+        const bool one_mask = mask0 == mask1;
+        const int64_t first_byte = (c0 - lead) >> 3, last_byte = (a.vocab - 1) >> 3;
+        const int shift = kTwo || kAligned ? 0 : static_cast<int>(c0 - lead) & 7;
+        uint32_t m0[2] = {0, 0}, m1[2] = {0, 0};
+        auto ask1 = [&](const uint8_t *mask, int at) -> uint32_t {
+            const int64_t byte = first_byte + at;
+            if (kTwo || kAligned) return ~static_cast<uint32_t>(__ldg(mask + min(byte, last_byte)));
+            const uint32_t lo = __ldg(mask + max(min(byte, last_byte), int64_t{0})), hi = __ldg(mask + min(byte + 1, last_byte));
+            return ~((lo | hi << 8) >> shift);
+        };
+        auto ask = [&](int tile) {
+            if (mask0) {
+                m0[0] = ask1(mask0, tile * (kTile / 8) + t);
+                m0[1] = ask1(mask0, tile * (kTile / 8) + t + kStreamThreads);
+            }
+            if (kTwo && mask1 && !one_mask) {
+                m1[0] = ask1(mask1, tile * (kTile / 8) + t);
+                m1[1] = ask1(mask1, tile * (kTile / 8) + t + kStreamThreads);
             }
         };
-        ask(c0 - lead_in(r, c0));
-        const char *const xrow = a.in[0].base + r * a.in[0].stride;
-        const char *const yrow = kTwo ? a.in[1].base + r * a.in[1].stride : nullptr;
+        ask(0);
+        uint32_t at_x = 0, at_y = 0;  // where the first tile's groups start in a stage (the others': aligned alike)
+        if (!kAligned) {
+            const int64_t row = kTwo ? a.rowid[i].x : r;
+            at_x = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.in[0].base + row * a.in[0].stride + (c0 - lead) * kXE)) & 15u;
+            if (kTwo) at_y = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(a.in[1].base + row * a.in[1].stride + c0 * kYE)) & 15u;
+        }
         Acc2 acc = acc2_init();
+        const int tiles = (len + lead + kTile - 1) / kTile;
+        int seg_left = kSegment / kTile;
+        int64_t state = kTwo ? (i * a.n_segs + c0 / kSegment) * kStates + warp : 0;
 #pragma unroll 1
-        for (int64_t tc = c0 - lead_in(r, c0); tc < c1; tc += kTile, ++it) {
-            const uint32_t s = it % a.n_stages;
-            const bool ok = wait_phase(&sm.full[s], (it / a.n_stages) & 1, &sm.abort_flag, a.status);
+        for (int tile = 0; tile < tiles; ++tile) {
+            const bool ok = wait_phase(&sm.full[stage], phase, &sm.abort_flag, a.status);
             if (__any_sync(0xffffffffu, !ok)) {
                 if (kTwo) return;
                 dead = true;
                 break;
             }
-            const char *stg = ring + static_cast<size_t>(s) * kStage;
+            const char *stg = ring + stage * kStage;
             Group8<kXBf16> gx[2];
             Group8<kYBf16> gy[2];
-            bool in[2] = {true, true};
-            if (kAligned && tc + kTile <= c1) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const uint32_t j = 8 * (t + g * kStreamThreads);
-                    ctl_shared8<kXBf16, true>(stg, j * kXE, gx[g]);
-                    if constexpr (kTwo) ctl_shared8<kYBf16, true>(stg + kStageX, j * kYE, gy[g]);
-                }
-            } else {
-                const int64_t f = max(tc, c0), e = min(tc + kTile, c1);
-                auto fetch = [&](auto &g8, const Plane &plane, const char *row, const char *from, int64_t j, auto kind) {
-                    constexpr bool kB = decltype(kind)::value;
-                    const Span x = span_of<elt<kB>()>(plane, row, f, e);
-                    if (j >= x.lo && j + 8 <= x.hi)
-                        ctl_shared8<kB, kAligned>(from, x.lead + static_cast<uint32_t>(j - f) * elt<kB>(), g8);
-                    else
-                        ctl_gather8<kB>(row, j, f, e, g8);
-                };
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
-                    in[g] = j < e && j + 8 > f;
-                    if (!in[g]) continue;
-                    fetch(gx[g], a.in[0], xrow, stg, j, std::integral_constant<bool, kXBf16>{});
-                    if constexpr (kTwo) fetch(gy[g], a.in[1], yrow, stg + kStageX, j, std::integral_constant<bool, kYBf16>{});
-                }
+            for (int g = 0; g < 2; ++g) {
+                const int j = 8 * (t + g * kStreamThreads);
+                // A first tile that starts in front of its unit was copied from
+                // the unit's first column on: its first group is the scouts',
+                // the others lie where a copy from the tile's start had them.
+                const uint32_t skew = !kAligned && !kTwo && tile == 0 && lead > 0
+                                          ? (at_x + lead * kXE & ~15u)
+                                          : 0u;
+                ctl_shared8<kXBf16, kAligned>(stg, max(static_cast<int>(at_x + j * kXE - skew), 0), gx[g]);
+                if constexpr (kTwo) ctl_shared8<kYBf16, kAligned>(stg + kStageX, at_y + j * kYE, gy[g]);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[s]);  // values are in registers now
-            uint32_t skip[2][Smem<kMode>::kSides];
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int side = 0; side < Smem<kMode>::kSides; ++side) skip[g][side] = in[g] ? masked[g][side] : 0xffu;
-            if (tc + kTile < c1) ask(tc + kTile);
+            if (lane == 0) mbar_arrive(&sm.empty[stage]);  // values are in registers now
+            if (++stage == a.n_stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            uint32_t s0[2] = {m0[0] & 0xffu, m0[1] & 0xffu}, s1[2] = {m1[0] & 0xffu, m1[1] & 0xffu};
+            if (one_mask) {
+                s1[0] = s0[0];
+                s1[1] = s0[1];
+            }
+            if (tile + 1 < tiles) ask(tile + 1);
+            const int left = len + lead - tile * kTile;  // columns from the tile's start on
             if constexpr (kTwo) {
-                const int64_t seg_end = min((tc / kSegment + 1) * kSegment, c1);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    if (!in[g]) continue;
-                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
-                    uint32_t more = reinterpret_cast<const uint8_t *>(sm.touched[b])[(j - c0) >> 3];
-                    if (j + 8 > c1) more |= 0xffu << (c1 - j) & 0xffu;
-                    skip[g][0] |= more;
-                    skip[g][1] |= more;
+                    const int group = t + g * kStreamThreads;
+                    const uint32_t out = left > 8 * group
+                                             ? reinterpret_cast<const uint8_t *>(sm.touched[b])[tile * (kTile / 8) + group]
+                                             : 0xffu;
+                    s0[g] |= none0 ? 0xffu : out;
+                    s1[g] |= none1 ? 0xffu : out;
                 }
-                if ((skip[0][0] & skip[0][1] & skip[1][0] & skip[1][1]) != 0xffu) {  // something is allowed
-                    float vt[16], vr[16];
+                if ((s0[0] & s0[1] & s1[0] & s1[1]) != 0xffu) {  // something is allowed
+                    if (s0[0] | s0[1] | s1[0] | s1[1]) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        if (skip[g][0]) ctl_fill8<kXBf16, kFillBits>(gx[g], sm.lanes[skip[g][0]]);
-                        if (skip[g][1]) ctl_fill8<kYBf16, kFillBits>(gy[g], sm.lanes[skip[g][1]]);
-                        ctl_unpack8<kXBf16>(gx[g], vt + 8 * g);
-                        ctl_unpack8<kYBf16>(gy[g], vr + 8 * g);
+                        for (int g = 0; g < 2; ++g) {
+                            ctl_fill8<kXBf16, kFillBits>(gx[g], sm.lanes[s0[g]]);
+                            ctl_fill8<kYBf16, kFillBits>(gy[g], sm.lanes[s1[g]]);
+                        }
                     }
                     f2_t pt[8], pr[8];
 #pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        pt[p] = f2(vt[2 * p], vt[2 * p + 1]);
-                        pr[p] = f2(vr[2 * p], vr[2 * p + 1]);
+                    for (int g = 0; g < 2; ++g) {
+                        float v[8];
+                        ctl_unpack8<kXBf16>(gx[g], v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) pt[4 * g + q] = f2(v[2 * q], v[2 * q + 1]);
+                        ctl_unpack8<kYBf16>(gy[g], v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) pr[4 * g + q] = f2(v[2 * q], v[2 * q + 1]);
                     }
                     if (!(same_scale && accumulate_near(pt, pr, acc, n_l, n_s))) {
 #pragma unroll
                         for (int p = 0; p < 8; ++p) {
-                            const uint32_t bt = skip[p >> 2][0] >> (2 * (p & 3)), br = skip[p >> 2][1] >> (2 * (p & 3));
+                            const uint32_t bt = s0[p >> 2] >> (2 * (p & 3)), br = s1[p >> 2] >> (2 * (p & 3));
                             pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(pt[p]), bt & 2u ? -INFINITY : f2_hi(pt[p]));
                             pr[p] = f2(br & 1u ? -INFINITY : f2_lo(pr[p]), br & 2u ? -INFINITY : f2_hi(pr[p]));
                         }
                         accumulate_far(pt, pr, acc, n_lt, n_l);
                     }
                 }
-                if (tc + kTile >= seg_end) {
+                if (--seg_left == 0 || tile + 1 == tiles) {
                     const Acc w = warp_reduce_acc<false>(acc2_fold(acc), n_lt, n_l);
                     if (lane == 0) {
-                        const int64_t o = (i * a.n_segs + tc / kSegment) * kStates + warp;
-                        a.part_a[o] = make_float4(w.mt, w.st, w.dd, w.mr);
-                        a.part_b[o] = w.sr;
+                        a.part_a[state] = make_float4(w.mt, w.st, w.dd, w.mr);
+                        a.part_b[state] = w.sr;
                     }
+                    state += kStates;
+                    seg_left = kSegment / kTile;
                     acc = acc2_init();
                 }
             } else {
@@ -910,8 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 const f2_t s2f = f2(n_s, n_s);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    if (!in[g]) continue;
-                    const int64_t j = tc + 8 * (t + g * kStreamThreads);
+                    const int group = t + g * kStreamThreads, j = tile * kTile + 8 * group - lead;
                     float v[8];
                     ctl_unpack8<kXBf16>(gx[g], v);
 #pragma unroll
@@ -924,15 +964,13 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     Group8<kYBf16> w;
                     ctl_pack8<kYBf16>(v, w);
                     constexpr uint32_t kMasked = kMode == kApply ? 0xff80u : 0u;  // -inf, or no gradient
-                    if (skip[g][0]) ctl_fill8<kYBf16, kMasked>(w, sm.lanes[skip[g][0]]);
-                    if (j >= c0 && j + 8 <= c1) ctl_store8<kYBf16>(orow, j, w);
-                    else ctl_scatter8<kYBf16>(orow, j, c0, c1, w);
+                    const uint32_t skip = none0 ? 0xffu : s0[g];
+                    if (skip) ctl_fill8<kYBf16, kMasked>(w, sm.lanes[skip]);
+                    if (j >= 0 && left >= 8 * group + 8) ctl_store8<kYBf16>(orow, j, w);  // (the others are the scouts')
                 }
             }
         }
-        if (!kTwo && dead) {
-            fill(CUDART_NAN_F);
-        }
+        if (!kTwo && dead) fill(CUDART_NAN_F);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.done[b]);
         ++n_live;
