@@ -274,19 +274,23 @@ __device__ __forceinline__ void raise_refs(Acc2 &a, float nmt, float nmr, float 
     a.mr = nmr;
 }
 
+// The references raised to take in two maxima.  References that are near each
+// other are kept equal: the exponents are then x l - (m l) with one rounded
+// m l for both sides, which leaves their difference untouched.
+__device__ __forceinline__ void raise_to(Acc2 &a, float ct, float cr, float lt, float lr) {
+    float nt = fmaxf(a.mt, ct), nr = fmaxf(a.mr, cr);
+    if (fabsf(__fsub_rn(nt, nr)) <= 8.f) nt = nr = fmaxf(nt, nr);
+    raise_refs(a, nt, nr, lt, lr);
+}
+
 // Sixteen columns of two sides that nearly agree; false where they do not (the
 // state is valid either way).  A NaN fails the comparison of the sum of
-// squares.  The exponent is one multiply-add: the rounding of m l is the same
-// for both sides.
+// squares.
 __device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, Acc2 &a, float l, float s) {
     const float cm = max16(vr);
     if (!(cm > kFloorZ)) return false;
-    if (cm > a.mr) raise_refs(a, fmaxf(a.mt, cm), cm, l, l);
-    if (a.mt != a.mr) {  // only where some columns in front did not agree
-        if (fabsf(__fsub_rn(a.mt, a.mr)) > 8.f) return false;
-        const float m = fmaxf(a.mt, a.mr);
-        raise_refs(a, m, m, l, l);
-    }
+    if (cm > a.mr) raise_to(a, cm, cm, l, l);
+    if (a.mt != a.mr) return false;
     const float ml = __fmul_rn(-a.mr, l), h = __fmul_rn(0.5f, l);
     const f2_t s2 = f2(s, s), ml2 = f2(ml, ml), h2 = f2(h, h);
     f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;
@@ -310,16 +314,35 @@ __device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, 
     return true;
 }
 
+// Rows whose largest logits are below kFloorZ (a type's lowest value as a mask
+// over everything): m l could overflow, so the difference is formed first.
+__device__ __noinline__ void accumulate_low(const f2_t *vt, const f2_t *vr, Acc2 &a, float lt, float lr) {
+    accumulate16(vt, vr, a, lt, lr);
+}
+
 // Sixteen columns of any two sides, each with an exponential of its own; -inf
-// adds nothing (the floor of the references keeps x - m defined).
+// adds nothing.
 __device__ __forceinline__ void accumulate_far(const f2_t *vt, const f2_t *vr, Acc2 &a, float lt, float lr) {
     const float ct = max16(vt), cr = max16(vr);
-    if (ct > a.mt || cr > a.mr) raise_refs(a, fmaxf(a.mt, ct), fmaxf(a.mr, cr), lt, lr);
-    const f2_t mt2 = f2(a.mt, a.mt), mr2 = f2(a.mr, a.mr), lt2 = f2(lt, lt), lr2 = f2(lr, lr);
+    if (ct > a.mt || cr > a.mr) raise_to(a, ct, cr, lt, lr);
+    if (!(fminf(a.mt, a.mr) > kFloorZ)) {
+        f2_t t[8], r[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            t[p] = vt[p];
+            r[p] = vr[p];
+        }
+        Acc2 c = a;
+        accumulate_low(t, r, c, lt, lr);
+        a = c;
+        return;
+    }
+    const float ft = __fmul_rn(-a.mt, lt), fr = __fmul_rn(-a.mr, lr);
+    const f2_t ft2 = f2(ft, ft), fr2 = f2(fr, fr), lt2 = f2(lt, lt), lr2 = f2(lr, lr);
     f2_t st = f2(0.f, 0.f), sr = st, sd = st;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const f2_t et = ex2_2(mul2(sub2(vt[p], mt2), lt2)), er = ex2_2(mul2(sub2(vr[p], mr2), lr2));
+        const f2_t et = ex2_2(fma2(vt[p], lt2, ft2)), er = ex2_2(fma2(vr[p], lr2, fr2));
         st = add2(st, et);
         sr = add2(sr, er);
         sd = add2(sd, sub2(et, er));
@@ -332,19 +355,20 @@ __device__ __forceinline__ void accumulate_far(const f2_t *vt, const f2_t *vr, A
 // One pair of controlled logits (h + l of each side) into the state; an -inf
 // adds nothing.
 __device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float lt, float lr, float s, bool same_scale) {
-    if (xt.h > a.mt || xr.h > a.mr) raise_refs(a, fmaxf(a.mt, xt.h), fmaxf(a.mr, xr.h), lt, lr);
+    if (xt.h > a.mt || xr.h > a.mr) raise_to(a, xt.h, xr.h, lt, lr);
     const float er = ex2(__fmaf_rn(xr.l, lr, __fmul_rn(__fsub_rn(xr.h, a.mr), lr)));
     const float u = __fmul_rn(
         __fadd_rn(__fsub_rn(__fsub_rn(xt.h, xr.h), __fsub_rn(a.mt, a.mr)), __fsub_rn(xt.l, xr.l)), s);
-    float d;
+    float d, et;
     if (same_scale && fabsf(u) <= 0.25f) {
         d = __fmul_rn(__fmul_rn(er, u), expm1_ratio(u));
+        et = __fadd_rn(er, d);
     } else {
-        const float et = ex2(__fmaf_rn(xt.l, lt, __fmul_rn(__fsub_rn(xt.h, a.mt), lt)));
+        et = ex2(__fmaf_rn(xt.l, lt, __fmul_rn(__fsub_rn(xt.h, a.mt), lt)));
         d = __fsub_rn(et, er);
     }
     a.sr = add2(a.sr, f2(er, 0.f));
-    a.st = add2(a.st, f2(__fadd_rn(er, d), 0.f));
+    a.st = add2(a.st, f2(et, 0.f));
     a.dd = add2(a.dd, f2(d, 0.f));
 }
 
@@ -831,13 +855,15 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         const bool none0 = num.none[0] != 0, none1 = kTwo && num.none[kTwo ? 1 : 0] != 0;
         const uint8_t *const mask0 = num.mask[0], *const mask1 = kTwo ? num.mask[1] : nullptr;
         const bool one_mask = mask0 == mask1;
-        const int64_t first_byte = (c0 - lead) >> 3, last_byte = (a.vocab - 1) >> 3;
+        const int64_t first_byte = (c0 - lead) >> 3;
+        const int last_byte = static_cast<int>(((a.vocab - 1) >> 3) - first_byte);
         const int shift = kTwo || kAligned ? 0 : static_cast<int>(c0 - lead) & 7;
         uint32_t m0[2] = {0, 0}, m1[2] = {0, 0};
         auto ask1 = [&](const uint8_t *mask, int at) -> uint32_t {
-            const int64_t byte = first_byte + at;
-            if (kTwo || kAligned) return ~static_cast<uint32_t>(__ldg(mask + min(byte, last_byte)));
-            const uint32_t lo = __ldg(mask + max(min(byte, last_byte), int64_t{0})), hi = __ldg(mask + min(byte + 1, last_byte));
+            const uint8_t *p = mask + first_byte;
+            if (kTwo || kAligned) return ~static_cast<uint32_t>(__ldg(p + min(at, last_byte)));
+            const int low = first_byte < 0 ? 1 : 0;
+            const uint32_t lo = __ldg(p + max(min(at, last_byte), low)), hi = __ldg(p + max(min(at + 1, last_byte), low));
             return ~((lo | hi << 8) >> shift);
         };
         auto ask = [&](int tile) {
