@@ -283,11 +283,45 @@ __device__ __forceinline__ void raise_to(Acc2 &a, float ct, float cr, float lt, 
     raise_refs(a, nt, nr, lt, lr);
 }
 
+// Columns 2 q and 2 q + 1 of a group, and the largest of two groups.  Both work
+// on the raw words, so that no more than a pair is held widened at a time.
+template <bool kBf16>
+__device__ __forceinline__ f2_t group_pair(const Group8<kBf16> &g, int q) {
+    if constexpr (kBf16) {
+        const uint32_t w = q == 0 ? g.w[0].x : q == 1 ? g.w[0].y : q == 2 ? g.w[0].z : g.w[0].w;
+        return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    } else {
+        const uint4 &w = g.w[kBf16 ? 0 : q >> 1];
+        return q & 1 ? f2(__uint_as_float(w.z), __uint_as_float(w.w)) : f2(__uint_as_float(w.x), __uint_as_float(w.y));
+    }
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <bool kBf16>
+__device__ __forceinline__ float groups_max(const Group8<kBf16> *g) {
+    if constexpr (kBf16) {
+        const uint32_t a = max_bf16x2(max_bf16x2(g[0].w[0].x, g[0].w[0].y), max_bf16x2(g[0].w[0].z, g[0].w[0].w));
+        const uint32_t b = max_bf16x2(max_bf16x2(g[1].w[0].x, g[1].w[0].y), max_bf16x2(g[1].w[0].z, g[1].w[0].w));
+        const uint32_t c = max_bf16x2(a, b);
+        return fmaxf(__uint_as_float(c << 16), __uint_as_float(c & 0xffff0000u));
+    } else {
+        f2_t v[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) v[p] = group_pair<kBf16>(g[p >> 2], p & 3);
+        return max16(v);
+    }
+}
+
 // Sixteen columns of two sides that nearly agree; false where they do not (the
 // state is valid either way).  A NaN fails the comparison of the sum of
 // squares.
-__device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, Acc2 &a, float l, float s) {
-    const float cm = max16(vr);
+template <bool kTBf16, bool kRBf16>
+__device__ __forceinline__ bool accumulate_near(const Group8<kTBf16> *gt, const Group8<kRBf16> *gr, Acc2 &a, float l,
+                                                float s) {
+    const float cm = groups_max(gr);
     if (!(cm > kFloorZ)) return false;
     if (cm > a.mr) raise_to(a, cm, cm, l, l);
     if (a.mt != a.mr) return false;
@@ -296,8 +330,9 @@ __device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, 
     f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const f2_t u = mul2(sub2(vt[p], vr[p]), s2);
-        const f2_t e = ex2_2(fma2(add2(vt[p], vr[p]), h2, ml2));
+        const f2_t xt = group_pair(gt[p >> 2], p & 3), xr = group_pair(gr[p >> 2], p & 3);
+        const f2_t u = mul2(sub2(xt, xr), s2);
+        const f2_t e = ex2_2(fma2(add2(xt, xr), h2, ml2));
         const f2_t v = mul2(u, u), w = mul2(e, u);
         q = add2(q, v);
         e0 = add2(e0, e);
@@ -314,35 +349,17 @@ __device__ __forceinline__ bool accumulate_near(const f2_t *vt, const f2_t *vr, 
     return true;
 }
 
-// Rows whose largest logits are below kFloorZ (a type's lowest value as a mask
-// over everything): m l could overflow, so the difference is formed first.
-__device__ __noinline__ void accumulate_low(const f2_t *vt, const f2_t *vr, Acc2 &a, float lt, float lr) {
-    accumulate16(vt, vr, a, lt, lr);
-}
-
 // Sixteen columns of any two sides, each with an exponential of its own; -inf
-// adds nothing.
+// adds nothing.  The differences to the references come first: a type's lowest
+// value times the scale could overflow.
 __device__ __forceinline__ void accumulate_far(const f2_t *vt, const f2_t *vr, Acc2 &a, float lt, float lr) {
     const float ct = max16(vt), cr = max16(vr);
     if (ct > a.mt || cr > a.mr) raise_to(a, ct, cr, lt, lr);
-    if (!(fminf(a.mt, a.mr) > kFloorZ)) {
-        f2_t t[8], r[8];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            t[p] = vt[p];
-            r[p] = vr[p];
-        }
-        Acc2 c = a;
-        accumulate_low(t, r, c, lt, lr);
-        a = c;
-        return;
-    }
-    const float ft = __fmul_rn(-a.mt, lt), fr = __fmul_rn(-a.mr, lr);
-    const f2_t ft2 = f2(ft, ft), fr2 = f2(fr, fr), lt2 = f2(lt, lt), lr2 = f2(lr, lr);
+    const f2_t mt2 = f2(a.mt, a.mt), mr2 = f2(a.mr, a.mr), lt2 = f2(lt, lt), lr2 = f2(lr, lr);
     f2_t st = f2(0.f, 0.f), sr = st, sd = st;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const f2_t et = ex2_2(fma2(vt[p], lt2, ft2)), er = ex2_2(fma2(vr[p], lr2, fr2));
+        const f2_t et = ex2_2(mul2(sub2(vt[p], mt2), lt2)), er = ex2_2(mul2(sub2(vr[p], mr2), lr2));
         st = add2(st, et);
         sr = add2(sr, er);
         sd = add2(sd, sub2(et, er));
@@ -941,23 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                             ctl_fill8<kYBf16, kFillBits>(gy[g], sm.lanes[s1[g]]);
                         }
                     }
-                    f2_t pt[8], pr[8];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float v[8];
-                        ctl_unpack8<kXBf16>(gx[g], v);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) pt[4 * g + q] = f2(v[2 * q], v[2 * q + 1]);
-                        ctl_unpack8<kYBf16>(gy[g], v);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) pr[4 * g + q] = f2(v[2 * q], v[2 * q + 1]);
-                    }
-                    if (!(same_scale && accumulate_near(pt, pr, acc, n_l, n_s))) {
+                    if (!(same_scale && accumulate_near(gx, gy, acc, n_l, n_s))) {
+                        f2_t pt[8], pr[8];
 #pragma unroll
                         for (int p = 0; p < 8; ++p) {
                             const uint32_t bt = s0[p >> 2] >> (2 * (p & 3)), br = s1[p >> 2] >> (2 * (p & 3));
-                            pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(pt[p]), bt & 2u ? -INFINITY : f2_hi(pt[p]));
-                            pr[p] = f2(br & 1u ? -INFINITY : f2_lo(pr[p]), br & 2u ? -INFINITY : f2_hi(pr[p]));
+                            const f2_t xt = group_pair(gx[p >> 2], p & 3), xr = group_pair(gy[p >> 2], p & 3);
+                            pt[p] = f2(bt & 1u ? -INFINITY : f2_lo(xt), bt & 2u ? -INFINITY : f2_hi(xt));
+                            pr[p] = f2(br & 1u ? -INFINITY : f2_lo(xr), br & 2u ? -INFINITY : f2_hi(xr));
                         }
                         accumulate_far(pt, pr, acc, n_lt, n_l);
                     }
