@@ -46,10 +46,10 @@ constexpr int kThreads = kStreamThreads + kScoutThreads + 32;  // the producer's
 // bits do not depend on how many rows there are.
 constexpr int kSegment = 7 * 8192;
 constexpr int kStates = kStreamWarps + kScoutWarps;
-static_assert(kSegment % kTile == 0, "segments of whole tiles");
+static_assert(kSegment % kTile == 0 && kSegment % 4096 == 0, "segments of whole tiles and bitmap lines");
 constexpr int kMaxWidth = 3 * kSegment;        // columns of a unit: the bitmaps' room
 constexpr int kWords = kMaxWidth / 32;
-constexpr int kLines = kWords / 32;            // lines of 32 bitmap words, one warp's scan each
+constexpr int kLines = (kWords + 127) / 128;   // lines of 128 bitmap words, one warp's scan each: four words a lane
 // touched tokens at a time (more take several passes over the history)
 constexpr int cap_of(int mode) { return mode == kScore ? 1536 : 4096; }
 constexpr int kKept = 8;                       // history tokens that a scout keeps between its two passes
@@ -174,11 +174,11 @@ struct Smem {
     int line_base[kLines + 1];                  // touched columns in the lines in front
     float gs, ll;                               // kGrad: grad * scale, the lower part of lse2
     alignas(16) uint4 lanes[256];
-    uint32_t touched[kSides][kWords];           // kScore: [unit parity], the stream leaves these out
-    uint16_t before[kWords];                    // touched columns in the words in front, of the same line
+    alignas(16) uint32_t touched[kSides][kLines * 128];  // kScore: [unit parity], the stream leaves these out
+    alignas(8) uint16_t before[kLines * 128];   // touched columns in the words in front, of the same line
     uint32_t word[2][kCap];                     // kScore: a side's count words; else [unit parity], the values
     uint32_t list[kSides == 2 ? 1 : 2][kCap];   // their columns in the unit
-    int32_t bias_ids[kSides][kStagedBias];      // the row's biases
+    alignas(16) int32_t bias_ids[kSides][kStagedBias];  // the row's biases
     float bias[kSides][kStagedBias];
 };
 template <int kMode>
@@ -315,16 +315,15 @@ __device__ __forceinline__ float groups_max(const Group8<kBf16> *g) {
     }
 }
 
-// Sixteen columns of two sides that nearly agree; false where they do not (the
-// state is valid either way).  A NaN fails the comparison of the sum of
+// Sixteen columns of two sides that nearly agree, by all lanes of a warp; false
+// where they do not (the state is valid either way).  A NaN fails the comparison of the sum of
 // squares.
 template <bool kTBf16, bool kRBf16>
 __device__ __forceinline__ bool accumulate_near(const Group8<kTBf16> *gt, const Group8<kRBf16> *gr, Acc2 &a, float l,
                                                 float s) {
     const float cm = groups_max(gr);
-    if (!(cm > kFloorZ)) return false;
-    if (cm > a.mr) raise_to(a, cm, cm, l, l);
-    if (a.mt != a.mr) return false;
+    const bool fit = cm > kFloorZ;
+    if (__any_sync(0xffffffffu, fit && cm > a.mr)) raise_to(a, fit ? cm : a.mt, fit ? cm : a.mr, l, l);
     const float ml = __fmul_rn(-a.mr, l), h = __fmul_rn(0.5f, l);
     const f2_t s2 = f2(s, s), ml2 = f2(ml, ml), h2 = f2(h, h);
     f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;
@@ -340,7 +339,8 @@ __device__ __forceinline__ bool accumulate_near(const Group8<kTBf16> *gt, const 
         e2 = fma2(e, v, e2);
         e3 = fma2(w, v, e3);
     }
-    if (!(__fadd_rn(f2_lo(q), f2_hi(q)) <= kNear2)) return false;
+    // (references apart: only where columns in front did not agree)
+    if (!(fit && a.mt == a.mr && __fadd_rn(f2_lo(q), f2_hi(q)) <= kNear2)) return false;
     const f2_t d = fma2(e3, f2(1.f / 24.f, 1.f / 24.f), e1);       // e_t - e_r
     const f2_t m = fma2(e2, f2(0.125f, 0.125f), e0);               // their mean
     a.dd = add2(a.dd, d);
@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 sm.id_word = 0;
             }
             if (kTwo && st == 32) sm.row[1] = ctl_row(a.c[1], r);
-            for (int w = st; w < (words + 31) / 32 * 32; w += kScoutThreads) touched[w] = 0;
+            const int lines = (words + 127) / 128;
+            for (int w = st; w < lines * 32; w += kScoutThreads) reinterpret_cast<uint4 *>(touched)[w] = make_uint4(0, 0, 0, 0);
             scout_sync();
             int32_t kept[2][kKept];
 #pragma unroll
@@ -602,6 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                             else atomicOr(&sm.id_word, kSeen);
                         }
                     });
+                // staged ids are padded to a multiple of four
+                if (a.c[side].n_bias + st < min((a.c[side].n_bias + 3) & ~3, kStagedBias))
+                    sm.bias_ids[side][a.c[side].n_bias + st] = -1;
                 for (int e = st; e < a.c[side].n_bias; e += kScoutThreads) {
                     const int32_t tok = __ldg(a.c[side].bias_ids + r * a.c[side].n_bias + e);
                     if (a.c[side].n_bias <= kStagedBias) {
@@ -623,11 +627,31 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 if (at < up) atomicOr(&touched[at >> 5], 1u << (at & 31));
             }
             scout_sync();
-            auto value = [&](int side, float x, uint32_t w, int64_t token, float *slope) -> Two {
-                const int n = a.c[side].n_bias;
-                const bool staged = n <= kStagedBias;
-                return ctl_value(x, w, sm.row[side], staged ? sm.bias_ids[side] : a.c[side].bias_ids + r * n,
-                                 staged ? sm.bias[side] : a.c[side].bias + r * n, n, token, slope);
+            // the bias of a token on each side (one search where the sides share their ids)
+            auto bias_of = [&](int32_t token, Two *v) {
+                int at = -1, found = 0;
+#pragma unroll
+                for (int side = 0; side <= kLast; ++side) {
+                    const int n = a.c[side].n_bias;
+                    v[side] = Two{0.f, 0.f};
+                    if (n == 0) continue;
+                    const bool staged = n <= kStagedBias;
+                    const int32_t *ids = staged ? sm.bias_ids[side] : a.c[side].bias_ids + r * n;
+                    if (side == 0 || !a.same) {
+                        at = -1;
+                        found = 0;
+                        if (staged) {
+                            at = bias_find(reinterpret_cast<const int4 *>(ids), n, token, &found);
+                        } else {
+                            for (int e = 0; e < n; ++e)
+                                if (ids[e] == token) {
+                                    at = e;
+                                    ++found;
+                                }
+                        }
+                    }
+                    v[side] = bias_sum(ids, staged ? sm.bias[side] : a.c[side].bias + r * n, n, token, at, found);
+                }
             };
             // the row's numbers for the stream
             if (st == 0) {
@@ -648,7 +672,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     const CtlRow &o = sm.row[0];
                     double z = -CUDART_INF;
                     if (ctl_allows(o, id)) {
-                        const Two v = value(0, ctl_elem<kXBf16>(xrow, id), sm.id_word, id, nullptr);
+                        Two bias[kLast + 1];
+                        bias_of(static_cast<int32_t>(id), bias);
+                        const Two v = ctl_value(ctl_elem<kXBf16>(xrow, id), sm.id_word, o, bias[0], nullptr);
                         z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
                     }
                     const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
@@ -661,22 +687,25 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 if (!a.late) mbar_arrive(&sm.ready[b]);
             }
             // each word's rank within its line
-            for (int line = kScoutWarps - 1 - (warp - kStreamWarps); 32 * line < words; line += kScoutWarps) {
+            for (int line = kScoutWarps - 1 - (warp - kStreamWarps); line < lines; line += kScoutWarps) {
                 const int w = 32 * line + lane;
-                const int n = __popc(touched[w]);
+                const uint4 bits = reinterpret_cast<const uint4 *>(touched)[w];
+                const int n0 = __popc(bits.x), n1 = n0 + __popc(bits.y), n2 = n1 + __popc(bits.z), n = n2 + __popc(bits.w);
                 int incl = n;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, incl, off);
                     if (lane >= off) incl += v;
                 }
-                sm.before[w] = static_cast<uint16_t>(incl - n);
+                const int at = incl - n;
+                reinterpret_cast<ushort4 *>(sm.before)[w] =
+                    make_ushort4(static_cast<uint16_t>(at), static_cast<uint16_t>(at + n0), static_cast<uint16_t>(at + n1),
+                                 static_cast<uint16_t>(at + n2));
                 if (lane == 31) sm.line_base[line] = incl;
             }
             scout_sync();
             if (warp == kStreamWarps) {
                 // the lines' sums become what lies in front of them
-                const int lines = (words + 31) / 32;
                 int sum = 0;
                 for (int l0 = 0; l0 <= lines; l0 += 32) {
                     const int n = l0 + lane < lines ? sm.line_base[l0 + lane] : 0;
@@ -703,23 +732,34 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     w0[q] = 0;
                     if (kTwo) w1[q] = 0;
                 }
-                for (int w = st; w < words; w += kScoutThreads) {
-                    uint32_t bits = touched[w];
-                    int at = sm.line_base[w >> 5] + sm.before[w] - base;
-                    for (; bits; bits &= bits - 1, ++at)
-                        if (at >= 0 && at < m) list[at] = static_cast<uint32_t>(32 * w + __ffs(bits) - 1);
-                }
                 scout_sync();
+                // a column's rank among the window's; every mark of a column
+                // writes it down there (the same value, so their order is free)
+                auto enter = [&](uint32_t j) -> int {
+                    const int p = sm.line_base[j >> 12] + sm.before[j >> 5] + __popc(touched[j >> 5] & ((1u << (j & 31)) - 1u)) - base;
+                    if (p < 0 || p >= m) return -1;
+                    list[p] = j;
+                    // its logits and mask word will be wanted soon
+                    prefetch_l1(xrow + (c0 + j) * kXE);
+                    if (kTwo) prefetch_l1(yrow + (c0 + j) * kYE);
+                    if (sm.row[0].mask) prefetch_l1(sm.row[0].mask + (c0 + j) / 32);
+                    return p;
+                };
+                auto place = [&](int32_t tok) -> int {
+                    const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
+                    return j < len ? enter(static_cast<uint32_t>(j)) : -1;
+                };
+                {
+                    int64_t head, tail;
+                    edges<kMode>(c0, c1, a.vocab, head, tail);
+                    const int n_head = static_cast<int>(head - c0);
+                    const int at = st < n_head ? st : static_cast<int>(tail - c0) + st - n_head;
+                    if (at < static_cast<int>(len)) enter(static_cast<uint32_t>(at));
+                    if (kMode == kGrad && st == kScoutThreads - 1) place(static_cast<int32_t>(id));
+                }
 #pragma unroll
                 for (int side = 0; side <= kLast; ++side) {
                     uint32_t *const word = side ? w1 : w0;
-                    auto place = [&](int32_t tok) -> int {
-                        const uint64_t j = static_cast<uint64_t>(static_cast<int64_t>(tok) - c0);
-                        if (j >= len) return -1;
-                        const uint32_t bits = touched[j >> 5];
-                        const int p = sm.line_base[j >> 10] + sm.before[j >> 5] + __popc(bits & ((1u << (j & 31)) - 1u)) - base;
-                        return p < m ? p : -1;
-                    };
                     if (counts[side])
                         each_token(a.c[side], sm.row[side], st, kept[side], [&](int32_t tok, bool gen) {
                             const int p = place(tok);
@@ -748,8 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                         ctl_allows(sm.row[1], id) ? static_cast<double>(ctl_elem<kYBf16>(yrow, id)) : -CUDART_INF);
                 if (total > 0 && total <= kCap) count(0, total);
                 for (int64_t f = c0; f < c1; f += kSegment) {
-                    const int first = sm.line_base[(f - c0) >> 10];
-                    const int end = f + kSegment < c1 ? sm.line_base[(f + kSegment - c0) >> 10] : total;
+                    const int first = sm.line_base[(f - c0) >> 12];
+                    const int end = f + kSegment < c1 ? sm.line_base[(f + kSegment - c0) >> 12] : total;
                     Acc2 acc = acc2_init();
                     for (int base = first; base < end; base += kCap) {
                         const int m = min(kCap, end - base);
@@ -760,8 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                             const float x0 = ctl_elem<kXBf16>(xrow, col), x1 = ctl_elem<kYBf16>(yrow, col);
                             const bool in0 = ctl_allows(sm.row[0], col), in1 = ctl_allows(sm.row[1], col);
                             Two vt{-INFINITY, 0.f}, vr{-INFINITY, 0.f};
-                            if (in0) vt = value(0, x0, w0[at + q], col, nullptr);
-                            if (in1) vr = value(1, x1, a.same ? w0[at + q] : w1[at + q], col, nullptr);
+                            const uint32_t t0 = w0[at + q], t1 = a.same ? t0 : w1[at + q];
+                            Two bias[2] = {Two{0.f, 0.f}, Two{0.f, 0.f}};
+                            if ((t0 | t1) & kBiased) bias_of(static_cast<int32_t>(col), bias);
+                            if (in0) vt = ctl_value(x0, t0, sm.row[0], bias[0], nullptr);
+                            if (in1) vr = ctl_value(x1, t1, sm.row[1], bias[1], nullptr);
                             accumulate_pair(vt, vr, acc, lt, lr, s_r, same_scale);
                             if (col == id)
                                 a.pick[i] = make_double2(static_cast<double>(vt.h) + static_cast<double>(vt.l),
@@ -785,7 +828,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     const bool in0 = ctl_allows(sm.row[0], col);
                     if (!in0) return kMode == kApply ? -INFINITY : 0.f;
                     float slope;
-                    const Two v = value(0, x0, w0[q], col, &slope);
+                    Two bias[kLast + 1] = {Two{0.f, 0.f}};
+                    if (w0[q] & kBiased) bias_of(static_cast<int32_t>(col), bias);
+                    const Two v = ctl_value(x0, w0[q], sm.row[0], bias[0], &slope);
                     if (kMode == kApply) return __fmaf_rn(v.h, s, __fmul_rn(v.l, s));
                     const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -sm.num[b].lse2), sm.ll), __fmul_rn(v.l, f)));
                     return __fmul_rn(__fmul_rn(sm.gs, slope), __fsub_rn(col == id ? 1.f : 0.f, p));
@@ -950,15 +995,17 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     s0[g] |= none0 ? 0xffu : out;
                     s1[g] |= none1 ? 0xffu : out;
                 }
-                if ((s0[0] & s0[1] & s1[0] & s1[1]) != 0xffu) {  // something is allowed
-                    if (s0[0] | s0[1] | s1[0] | s1[1]) {
+                if (__any_sync(0xffffffffu, (s0[0] & s0[1] & s1[0] & s1[1]) != 0xffu)) {  // something is allowed
+                    if (__any_sync(0xffffffffu, (s0[0] | s0[1] | s1[0] | s1[1]) != 0u)) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             ctl_fill8<kXBf16, kFillBits>(gx[g], sm.lanes[s0[g]]);
                             ctl_fill8<kYBf16, kFillBits>(gy[g], sm.lanes[s1[g]]);
                         }
                     }
-                    if (!(same_scale && accumulate_near(gx, gy, acc, n_l, n_s))) {
+                    const bool any = (s0[0] & s0[1] & s1[0] & s1[1]) != 0xffu;
+                    const bool near = same_scale && accumulate_near(gx, gy, acc, n_l, n_s);
+                    if (any && !near) {
                         f2_t pt[8], pr[8];
 #pragma unroll
                         for (int p = 0; p < 8; ++p) {

@@ -94,22 +94,40 @@ __device__ __forceinline__ Two two_add(Two a, float b) {
     return Two{s, __fadd_rn(a.l, e)};
 }
 
-// Sum of the row's bias entries of one token, in double (at most 1024 terms,
-// so the sum is exact to far below a float's step in any order).
-__device__ __forceinline__ double bias_sum(const int32_t *ids, const float *values, int n, int64_t token) {
+// The row's bias entries of one token: the last one's index (-1: none) and how
+// many there are.  ids: padded with -1 to a multiple of four, 16-byte aligned.
+__device__ __forceinline__ int bias_find(const int4 *ids, int n, int32_t token, int *found) {
+    int at = -1, k = 0;
+#pragma unroll 2
+    for (int e = 0; e < n; e += 4) {
+        const int4 v = ids[e >> 2];
+        at = v.x == token ? e : at;
+        at = v.y == token ? e + 1 : at;
+        at = v.z == token ? e + 2 : at;
+        at = v.w == token ? e + 3 : at;
+        k += (v.x == token) + (v.y == token) + (v.z == token) + (v.w == token);
+    }
+    *found = k;
+    return at;
+}
+// Their sum as two floats.  Almost always there is one entry; several are added
+// in double (at most 1024 terms, so the sum is exact to far below a float's
+// step in any order).
+__device__ __forceinline__ Two bias_sum(const int32_t *ids, const float *values, int n, int32_t token, int at,
+                                        int found) {
+    if (found <= 1) return Two{found ? values[at] : 0.f, 0.f};
     double s = 0.0;
-#pragma unroll 4
     for (int e = 0; e < n; ++e)
         if (ids[e] == token) s += static_cast<double>(values[e]);
-    return s;
+    const float h = static_cast<float>(s);
+    return Two{h, static_cast<float>(s - static_cast<double>(h))};
 }
 
 // x3 of a touched, allowed token with count word w.  Two floats, so that the
 // logit's rounding (a step of 1e-6 at a logit of 20) stays out of the logprob
 // difference of two sides that nearly agree; `slope` (may be null) receives
 // dx3/dx.
-__device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, const int32_t *bias_ids,
-                                         const float *bias, int n_bias, int64_t token, float *slope) {
+__device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, Two bias, float *slope) {
     Two v{x, 0.f};
     float d = 1.f;
     if ((w & ~kBiased) != 0u) {
@@ -132,10 +150,8 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, c
         }
     }
     if (w & kBiased) {
-        const double b = bias_sum(bias_ids, bias, n_bias, token);
-        const float bh = static_cast<float>(b);
-        v = two_add(v, bh);
-        v = two_add(v, static_cast<float>(b - static_cast<double>(bh)));
+        v = two_add(v, bias.h);
+        v = two_add(v, bias.l);
     }
     const float s = __fadd_rn(v.h, v.l);
     // an infinite or NaN logit has no low part
@@ -143,6 +159,8 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, c
     if (slope) *slope = d;
     return v;
 }
+
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // Whether the row's mask lets a token through.
 __device__ __forceinline__ bool ctl_allows(const CtlRow &o, int64_t token) {
