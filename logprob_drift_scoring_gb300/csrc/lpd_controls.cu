@@ -117,8 +117,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volat
                                            bool honour_abort = true) {
     return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag, status, honour_abort);
 }
-// All scouts reach it or none does: what one of them waits for, they all learn from it.
-__device__ __forceinline__ void scout_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kScoutThreads) : "memory"); }
+// All scouts reach it or none does: what one of them waits for, they all learn
+// from it.  The barrier counts whole warps, so a warp's lanes meet first: one
+// that left a loop early would otherwise arrive for the others.
+__device__ __forceinline__ void scout_sync() {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(kScoutThreads) : "memory");
+}
 
 // ---- arguments ---------------------------------------------------------------------
 // One [rows, vocab] tensor as the stream reads it.
@@ -795,20 +800,38 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                         const int m = min(kCap, end - base);
                         if (total > kCap) count(base, m);
                         const int at = total > kCap ? 0 : base;  // list position of rank `base`
-                        for (int q = st; q < m; q += kScoutThreads) {
-                            const int64_t col = c0 + list[at + q];
-                            const float x0 = ctl_elem<kXBf16>(xrow, col), x1 = ctl_elem<kYBf16>(yrow, col);
-                            const bool in0 = ctl_allows(sm.row[0], col), in1 = ctl_allows(sm.row[1], col);
-                            Two vt{-INFINITY, 0.f}, vr{-INFINITY, 0.f};
-                            const uint32_t t0 = w0[at + q], t1 = a.same ? t0 : w1[at + q];
-                            Two bias[2] = {Two{0.f, 0.f}, Two{0.f, 0.f}};
-                            if ((t0 | t1) & kBiased) bias_of(static_cast<int32_t>(col), bias);
-                            if (in0) vt = ctl_value(x0, t0, sm.row[0], bias[0], nullptr);
-                            if (in1) vr = ctl_value(x1, t1, sm.row[1], bias[1], nullptr);
-                            accumulate_pair(vt, vr, acc, lt, lr, s_r, same_scale);
-                            if (col == id)
-                                a.pick[i] = make_double2(static_cast<double>(vt.h) + static_cast<double>(vt.l),
-                                                         static_cast<double>(vr.h) + static_cast<double>(vr.l));
+                        // two tokens at a time: their chains of arithmetic are independent
+                        for (int q0 = st; q0 < m; q0 += 2 * kScoutThreads) {
+                            Two vt[2], vr[2];
+                            int64_t col[2];
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                const int q = q0 + v * kScoutThreads;
+                                vt[v] = vr[v] = Two{-INFINITY, 0.f};
+                                col[v] = -1;
+                                if (q >= m) continue;
+                                col[v] = c0 + list[at + q];
+                                const float x0 = ctl_elem<kXBf16>(xrow, col[v]), x1 = ctl_elem<kYBf16>(yrow, col[v]);
+                                const uint32_t t0 = w0[at + q], t1 = a.same ? t0 : w1[at + q];
+                                Two bias[2] = {Two{0.f, 0.f}, Two{0.f, 0.f}};
+                                if ((t0 | t1) & kBiased) bias_of(static_cast<int32_t>(col[v]), bias);
+                                const bool in0 = ctl_allows(sm.row[0], col[v]);
+                                const bool in1 = sm.row[0].mask == sm.row[1].mask && sm.row[0].none == sm.row[1].none
+                                                     ? in0
+                                                     : ctl_allows(sm.row[1], col[v]);
+                                const Two y0 = ctl_value(x0, t0, sm.row[0], bias[0], nullptr);
+                                const Two y1 = ctl_value(x1, t1, sm.row[1], bias[1], nullptr);
+                                if (in0) vt[v] = y0;
+                                if (in1) vr[v] = y1;
+                            }
+#pragma unroll
+                            for (int v = 0; v < 2; ++v) {
+                                if (col[v] < 0) continue;
+                                accumulate_pair(vt[v], vr[v], acc, lt, lr, s_r, same_scale);
+                                if (col[v] == id)
+                                    a.pick[i] = make_double2(static_cast<double>(vt[v].h) + static_cast<double>(vt[v].l),
+                                                             static_cast<double>(vr[v].h) + static_cast<double>(vr[v].l));
+                            }
                         }
                         if (total > kCap) scout_sync();
                     }
@@ -972,8 +995,12 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 ctl_shared8<kXBf16, kAligned>(stg, max(static_cast<int>(at_x + j * kXE - skew), 0), gx[g]);
                 if constexpr (kTwo) ctl_shared8<kYBf16, kAligned>(stg + kStageX, at_y + j * kYE, gy[g]);
             }
+            // The stage's next copy is the async proxy's: it is ordered behind
+            // these reads by the proxy fence, not by the barrier alone (without
+            // it one row in two hundred of a long run read a later tile).
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[stage]);  // values are in registers now
+            if (lane == 0) mbar_arrive(&sm.empty[stage]);
             if (++stage == a.n_stages) {
                 stage = 0;
                 phase ^= 1;

@@ -336,6 +336,31 @@ def test_batch_invariance_over_unit_shapes():
         assert abs(float(full[0][r]) - want) <= 1e-5 + 2.0 ** -23 * abs(want)
 
 
+def test_repeated_calls_give_the_same_bits():
+    """Long rows, ring stages reused at once: every call gives the first call's bits."""
+    rng = np.random.default_rng(25)
+    rows, vocab = 330, 130000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    h = to_device(ref.random_controls(rng, rows, vocab, keep=ids, history=6000, masks=3, bias=5))
+    x = torch.randn(rows, vocab, device=DEV, generator=torch.Generator(DEV).manual_seed(6)).mul_(3).to(torch.bfloat16)
+    y = (x.float() + 1e-3).to(torch.bfloat16)
+    idt, act = torch.from_numpy(ids).to(DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    first = B.score_controlled(x, y, idt, act, h, h)
+    z = B.controls_apply(x, h)
+    g = torch.empty_like(x)
+    B.lpd_logprob_backward_controlled(x, h, idt, act, first.logp_train, first.dlogp, g)
+    for _ in range(24):
+        r = B.score_controlled(x, y, idt, act, h, h)
+        for k in ("logp_train", "logp_rollout", "dlogp"):
+            assert torch.equal(getattr(first, k), getattr(r, k)), k
+    out = torch.empty_like(x)
+    for _ in range(12):
+        B.lpd_controls_apply(x, h, out)
+        assert torch.equal(out, z)
+        B.lpd_logprob_backward_controlled(x, h, idt, act, first.logp_train, first.dlogp, out)
+        assert torch.equal(out, g)
+
+
 def test_more_touched_tokens_than_counted_at_a_time():
     """Elementwise forms with thousands of distinct tokens in a unit, in place too, and a long bias list."""
     rng = np.random.default_rng(24)
