@@ -245,24 +245,36 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(cons
 
 // ==================================================================== product
 // One persistent CTA per SM.  Warpgroup 0: warp 0 streams 128-wide k blocks of A (128 rows)
-// and B (256 rows) through a four-stage ring (TMA, 128-byte swizzle), warp 1
+// and B (256 rows) through a three-stage ring (TMA, 128-byte swizzle), warp 1
 // issues four M=128 N=256 K=32 MMAs a block into one of two accumulators in
 // tensor memory, and eight warps read each accumulator back, scale it and add
 // it to 128 fp32 registers a thread: a row is a lane, a warp takes half of the
 // 256 columns.  Two accumulators let the MMAs of block kb + 1 run under the
 // read-back of block kb; at the full MMA rate a block takes 512 cycles, its
-// read-back 256 (32768 values at 128 lanes) and its multiply-adds 256.
+// read-back 256 (32768 values at 128 lanes) and its multiply-adds 256.  The
+// read-back is bound by its instructions: the block loop is unrolled over the
+// four blocks whose scales are fetched together, the multiply-adds are scalar
+// (packed pairs cost a move each after a read of tensor memory), and sixteen
+// warps of 64 registers were slower, as each block's overhead is a warp's.
 constexpr int kTM = 128, kTN = 256;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kABytes = kTM * kBlk, kBBytes = kTN * kBlk;
 constexpr int kStageBytes = kABytes + kBBytes;  // 48 KB
 constexpr int kEpiWarps = 8;
+constexpr int kEpiCols = kTN / (kEpiWarps / 4);  // columns a warp
 constexpr int kMmThreads = (4 + kEpiWarps) * 32;  // a warpgroup for the copies and the MMAs, two for the read-back
 // registers a thread after the split (three warps a sub-partition, launched at
 // 168 each: 40 + 2 * 232 = 3 * 168)
 constexpr int kRegsFront = 40, kRegsEpi = 232;
-constexpr int kOutPitch = 80;                   // bytes a staged output row: 64 and 16 against bank conflicts
-constexpr int kOutBytes = kEpiWarps * 32 * kOutPitch;
+// Output staging, a warp's: two boxes of 32 rows x 128 bytes.  They leave by TMA
+// stores, which run under the next tile (stores by the warps themselves took
+// 4200 cycles a tile, an eighth of a 4096-deep one); output rows that are not
+// 16-byte aligned go through rows of kOutPitch bytes instead.
+constexpr int kBoxBytes = 32 * 128;
+constexpr int kOutPitch = 80;                   // 64 bytes a row and 16 against bank conflicts
+constexpr int kOutWarp = 2 * kBoxBytes;
+constexpr int kOutBytes = kEpiWarps * kOutWarp;
+static_assert(32 * kOutPitch <= kOutWarp, "staging of either kind");
 constexpr int kScaleGroup = 4;                  // k blocks whose scales are fetched together
 constexpr int kScaleBytes = 2 * kScaleGroup * kTN * 4;
 constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kScaleBytes;
@@ -301,16 +313,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 // Bounded wait; when it gives up it raises the CTA's abort flag and sets
-// LPD_STATUS_TIMEOUT in the workspace's first word.
+// LPD_STATUS_TIMEOUT in the workspace's first word.  The clock is read only
+// once a wait has been polled for long: a read costs more than a block's MMAs.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
                                            bool honour_abort = true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
+    unsigned long long t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 0; n < kWaitLimitIters; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 255u) == 0) {
+        if ((n & 255u) == 255u) {
             if (honour_abort && *abort_flag) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+            const unsigned long long now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) break;
         }
     }
     *abort_flag = 1;
@@ -324,19 +339,31 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
         "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-// K-major tile of 128-byte rows under the 128-byte swizzle (8-row groups of 1024 bytes).
-__device__ __forceinline__ uint64_t smem_desc(const void *tile) {
-    const uint64_t addr = (smem_u32(tile) & 0x3FFFFu) >> 4;
-    return addr | (1ull << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// Descriptor of a K-major tile of 128-byte rows under the 128-byte swizzle
+// (8-row groups of 1024 bytes): the lower word is the address / 16 (and the
+// unused leading offset), the upper word is the same for every tile.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(const void *tile) { return ((smem_u32(tile) & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                         uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
         : "memory");
+}
+// One lane of a warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -344,7 +371,7 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t *r) {
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%16];"
@@ -352,14 +379,34 @@ __device__ __forceinline__ void tmem_ld16_issue(uint32_t taddr, uint32_t *r) {
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// Until the stores so far have read their shared memory.
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 struct MmMaps {
     CUtensorMap a, b;
+    CUtensorMap out;  // (column, row, split); only where vec_out
 };
 
 struct MmArgs {
     const float *sa, *sb;
     int64_t sa_stride, sb_stride;
+    int vec_sa, vec_sb;        // 16-byte aligned scale rows, and splits of whole groups of four blocks
     int sa_shift, sb_shift;    // 0: a scale a row, 7: a scale for 128 rows
     int64_t m, n;
     int kb_total, kb_per_split, n_splits;
@@ -429,73 +476,90 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFront));
+        // Both loops are run by whole warps, so that the compiler sees uniform
+        // values (a lone thread's loop spent 855 cycles a block on issuing four
+        // MMAs, most of them on moves to uniform registers); one lane issues.
+        const bool leader = elect_one();
         if (warp == 0) {
             // ------------------------------------------------------------ producer
-            if (lane == 0) {
-                uint32_t it = 0;
-                bool ok = true;
-                for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
-                    int tm, tn, split;
-                    item_coords(w, a, tm, tn, split);
-                    const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
-                    for (int kb = split * a.kb_per_split; kb < kb1; ++kb, ++it) {
-                        const uint32_t s = it % kStages, round = it / kStages;
-                        if (round > 0 && !wait_phase(&empty[s], (round - 1) & 1, &abort_flag, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        char *st = smem + static_cast<size_t>(s) * kStageBytes;
+            uint32_t s = 0, phase = 1, issued = 0;  // the first turn finds every stage empty
+            bool ok = true;
+            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                int tm, tn, split;
+                item_coords(w, a, tm, tn, split);
+                const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
+#pragma unroll 1
+                for (int kb = split * a.kb_per_split; kb < kb1; ++kb) {
+                    ok = __all_sync(0xffffffffu, wait_phase(&empty[s], phase, &abort_flag, a.status));
+                    if (!ok) break;
+                    if (leader) {
+                        char *st = smem + s * kStageBytes;
                         mbar_arrive_expect_tx(&full[s], kStageBytes);
                         tma_load_2d(st, &maps.a, kb * kBlk, tm * kTM, &full[s]);
                         tma_load_2d(st + kABytes, &maps.b, kb * kBlk, tn * kTN, &full[s]);
                     }
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
                 }
-                // every copy issued must land before the CTA exits
-                const uint32_t first = it > static_cast<uint32_t>(kStages) ? it - kStages : 0;
-                for (uint32_t j = first; j < it; ++j)
-                    wait_phase(&full[j % kStages], (j / kStages) & 1, &abort_flag, a.status, false);
+            }
+            // every copy issued must land before the CTA exits: the last turn's
+            // stages, each in the phase of its last use
+            for (uint32_t j = 0; j < issued; ++j) {
+                if (s == 0) {
+                    s = kStages;
+                    phase ^= 1;
+                }
+                --s;
+                wait_phase(&full[s], phase ^ 1, &abort_flag, a.status, false);
             }
         } else if (warp == 1) {
             // ----------------------------------------------------------------- MMA
-            if (lane == 0) {
-                uint32_t it = 0;
-                bool ok = true, issued = false;
-                for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
-                    int tm, tn, split;
-                    item_coords(w, a, tm, tn, split);
-                    const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
-                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                        const uint32_t s = it % kStages, round = it / kStages, b = it & 1, use = it >> 1;
-                        if ((use > 0 && !wait_phase(&acc_empty[b], (use - 1) & 1, &abort_flag, a.status)) ||
-                            !wait_phase(&full[s], round & 1, &abort_flag, a.status)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const char *st = smem + static_cast<size_t>(s) * kStageBytes;
-                        const uint64_t da = smem_desc(st), db = smem_desc(st + kABytes);
+            uint32_t s = 0, phase = 0, b = 0, turn = 1;  // `turn`: the parity that an emptied accumulator shows
+            bool ok = true, issued = false;
+            const uint32_t base = desc_low(smem);
+            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                int tm, tn, split;
+                item_coords(w, a, tm, tn, split);
+                const int kbs = min(a.kb_total, (split + 1) * a.kb_per_split) - split * a.kb_per_split;
+#pragma unroll 1
+                for (int kb = 0; kb < kbs; ++kb) {
+                    ok = __all_sync(0xffffffffu, wait_phase(&acc_empty[b], turn, &abort_flag, a.status) &&
+                                                     wait_phase(&full[s], phase, &abort_flag, a.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t da = base + s * (kStageBytes >> 4), db = da + (kABytes >> 4);
 #pragma unroll
                         for (int k = 0; k < kBlk / 32; ++k)  // K = 32 bytes inside the swizzle row
                             umma_f8(tmem + b * kTN, da + 2 * k, db + 2 * k, a.idesc, k > 0 ? 1u : 0u);
                         umma_commit(&empty[s]);
                         umma_commit(&acc_full[b]);
-                        issued = true;
                     }
+                    issued = true;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                    b ^= 1;
+                    turn ^= b ^ 1;
                 }
-                if (issued) {
-                    umma_commit(&done);
-                    wait_phase(&done, 0, &abort_flag, a.status, false);
-                }
+            }
+            if (issued) {
+                if (leader) umma_commit(&done);
+                wait_phase(&done, 0, &abort_flag, a.status, false);
             }
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         // ------------------------------------------------------------ epilogue
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int quad = warp & 3, part = (warp - 4) >> 2;
         const int et = threadIdx.x - 128;  // 0..255
-        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * (kTN / 2);
-        char *const mine = staged + (warp - 4) * 32 * kOutPitch;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kEpiCols;
+        char *const mine = staged + (warp - 4) * kOutWarp;
         uint32_t it = 0, group = 0;  // k blocks and scale groups so far
         bool ok = true;
         for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
@@ -503,103 +567,151 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             item_coords(w, a, tm, tn, split);
             const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
             const int64_t row = static_cast<int64_t>(tm) * kTM + quad * 32 + lane;
-            const int64_t col0 = static_cast<int64_t>(tn) * kTN + half * (kTN / 2);
+            const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
             const float *sa = a.sa + (min(row, a.m - 1) >> a.sa_shift) * a.sa_stride;
             const int64_t sb_row = kVecB ? static_cast<int64_t>(tn) * kTN + et : col0;
             const float *sb = a.sb + (min(sb_row, a.n - 1) >> a.sb_shift) * a.sb_stride;
-            f2_t acc[64];
+            float acc[kEpiCols];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = f2(0.f, 0.f);
-            float ra[kScaleGroup], rb[kScaleGroup];
+            for (int j = 0; j < kEpiCols; ++j) acc[j] = 0.f;
+            // the next four blocks' scales are on their way while four are worked on
+            float na[kScaleGroup], nb[kScaleGroup];
+            auto fetch_of = [&](const float *from, bool vec, int kg, float (&to)[kScaleGroup]) {
+                if (vec && kg + kScaleGroup <= a.kb_total) {  // rows of scales on 16-byte boundaries: one load for four
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(from + kg));
+                    to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kScaleGroup; ++q) to[q] = __ldg(from + min(kg + q, kb1 - 1));
+                }
+            };
+            auto fetch = [&](int kg) {
+                fetch_of(sa, a.vec_sa != 0, kg, na);
+                fetch_of(sb, a.vec_sb != 0, kg, nb);
+            };
+            fetch(kb0);
 #pragma unroll 1
-            for (int kb = kb0; ok && kb < kb1; ++kb, ++it) {
-                const int g = (kb - kb0) & (kScaleGroup - 1);
-                if (g == 0) {
+            for (int kg = kb0; ok && kg < kb1; kg += kScaleGroup, ++group) {
+                // the scales of four blocks: the row's, and the columns' (one
+                // for 128 of them: their product; else through shared memory)
+                float s[kScaleGroup];
+                const float4 *cols = nullptr;
+                if (kVecB) {
+                    // two buffers: a warp that fills one for group i + 2 has
+                    // seen every warp arrive for group i + 1, so every warp is
+                    // done with group i
+                    float *dst = scales + (group & 1) * kScaleGroup * kTN;
 #pragma unroll
                     for (int q = 0; q < kScaleGroup; ++q) {
-                        const int k = min(kb + q, kb1 - 1);
-                        ra[q] = __ldg(sa + k);
-                        rb[q] = __ldg(sb + k);
+                        s[q] = na[q];
+                        dst[q * kTN + et] = nb[q];
                     }
-                    if (kVecB) {
-                        // two buffers: a warp that fills one for group i + 2
-                        // has seen every warp arrive for group i + 1, so every
-                        // warp is done with group i
-                        float *dst = scales + (group & 1) * kScaleGroup * kTN;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&scales_full[group & 1]);
+                    ok = wait_phase(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
+                    ok = !__any_sync(0xffffffffu, !ok);
+                    if (!ok) break;
+                    cols = reinterpret_cast<const float4 *>(scales + (group & 1) * kScaleGroup * kTN + part * kEpiCols);
+                } else {
 #pragma unroll
-                        for (int q = 0; q < kScaleGroup; ++q) dst[q * kTN + et] = rb[q];
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&scales_full[group & 1]);
-                        ok = wait_phase(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
-                        ok = !__any_sync(0xffffffffu, !ok);
-                        if (!ok) break;
-                    }
-                    ++group;
+                    for (int q = 0; q < kScaleGroup; ++q) s[q] = __fmul_rn(na[q], nb[q]);
                 }
-                float sav = ra[0], sbv = rb[0];
+                if (kg + kScaleGroup < kb1) fetch(kg + kScaleGroup);
 #pragma unroll
-                for (int q = 1; q < kScaleGroup; ++q) {
-                    sav = g == q ? ra[q] : sav;
-                    sbv = g == q ? rb[q] : sbv;
-                }
-                const uint32_t b = it & 1;
-                ok = wait_phase(&acc_full[b], (it >> 1) & 1, &abort_flag, a.status);
-                ok = !__any_sync(0xffffffffu, !ok);
-                if (!ok) break;
-                tc_fence_after();
-                const float s = kVecB ? sav : __fmul_rn(sav, sbv);
-                const f2_t s2 = f2(s, s);
-                const float4 *col_scales =
-                    reinterpret_cast<const float4 *>(scales + ((group - 1) & 1) * kScaleGroup * kTN + g * kTN + half * (kTN / 2));
-                uint32_t r[2][16];
-                tmem_ld16_issue(lane_addr + b * kTN, r[0]);
+                for (int g = 0; g < kScaleGroup; ++g) {
+                    if (kg + g >= kb1) break;
+                    const uint32_t b = it & 1;
+                    ok = wait_phase(&acc_full[b], (it >> 1) & 1, &abort_flag, a.status);
+                    ok = !__any_sync(0xffffffffu, !ok);
+                    if (!ok) break;
+                    ++it;
+                    tc_fence_after();
+                    const uint32_t from = lane_addr + b * kTN;
+                    constexpr int kPiece = kVecB ? 16 : 32;  // columns read at a time
+                    uint32_t r[2][kPiece];
+                    tmem_ld_issue(from, r[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait_ld();
-                    if (c < 7) {
-                        tmem_ld16_issue(lane_addr + b * kTN + (c + 1) * 16, r[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&acc_empty[b]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t *p = &r[c & 1][4 * j];
-                        const f2_t p0 = f2(__uint_as_float(p[0]), __uint_as_float(p[1]));
-                        const f2_t p1 = f2(__uint_as_float(p[2]), __uint_as_float(p[3]));
-                        f2_t &x0 = acc[c * 8 + 2 * j], &x1 = acc[c * 8 + 2 * j + 1];
-                        if (kVecB) {
-                            const float4 v = col_scales[c * 4 + j];
-                            x0 = fma2(p0, mul2(f2(v.x, v.y), s2), x0);
-                            x1 = fma2(p1, mul2(f2(v.z, v.w), s2), x1);
+                    for (int c = 0; c < kEpiCols / kPiece; ++c) {
+                        tmem_wait_ld();
+                        if (c + 1 < kEpiCols / kPiece) {
+                            tmem_ld_issue(from + (c + 1) * kPiece, r[(c + 1) & 1]);
                         } else {
-                            x0 = fma2(p0, s2, x0);
-                            x1 = fma2(p1, s2, x1);
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&acc_empty[b]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kPiece; j += 4) {
+                            const uint32_t *p = &r[c & 1][j];
+                            float *x = &acc[c * kPiece + j];
+                            if (kVecB) {
+                                const float4 v = cols[g * (kTN / 4) + (c * kPiece + j) / 4];
+                                x[0] = __fmaf_rn(__uint_as_float(p[0]), __fmul_rn(v.x, s[g]), x[0]);
+                                x[1] = __fmaf_rn(__uint_as_float(p[1]), __fmul_rn(v.y, s[g]), x[1]);
+                                x[2] = __fmaf_rn(__uint_as_float(p[2]), __fmul_rn(v.z, s[g]), x[2]);
+                                x[3] = __fmaf_rn(__uint_as_float(p[3]), __fmul_rn(v.w, s[g]), x[3]);
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) x[q] = __fmaf_rn(__uint_as_float(p[q]), s[g], x[q]);
+                            }
                         }
                     }
                 }
             }
             if (!ok) {  // a wait gave up: this tile reads as NaN
 #pragma unroll
-                for (int j = 0; j < 64; ++j) acc[j] = f2(CUDART_NAN_F, CUDART_NAN_F);
+                for (int j = 0; j < kEpiCols; ++j) acc[j] = CUDART_NAN_F;
             }
-            // 64-byte pieces of 32 rows through shared memory, so that a store
-            // covers whole sectors of a row
             char *const out = a.out + split * a.split_stride;
             const int64_t row0 = static_cast<int64_t>(tm) * kTM + quad * 32;
+            if (a.vec_out) {
+                // boxes of 32 rows x 128 bytes under the 128-byte swizzle: chunk
+                // q of row l lies at q ^ (l % 8), so a warp's stores hit all banks
+                constexpr int kBoxCols = kOutF32 ? 32 : 64;
+#pragma unroll
+                for (int box = 0; box < kEpiCols / kBoxCols; ++box) {
+                    if (box % 2 == 0) {  // both boxes' last stores have read them
+                        if (lane == 0) tma_store_wait_read();
+                        __syncwarp();
+                    }
+                    char *const dst = mine + (box & 1) * kBoxBytes;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (kOutF32) {
+                                v[e] = __float_as_uint(acc[box * kBoxCols + 4 * q + e]);
+                            } else {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[box * kBoxCols + 8 * q + 2 * e],
+                                                                               acc[box * kBoxCols + 8 * q + 2 * e + 1]);
+                                v[e] = *reinterpret_cast<const uint32_t *>(&h);
+                            }
+                        }
+                        *reinterpret_cast<uint4 *>(dst + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    const int64_t c = col0 + box * kBoxCols;
+                    if (lane == 0) {
+                        if (c < a.n && row0 < a.m)
+                            tma_store_3d(&maps.out, dst, static_cast<int>(c), static_cast<int>(row0), split);
+                        tma_store_commit();
+                    }
+                }
+                continue;
+            }
+            // 64-byte pieces of 32 rows through shared memory
             constexpr int kCols = kOutF32 ? 16 : 32;  // columns of a piece
 #pragma unroll
-            for (int p = 0; p < kTN / 2 / kCols; ++p) {
+            for (int p = 0; p < kEpiCols / kCols; ++p) {
                 uint32_t piece[16];
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {
                     if (kOutF32) {
-                        const f2_t v = acc[p * 8 + q / 2];
-                        piece[q] = __float_as_uint(q & 1 ? f2_hi(v) : f2_lo(v));
+                        piece[q] = __float_as_uint(acc[p * 16 + q]);
                     } else {
-                        const f2_t v = acc[p * 16 + q];
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(f2_lo(v), f2_hi(v));
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[p * 32 + 2 * q], acc[p * 32 + 2 * q + 1]);
                         piece[q] = *reinterpret_cast<const uint32_t *>(&h);
                     }
                 }
@@ -611,18 +723,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 __syncwarp();
                 const int64_t c = col0 + p * kCols;
                 if (c >= a.n) break;
-                if (a.vec_out && c + kCols <= a.n) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int rr = q * 8 + (lane >> 2);
-                        if (row0 + rr < a.m)
-                            __stcs(reinterpret_cast<uint4 *>(out + (row0 + rr) * a.out_stride + c * (kOutF32 ? 4 : 2)) + (lane & 3),
-                                   *reinterpret_cast<const uint4 *>(mine + rr * kOutPitch + 16 * (lane & 3)));
-                    }
-                } else {
-                    for (int q = 0; q < kCols; ++q) {
-                        const int rr = kOutF32 ? 2 * q + (lane >> 4) : q;
-                        const int cc = kOutF32 ? lane & 15 : lane;
+                {
+                    constexpr int kRowsAtOnce = 32 / kCols;
+                    for (int q = 0; q < 32 / kRowsAtOnce; ++q) {
+                        const int rr = q * kRowsAtOnce + lane / kCols, cc = lane % kCols;
                         if (row0 + rr < a.m && c + cc < a.n) {
                             char *dst = out + (row0 + rr) * a.out_stride + (c + cc) * (kOutF32 ? 4 : 2);
                             if (kOutF32) *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(mine + rr * kOutPitch + 4 * cc);
@@ -634,6 +738,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
     }
 
+    if (warp >= 4 && lane == 0) tma_store_wait_read();  // shared memory outlives the last stores' reads
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -683,11 +788,29 @@ bool make_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t k, int64_
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride)};
+    // (a single row's stride may be any: it is not used)
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : (k + 15) / 16 * 16)};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlk), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output (or its partial results) [splits, m, n] in boxes of 32 rows x 128
+// bytes, 128-byte swizzle.
+bool make_out_map(CUtensorMap *map, void *ptr, int64_t m, int64_t n, int64_t splits, int64_t row_bytes,
+                  int64_t split_bytes, bool f32) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m), static_cast<cuuint64_t>(splits)};
+    if (m == 1) row_bytes = (n * (f32 ? 4 : 2) + 15) / 16 * 16;  // neither stride is used where there is one row, one split
+    if (splits == 1) split_bytes = row_bytes;
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(split_bytes)};
+    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32u, 1u};
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box,
+              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -778,6 +901,12 @@ cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, in
     a.sb = y.scales;
     a.sa_stride = x.scale_stride;
     a.sb_stride = y.scale_stride;
+    const auto vec_scales = [&](const BlockOperand &o) {
+        return reinterpret_cast<uintptr_t>(o.scales) % 16 == 0 && o.scale_stride % kScaleGroup == 0 &&
+               (p.n_splits == 1 || p.kb_per_split % kScaleGroup == 0);
+    };
+    a.vec_sa = vec_scales(x);
+    a.vec_sb = vec_scales(y);
     a.sa_shift = x.block ? 7 : 0;
     a.sb_shift = y.block ? 7 : 0;
     a.m = m;
@@ -798,6 +927,8 @@ cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, in
     a.split_stride = split ? m * p.part_stride * 4 : 0;
     a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 16 == 0;
     const bool to_f32 = split || f32;
+    if (a.vec_out && !make_out_map(&maps.out, a.out, m, n, p.n_splits, a.out_stride, a.split_stride, to_f32))
+        return cudaErrorInvalidValue;
     cudaError_t e;
     if (to_f32) e = y.block ? product_typed<true, false>(maps, a, stream) : product_typed<true, true>(maps, a, stream);
     else e = y.block ? product_typed<false, false>(maps, a, stream) : product_typed<false, true>(maps, a, stream);
