@@ -276,7 +276,8 @@ constexpr int kOutWarp = 2 * kBoxBytes;
 constexpr int kOutBytes = kEpiWarps * kOutWarp;
 static_assert(32 * kOutPitch <= kOutWarp, "staging of either kind");
 constexpr int kScaleGroup = 4;                  // k blocks whose scales are fetched together
-constexpr int kScaleBytes = 2 * kScaleGroup * kTN * 4;
+constexpr int kScaleFloats = kScaleGroup * (kTN + kTM);  // of a group: the columns', then the rows'
+constexpr int kScaleBytes = 2 * kScaleFloats * 4;
 constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kScaleBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRaster = 16;                     // row tiles that share a B tile in L2
@@ -371,14 +372,16 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// 16 lanes x 32 columns: registers 4 i + j hold row lane / 4 + 8 (j / 2), column 8 i + 2 (lane % 4) + j % 2.
 __device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
+// 32 lanes x 32 columns: a row a lane.
 __device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     __shared__ int abort_flag;
     char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     char *const staged = smem + static_cast<size_t>(kStages) * kStageBytes;
-    float *const scales = reinterpret_cast<float *>(staged + kOutBytes);  // [2][kScaleGroup][kTN]
+    float *const scales = reinterpret_cast<float *>(staged + kOutBytes);  // [2][kScaleFloats]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits;
 
@@ -568,7 +571,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
             const int64_t row = static_cast<int64_t>(tm) * kTM + quad * 32 + lane;
             const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
-            const float *sa = a.sa + (min(row, a.m - 1) >> a.sa_shift) * a.sa_stride;
+            const int64_t sa_row = kVecB ? static_cast<int64_t>(tm) * kTM + (et & (kTM - 1)) : row;
+            const float *sa = a.sa + (min(sa_row, a.m - 1) >> a.sa_shift) * a.sa_stride;
             const int64_t sb_row = kVecB ? static_cast<int64_t>(tn) * kTN + et : col0;
             const float *sb = a.sb + (min(sb_row, a.n - 1) >> a.sb_shift) * a.sb_stride;
             float acc[kEpiCols];
@@ -592,26 +596,25 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             fetch(kb0);
 #pragma unroll 1
             for (int kg = kb0; ok && kg < kb1; kg += kScaleGroup, ++group) {
-                // the scales of four blocks: the row's, and the columns' (one
-                // for 128 of them: their product; else through shared memory)
+                // the scales of four blocks: the row's times its columns' (one
+                // for 128 of them), or both through shared memory
                 float s[kScaleGroup];
-                const float4 *cols = nullptr;
+                const float *const shared_scales = scales + (group & 1) * kScaleFloats;
                 if (kVecB) {
                     // two buffers: a warp that fills one for group i + 2 has
                     // seen every warp arrive for group i + 1, so every warp is
                     // done with group i
-                    float *dst = scales + (group & 1) * kScaleGroup * kTN;
+                    float *dst = scales + (group & 1) * kScaleFloats + et;
 #pragma unroll
                     for (int q = 0; q < kScaleGroup; ++q) {
-                        s[q] = na[q];
-                        dst[q * kTN + et] = nb[q];
+                        dst[q * kTN] = nb[q];
+                        if (et < kTM) dst[kScaleGroup * kTN + q * kTM] = na[q];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&scales_full[group & 1]);
                     ok = wait_phase(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
                     ok = !__any_sync(0xffffffffu, !ok);
                     if (!ok) break;
-                    cols = reinterpret_cast<const float4 *>(scales + (group & 1) * kScaleGroup * kTN + part * kEpiCols);
                 } else {
 #pragma unroll
                     for (int q = 0; q < kScaleGroup; ++q) s[q] = __fmul_rn(na[q], nb[q]);
@@ -627,33 +630,39 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     ++it;
                     tc_fence_after();
                     const uint32_t from = lane_addr + b * kTN;
-                    constexpr int kPiece = kVecB ? 16 : 32;  // columns read at a time
+                    // pieces of the accumulator, the next one's read under this one's arithmetic
+                    constexpr int kPiece = kVecB ? 16 : 32;  // registers of a piece
+                    const auto piece_at = [&](int c) { return kVecB ? from + (c >> 1) * 32 + ((c & 1) << 20) : from + c * 32; };
+                    float of_rows[4];
+                    float2 of_cols[4];
+                    if (kVecB) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            of_rows[i] = shared_scales[kScaleGroup * kTN + g * kTM + quad * 32 + i * 8 + (lane >> 2)];
+                    }
                     uint32_t r[2][kPiece];
-                    tmem_ld_issue(from, r[0]);
+                    tmem_ld_issue(piece_at(0), r[0]);
 #pragma unroll
                     for (int c = 0; c < kEpiCols / kPiece; ++c) {
+                        if (kVecB && (c & 1) == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                of_cols[i] = *reinterpret_cast<const float2 *>(&shared_scales[g * kTN + part * kEpiCols + c * 16 + i * 8 + (lane & 3) * 2]);
+                        }
                         tmem_wait_ld();
                         if (c + 1 < kEpiCols / kPiece) {
-                            tmem_ld_issue(from + (c + 1) * kPiece, r[(c + 1) & 1]);
+                            tmem_ld_issue(piece_at(c + 1), r[(c + 1) & 1]);
                         } else {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&acc_empty[b]);
                         }
 #pragma unroll
-                        for (int j = 0; j < kPiece; j += 4) {
-                            const uint32_t *p = &r[c & 1][j];
-                            float *x = &acc[c * kPiece + j];
-                            if (kVecB) {
-                                const float4 v = cols[g * (kTN / 4) + (c * kPiece + j) / 4];
-                                x[0] = __fmaf_rn(__uint_as_float(p[0]), __fmul_rn(v.x, s[g]), x[0]);
-                                x[1] = __fmaf_rn(__uint_as_float(p[1]), __fmul_rn(v.y, s[g]), x[1]);
-                                x[2] = __fmaf_rn(__uint_as_float(p[2]), __fmul_rn(v.z, s[g]), x[2]);
-                                x[3] = __fmaf_rn(__uint_as_float(p[3]), __fmul_rn(v.w, s[g]), x[3]);
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) x[q] = __fmaf_rn(__uint_as_float(p[q]), s[g], x[q]);
-                            }
+                        for (int j = 0; j < kPiece; ++j) {
+                            float &x = acc[c * kPiece + j];
+                            const float by = kVecB ? __fmul_rn(of_rows[(c & 1) * 2 + ((j >> 1) & 1)], (j & 1) ? of_cols[(j >> 2) & 3].y : of_cols[(j >> 2) & 3].x)
+                                                   : s[g];
+                            x = __fmaf_rn(__uint_as_float(r[c & 1][j]), by, x);
                         }
                     }
                 }
@@ -675,20 +684,36 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         __syncwarp();
                     }
                     char *const dst = mine + (box & 1) * kBoxBytes;
+                    constexpr int kWords = kOutF32 ? 32 : 64;  // accumulators a box and lane
+                    if (kVecB) {
+                        // (32-column pieces of 16 lanes: pairs of columns)
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        uint32_t v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                        for (int e = 0; e < kWords / 2; ++e) {
+                            const int i = e >> 1, q = ((i >> 3) << 2) + (i & 3);  // q: 8 columns of the box
+                            char *to = dst + ((((i >> 2) & 1) << 4) + ((e & 1) << 3) + (lane >> 2)) * 128;
+                            const float *v = &acc[box * kWords + 2 * e];
                             if (kOutF32) {
-                                v[e] = __float_as_uint(acc[box * kBoxCols + 4 * q + e]);
+                                *reinterpret_cast<float2 *>(to + ((((q & 3) * 2 + ((lane >> 1) & 1)) ^ (lane >> 2)) << 4) + (lane & 1) * 8) = make_float2(v[0], v[1]);
                             } else {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(acc[box * kBoxCols + 8 * q + 2 * e],
-                                                                               acc[box * kBoxCols + 8 * q + 2 * e + 1]);
-                                v[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                *reinterpret_cast<__nv_bfloat162 *>(to + ((q ^ (lane >> 2)) << 4) + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
                             }
                         }
-                        *reinterpret_cast<uint4 *>(dst + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (kOutF32) {
+                                    v[e] = __float_as_uint(acc[box * kBoxCols + 4 * q + e]);
+                                } else {
+                                    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[box * kBoxCols + 8 * q + 2 * e],
+                                                                                   acc[box * kBoxCols + 8 * q + 2 * e + 1]);
+                                    v[e] = *reinterpret_cast<const uint32_t *>(&h);
+                                }
+                            }
+                            *reinterpret_cast<uint4 *>(dst + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -705,21 +730,36 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             constexpr int kCols = kOutF32 ? 16 : 32;  // columns of a piece
 #pragma unroll
             for (int p = 0; p < kEpiCols / kCols; ++p) {
-                uint32_t piece[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    if (kOutF32) {
-                        piece[q] = __float_as_uint(acc[p * 16 + q]);
-                    } else {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[p * 32 + 2 * q], acc[p * 32 + 2 * q + 1]);
-                        piece[q] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                }
                 __syncwarp();
+                if (kVecB) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<uint4 *>(mine + lane * kOutPitch + 16 * q) =
-                        make_uint4(piece[4 * q], piece[4 * q + 1], piece[4 * q + 2], piece[4 * q + 3]);
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < kCols / 8; ++i)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                char *to = mine + (h * 16 + half * 8 + (lane >> 2)) * kOutPitch;
+                                const int group8 = p * (kCols / 8) + i;  // 8 columns of the warp's 128
+                                const float *v = &acc[(((group8 >> 2) * 2 + h) * 4 + (group8 & 3)) * 4 + half * 2];
+                                if (kOutF32) *reinterpret_cast<float2 *>(to + i * 32 + (lane & 3) * 8) = make_float2(v[0], v[1]);
+                                else *reinterpret_cast<__nv_bfloat162 *>(to + i * 16 + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
+                            }
+                } else {
+                    uint32_t piece[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        if (kOutF32) {
+                            piece[q] = __float_as_uint(acc[p * 16 + q]);
+                        } else {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[p * 32 + 2 * q], acc[p * 32 + 2 * q + 1]);
+                            piece[q] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4 *>(mine + lane * kOutPitch + 16 * q) =
+                            make_uint4(piece[4 * q], piece[4 * q + 1], piece[4 * q + 2], piece[4 * q + 3]);
+                }
                 __syncwarp();
                 const int64_t c = col0 + p * kCols;
                 if (c >= a.n) break;
