@@ -276,6 +276,7 @@ constexpr int kOutWarp = 2 * kBoxBytes;
 constexpr int kOutBytes = kEpiWarps * kOutWarp;
 static_assert(32 * kOutPitch <= kOutWarp, "staging of either kind");
 constexpr int kScaleGroup = 4;                  // k blocks whose scales are fetched together
+constexpr int kScaleThreads = 64;
 constexpr int kScaleFloats = kScaleGroup * (kTN + kTM);  // of a group: the columns', then the rows'
 constexpr int kScaleBytes = 2 * kScaleFloats * 4;
 constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kScaleBytes;
@@ -313,25 +314,31 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Bounded wait; when it gives up it raises the CTA's abort flag and sets
+// Bounded wait of a whole warp, the same answer in every lane (so that no lane
+// goes its own way); when it gives up it raises the CTA's abort flag and sets
 // LPD_STATUS_TIMEOUT in the workspace's first word.  The clock is read only
 // once a wait has been polled for long: a read costs more than a block's MMAs.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
-                                           bool honour_abort = true) {
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
+                                          bool honour_abort = true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     unsigned long long t0 = 0;
 #pragma unroll 1
-    for (uint32_t n = 0; n < kWaitLimitIters; ++n) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 255u) == 255u) {
-            if (honour_abort && *abort_flag) return false;
+    for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((n & 255u) == 0) {
             const unsigned long long now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            if (now - t0 > kWaitLimitNs) break;
+            if (__any_sync(0xffffffffu, (honour_abort && *abort_flag) || now - t0 > kWaitLimitNs)) break;
         }
     }
-    *abort_flag = 1;
-    atomicOr(status, LPD_STATUS_TIMEOUT);
+    if ((threadIdx.x & 31) == 0) {
+        *abort_flag = 1;
+        atomicOr(status, LPD_STATUS_TIMEOUT);
+    }
     return false;
+}
+__device__ __forceinline__ void copy_async_4(float *dst, const float *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile(
@@ -381,10 +388,9 @@ __device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[16])
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
-// 32 lanes x 32 columns: a row a lane.
-__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32]) {  // the same, 64 columns
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
@@ -409,7 +415,6 @@ struct MmMaps {
 struct MmArgs {
     const float *sa, *sb;
     int64_t sa_stride, sb_stride;
-    int vec_sa, vec_sb;        // 16-byte aligned scale rows, and splits of whole groups of four blocks
     int sa_shift, sb_shift;    // 0: a scale a row, 7: a scale for 128 rows
     int64_t m, n;
     int kb_total, kb_per_split, n_splits;
@@ -442,10 +447,10 @@ template <bool kOutF32, bool kVecB>
 __global__ void __launch_bounds__(kMmThreads, 1)
     product_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
     extern __shared__ __align__(1024) char smem_raw[];
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scales_full[2], done;
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], scales_full[2], scales_empty[2], done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    char *smem = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    char *const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset keeps the loads shared ones)
     char *const staged = smem + static_cast<size_t>(kStages) * kStageBytes;
     float *const scales = reinterpret_cast<float *>(staged + kOutBytes);  // [2][kScaleFloats]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -460,7 +465,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], kEpiWarps);
-            mbar_init(&scales_full[b], kEpiWarps);
+            mbar_init(&scales_full[b], kScaleThreads);
+            mbar_init(&scales_empty[b], kEpiWarps);
         }
         mbar_init(&done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
 #pragma unroll 1
                 for (int kb = split * a.kb_per_split; kb < kb1; ++kb) {
-                    ok = __all_sync(0xffffffffu, wait_phase(&empty[s], phase, &abort_flag, a.status));
+                    ok = wait_warp(&empty[s], phase, &abort_flag, a.status);
                     if (!ok) break;
                     if (leader) {
                         char *st = smem + s * kStageBytes;
@@ -516,7 +522,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     phase ^= 1;
                 }
                 --s;
-                wait_phase(&full[s], phase ^ 1, &abort_flag, a.status, false);
+                wait_warp(&full[s], phase ^ 1, &abort_flag, a.status, false);
             }
         } else if (warp == 1) {
             // ----------------------------------------------------------------- MMA
@@ -529,8 +535,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 const int kbs = min(a.kb_total, (split + 1) * a.kb_per_split) - split * a.kb_per_split;
 #pragma unroll 1
                 for (int kb = 0; kb < kbs; ++kb) {
-                    ok = __all_sync(0xffffffffu, wait_phase(&acc_empty[b], turn, &abort_flag, a.status) &&
-                                                     wait_phase(&full[s], phase, &abort_flag, a.status));
+                    ok = wait_warp(&acc_empty[b], turn, &abort_flag, a.status) && wait_warp(&full[s], phase, &abort_flag, a.status);
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {
@@ -552,15 +557,47 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             }
             if (issued) {
                 if (leader) umma_commit(&done);
-                wait_phase(&done, 0, &abort_flag, a.status, false);
+                wait_warp(&done, 0, &abort_flag, a.status, false);
             }
             __syncwarp();
+        } else {
+            // -------------------------------------------------------------- scales
+            // of four blocks at a time, the 256 columns' and the 128 rows', one
+            // group ahead of the read-back (a scale for 128 of them is copied
+            // 128 times: the read-back then knows one layout)
+            const int u = threadIdx.x - 64;
+            uint32_t group = 0;
+            bool ok = true;
+            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                int tm, tn, split;
+                item_coords(w, a, tm, tn, split);
+                const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
+#pragma unroll 1
+                for (int kg = kb0; kg < kb1; kg += kScaleGroup, ++group) {
+                    ok = wait_warp(&scales_empty[group & 1], ((group >> 1) & 1) ^ 1, &abort_flag, a.status);
+                    if (!ok) break;
+                    float *const dst = scales + (group & 1) * kScaleFloats;
+#pragma unroll 1
+                    for (int i = u; i < kTN; i += kScaleThreads) {
+                        const float *src = a.sb + (min(static_cast<int64_t>(tn) * kTN + i, a.n - 1) >> a.sb_shift) * a.sb_stride;
+#pragma unroll
+                        for (int q = 0; q < kScaleGroup; ++q) copy_async_4(dst + q * kTN + i, src + min(kg + q, kb1 - 1));
+                    }
+#pragma unroll 1
+                    for (int i = u; i < kTM; i += kScaleThreads) {
+                        const float *src = a.sa + (min(static_cast<int64_t>(tm) * kTM + i, a.m - 1) >> a.sa_shift) * a.sa_stride;
+#pragma unroll
+                        for (int q = 0; q < kScaleGroup; ++q) copy_async_4(dst + kScaleGroup * kTN + q * kTM + i, src + min(kg + q, kb1 - 1));
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&scales_full[group & 1])) : "memory");
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
         // ------------------------------------------------------------ epilogue
         const int quad = warp & 3, part = (warp - 4) >> 2;
-        const int et = threadIdx.x - 128;  // 0..255
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kEpiCols;
         char *const mine = staged + (warp - 4) * kOutWarp;
         uint32_t it = 0, group = 0;  // k blocks and scale groups so far
@@ -569,89 +606,51 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             int tm, tn, split;
             item_coords(w, a, tm, tn, split);
             const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
-            const int64_t row = static_cast<int64_t>(tm) * kTM + quad * 32 + lane;
             const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
-            const int64_t sa_row = kVecB ? static_cast<int64_t>(tm) * kTM + (et & (kTM - 1)) : row;
-            const float *sa = a.sa + (min(sa_row, a.m - 1) >> a.sa_shift) * a.sa_stride;
-            const int64_t sb_row = kVecB ? static_cast<int64_t>(tn) * kTN + et : col0;
-            const float *sb = a.sb + (min(sb_row, a.n - 1) >> a.sb_shift) * a.sb_stride;
+            // A block's accumulator comes in pieces of 16 rows, each read under
+            // the arithmetic of the one before it: their registers, number and
+            // 8-column groups (columns of one scale each leave the registers
+            // for half as many)
+            constexpr int kPiece = kVecB ? 16 : 32, kPieces = kEpiCols / kPiece, kGroups = kPiece / 4;
+            // the pair of columns that a lane has of 8-column group g8 and row 16 h + 8 half + lane / 4
+            const auto pair_of = [](int g8, int h, int half) { return (((g8 / kGroups) * 2 + h) * kGroups + g8 % kGroups) * 4 + half * 2; };
             float acc[kEpiCols];
 #pragma unroll
             for (int j = 0; j < kEpiCols; ++j) acc[j] = 0.f;
-            // the next four blocks' scales are on their way while four are worked on
-            float na[kScaleGroup], nb[kScaleGroup];
-            auto fetch_of = [&](const float *from, bool vec, int kg, float (&to)[kScaleGroup]) {
-                if (vec && kg + kScaleGroup <= a.kb_total) {  // rows of scales on 16-byte boundaries: one load for four
-                    const float4 v = __ldg(reinterpret_cast<const float4 *>(from + kg));
-                    to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < kScaleGroup; ++q) to[q] = __ldg(from + min(kg + q, kb1 - 1));
-                }
-            };
-            auto fetch = [&](int kg) {
-                fetch_of(sa, a.vec_sa != 0, kg, na);
-                fetch_of(sb, a.vec_sb != 0, kg, nb);
-            };
-            fetch(kb0);
 #pragma unroll 1
             for (int kg = kb0; ok && kg < kb1; kg += kScaleGroup, ++group) {
-                // the scales of four blocks: the row's times its columns' (one
-                // for 128 of them), or both through shared memory
-                float s[kScaleGroup];
-                const float *const shared_scales = scales + (group & 1) * kScaleFloats;
-                if (kVecB) {
-                    // two buffers: a warp that fills one for group i + 2 has
-                    // seen every warp arrive for group i + 1, so every warp is
-                    // done with group i
-                    float *dst = scales + (group & 1) * kScaleFloats + et;
-#pragma unroll
-                    for (int q = 0; q < kScaleGroup; ++q) {
-                        dst[q * kTN] = nb[q];
-                        if (et < kTM) dst[kScaleGroup * kTN + q * kTM] = na[q];
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&scales_full[group & 1]);
-                    ok = wait_phase(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
-                    ok = !__any_sync(0xffffffffu, !ok);
-                    if (!ok) break;
-                } else {
-#pragma unroll
-                    for (int q = 0; q < kScaleGroup; ++q) s[q] = __fmul_rn(na[q], nb[q]);
-                }
-                if (kg + kScaleGroup < kb1) fetch(kg + kScaleGroup);
+                const float *const group_scales = scales + (group & 1) * kScaleFloats;
+                ok = wait_warp(&scales_full[group & 1], (group >> 1) & 1, &abort_flag, a.status);
+                if (!ok) break;
+                const float *const of_row = group_scales + kScaleGroup * kTN + quad * 32 + (lane >> 2);
+                const float *const of_col = group_scales + part * kEpiCols + (kVecB ? (lane & 3) * 2 : 0);
 #pragma unroll
                 for (int g = 0; g < kScaleGroup; ++g) {
                     if (kg + g >= kb1) break;
                     const uint32_t b = it & 1;
-                    ok = wait_phase(&acc_full[b], (it >> 1) & 1, &abort_flag, a.status);
-                    ok = !__any_sync(0xffffffffu, !ok);
+                    ok = wait_warp(&acc_full[b], (it >> 1) & 1, &abort_flag, a.status);
                     if (!ok) break;
                     ++it;
                     tc_fence_after();
-                    const uint32_t from = lane_addr + b * kTN;
-                    // pieces of the accumulator, the next one's read under this one's arithmetic
-                    constexpr int kPiece = kVecB ? 16 : 32;  // registers of a piece
-                    const auto piece_at = [&](int c) { return kVecB ? from + (c >> 1) * 32 + ((c & 1) << 20) : from + c * 32; };
-                    float of_rows[4];
-                    float2 of_cols[4];
-                    if (kVecB) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            of_rows[i] = shared_scales[kScaleGroup * kTN + g * kTM + quad * 32 + i * 8 + (lane >> 2)];
-                    }
                     uint32_t r[2][kPiece];
-                    tmem_ld_issue(piece_at(0), r[0]);
+                    const auto issue = [&](int c) {
+                        tmem_ld_issue(lane_addr + b * kTN + (c >> 1) * (8 * kGroups) + ((c & 1) << 20), r[c & 1]);
+                    };
+                    issue(0);
+                    float by_row[4];  // times the columns', where those share one
+                    float2 by_col[kGroups];
 #pragma unroll
-                    for (int c = 0; c < kEpiCols / kPiece; ++c) {
+                    for (int i = 0; i < 4; ++i) by_row[i] = kVecB ? of_row[g * kTM + i * 8] : __fmul_rn(of_row[g * kTM + i * 8], of_col[g * kTN]);
+#pragma unroll
+                    for (int c = 0; c < kPieces; ++c) {
                         if (kVecB && (c & 1) == 0) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                of_cols[i] = *reinterpret_cast<const float2 *>(&shared_scales[g * kTN + part * kEpiCols + c * 16 + i * 8 + (lane & 3) * 2]);
+                            for (int i = 0; i < kGroups; ++i)
+                                by_col[i] = *reinterpret_cast<const float2 *>(&of_col[g * kTN + (c / 2 * kGroups + i) * 8]);
                         }
                         tmem_wait_ld();
-                        if (c + 1 < kEpiCols / kPiece) {
-                            tmem_ld_issue(piece_at(c + 1), r[(c + 1) & 1]);
+                        if (c + 1 < kPieces) {
+                            issue(c + 1);
                         } else {
                             tc_fence_before();
                             __syncwarp();
@@ -659,13 +658,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         }
 #pragma unroll
                         for (int j = 0; j < kPiece; ++j) {
+                            float by = by_row[(c & 1) * 2 + ((j >> 1) & 1)];
+                            if (kVecB) by = __fmul_rn(by, (j & 1) ? by_col[j >> 2].y : by_col[j >> 2].x);
                             float &x = acc[c * kPiece + j];
-                            const float by = kVecB ? __fmul_rn(of_rows[(c & 1) * 2 + ((j >> 1) & 1)], (j & 1) ? of_cols[(j >> 2) & 3].y : of_cols[(j >> 2) & 3].x)
-                                                   : s[g];
                             x = __fmaf_rn(__uint_as_float(r[c & 1][j]), by, x);
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&scales_empty[group & 1]);
             }
             if (!ok) {  // a wait gave up: this tile reads as NaN
 #pragma unroll
@@ -684,37 +685,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         __syncwarp();
                     }
                     char *const dst = mine + (box & 1) * kBoxBytes;
-                    constexpr int kWords = kOutF32 ? 32 : 64;  // accumulators a box and lane
-                    if (kVecB) {
-                        // (32-column pieces of 16 lanes: pairs of columns)
 #pragma unroll
-                        for (int e = 0; e < kWords / 2; ++e) {
-                            const int i = e >> 1, q = ((i >> 3) << 2) + (i & 3);  // q: 8 columns of the box
-                            char *to = dst + ((((i >> 2) & 1) << 4) + ((e & 1) << 3) + (lane >> 2)) * 128;
-                            const float *v = &acc[box * kWords + 2 * e];
-                            if (kOutF32) {
-                                *reinterpret_cast<float2 *>(to + ((((q & 3) * 2 + ((lane >> 1) & 1)) ^ (lane >> 2)) << 4) + (lane & 1) * 8) = make_float2(v[0], v[1]);
-                            } else {
-                                *reinterpret_cast<__nv_bfloat162 *>(to + ((q ^ (lane >> 2)) << 4) + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
-                            }
+                    for (int q = 0; q < kBoxCols / 8; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            char *to = dst + (e * 8 + (lane >> 2)) * 128;
+                            const float *v = &acc[pair_of(box * (kBoxCols / 8) + q, e >> 1, e & 1)];
+                            if (kOutF32) *reinterpret_cast<float2 *>(to + (((q * 2 + ((lane >> 1) & 1)) ^ (lane >> 2)) << 4) + (lane & 1) * 8) = make_float2(v[0], v[1]);
+                            else *reinterpret_cast<__nv_bfloat162 *>(to + ((q ^ (lane >> 2)) << 4) + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (kOutF32) {
-                                    v[e] = __float_as_uint(acc[box * kBoxCols + 4 * q + e]);
-                                } else {
-                                    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[box * kBoxCols + 8 * q + 2 * e],
-                                                                                   acc[box * kBoxCols + 8 * q + 2 * e + 1]);
-                                    v[e] = *reinterpret_cast<const uint32_t *>(&h);
-                                }
-                            }
-                            *reinterpret_cast<uint4 *>(dst + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
-                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     const int64_t c = col0 + box * kBoxCols;
@@ -731,35 +710,15 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 #pragma unroll
             for (int p = 0; p < kEpiCols / kCols; ++p) {
                 __syncwarp();
-                if (kVecB) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int q = 0; q < kCols / 8; ++q)
 #pragma unroll
-                        for (int i = 0; i < kCols / 8; ++i)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                char *to = mine + (h * 16 + half * 8 + (lane >> 2)) * kOutPitch;
-                                const int group8 = p * (kCols / 8) + i;  // 8 columns of the warp's 128
-                                const float *v = &acc[(((group8 >> 2) * 2 + h) * 4 + (group8 & 3)) * 4 + half * 2];
-                                if (kOutF32) *reinterpret_cast<float2 *>(to + i * 32 + (lane & 3) * 8) = make_float2(v[0], v[1]);
-                                else *reinterpret_cast<__nv_bfloat162 *>(to + i * 16 + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
-                            }
-                } else {
-                    uint32_t piece[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        if (kOutF32) {
-                            piece[q] = __float_as_uint(acc[p * 16 + q]);
-                        } else {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(acc[p * 32 + 2 * q], acc[p * 32 + 2 * q + 1]);
-                            piece[q] = *reinterpret_cast<const uint32_t *>(&h);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        char *to = mine + (e * 8 + (lane >> 2)) * kOutPitch;
+                        const float *v = &acc[pair_of(p * (kCols / 8) + q, e >> 1, e & 1)];
+                        if (kOutF32) *reinterpret_cast<float2 *>(to + q * 32 + (lane & 3) * 8) = make_float2(v[0], v[1]);
+                        else *reinterpret_cast<__nv_bfloat162 *>(to + q * 16 + (lane & 3) * 4) = __floats2bfloat162_rn(v[0], v[1]);
                     }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<uint4 *>(mine + lane * kOutPitch + 16 * q) =
-                            make_uint4(piece[4 * q], piece[4 * q + 1], piece[4 * q + 2], piece[4 * q + 3]);
-                }
                 __syncwarp();
                 const int64_t c = col0 + p * kCols;
                 if (c >= a.n) break;
@@ -941,12 +900,6 @@ cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, in
     a.sb = y.scales;
     a.sa_stride = x.scale_stride;
     a.sb_stride = y.scale_stride;
-    const auto vec_scales = [&](const BlockOperand &o) {
-        return reinterpret_cast<uintptr_t>(o.scales) % 16 == 0 && o.scale_stride % kScaleGroup == 0 &&
-               (p.n_splits == 1 || p.kb_per_split % kScaleGroup == 0);
-    };
-    a.vec_sa = vec_scales(x);
-    a.vec_sb = vec_scales(y);
     a.sa_shift = x.block ? 7 : 0;
     a.sb_shift = y.block ? 7 : 0;
     a.m = m;
