@@ -27,7 +27,12 @@ constexpr int kBlk = 128;  // values along k that share one scale
 // A block takes a tile of 128 x 128 input values: 16 lanes a row with 8 values
 // each, two rows a warp and pass, 16 rows a pass, eight passes, all held in
 // registers, so the input is read once and each maximum is known before the
-// first value is rounded.  Transposed output goes through shared memory.
+// first value is rounded.  For transposed output a thread takes 8 neighbouring
+// rows instead: it then has 8 bytes of each of its 8 output rows, which turn
+// through shared memory in 8-byte chunks.  Chunk g of output row c lies at
+// g ^ (c / 8 % 16), so that the 16 columns a half-warp stores at once meet all
+// banks, and so do the 128 bytes of a row when they are read (bytes stored one
+// at a time kept the shared memory 96 % busy: 1085 us for 151936 x 4096).
 // Bound: HBM (input bytes + one byte a value).
 constexpr int kQThreads = 256;
 constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a scale is made for
@@ -46,13 +51,9 @@ struct QuantArgs {
 };
 
 template <bool kE5>
-__device__ __forceinline__ uint32_t pack4(const float *v, float inv) {
-    constexpr __nv_fp8_interpretation_t kKind = kE5 ? __NV_E5M2 : __NV_E4M3;
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(v[0], inv), __fmul_rn(v[1], inv)), __NV_SATFINITE, kKind);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fmul_rn(v[2], inv), __fmul_rn(v[3], inv)), __NV_SATFINITE, kKind);
-    return lo | hi << 16;
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, float inv) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)), __NV_SATFINITE,
+                                    kE5 ? __NV_E5M2 : __NV_E4M3);
 }
 
 // scale and the factor onto the 8-bit range from the block's largest magnitude
@@ -81,18 +82,19 @@ __device__ __forceinline__ void scale_of(uint32_t top_bits, int pow2, float *sca
 template <bool kBf16, bool kE5, bool kBlock, bool kTranspose>
 __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
     __shared__ uint32_t tops[kTranspose && !kBlock ? 8 * kBlk : 8];
-    __shared__ __align__(16) uint8_t turned[kTranspose ? kBlk * (kBlk + 16) : 16];
+    __shared__ __align__(16) uint8_t turned[kTranspose ? kBlk * kBlk : 16];
     constexpr int kElt = kBf16 ? 2 : 4;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t tile_r = blockIdx.x / a.n_tiles_c, tile_c = blockIdx.x % a.n_tiles_c;
     const int64_t r0 = tile_r * kBlk, c0 = tile_c * kBlk;
     const int col = (lane & 15) * 8;
-    const int row_in_pass = warp * 2 + (lane >> 4);
+    const int row_group = warp * 2 + (lane >> 4);
+    const auto row_of = [&](int p) { return kTranspose ? row_group * 8 + p : p * 16 + row_group; };
     // raw words of the thread's 8 passes: 8 values each, outside the tensor 0
     uint4 raw[8][kBf16 ? 1 : 2];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-        const int64_t r = r0 + p * 16 + row_in_pass, c = c0 + col;
+        const int64_t r = r0 + row_of(p), c = c0 + col;
         const char *src = a.x + r * a.x_stride + c * kElt;
 #pragma unroll
         for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = make_uint4(0, 0, 0, 0);
@@ -182,55 +184,32 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(cons
             if (t < 16 && c0 + col + q < a.cols) a.scales[(c0 + col + q) * a.scale_stride + tile_r] = s;
         }
     }
-#pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const int row = p * 16 + row_in_pass;
-        const int64_t r = r0 + row, c = c0 + col;
-        float v[8];
-        values(p, v);
-        float inv = inv_all;
-        if constexpr (!kBlock && !kTranspose) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-            float s;
-            scale_of<kE5>(m, a.pow2, &s, &inv);
-            if ((lane & 15) == 0 && r < a.rows) a.scales[r * a.scale_stride + tile_c] = s;
-        }
-        if constexpr (!kBlock && kTranspose) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], inv_col[q]);
-            inv = 1.f;
-        }
-        const uint32_t w0 = pack4<kE5>(v, inv), w1 = pack4<kE5>(v + 4, inv);
-        if constexpr (kTranspose) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                turned[(col + q) * (kBlk + 16) + row] = static_cast<uint8_t>(w0 >> (8 * q));
-                turned[(col + 4 + q) * (kBlk + 16) + row] = static_cast<uint8_t>(w1 >> (8 * q));
-            }
-        } else if (r < a.rows && c < a.cols) {
-            uint8_t *dst = a.out + r * a.out_stride + c;
-            if (a.vec_out && c + 8 <= a.cols) {
-                __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w0, w1));
-            } else {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (c + q < a.cols) dst[q] = static_cast<uint8_t>((q < 4 ? w0 : w1) >> (8 * (q & 3)));
-            }
-        }
-    }
     if constexpr (kTranspose) {
-        // 128 output rows (input columns) of 128 bytes: 8 lanes a row with 16 bytes each
+        uint32_t words[2][8];  // rows 0..3 and 4..7 of each column
+#pragma unroll
+        for (int p = 0; p < 8; p += 2) {
+            float v[2][8];
+            values(p, v[0]);
+            values(p + 1, v[1]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t two = pack2<kE5>(v[0][q], v[1][q], kBlock ? inv_all : inv_col[kBlock ? 0 : q]);
+                if (p & 2) words[p >> 2][q] |= two << 16;
+                else words[p >> 2][q] = two;
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint2 *>(&turned[(col + q) * kBlk + ((row_group ^ (col >> 3)) << 3)]) = make_uint2(words[0][q], words[1][q]);
         __syncthreads();
+        // 128 output rows (input columns) of 128 bytes: 8 lanes a row with 16 bytes each
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const int row = p * 32 + (t >> 3), at = (t & 7) * 16;
-            const int64_t orow = c0 + row, oc = r0 + at;
+            const int row = p * 32 + (t >> 3), at = t & 7, key = row >> 3;
+            const int64_t orow = c0 + row, oc = r0 + at * 16;
             if (orow >= a.cols || oc >= a.rows) continue;
-            const uint4 w = *reinterpret_cast<const uint4 *>(&turned[row * (kBlk + 16) + at]);
+            uint4 w = *reinterpret_cast<const uint4 *>(&turned[row * kBlk + ((at ^ (key >> 1)) << 4)]);
+            if (key & 1) w = make_uint4(w.z, w.w, w.x, w.y);
             uint8_t *dst = a.out + orow * a.out_stride + oc;
             if (a.vec_out && oc + 16 <= a.rows) {
                 __stcs(reinterpret_cast<uint4 *>(dst), w);
@@ -238,6 +217,36 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(cons
                 const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
                 for (int q = 0; q < 16 && oc + q < a.rows; ++q)
                     dst[q] = static_cast<uint8_t>(ws[q >> 2] >> (8 * (q & 3)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const int64_t r = r0 + row_of(p), c = c0 + col;
+            float v[8];
+            values(p, v);
+            float inv = inv_all;
+            if constexpr (!kBlock) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+                float s;
+                scale_of<kE5>(m, a.pow2, &s, &inv);
+                if ((lane & 15) == 0 && r < a.rows) a.scales[r * a.scale_stride + tile_c] = s;
+            }
+            if (r >= a.rows || c >= a.cols) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] = pack2<kE5>(v[2 * q], v[2 * q + 1], inv);
+            uint8_t *dst = a.out + r * a.out_stride + c;
+            if (a.vec_out && c + 8 <= a.cols) {
+                __stcs(reinterpret_cast<uint2 *>(dst), make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16));
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c + q < a.cols) dst[q] = static_cast<uint8_t>(w[q >> 1] >> (8 * (q & 1)));
             }
         }
     }
