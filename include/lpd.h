@@ -557,7 +557,9 @@ typedef struct {
  * once.  Logits in masked places are not looked at: they may be NaN or
  * infinite.  A row whose mask allows nothing is -inf throughout.  `out` may be
  * the logits themselves (same pointer, type and stride, else
- * LPD_ERR_UNSUPPORTED); it may not overlap them otherwise, nor the controls.
+ * LPD_ERR_UNSUPPORTED); it may not overlap them otherwise, nor the controls.  If
+ * an internal wait gives up (after 4 s, never expected), what had not been
+ * written by then is NaN.
  * controls NULL copies (and converts). */
 int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows, int64_t vocab,
                        void *out, int32_t out_dtype, int64_t out_row_stride, void *stream);
@@ -584,7 +586,7 @@ int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, con
  * 1 for the others; masked places get 0.  The controls themselves get no
  * gradient.  Arguments, inactive rows and ids outside [0, vocab) as
  * lpd_logprob_backward; a selected token that is masked gives NaN. out may not
- * overlap the logits. */
+ * overlap the logits.  Waits as in lpd_controls_apply. */
 int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows,
                                     int64_t vocab, const int32_t *token_ids, const uint8_t *action_mask,
                                     const float *logp, const float *grad_logp, void *out_dlogits,

@@ -33,7 +33,10 @@ constexpr int kBlk = 128;  // values along k that share one scale
 // g ^ (c / 8 % 16), so that the 16 columns a half-warp stores at once meet all
 // banks, and so do the 128 bytes of a row when they are read (bytes stored one
 // at a time kept the shared memory 96 % busy: 1085 us for 151936 x 4096).
-// Bound: HBM (input bytes + one byte a value).
+// Bound: HBM (input bytes + one byte a value): 151936 x 4096 bf16 in 276 us
+// transposed and 272 us as it lies with 128 x 128 blocks (6.8 TB/s, the measured
+// copy rate), 297 and 285 us with 1 x 128 blocks; 1024 x 4096 in 11 us is a launch
+// and one block's load, reduction and store in turn.
 constexpr int kQThreads = 256;
 constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a scale is made for
 
@@ -273,18 +276,31 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(cons
 }
 
 // ==================================================================== product
-// One persistent CTA per SM.  Warpgroup 0: warp 0 streams 128-wide k blocks of A (128 rows)
-// and B (256 rows) through a three-stage ring (TMA, 128-byte swizzle), warp 1
-// issues four M=128 N=256 K=32 MMAs a block into one of two accumulators in
-// tensor memory, and eight warps read each accumulator back, scale it and add
-// it to 128 fp32 registers a thread: a row is a lane, a warp takes half of the
-// 256 columns.  Two accumulators let the MMAs of block kb + 1 run under the
-// read-back of block kb; at the full MMA rate a block takes 512 cycles, its
-// read-back 256 (32768 values at 128 lanes) and its multiply-adds 256.  The
-// read-back is bound by its instructions: the block loop is unrolled over the
-// four blocks whose scales are fetched together, the multiply-adds are scalar
-// (packed pairs cost a move each after a read of tensor memory), and sixteen
-// warps of 64 registers were slower, as each block's overhead is a warp's.
+// One persistent CTA per SM.  Warpgroup 0: warp 0 streams 128-wide k blocks of A
+// (128 rows) and B (256 rows) through a three-stage ring (TMA, 128-byte
+// swizzle), warp 1 issues four M=128 N=256 K=32 MMAs a block into one of two
+// accumulators in tensor memory, and warps 2 and 3 copy the scales of four
+// blocks at a time into shared memory, one group ahead.  Warpgroups 1 and 2, the
+// read-back, take each accumulator, scale it and add it to 128 fp32 registers a
+// thread, a warp 32 rows and half of the 256 columns; two accumulators let the
+// MMAs of block kb + 1 run under the read-back of block kb.  It reads 16 rows at
+// a time, a lane four rows and every fourth pair of columns, so that a lane
+// needs 4 + 32 scales a block (one row a lane needs 1 + 128: with 1 x 128 scales
+// on both sides, 1024 cycles of shared-memory returns a block, and a weight
+// gradient took 651 us instead of 473).
+//
+// Bound: tensor cores by the operations, 512 cycles a block; the read-back by
+// measurement.  4096 x 128256 x 4096 takes 2.1 ms (2.0 PFLOP/s; 2.5 us a tile and
+// 0.55 us a block); with the multiply-adds left out 1.53 ms, with the copies left
+// out as well 1.30 ms.  128 multiply-adds a lane and block take 256 cycles of a
+// sub-partition's 512, and each piece's read of tensor memory stands before them
+// (tcgen05.wait::ld waits for all reads, so only one piece can be on its way).
+// Tried and slower: sixteen warps of 64 registers (2.2 to 2.4 ms), pieces of half
+// the size (2.2 ms), the next block's first piece under this one's last
+// (4.2 ms: its registers spill), packed multiply-adds (a move each after a read
+// of tensor memory), calling B into L2 ahead (no change; few rows 5 to 30 %
+// slower).  A product of few rows (16 x 151936 x 4096: 136 us, 4.6 TB/s) waits
+// for its 128-byte pieces of B's rows from HBM.
 constexpr int kTM = 128, kTN = 256;
 constexpr int kStages = 3;
 constexpr int kABytes = kTM * kBlk, kBBytes = kTN * kBlk;
@@ -297,7 +313,7 @@ constexpr int kMmThreads = (4 + kEpiWarps) * 32;  // a warpgroup for the copies 
 constexpr int kRegsFront = 40, kRegsEpi = 232;
 // Output staging, a warp's: two boxes of 32 rows x 128 bytes.  They leave by TMA
 // stores, which run under the next tile (stores by the warps themselves took
-// 4200 cycles a tile, an eighth of a 4096-deep one); output rows that are not
+// 4200 cycles a tile); output rows that are not
 // 16-byte aligned go through rows of kOutPitch bytes instead.
 constexpr int kBoxBytes = 32 * 128;
 constexpr int kOutPitch = 80;                   // 64 bytes a row and 16 against bank conflicts

@@ -9,7 +9,7 @@
 //   z  = allowed(j) ? scale * x3 : -inf
 // Only the tokens of the history and of the bias list ("touched" tokens) need
 // more than the scale and the mask, and they are few: a thousand of a hundred
-// thousand.  Four warps of a block (the scouts) look for them while sixteen
+// thousand.  Seven warps of a block (the scouts) look for them while sixteen
 // others stream the row: they mark the touched columns of the unit in a bitmap,
 // and with the bitmap's prefix sums a token's rank among the touched ones is a
 // look-up and a popcount, so that a second pass over the history counts
