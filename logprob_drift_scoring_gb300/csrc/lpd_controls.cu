@@ -1183,18 +1183,21 @@ Plane plane(const void *base, int64_t stride_bytes, int elt_bytes, int64_t rows,
     return Plane{b, stride_bytes, b + (rows - 1) * stride_bytes + vocab * elt_bytes};
 }
 
-// Units of the elementwise forms: as few as the bitmaps allow where there are
-// rows enough for four a block, else more and narrower ones, down to 2048
-// columns (a decode step's one row is cut in 63 units of a 128256-column
-// vocabulary).  In place a unit is no wider than the touched values it can
-// hold, where the history might bring more.  Rows that are not 16-byte aligned
-// start up to seven columns early, which a full last tile could not take.
+// Units of the elementwise forms: as few as the bitmaps allow, and with fewer
+// rows than blocks as many as keep every block to one unit, down to 2048 columns
+// (a decode step's one row is cut in 63 units of a 128256-column vocabulary).
+// Every unit of a row looks through its whole history, so more units a block
+// cost more than the idle blocks that they avoid: 256 rows of 151936 with 12288
+// tokens of history in 107 us as whole rows, 146 us as three units each; 100
+// rows in 62 us, 83 us as two units each.  In place a unit is no wider than the
+// touched values it can hold, where the history might bring more.  Rows that are
+// not 16-byte aligned start up to seven columns early, which a full last tile
+// could not take.
 void set_units(StreamArgs &a, bool aligned) {
-    const int64_t want = 4 * static_cast<int64_t>(device_sm_count());
     int64_t most = kMaxWidth - (aligned ? 0 : 32);
     if (a.late && a.c[0].n_history + a.c[0].n_bias > cap_of(kApply)) most = cap_of(kApply);
     int64_t n = (a.vocab + most - 1) / most;
-    if (a.n_rows * n < want) n = std::max(n, std::min((want + a.n_rows - 1) / a.n_rows, (a.vocab + 2047) / 2048));
+    n = std::max(n, std::min(device_sm_count() / a.n_rows, (a.vocab + 2047) / 2048));
     a.width = static_cast<int>(((a.vocab + n - 1) / n + 31) / 32 * 32);
     a.n_units = static_cast<int>((a.vocab + a.width - 1) / a.width);
 }
