@@ -469,6 +469,7 @@ struct MmArgs {
     int64_t out_stride;        // bytes
     int64_t split_stride;      // bytes between the partial results of two splits
     int vec_out;               // 16-byte aligned output rows
+    int whole_out;             // ... of whole 16-byte pieces
     uint32_t *status;
 };
 
@@ -719,7 +720,9 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             }
             char *const out = a.out + split * a.split_stride;
             const int64_t row0 = static_cast<int64_t>(tm) * kTM + quad * 32;
-            if (a.vec_out) {
+            // (a TMA store writes whole 16-byte pieces: columns behind an n
+            // between two of them are not the product's to write)
+            if (a.vec_out && (a.whole_out || col0 + kEpiCols <= a.n)) {
                 // boxes of 32 rows x 128 bytes under the 128-byte swizzle: chunk
                 // q of row l lies at q ^ (l % 8), so a warp's stores hit all banks
                 constexpr int kBoxCols = kOutF32 ? 32 : 64;
@@ -751,6 +754,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 continue;
             }
             // 64-byte pieces of 32 rows through shared memory
+            if (lane == 0) tma_store_wait_read();  // the last tile's boxes lay there
             constexpr int kCols = kOutF32 ? 16 : 32;  // columns of a piece
 #pragma unroll
             for (int p = 0; p < kEpiCols / kCols; ++p) {
@@ -965,7 +969,10 @@ cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, in
     a.split_stride = split ? m * p.part_stride * 4 : 0;
     a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 16 == 0;
     const bool to_f32 = split || f32;
-    if (a.vec_out && !make_out_map(&maps.out, a.out, m, n, p.n_splits, a.out_stride, a.split_stride, to_f32))
+    // (partial results have room up to their row stride)
+    const int64_t n_written = split ? p.part_stride : n;
+    a.whole_out = n_written % (to_f32 ? 4 : 8) == 0;
+    if (a.vec_out && !make_out_map(&maps.out, a.out, m, n_written, p.n_splits, a.out_stride, a.split_stride, to_f32))
         return cudaErrorInvalidValue;
     cudaError_t e;
     if (to_f32) e = y.block ? product_typed<true, false>(maps, a, stream) : product_typed<true, true>(maps, a, stream);

@@ -203,6 +203,50 @@ def test_product_rows_do_not_depend_on_the_batch():
         assert torch.equal(B.block_matmul(part, b, torch.float32), full[lo:hi])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k,b_block", [(2000, 4099, 300, True), (2000, 4099, 300, False), (130, 261, 900, False), (70, 259, 9000, True)])
+def test_product_leaves_aligned_padding(m, n, k, b_block, kind):
+    """Output rows on 16-byte boundaries with columns behind them: several tiles a
+    multiprocessor, an odd last column, no split of k and one."""
+    rng = np.random.default_rng(7)
+    a, b = operand(rng, m, k, "e5m2", False), operand(rng, n, k, "e4m3", b_block)
+    wide = torch.full((m + 3, -(-n // 8) * 8 + 8), 9.0, dtype=KINDS[kind], device=DEV)
+    ws = torch.zeros(B.lpd_block_workspace_size(m, n, k), dtype=torch.uint8, device=DEV)
+    B.lpd_block_matmul(a, b, wide[:m, :n], ws)
+    check_product(a, b, wide[:m, :n], kind)
+    assert bool((wide[:, n:] == 9).all()) and bool((wide[m:] == 9).all())
+    again = torch.empty(m, n, dtype=KINDS[kind], device=DEV)  # rows on no boundary: the other way out
+    B.lpd_block_matmul(a, b, again, ws)
+    assert torch.equal(again, wide[:m, :n])
+
+
+def test_product_one_row_of_any_stride():
+    """A single row's strides are never used, whatever they are."""
+    rng = np.random.default_rng(8)
+    a, b = operand(rng, 1, 700, "e4m3", False), operand(rng, 500, 700, "e4m3", True)
+    room = torch.full((508,), 9.0, device=DEV)
+    ws = torch.empty(B.lpd_block_workspace_size(1, 500, 700), dtype=torch.uint8, device=DEV)
+    B.lpd_block_matmul(a, b, room.as_strided((1, 500), (2 ** 41, 1)), ws)
+    check_product(a, b, room[None, :500], "f32")
+    assert bool((room[500:] == 9).all())
+
+
+def test_two_products_at_once():
+    rng = np.random.default_rng(9)
+    pairs = [(operand(rng, 300, 2000, "e4m3", False), operand(rng, 5000, 2000, "e4m3", True)) for _ in range(2)]
+    want = [B.block_matmul(a, b) for a, b in pairs]
+    streams = [torch.cuda.Stream() for _ in pairs]
+    rooms = [(torch.empty_like(w), torch.empty(B.lpd_block_workspace_size(300, 5000, 2000), dtype=torch.uint8, device=DEV))
+             for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (a, b), s, (out, ws) in zip(pairs, streams, rooms):
+            B.lpd_block_matmul(a, b, out, ws, s)
+    torch.cuda.synchronize()
+    for w, (out, _) in zip(want, rooms):
+        assert torch.equal(out, w)
+
+
 def test_product_streams_graph_and_determinism():
     rng = np.random.default_rng(5)
     shapes = [(50, 700, 6000), (200, 2000, 512)]  # one splits the k axis, one does not
