@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "lpd_internal.cuh"
+#include "lpd_operators.cuh"
 #include "lpd_xform.cuh"
 
 namespace lpd {

@@ -17,6 +17,7 @@
 
 #include "lpd_acc.cuh"
 #include "lpd_internal.cuh"
+#include "lpd_operators.cuh"
 
 namespace lpd {
 namespace {

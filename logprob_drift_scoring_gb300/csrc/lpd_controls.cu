@@ -1187,7 +1187,7 @@ Plane plane(const void *base, int64_t stride_bytes, int elt_bytes, int64_t rows,
 // rows than blocks as many as keep every block to one unit, down to 2048 columns
 // (a decode step's one row is cut in 63 units of a 128256-column vocabulary).
 // Every unit of a row looks through its whole history, so more units a block
-// cost more than the idle blocks that they avoid: 256 rows of 151936 with 12288
+// cost more than the idle blocks that they avoid: 256 rows of 151936 with 8192
 // tokens of history in 107 us as whole rows, 146 us as three units each; 100
 // rows in 62 us, 83 us as two units each.  In place a unit is no wider than the
 // touched values it can hold, where the history might bring more.  Rows that are
