@@ -151,7 +151,7 @@ struct StreamArgs {
     // kApply, kGrad
     char *out;
     int64_t out_stride;  // bytes
-    int late;            // in place: the stream starts once the touched logits have been read
+    int in_place;        // kApply: the stream writes touched columns back as they are, for the scouts to read
     const int32_t *ids;
     const uint8_t *mask;
     const float *logp, *grad;
@@ -185,7 +185,7 @@ struct Smem {
     int line_base[kLines + 1];                  // touched columns in the lines in front
     float gs, ll;                               // kGrad: grad * scale, the lower part of lse2
     alignas(16) uint4 lanes[256];
-    alignas(16) uint32_t touched[kSides][kLines * 128];  // kScore: [unit parity], the stream leaves these out
+    alignas(16) uint32_t touched[kMode == kGrad ? 1 : 2][kLines * 128];  // [unit parity] where the stream looks: it leaves these out
     alignas(8) uint16_t before[kLines * 128];   // touched columns in the words in front, of the same line
     uint32_t word[2][kCap];                     // kScore: a side's count words; else [unit parity], the values
     uint32_t list[kSides == 2 ? 1 : 2][kCap];   // their columns in the unit
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
             const int words = static_cast<int>((len + 31) / 32);
             const char *xrow = a.in[0].base + r * a.in[0].stride;
             const char *yrow = kTwo ? a.in[1].base + r * a.in[1].stride : nullptr;
-            uint32_t *const touched = sm.touched[kTwo ? b : 0];
+            uint32_t *const touched = sm.touched[kMode == kGrad ? 0 : b];
             // the bitmap of this parity belongs to the unit before the last;
             // (store_held has waited for it in the elementwise forms)
             if (kTwo && n_live >= 2 && !wait_all(&sm.done[b], ((n_live >> 1) - 1) & 1)) return;
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     num.lse2 = h;
                     num.g = __fmul_rn(-gs, ex2(-sm.ll));
                 }
-                if (!a.late) mbar_arrive(&sm.ready[b]);
+                mbar_arrive(&sm.ready[b]);
             }
             // each word's rank within its line
             for (int line = kScoutWarps - 1 - (warp - kStreamWarps); line < lines; line += kScoutWarps) {
@@ -870,14 +870,14 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     for (int q = st; q < m; q += kScoutThreads) w0[q] = __float_as_uint(result(q));
                 }
                 scout_sync();
-                if (a.late && st == 0) mbar_arrive(&sm.ready[b]);
                 // the last unit's values, now that the stream has this one to go on with
                 if (held_row >= 0 && !store_held(n_live - 1)) return;
                 held_row = r;
                 held_c0 = c0;
                 held_n = m;
                 if (total > kCap) {
-                    // more than kCap (never in place): straight to the output, behind the stream
+                    // more than kCap: straight to the output, behind the stream
+                    // (in place it has left them as they were)
                     if (!store_held(n_live)) return;
                     for (int base = kCap; base < total; base += kCap) {
                         const int n = min(kCap, total - base);
@@ -1080,7 +1080,15 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     constexpr uint32_t kMasked = kMode == kApply ? 0xff80u : 0u;  // -inf, or no gradient
                     const uint32_t skip = none0 ? 0xffu : s0[g];
                     if (skip) ctl_fill8<kYBf16, kMasked>(w, sm.lanes[skip]);
-                    if (j >= 0 && left >= 8 * group + 8) ctl_store8<kYBf16>(orow, j, w);  // (the others are the scouts')
+                    if (j < 0 || left < 8 * group + 8) continue;  // the scouts'
+                    if constexpr (kMode == kApply && kXBf16 == kYBf16) {
+                        if (a.in_place) {
+                            const uint8_t *bits = reinterpret_cast<const uint8_t *>(sm.touched[b]) + (j >> 3);
+                            const uint32_t keep = kAligned ? bits[0] : (bits[0] | bits[1] << 8) >> (j & 7) & 0xffu;
+                            if (keep) ctl_keep8<kYBf16>(w, gx[g], sm.lanes[keep]);
+                        }
+                    }
+                    ctl_store8<kYBf16>(orow, j, w);
                 }
             }
         }
@@ -1189,13 +1197,10 @@ Plane plane(const void *base, int64_t stride_bytes, int elt_bytes, int64_t rows,
 // Every unit of a row looks through its whole history, so more units a block
 // cost more than the idle blocks that they avoid: 256 rows of 151936 with 8192
 // tokens of history in 107 us as whole rows, 146 us as three units each; 100
-// rows in 62 us, 83 us as two units each.  In place a unit is no wider than the
-// touched values it can hold, where the history might bring more.  Rows that are
-// not 16-byte aligned start up to seven columns early, which a full last tile
-// could not take.
+// rows in 62 us, 83 us as two units each.  Rows that are not 16-byte aligned
+// start up to seven columns early, which a full last tile could not take.
 void set_units(StreamArgs &a, bool aligned) {
-    int64_t most = kMaxWidth - (aligned ? 0 : 32);
-    if (a.late && a.c[0].n_history + a.c[0].n_bias > cap_of(kApply)) most = cap_of(kApply);
+    const int64_t most = kMaxWidth - (aligned ? 0 : 32);
     int64_t n = (a.vocab + most - 1) / most;
     n = std::max(n, std::min(device_sm_count() / a.n_rows, (a.vocab + 2047) / 2048));
     a.width = static_cast<int>(((a.vocab + n - 1) / n + 31) / 32 * 32);
@@ -1218,7 +1223,7 @@ cudaError_t launch_controls_apply(const CtlSide &c, const void *x, int x_dtype, 
     a.out_stride = out_stride_elems * (ob ? 2 : 4);
     a.n_rows = n_rows;
     a.vocab = vocab;
-    a.late = x == out ? 1 : 0;
+    a.in_place = x == out ? 1 : 0;
     const bool aligned = aligned_rows(x, a.in[0].stride) && aligned_rows(out, a.out_stride);
     set_units(a, aligned);
     return aligned ? launch_kinds<kApply, true>(a, xb, ob, n_rows, stream) : launch_kinds<kApply, false>(a, xb, ob, n_rows, stream);

@@ -306,6 +306,29 @@ __device__ __forceinline__ void ctl_fill8(Group8<kBf16> &g, const uint4 &m) {
     }
 }
 
+// The columns of mask `m` taken from `from`, bit for bit.
+template <bool kBf16>
+__device__ __forceinline__ void ctl_keep8(Group8<kBf16> &g, const Group8<kBf16> &from, const uint4 &m) {
+    auto put = [](uint32_t &w, uint32_t f, uint32_t lanes) { w = (w & ~lanes) | (f & lanes); };
+    if constexpr (kBf16) {
+        put(g.w[0].x, from.w[0].x, m.x);
+        put(g.w[0].y, from.w[0].y, m.y);
+        put(g.w[0].z, from.w[0].z, m.z);
+        put(g.w[0].w, from.w[0].w, m.w);
+    } else {
+        auto wide = [](uint32_t two, int half) { return __byte_perm(two, 0, half ? 0x3232 : 0x1010); };
+        constexpr int kHi = kBf16 ? 0 : 1;
+        put(g.w[0].x, from.w[0].x, wide(m.x, 0));
+        put(g.w[0].y, from.w[0].y, wide(m.x, 1));
+        put(g.w[0].z, from.w[0].z, wide(m.y, 0));
+        put(g.w[0].w, from.w[0].w, wide(m.y, 1));
+        put(g.w[kHi].x, from.w[kHi].x, wide(m.z, 0));
+        put(g.w[kHi].y, from.w[kHi].y, wide(m.z, 1));
+        put(g.w[kHi].z, from.w[kHi].z, wide(m.w, 0));
+        put(g.w[kHi].w, from.w[kHi].w, wide(m.w, 1));
+    }
+}
+
 // Columns [j, j + 8) of an output row on a 16-byte boundary.
 template <bool kBf16>
 __device__ __forceinline__ void ctl_store8(char *row, int64_t j, const Group8<kBf16> &g) {

@@ -382,6 +382,25 @@ def test_more_touched_tokens_than_counted_at_a_time():
     assert torch.equal(xs, got)
 
 
+@pytest.mark.parametrize("kind,vocab,pad", [("bf16", 9001, 7), ("bf16", 20000, 0), ("f32", 12003, 2), ("f32", 8192, 0)])
+@pytest.mark.parametrize("rows", [1, 60, 500])
+def test_apply_in_place_over_many_units(kind, vocab, pad, rows):
+    """Several rows a block and several units a row, on 16-byte boundaries and
+    off them, some rows with more touched tokens than are counted at a time."""
+    rng = np.random.default_rng(25)
+    c = ref.random_controls(rng, rows, vocab, history=16000, masks=3, bias=9)
+    wide = rng.random(rows) < 0.3
+    c["hist_begin"][wide], c["hist_end"][wide] = 0, 16000
+    h = to_device(c)
+    x = tensor(rng.normal(0, 3, (rows, vocab)), kind, pad)
+    want = B.controls_apply(x, h)
+    for _ in range(3):
+        y = tensor(np.zeros((rows, vocab)), kind, pad)
+        y.copy_(x)
+        B.lpd_controls_apply(y, h, y)
+        assert torch.equal(y, want)
+
+
 @pytest.mark.parametrize("what", ["masked_id", "nothing_allowed", "bad_scale", "nan_logit", "oob"])
 def test_score_status(what):
     rng = np.random.default_rng(14)
