@@ -558,8 +558,8 @@ typedef struct {
  * infinite.  A row whose mask allows nothing is -inf throughout.  `out` may be
  * the logits themselves (same pointer, type and stride, else
  * LPD_ERR_UNSUPPORTED); it may not overlap them otherwise, nor the controls.  If
- * an internal wait gives up (after 4 s, never expected), what had not been
- * written by then is NaN.
+ * an internal wait gives up (after 4 s, never expected), what was not begun by
+ * then is NaN and the rows in hand, up to two a multiprocessor, are incomplete.
  * controls NULL copies (and converts). */
 int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows, int64_t vocab,
                        void *out, int32_t out_dtype, int64_t out_row_stride, void *stream);
