@@ -239,6 +239,13 @@ def _stream(stream) -> int | None:
     return getattr(stream, "cuda_stream", stream)
 
 
+def _row_stride(t) -> int:
+    """Elements between the rows of a 2-D tensor.  A single row's stride has no
+    meaning in torch, so its width serves; rows that overlap or repeat keep
+    theirs, which the library refuses (LPD_ERR_BAD_STRIDE)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def logits_struct(t) -> LpdLogits:
     """lpd_logits for a 2-D tensor with unit column stride (rows may be padded)."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
@@ -712,7 +719,7 @@ def lpd_block_quantize(x, out, transpose=False, pow2=False, stream=None) -> None
     if out.values.device != x.device:
         raise ValueError(f"x on {x.device}, out on {out.values.device}")
     with _on(x):
-        rc = lib().lpd_block_quantize(_ptr(x), _dtype_code(x), max(x.stride(0), x.shape[1]), x.shape[0], x.shape[1],
+        rc = lib().lpd_block_quantize(_ptr(x), _dtype_code(x), _row_stride(x), x.shape[0], x.shape[1],
                                       int(bool(transpose)), int(bool(pow2)), ctypes.byref(out._struct),
                                       _stream(stream))
     _check(rc, "lpd_block_quantize")
@@ -733,7 +740,7 @@ def lpd_block_matmul(a, b, out, workspace, stream=None) -> None:
         raise ValueError("the operands, out and the workspace must be on one device")
     with _on(out):
         rc = lib().lpd_block_matmul(ctypes.byref(a._struct), ctypes.byref(b._struct), m, n, k, _ptr(out),
-                                    _dtype_code(out), max(out.stride(0), n), _ptr(workspace),
+                                    _dtype_code(out), _row_stride(out), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream(stream))
     _check(rc, "lpd_block_matmul")
 

@@ -1,5 +1,6 @@
 """The 8-bit operands' host side: arguments refused before anything is launched
 (fake device addresses, no GPU), and the binding's checks."""
+import contextlib
 import ctypes
 
 import pytest
@@ -98,3 +99,44 @@ def test_block_empty_rows_fit_the_product():
     assert B.block_empty(300, 130, torch.float8_e4m3fn, True, "cpu").scales.shape == (3, 2)
     one = B.block_empty(1, 20, torch.float8_e4m3fn, device="cpu")
     assert one._struct.row_stride == 32 and one._struct.scale_stride == 1
+
+
+class Recorder:
+    """In place of the library: the arguments of each call, nothing launched."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        monkeypatch.setattr(B, "lib", lambda: self)
+        monkeypatch.setattr(B, "_on", lambda t: contextlib.nullcontext())
+
+    def __getattr__(self, name):
+        return lambda *a: self.calls.append((name, a)) or B.LPD_OK
+
+
+def overlapping(rows, cols, dtype=torch.bfloat16):
+    """A repeated row and rows one element apart: strides (0, 1) and (1, 1)."""
+    return torch.zeros(cols, dtype=dtype).expand(rows, cols), torch.zeros(rows + cols - 1, dtype=dtype).unfold(0, cols, 1)
+
+
+def test_rows_that_overlap_keep_their_stride(monkeypatch):
+    """The quantiser's input and the product's output are handed over with the stride that they have, and
+    the library refuses it: their storage is smaller than rows x width."""
+    assert quantize_rc(stride=0) == quantize_rc(stride=1) == B.LPD_ERR_BAD_STRIDE
+    assert matmul_rc(out_stride=0) == matmul_rc(out_stride=1) == B.LPD_ERR_BAD_STRIDE
+    a, b = (B.block_empty(r, 256, torch.float8_e4m3fn, device="cpu") for r in (40, 130))
+    ws = torch.zeros(256, dtype=torch.uint8)
+    lib = Recorder(monkeypatch)
+    for x, stride in zip(overlapping(40, 256), (0, 1)):
+        B.lpd_block_quantize(x, a, stream=0)
+        assert lib.calls[-1][1][2] == stride
+    for out, stride in zip(overlapping(40, 130), (0, 1)):
+        B.lpd_block_matmul(a, b, out, ws, stream=0)
+        assert lib.calls[-1][1][7] == stride
+    # padded rows; a single row may have any stride
+    B.lpd_block_quantize(torch.zeros(40, 300)[:, :256], a, stream=0)
+    assert lib.calls[-1][1][2] == 300
+    one = B.block_empty(1, 256, torch.float8_e4m3fn, device="cpu")
+    B.lpd_block_quantize(torch.zeros(256).expand(1, 256), one, stream=0)
+    assert lib.calls[-1][1][2] == 256
+    B.lpd_block_matmul(one, b, torch.zeros(130).expand(1, 130), ws, stream=0)
+    assert lib.calls[-1][1][7] == 130
