@@ -590,6 +590,10 @@ def _controls(c, logits):
         raise ValueError(f"controls of {c._rows} rows for {logits.shape[0]} logits rows")
     if c._device is not None and c._device != logits.device:
         raise ValueError(f"controls on {c._device}, logits on {logits.device}")
+    words = -(-logits.shape[1] // 32)
+    if c.mask is not None and c.mask.shape[1] < words:
+        # (the library sees the stride between rows only, which a slice keeps)
+        raise ValueError(f"mask has {c.mask.shape[1]} words a row, {logits.shape[1]} columns need {words}")
     return ctypes.byref(c._struct)
 
 

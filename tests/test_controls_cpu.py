@@ -1,6 +1,7 @@
 """The sampling controls' host side: arguments that are refused before anything
 is launched (fake device addresses, no GPU), and the definition that the GPU
 tests use against hand-worked values."""
+import contextlib
 import ctypes
 
 import numpy as np
@@ -167,3 +168,43 @@ def test_definition_by_hand():
     # 4 / 2; (-1 * 2 - 2 * 0.5 - 0.25); 1 + 1.5; masked; all times 2
     assert z.tolist() == [4.0, -6.5, 5.0, -np.inf]
     assert slope.tolist() == [1.0, 4.0, 2.0, 0.0]
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """The library's calls, by their arguments; nothing is launched."""
+    calls = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a)) or B.LPD_OK
+
+    monkeypatch.setattr(B, "lib", lambda: Recorder())
+    monkeypatch.setattr(B, "_on", lambda t: contextlib.nullcontext())
+    return calls
+
+
+def call_all(c, x):
+    """Each controlled entry point once, on logits x."""
+    n = x.shape[0]
+    ids, act = torch.zeros(n, dtype=torch.int32), torch.ones(n, dtype=torch.uint8)
+    f = torch.zeros(n)
+    met, ws = torch.zeros(B.METRICS_BYTES, dtype=torch.uint8), torch.zeros(1 << 16, dtype=torch.uint8)
+    return [lambda: B.lpd_controls_apply(x, c, torch.empty_like(x), stream=0),
+            lambda: B.lpd_score_controlled(x, x, c, None, ids, act, 0.8, 1.2, f, f, f, met, ws, stream=0),
+            lambda: B.lpd_score_controlled(x, x, None, c, ids, act, 0.8, 1.2, f, f, f, met, ws, stream=0),
+            lambda: B.lpd_logprob_backward_controlled(x, c, ids, act, f, f, torch.empty_like(x), stream=0)]
+
+
+def test_a_mask_slice_narrower_than_the_vocabulary_is_refused(recorded):
+    """A slice keeps its rows' stride, which is what the library checks: the last row's words would be read
+    behind the table."""
+    table = torch.zeros(4, 10, dtype=torch.int32)
+    c = B.Controls(mask=table[:, 5:])  # 5 words a row, 10 apart
+    for call in call_all(c, torch.zeros(4, 161)):
+        with pytest.raises(ValueError, match="words a row"):
+            call()
+    assert recorded == []
+    for call in call_all(c, torch.zeros(4, 160)):
+        call()
+    assert len(recorded) == 4
