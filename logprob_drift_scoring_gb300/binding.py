@@ -570,10 +570,13 @@ class Controls:
             raise ValueError("bias and bias_ids must have one shape")
         m = self.mask
         n = lambda t: t.shape[0] if t is not None else 0  # noqa: E731
+        # A table of no rows has no memory in torch, and NULL would mean "no
+        # mask": it gets an address, through which nothing is read.
+        mask_ptr = (m.data_ptr() or 256) if m is not None else None
         struct = LpdControls(_ptr(self.history), n(self.history), _ptr(self.hist_begin), _ptr(self.hist_split),
                              _ptr(self.hist_end), _ptr(self.repetition), _ptr(self.frequency), _ptr(self.presence),
                              _ptr(self.scale), _ptr(self.bias_ids), _ptr(self.bias),
-                             self.bias.shape[1] if self.bias is not None else 0, _ptr(m), n(m),
+                             self.bias.shape[1] if self.bias is not None else 0, mask_ptr, n(m),
                              (m.stride(0) if m.shape[0] > 1 else m.shape[1]) if m is not None else 0,
                              _ptr(self.mask_row))
         object.__setattr__(self, "_struct", struct)

@@ -208,3 +208,19 @@ def test_a_mask_slice_narrower_than_the_vocabulary_is_refused(recorded):
     for call in call_all(c, torch.zeros(4, 160)):
         call()
     assert len(recorded) == 4
+
+
+def test_a_mask_table_of_no_rows_is_not_no_mask(recorded):
+    """Its rows allow nothing; without mask_row it has too few rows."""
+    table = torch.zeros(0, 5, dtype=torch.int32)
+    x = torch.zeros(4, 160)
+    for call in call_all(B.Controls(mask=table, mask_row=torch.zeros(4, dtype=torch.int32)), x):
+        call()
+    side = {"lpd_controls_apply": (1,), "lpd_score_controlled": (2, 3), "lpd_logprob_backward_controlled": (1,)}
+    for name, args in recorded:
+        c = next(args[k] for k in side[name] if args[k] is not None)._obj
+        assert c.mask and c.n_masks == 0 and c.mask_stride == 5
+
+
+def test_a_mask_table_of_no_rows_needs_mask_row():
+    assert apply_rc(c=B.Controls(mask=torch.zeros(0, 2, dtype=torch.int32))._struct) == B.LPD_ERR_BAD_SIZE

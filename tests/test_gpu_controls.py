@@ -575,3 +575,16 @@ def test_streams_graphs_and_determinism():
     for a, b in zip(replayed, results(sets[0])):
         assert torch.equal(a, b)
     assert not torch.equal(replayed[0], want[0])
+
+
+def test_a_mask_table_of_no_rows_allows_nothing():
+    rng = np.random.default_rng(31)
+    rows, vocab = 4, 300
+    c = {"mask": np.zeros((0, 10), np.int32), "mask_row": np.array([0, -1, 3, -1], np.int32)}
+    x = tensor(rng.normal(0, 3, (rows, vocab)), "f32")
+    out = B.controls_apply(x, to_device(c))
+    check_apply(c, x, "f32", out)
+    assert bool(torch.isneginf(out[::2]).all()) and torch.equal(out[1::2], x[1::2])
+    ids, act = torch.zeros(rows, dtype=torch.int32, device=DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    s = B.score_controlled(x, x, ids, act, to_device(c), None)
+    assert s.metrics["status"] == B.LPD_STATUS_NONFINITE and bool(torch.isfinite(s.logp_train[1::2]).all())
