@@ -554,7 +554,7 @@ class Controls:
             if t.dim() != (2 if name in ("bias_ids", "bias", "mask") else 1):
                 raise ValueError(f"{name} has {t.dim()} dimensions")
             if name == "mask":
-                if t.shape[1] > 1 and t.stride(1) != 1:
+                if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
                     raise ValueError("mask must have contiguous words")
             elif not t.is_contiguous():
                 raise ValueError(f"{name} must be dense")
