@@ -203,7 +203,7 @@ constexpr size_t kSmemMost = 232448 - 1024;  // what a block may have, less the 
 // to them as far as the tensor goes.  Column c of the tile's range sits at byte
 // `lead` + (c - first) * size of the stage.  At the tensor's two ends up to
 // seven columns may be missing there; the scouts take a row's first eight
-// columns and its last eight to fifteen always (of a unit's, in the elementwise
+// columns and its last eight to fifteen always (each unit's, in the elementwise
 // forms), whether they are missing or not, so that a row's arithmetic does not
 // depend on its place.
 struct Span {
@@ -224,12 +224,19 @@ __device__ __forceinline__ Span span_of(const Plane &p, const char *row, int64_t
     return s;
 }
 // The columns of a unit [c0, c1) that are the scouts' for their place: [c0,
-// head) and [tail, c1).
+// head) and [tail, c1).  When scoring they are the row's, whatever its units: a
+// last unit of a few columns leaves the ends of the tensor's last row in the
+// unit in front of it, and the split of a row between stream and scouts does
+// not depend on its units.
 template <int kMode>
 __device__ __forceinline__ void edges(int64_t c0, int64_t c1, int64_t vocab, int64_t &head, int64_t &tail) {
-    const bool first = kMode != kScore || c0 == 0, last = kMode != kScore || c1 == vocab;
-    head = first ? min(c0 + 8, c1) : c0;
-    tail = last ? max(c1 / 8 * 8 - 8, head) : c1;
+    if (kMode == kScore) {
+        head = max(c0, min(static_cast<int64_t>(8), c1));
+        tail = min(max(vocab / 8 * 8 - 8, head), c1);
+    } else {
+        head = min(c0 + 8, c1);
+        tail = max(c1 / 8 * 8 - 8, head);
+    }
 }
 
 // Unit u: the row (kScore: its place among the active rows) and which of its

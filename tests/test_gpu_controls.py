@@ -588,3 +588,66 @@ def test_a_mask_table_of_no_rows_allows_nothing():
     ids, act = torch.zeros(rows, dtype=torch.int32, device=DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
     s = B.score_controlled(x, x, ids, act, to_device(c), None)
     assert s.metrics["status"] == B.LPD_STATUS_NONFINITE and bool(torch.isfinite(s.logp_train[1::2]).all())
+
+
+def logp64(z, ids):
+    """Selected logprobs of float64 rows on the device."""
+    return torch.gather(z, 1, ids.long()[:, None])[:, 0] - torch.logsumexp(z, 1)
+
+
+@pytest.mark.parametrize("vocab", [57345, 57347, 57350, 114690, 172033])
+@pytest.mark.parametrize("xk,yk", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
+def test_score_where_a_segment_of_few_columns_is_left(vocab, xk, yk):
+    """The last columns carry most of each row's sum, so none of them may be lost or read twice, in the tensor's
+    last row neither; and a row's bits are the same alone (a unit a segment) and among many (whole rows), on
+    16-byte boundaries and off them."""
+    gen = torch.Generator(DEV).manual_seed(vocab)
+    many = 310
+    x = torch.randn(many, vocab, device=DEV, generator=gen)
+    x[:, -24:] += 8
+    y = x + 2e-3 * torch.randn(many, vocab, device=DEV, generator=gen)
+    ids = (vocab - 1 - torch.arange(many, device=DEV) % 20).int()
+
+    def run(at, pad):
+        n = len(at)
+        room = torch.full((n, vocab + pad), 50.0, device=DEV)
+        sides = []
+        for v, k in ((x, xk), (y, yk)):
+            t = room.to(KINDS[k])
+            t[:, :vocab] = v[at].to(KINDS[k])
+            sides.append(t[:, :vocab] if pad else t[:, :vocab].contiguous())
+        act = torch.ones(n, dtype=torch.uint8, device=DEV)
+        r = B.score_controlled(*sides, ids[at].contiguous(), act)
+        assert r.metrics["status"] == 0
+        for got, t in ((r.logp_train, sides[0]), (r.logp_rollout, sides[1])):
+            want = logp64(t[-4:].double(), ids[at][-4:])
+            err = (got[-4:].double() - want).abs()
+            assert bool((err <= 1e-5 + 2.0 ** -23 * want.abs()).all()), (n, pad, err)
+        return [r.logp_train, r.logp_rollout, r.dlogp]
+
+    full = run(torch.arange(many), 0)
+    for at in (torch.arange(many - 3, many), torch.tensor([7]), torch.tensor([3, 200])):
+        for pad in (0, 1, -vocab % 8):
+            for a, b in zip(full, run(at, pad)):
+                assert torch.equal(a[at], b), (at, pad)
+    for a, b in zip(full, run(torch.arange(many), -vocab % 8)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 57346), (2, 114689)])
+def test_score_controlled_at_a_small_last_segment(rows, vocab):
+    """The same place with controls that touch the columns around it."""
+    rng = np.random.default_rng(vocab)
+    ids = np.array([vocab - 2, vocab - 1], np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=60, bias=6)
+    c["history"][:12] = np.arange(vocab - 12, vocab)
+    c["hist_begin"][:], c["hist_split"][:], c["hist_end"][:] = 0, 5, 40
+    c["bias_ids"][:, :3] = [[vocab - 3, vocab - 9, vocab - 1]] * 2
+    x = rng.normal(0, 1, (rows, vocab))
+    x[:, -20:] += 8
+    y = x + rng.normal(0, 2e-3, x.shape)
+    xt, yt = tensor(x, "bf16"), tensor(y, "bf16")
+    h = to_device(c)
+    act = np.ones(rows, np.uint8)
+    res = B.score_controlled(xt, yt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), h, h)
+    check_score(c, c, xt, yt, ids, act, res)
