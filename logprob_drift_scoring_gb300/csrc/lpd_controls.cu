@@ -292,12 +292,25 @@ __device__ __forceinline__ void raise_refs(Acc2 &a, float nmt, float nmr, float 
     a.mr = nmr;
 }
 
-// The references raised to take in two maxima.  References that are near each
-// other are kept equal: the exponents are then x l - (m l) with one rounded
-// m l for both sides, which leaves their difference untouched.
+// The references raised to take in the maxima (ct, cr) of columns that are
+// added next.  Two sides of one scale get one reference where neither can lose
+// terms by it, as the sums of two sides that nearly agree need (see
+// accumulate_near): the lower side goes up with the higher one only if its sum
+// stays at 2^-8 of the reference's term or more, by what it holds or by what
+// comes.  A sum's terms are flushed below 2^-126, so each side keeps all that
+// counts, whatever the scale and however far the sides' peaks lie apart.
+constexpr float kTied = 8.f;  // octaves
 __device__ __forceinline__ void raise_to(Acc2 &a, float ct, float cr, float lt, float lr) {
     float nt = fmaxf(a.mt, ct), nr = fmaxf(a.mr, cr);
-    if (fabsf(__fsub_rn(nt, nr)) <= 8.f) nt = nr = fmaxf(nt, nr);
+    if (nt != nr && lt == lr) {
+        const bool t_low = nt < nr;
+        const float top = t_low ? nr : nt, c = t_low ? ct : cr, m = t_low ? a.mt : a.mr;
+        const f2_t held = t_low ? a.st : a.sr;
+        const float sum = __fadd_rn(f2_lo(held), f2_hi(held));
+        if (__fmul_rn(__fsub_rn(top, c), lr) <= kTied ||
+            __fmul_rn(sum, ex2(__fmul_rn(__fsub_rn(m, top), lr))) >= 0.00390625f)
+            nt = nr = top;
+    }
     raise_refs(a, nt, nr, lt, lr);
 }
 
@@ -339,9 +352,10 @@ __device__ __forceinline__ float groups_max(const Group8<kBf16> *g) {
 template <bool kTBf16, bool kRBf16>
 __device__ __forceinline__ bool accumulate_near(const Group8<kTBf16> *gt, const Group8<kRBf16> *gr, Acc2 &a, float l,
                                                 float s) {
-    const float cm = groups_max(gr);
-    const bool fit = cm > kFloorZ;
-    if (__any_sync(0xffffffffu, fit && cm > a.mr)) raise_to(a, fit ? cm : a.mt, fit ? cm : a.mr, l, l);
+    const float ct = groups_max(gt), cr = groups_max(gr);
+    const bool fit = fminf(ct, cr) > kFloorZ;
+    if (__any_sync(0xffffffffu, fit && (ct > a.mt || cr > a.mr)))
+        raise_to(a, fit ? ct : -INFINITY, fit ? cr : -INFINITY, l, l);
     const float ml = __fmul_rn(-a.mr, l), h = __fmul_rn(0.5f, l);
     const f2_t s2 = f2(s, s), ml2 = f2(ml, ml), h2 = f2(h, h);
     f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;

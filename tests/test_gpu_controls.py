@@ -651,3 +651,84 @@ def test_score_controlled_at_a_small_last_segment(rows, vocab):
     act = np.ones(rows, np.uint8)
     res = B.score_controlled(xt, yt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), h, h)
     check_score(c, c, xt, yt, ids, act, res)
+
+
+def check_float64(ct, cr, x, y, ids, res):
+    """Logprobs and their difference within the bounds at the head of this file."""
+    xh, yh = host(x), host(y)
+    assert res.metrics["status"] == 0
+    for r, j in enumerate(ids):
+        t, u = ref.logp(ref.row(ct, xh[r], r)[0], j), ref.logp(ref.row(cr, yh[r], r)[0], j)
+        for got, want, off in ((res.logp_train, t, 1e-5), (res.logp_rollout, u, 1e-5), (res.dlogp, t - u, 2e-5)):
+            assert abs(float(got[r]) - want) <= off + 2.0 ** -23 * abs(want), (r, off, float(got[r]), want)
+
+
+def score_sides(ct, cr, x, y, ids):
+    ht, hr = (to_device(c) if c else None for c in (ct, cr))
+    if ct is cr:
+        hr = ht
+    return B.score_controlled(x, y, torch.from_numpy(ids).to(DEV), torch.ones(len(ids), dtype=torch.uint8, device=DEV), ht, hr)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1.0, 20.0, 100.0])
+@pytest.mark.parametrize("how", ["rollout_mask", "train_mask", "rollout_only", "train_only", "penalty", "bias"])
+def test_score_sides_whose_peaks_lie_apart(kind, scale, how):
+    """One side's controls take the other's peak away: at a low temperature the sides' sums then lie hundreds of
+    octaves apart, and each has to be kept beside its own maximum."""
+    rng = np.random.default_rng(41)
+    rows, vocab = 6, 20000
+    x = rng.normal(0, 3, (rows, vocab))
+    y = x + rng.normal(0, 2e-3, x.shape)
+    xt, yt = tensor(x, kind), tensor(y, kind)
+    top = [np.argsort(host(t), 1)[:, -40:] for t in (xt, yt)]
+    ids = np.array([np.setdiff1d(np.arange(500), top[0][r])[r] for r in range(rows)], np.int32)
+    s = np.full(rows, scale, np.float32)
+    one = {"scale": s}
+    if how in ("rollout_mask", "train_mask"):
+        words = np.full((rows, vocab // 32), 0xFFFFFFFF, np.uint32)
+        for r in range(rows):
+            for j in top[0][r]:
+                words[r, j // 32] &= ~np.uint32(1 << (j % 32))
+        masked = {"scale": s, "mask": words.view(np.int32)}
+        ct, cr = (one, masked) if how == "rollout_mask" else (masked, one)
+    elif how in ("rollout_only", "train_only"):
+        ct, cr = ({}, one) if how == "rollout_only" else (one, {})
+    elif how == "penalty":
+        hist = top[0].reshape(-1).astype(np.int32)
+        at = np.arange(rows, dtype=np.int64) * top[0].shape[1]
+        cr = {"scale": s, "history": hist, "hist_begin": at, "hist_split": at, "hist_end": at + top[0].shape[1],
+              "repetition": np.full(rows, 2.5, np.float32), "presence": np.full(rows, 4, np.float32)}
+        ct = one
+    else:
+        ct = {"scale": s, "bias_ids": top[0].astype(np.int32), "bias": np.full(top[0].shape, -30, np.float32)}
+        cr = one
+    check_float64(ct, cr, xt, yt, ids, score_sides(ct, cr, xt, yt, ids))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [150.0, -150.0, 3.0])
+@pytest.mark.parametrize("scale", [None, 10.0])
+def test_score_sides_shifted_against_each_other(kind, shift, scale):
+    """A shift of one side's logits leaves its logprobs as they are."""
+    rng = np.random.default_rng(42)
+    rows, vocab = 5, 30000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = {} if scale is None else {"scale": np.full(rows, scale, np.float32)}
+    x = rng.normal(0, 3, (rows, vocab))
+    xt, yt = tensor(x, kind), tensor(x + shift, kind)
+    check_float64(c, c, xt, yt, ids, score_sides(c, c, xt, yt, ids))
+
+
+@pytest.mark.parametrize("side", ["train", "rollout"])
+def test_score_one_side_rising(side):
+    """One side rises by 5 with each of a thread's tiles and the other stays, at a scale of 4: the rising side's
+    maximum may not carry the other's reference along."""
+    rng = np.random.default_rng(43)
+    rows, vocab = 4, 57344
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = {"scale": np.full(rows, 4, np.float32)}
+    flat = rng.normal(0, 1, (rows, vocab))
+    flat, rising = tensor(flat, "f32"), tensor(flat + 5.0 * (np.arange(vocab) // 8192), "f32")
+    x, y = (rising, flat) if side == "train" else (flat, rising)
+    check_float64(c, c, x, y, ids, score_sides(c, c, x, y, ids))
