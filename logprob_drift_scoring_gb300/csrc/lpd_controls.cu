@@ -356,14 +356,15 @@ __device__ __forceinline__ bool accumulate_near(const Group8<kTBf16> *gt, const 
     const bool fit = fminf(ct, cr) > kFloorZ;
     if (__any_sync(0xffffffffu, fit && (ct > a.mt || cr > a.mr)))
         raise_to(a, fit ? ct : -INFINITY, fit ? cr : -INFINITY, l, l);
-    const float ml = __fmul_rn(-a.mr, l), h = __fmul_rn(0.5f, l);
-    const f2_t s2 = f2(s, s), ml2 = f2(ml, ml), h2 = f2(h, h);
+    const f2_t s2 = f2(s, s), m2 = f2(a.mr, a.mr), l2 = f2(l, l), h2 = f2(0.5f * kLog2e, 0.5f * kLog2e);
     f2_t q = f2(0.f, 0.f), e0 = q, e1 = q, e2 = q, e3 = q;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
+        // the mean exponent from the difference to the reference: its rounding
+        // goes by the row's spread, not by where the row lies
         const f2_t xt = group_pair(gt[p >> 2], p & 3), xr = group_pair(gr[p >> 2], p & 3);
         const f2_t u = mul2(sub2(xt, xr), s2);
-        const f2_t e = ex2_2(fma2(add2(xt, xr), h2, ml2));
+        const f2_t e = ex2_2(fma2(u, h2, mul2(sub2(xr, m2), l2)));
         const f2_t v = mul2(u, u), w = mul2(e, u);
         q = add2(q, v);
         e0 = add2(e0, e);

@@ -732,3 +732,18 @@ def test_score_one_side_rising(side):
     flat, rising = tensor(flat, "f32"), tensor(flat + 5.0 * (np.arange(vocab) // 8192), "f32")
     x, y = (rising, flat) if side == "train" else (flat, rising)
     check_float64(c, c, x, y, ids, score_sides(c, c, x, y, ids))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", [60.0, 500.0, 1000.0, -700.0])
+@pytest.mark.parametrize("scale", [None, 10.0])
+def test_score_of_logits_with_an_offset(kind, offset, scale):
+    """A row's common offset is not part of its spread, so the logprobs' error may not grow with it."""
+    rng = np.random.default_rng(44)
+    rows, vocab = 5, 60000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    c = {} if scale is None else {"scale": np.full(rows, scale, np.float32)}
+    x = rng.normal(0, 3, (rows, vocab)) + offset
+    xt, yt = tensor(x, kind), tensor(x + rng.normal(0, 2e-3, x.shape), kind)
+    check_float64(c, c, xt, yt, ids, score_sides(c, c, xt, yt, ids))
+    check_float64(c, c, xt, xt, ids, score_sides(c, c, xt, xt, ids))
