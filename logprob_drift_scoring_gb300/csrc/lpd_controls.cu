@@ -167,7 +167,7 @@ struct StreamArgs {
 struct RowNumbers {
     float s, l, lt;    // scale (kScore: the rollout's), times log2 e, the train side's
     int same_scale;
-    float lse2, g;     // kGrad: lse in base 2 (upper part), -grad * scale * 2^(-lower part)
+    float at, top, g;  // kGrad: a logit, log2 p there (upper part), -grad * scale * 2^(lower part)
     const uint8_t *mask[2];  // each side's mask bits, null: everything allowed
     int none[2];             // nothing allowed
 };
@@ -183,7 +183,7 @@ struct Smem {
     int ok, abort_flag;
     int total;
     int line_base[kLines + 1];                  // touched columns in the lines in front
-    float gs, ll;                               // kGrad: grad * scale, the lower part of lse2
+    float gs, low;                              // kGrad: grad * scale, the lower part of log2 p at num.at
     alignas(16) uint4 lanes[256];
     alignas(16) uint32_t touched[kMode == kGrad ? 1 : 2][kLines * 128];  // [unit parity] where the stream looks: it leaves these out
     alignas(8) uint16_t before[kLines * 128];   // touched columns in the words in front, of the same line
@@ -703,19 +703,33 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 }
                 if (kMode == kGrad) {
                     const CtlRow &o = sm.row[0];
-                    double z = -CUDART_INF;
+                    // p_j = 2^(log2 p + (x_j - at) scale log2 e) from a logit `at` whose
+                    // probability is known, so that the exponents' rounding goes by the
+                    // row's spread, not by where it lies: the selected token, or, where
+                    // that lies far below, the log-sum-exp's own place.  A masked token
+                    // gives NaN.
+                    double at = 0.0, top = CUDART_NAN;
                     if (ctl_allows(o, id)) {
                         Two bias[kLast + 1];
                         bias_of(static_cast<int32_t>(id), bias);
                         const Two v = ctl_value(ctl_elem<kXBf16>(xrow, id), sm.id_word, o, bias[0], nullptr);
-                        z = (static_cast<double>(v.h) + static_cast<double>(v.l)) * static_cast<double>(o.scale);
+                        const double sc = o.scale, lp = a.logp[r];
+                        if (lp > -32.0) {
+                            at = v.h;
+                            top = lp - static_cast<double>(v.l) * sc;
+                        } else {
+                            const double lse = (static_cast<double>(v.h) + static_cast<double>(v.l)) * sc - lp;
+                            at = static_cast<float>(lse / sc);
+                            top = at * sc - lse;
+                        }
                     }
-                    const double l2 = (z - static_cast<double>(a.logp[r])) * 1.4426950408889634;
-                    const float h = static_cast<float>(l2), gs = __fmul_rn(a.grad[r], o.scale);
-                    sm.ll = static_cast<float>(l2 - static_cast<double>(h));
+                    top *= 1.4426950408889634;
+                    const float h = static_cast<float>(top), gs = __fmul_rn(a.grad[r], o.scale);
+                    sm.low = static_cast<float>(top - static_cast<double>(h));
                     sm.gs = gs;
-                    num.lse2 = h;
-                    num.g = __fmul_rn(-gs, ex2(-sm.ll));
+                    num.at = static_cast<float>(at);
+                    num.top = h;
+                    num.g = __fmul_rn(-gs, ex2(sm.low));
                 }
                 mbar_arrive(&sm.ready[b]);
             }
@@ -883,7 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     if (w0[q] & kBiased) bias_of(static_cast<int32_t>(col), bias);
                     const Two v = ctl_value(x0, w0[q], sm.row[0], bias[0], &slope);
                     if (kMode == kApply) return __fmaf_rn(v.h, s, __fmul_rn(v.l, s));
-                    const float p = ex2(__fadd_rn(__fsub_rn(__fmaf_rn(v.h, f, -sm.num[b].lse2), sm.ll), __fmul_rn(v.l, f)));
+                    const float e = __fmaf_rn(__fsub_rn(v.h, sm.num[b].at), f, sm.num[b].top);
+                    const float p = ex2(__fadd_rn(__fadd_rn(e, sm.low), __fmul_rn(v.l, f)));
                     return __fmul_rn(__fmul_rn(sm.gs, slope), __fsub_rn(col == id ? 1.f : 0.f, p));
                 };
                 const int m = min(kCap, total);
@@ -962,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
         const RowNumbers &num = sm.num[b];
         const bool same_scale = kTwo && num.same_scale != 0;
         const float n_s = num.s, n_l = num.l, n_lt = kTwo ? num.lt : 0.f;
-        const float n_lse2 = kMode == kGrad ? num.lse2 : 0.f, n_g = kMode == kGrad ? num.g : 0.f;
+        const float n_at = kMode == kGrad ? num.at : 0.f, n_top = kMode == kGrad ? num.top : 0.f, n_g = kMode == kGrad ? num.g : 0.f;
         // Masked columns, eight bits a group.  The mask's bytes come from global
         // memory, asked for a tile ahead; `last` keeps them inside the row's.
         const bool none0 = num.none[0] != 0, none1 = kTwo && num.none[kTwo ? 1 : 0] != 0;
@@ -1083,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                     acc = acc2_init();
                 }
             } else {
-                const f2_t f2f = f2(n_l, n_l), l2f = f2(-n_lse2, -n_lse2), g2f = f2(n_g, n_g);
+                const f2_t f2f = f2(n_l, n_l), at2 = f2(n_at, n_at), top2 = f2(n_top, n_top), g2f = f2(n_g, n_g);
                 const f2_t s2f = f2(n_s, n_s);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -1093,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const f2_t z = f2(v[2 * q], v[2 * q + 1]);
-                        const f2_t d = kMode == kApply ? mul2(z, s2f) : mul2(g2f, ex2_2(fma2(z, f2f, l2f)));
+                        const f2_t d = kMode == kApply ? mul2(z, s2f) : mul2(g2f, ex2_2(fma2(sub2(z, at2), f2f, top2)));
                         v[2 * q] = f2_lo(d);
                         v[2 * q + 1] = f2_hi(d);
                     }

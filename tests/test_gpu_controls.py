@@ -747,3 +747,34 @@ def test_score_of_logits_with_an_offset(kind, offset, scale):
     xt, yt = tensor(x, kind), tensor(x + rng.normal(0, 2e-3, x.shape), kind)
     check_float64(c, c, xt, yt, ids, score_sides(c, c, xt, yt, ids))
     check_float64(c, c, xt, xt, ids, score_sides(c, c, xt, xt, ids))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", [0.0, 60.0, 1000.0, -700.0])
+@pytest.mark.parametrize("scale", [1.0, 10.0])
+@pytest.mark.parametrize("vocab", [9001, 20000])
+def test_gradient_of_logits_with_an_offset(kind, offset, scale, vocab):
+    """The bound of test_gradient holds wherever the row lies; some columns touched, one row's token far below
+    the peak."""
+    rng = np.random.default_rng(45)
+    rows = 5
+    x = tensor(rng.normal(0, 3, (rows, vocab)) + offset, kind)
+    xh = host(x)
+    ids = np.argsort(xh, 1)[:, -7].astype(np.int32)
+    ids[1] = np.argmin(xh[1])
+    c = {"scale": np.full(rows, scale, np.float32), "bias_ids": ids[:, None] + np.array([[0, -1, 1]], np.int32),
+         "bias": rng.normal(0, 0.5, (rows, 3)).astype(np.float32)}
+    lp = np.array([ref.logp(ref.row(c, xh[r], r)[0], ids[r]) for r in range(rows)]).astype(np.float32)
+    g = rng.normal(0, 1, rows).astype(np.float32)
+    act = np.ones(rows, np.uint8)
+    out = torch.empty(rows, vocab, device=DEV)
+    B.lpd_logprob_backward_controlled(x, to_device(c), *(torch.from_numpy(v).to(DEV) for v in (ids, act, lp, g)), out)
+    got = host(out)
+    for r in range(rows):
+        z, slope = ref.row(c, xh[r], r)
+        p = np.exp(z - z[ids[r]] + np.float64(lp[r]))
+        hot = np.arange(vocab) == ids[r]
+        want = g[r] * slope * (hot - p)
+        # (a p below float32's smallest normal number, 2^-126, becomes 0: exponents are flushed)
+        tol = np.abs(g[r] * slope) * (1e-5 * p + 2.0 ** -24 * hot + 2.0 ** -126) + 2.0 ** -21 * np.abs(want)
+        assert np.all(np.abs(got[r] - want) <= tol), (r, np.max(np.abs(got[r] - want) - tol))
