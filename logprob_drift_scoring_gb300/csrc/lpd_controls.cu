@@ -166,7 +166,7 @@ struct StreamArgs {
 // What the stream needs of a row, written by the scouts.
 struct RowNumbers {
     float s, l, lt;    // scale (kScore: the rollout's), times log2 e, the train side's
-    int same_scale;
+    int same_scale;    // of at least kLeastNearScale
     float at, top, g;  // kGrad: a logit, log2 p there (upper part), -grad * scale * 2^(lower part)
     const uint8_t *mask[2];  // each side's mask bits, null: everything allowed
     int none[2];             // nothing allowed
@@ -270,6 +270,17 @@ constexpr float kNear2 = 0.015625f;  // sum of u^2 over a thread's sixteen colum
 // kFloorZ leave this path.
 constexpr uint32_t kFillBits = 0xf149u;
 constexpr float kFloorZ = -1e29f;
+// Below this scale -1e30 need not be far below the others: each side of a column
+// is then summed by itself, and a masked one left out.
+constexpr float kLeastNearScale = 1e-20f;
+
+// A side's factor from logits to base-2 exponents.  Scales from 2.4e38 on would
+// make it infinite (and 0 times it NaN); differences that the largest number
+// does not push below 2^-126 are below 4e-37.
+__device__ __forceinline__ float exponent_factor(float scale) {
+    const float l = __fmul_rn(scale, kLog2e);
+    return l > FLT_MAX ? FLT_MAX : l;
+}
 
 // expm1(u) / u up to u^5 / 720: the next term is u^6 / 5040 = 5e-8 at 1/4
 __device__ __forceinline__ float expm1_ratio(float u) {
@@ -691,10 +702,10 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                 RowNumbers &num = sm.num[b];
                 const float s = sm.row[kLast].scale;
                 num.s = s;
-                num.l = __fmul_rn(s, kLog2e);
+                num.l = exponent_factor(s);
                 if (kTwo) {
-                    num.lt = __fmul_rn(sm.row[0].scale, kLog2e);
-                    num.same_scale = sm.row[0].scale == s ? 1 : 0;
+                    num.lt = exponent_factor(sm.row[0].scale);
+                    num.same_scale = sm.row[0].scale == s && s >= kLeastNearScale ? 1 : 0;
                 }
 #pragma unroll
                 for (int side = 0; side <= kLast; ++side) {
@@ -1150,7 +1161,7 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_consta
     float s_t = a.c[0].scale ? a.c[0].scale[r] : 1.f, s_r = a.c[1].scale ? a.c[1].scale[r] : 1.f;
     if (!(s_t > 0.f && s_t <= FLT_MAX)) s_t = CUDART_NAN_F;
     if (!(s_r > 0.f && s_r <= FLT_MAX)) s_r = CUDART_NAN_F;
-    const float lt = __fmul_rn(s_t, kLog2e), lr = __fmul_rn(s_r, kLog2e);
+    const float lt = exponent_factor(s_t), lr = exponent_factor(s_r);
     Acc acc = acc_init();
     const int n = a.n_segs * kStates;
     for (int k = lane; k < n; k += 32) {
@@ -1176,12 +1187,13 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_consta
         bad = LPD_STATUS_TOKEN_OOB;
     } else {
         const double2 x = a.pick[i];
-        const double mt = static_cast<double>(s_t) * acc.mt, mr = static_cast<double>(s_r) * acc.mr;
-        const double xt = s_t * x.x, xr = s_r * x.y;
+        // differences to the maxima before the scale: at a scale of 1e15 a
+        // logarithm is lost beside the scaled maximum even in double
+        const double xt = s_t * (x.x - acc.mt), xr = s_r * (x.y - acc.mr);
         const double st = acc.st, sr = acc.sr, dd = acc.dd;
-        const double lse_t = mt + log(st), lse_r = mr + log(sr);
+        const double lse_t = log(st), lse_r = log(sr);  // above the scaled maxima
         const double ratio = fabs(dd) < 0.5 * st ? log1p(-dd / st) : log(sr / st);
-        d = ((xt - xr) - (mt - mr)) + ratio;
+        d = (xt - xr) + ratio;
         pt = xt - lse_t;
         pr = xr - lse_r;
         if (!(isfinite(lse_t) && isfinite(lse_r) && isfinite(xt) && isfinite(xr))) bad = LPD_STATUS_NONFINITE;

@@ -778,3 +778,38 @@ def test_gradient_of_logits_with_an_offset(kind, offset, scale, vocab):
         # (a p below float32's smallest normal number, 2^-126, becomes 0: exponents are flushed)
         tol = np.abs(g[r] * slope) * (1e-5 * p + 2.0 ** -24 * hot + 2.0 ** -126) + 2.0 ** -21 * np.abs(want)
         assert np.all(np.abs(got[r] - want) <= tol), (r, np.max(np.abs(got[r] - want) - tol))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e-20, 1e6, 1e20, 1e37, 3e38])
+def test_scales_at_the_ends_of_their_range(kind, scale):
+    """Any finite scale > 0: nothing masked counts at a tiny one, equal maxima share the sum at a huge one."""
+    rng = np.random.default_rng(46)
+    rows, vocab = 4, 20000
+    # (the differences times the scale stay inside float32, as the logprobs have to)
+    x = rng.integers(-60, 60, (rows, vocab)) / 64
+    top = tensor(x, kind)
+    xh = host(top)
+    words = rng.integers(0, 1 << 32, (rows, vocab // 32), dtype=np.uint64).astype(np.uint32)
+    ids = np.array([rng.choice(np.flatnonzero(xh[r] == xh[r].max())) for r in range(rows)], np.int32)
+    for r in range(rows):
+        words[r, ids[r] // 32] |= np.uint32(1 << (ids[r] % 32))
+    c = {"scale": np.full(rows, scale, np.float32), "mask": words.view(np.int32)}
+    if scale < 1e38:  # (else the logprob passes float32)
+        ids[1] = np.flatnonzero(np.isfinite(ref.row(c, xh[1], 1)[0]) & (xh[1] < 0.3) & (xh[1] > 0.2))[0]
+    s = score_sides(c, c, top, top, ids)
+    check_float64(c, c, top, top, ids, s)
+    y = tensor(x + rng.integers(0, 2, x.shape) / 128, kind)
+    check_float64(c, c, top, y, ids, score_sides(c, c, top, y, ids))
+    g = torch.ones(rows, device=DEV)
+    out = torch.empty(rows, vocab, device=DEV)
+    act = torch.ones(rows, dtype=torch.uint8, device=DEV)
+    B.lpd_logprob_backward_controlled(top, to_device(c), torch.from_numpy(ids).to(DEV), act, s.logp_train, g, out)
+    got, lp = host(out), host(s.logp_train)
+    for r in (0, 2, 3):  # (row 1's logprob says little about the others' where the scale is huge)
+        z, slope = ref.row(c, xh[r], r)
+        p = np.exp(z - z[ids[r]] + lp[r])
+        hot = np.arange(vocab) == ids[r]
+        want = slope * (hot - p)
+        tol = np.abs(slope) * (1e-5 * p + 2.0 ** -24 * hot) + 2.0 ** -21 * np.abs(want)
+        assert np.all(np.abs(got[r] - want) <= tol + 1e-37), (r, np.max(np.abs(got[r] - want) - tol))
