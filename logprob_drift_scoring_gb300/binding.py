@@ -608,6 +608,16 @@ def _same_rows(n, device, **tensors):
             raise ValueError(f"{name} must be a dense {kind} tensor of {n} values on {device}")
 
 
+def _bytes(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def _buffer(name, t, device, size=0):
+    """A dense tensor's storage that the library writes as bytes (None: its own check)."""
+    if t is not None and (not t.is_contiguous() or t.device != device or _bytes(t) < size):
+        raise ValueError(f"{name} must be a dense tensor on {device}, of {size} bytes at least")
+
+
 class _on:
     """The device of the call's tensors made current, where it is not."""
 
@@ -649,13 +659,14 @@ def lpd_score_controlled(train, rollout, train_controls, rollout_controls, token
     _same_rows(train.shape[0], train.device, token_ids=(token_ids, torch.int32), action_mask=(action_mask, torch.uint8),
                out_logp_train=(out_logp_train, torch.float32), out_logp_rollout=(out_logp_rollout, torch.float32),
                out_dlogp=(out_dlogp, torch.float32))
+    _buffer("out_metrics", out_metrics, train.device, METRICS_BYTES)
+    _buffer("workspace", workspace, train.device)
     ct, cr = _controls(train_controls, train), _controls(rollout_controls, rollout)
     with _on(train):
         rc = lib().lpd_score_controlled(ctypes.byref(t), ctypes.byref(r), ct, cr, train.shape[0], train.shape[1],
                                         _ptr(token_ids), _ptr(action_mask), float(clip_lo), float(clip_hi),
                                         _ptr(out_logp_train), _ptr(out_logp_rollout), _ptr(out_dlogp),
-                                        _ptr(out_metrics), _ptr(workspace),
-                                        workspace.numel() if workspace is not None else 0, _stream(stream))
+                                        _ptr(out_metrics), _ptr(workspace), _bytes(workspace), _stream(stream))
     _check(rc, "lpd_score_controlled")
 
 
@@ -743,12 +754,13 @@ def lpd_block_matmul(a, b, out, workspace, stream=None) -> None:
         raise ValueError(f"A {[m, k]}, B {list(b.values.shape)} and out {list(out.shape)} do not fit")
     if out.dim() != 2 or (n > 1 and out.stride(1) != 1):
         raise ValueError("out must have contiguous columns")
-    if not a.values.device == b.values.device == out.device == workspace.device:
-        raise ValueError("the operands, out and the workspace must be on one device")
+    if not a.values.device == b.values.device == out.device:
+        raise ValueError("the operands and out must be on one device")
+    _buffer("workspace", workspace, out.device)
     with _on(out):
         rc = lib().lpd_block_matmul(ctypes.byref(a._struct), ctypes.byref(b._struct), m, n, k, _ptr(out),
                                     _dtype_code(out), _row_stride(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(stream))
+                                    _bytes(workspace), _stream(stream))
     _check(rc, "lpd_block_matmul")
 
 

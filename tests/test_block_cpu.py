@@ -140,3 +140,15 @@ def test_rows_that_overlap_keep_their_stride(monkeypatch):
     assert lib.calls[-1][1][2] == 256
     B.lpd_block_matmul(one, b, torch.zeros(130).expand(1, 130), ws, stream=0)
     assert lib.calls[-1][1][7] == 130
+
+
+def test_a_product_workspace_of_repeated_elements_or_elsewhere_is_refused(monkeypatch):
+    a, b = (B.block_empty(r, 256, torch.float8_e4m3fn, device="cpu") for r in (40, 130))
+    out = torch.zeros(40, 130)
+    lib = Recorder(monkeypatch)
+    for bad in (torch.zeros(1).expand(4096), torch.zeros(4096, device="meta"), torch.zeros(8192)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            B.lpd_block_matmul(a, b, out, bad, stream=0)
+    assert lib.calls == []
+    B.lpd_block_matmul(a, b, out, torch.zeros(4096), stream=0)
+    assert lib.calls[-1][1][9] == 4096 * 4

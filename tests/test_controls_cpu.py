@@ -224,3 +224,27 @@ def test_a_mask_table_of_no_rows_is_not_no_mask(recorded):
 
 def test_a_mask_table_of_no_rows_needs_mask_row():
     assert apply_rc(c=B.Controls(mask=torch.zeros(0, 2, dtype=torch.int32))._struct) == B.LPD_ERR_BAD_SIZE
+
+
+def test_score_buffers_that_are_too_small_or_elsewhere_are_refused(recorded):
+    """The library takes addresses: a repeated element's storage, a short record or another device's memory
+    would be written past its end."""
+    x, f = torch.zeros(4, 160), torch.zeros(4)
+    ids, act = torch.zeros(4, dtype=torch.int32), torch.ones(4, dtype=torch.uint8)
+    byte = lambda n, **kw: torch.zeros(n, dtype=torch.uint8, **kw)  # noqa: E731
+    met, ws = byte(B.METRICS_BYTES), byte(1 << 16)
+
+    def call(met, ws):
+        B.lpd_score_controlled(x, x, None, None, ids, act, 0.8, 1.2, f, f, f, met, ws, stream=0)
+
+    for bad in (byte(B.METRICS_BYTES - 1), byte(1).expand(B.METRICS_BYTES), byte(2 * B.METRICS_BYTES)[::2],
+                byte(B.METRICS_BYTES, device="meta")):
+        with pytest.raises(ValueError, match="out_metrics"):
+            call(bad, ws)
+    for bad in (byte(1).expand(1 << 16), byte(1 << 17)[::2], byte(1 << 16, device="meta")):
+        with pytest.raises(ValueError, match="workspace"):
+            call(met, bad)
+    assert recorded == []
+    call(met, ws.view(torch.float32))
+    assert recorded[0][1][-2] == 1 << 16
+    call(None, None)  # (NULL: the library's to refuse)
