@@ -24,6 +24,7 @@
 // kernel's instructions).
 #pragma once
 
+#include <cfloat>
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -121,7 +122,8 @@ __device__ __forceinline__ Two bias_sum(const int32_t *ids, const float *values,
     for (int e = 0; e < n; ++e)
         if (ids[e] == token) s += static_cast<double>(values[e]);
     const float h = static_cast<float>(s);
-    return Two{h, static_cast<float>(s - static_cast<double>(h))};
+    // an infinite sum (a ban) has no low part
+    return Two{h, fabsf(h) <= FLT_MAX ? static_cast<float>(s - static_cast<double>(h)) : 0.f};
 }
 
 // x3 of a touched, allowed token with count word w.  Two floats, so that the

@@ -813,3 +813,30 @@ def test_scales_at_the_ends_of_their_range(kind, scale):
         want = slope * (hot - p)
         tol = np.abs(slope) * (1e-5 * p + 2.0 ** -24 * hot) + 2.0 ** -21 * np.abs(want)
         assert np.all(np.abs(got[r] - want) <= tol + 1e-37), (r, np.max(np.abs(got[r] - want) - tol))
+
+
+def test_a_bias_of_minus_infinity_bans_a_token():
+    """Alone, beside another bias of the same token, and on a token with a penalty."""
+    rng = np.random.default_rng(52)
+    rows, vocab = 4, 5000
+    x = rng.normal(0, 3, (rows, vocab))
+    xt = tensor(x, "bf16")
+    ids = rng.integers(100, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=50, masks=0, bias=0)
+    c["history"][:20] = np.arange(20)
+    c["hist_begin"][:], c["hist_split"][:], c["hist_end"][:] = 0, 5, 40
+    c["bias_ids"] = np.tile(np.array([[7, 30, 30, 2, 50]], np.int32), (rows, 1))
+    c["bias"] = np.tile(np.array([[-np.inf, -np.inf, 4.0, -np.inf, 1.0]], np.float32), (rows, 1))
+    h = to_device(c)
+    out = B.controls_apply(xt, h, torch.float32)
+    check_apply(c, xt, "f32", out)
+    assert bool(torch.isneginf(out[:, [7, 30, 2]]).all()) and int(torch.isinf(out).sum()) == 3 * rows
+    act = np.ones(rows, np.uint8)
+    for ct, cr, ht, hr in ((c, c, h, h), (c, {}, h, None)):
+        s = B.score_controlled(xt, xt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), ht, hr)
+        check_float64(ct, cr, xt, xt, ids, s)
+    dx = torch.empty(rows, vocab, device=DEV)
+    B.lpd_logprob_backward_controlled(xt, h, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV),
+                                      B.score_controlled(xt, xt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), h, h).logp_train,
+                                      torch.ones(rows, device=DEV), dx)
+    assert bool(torch.isfinite(dx).all()) and bool((dx[:, [7, 30, 2]] == 0).all())
