@@ -148,7 +148,7 @@ __device__ __forceinline__ Two ctl_value(float x, uint32_t w, const CtlRow &o, T
             const float nf = static_cast<float>(n);
             const float f = __fmul_rn(o.freq, nf);
             v = two_add(v, -f);
-            v = two_add(v, -__fmaf_rn(o.freq, nf, -f));
+            if (fabsf(f) <= FLT_MAX) v = two_add(v, -__fmaf_rn(o.freq, nf, -f));  // (an infinite one has no residual)
             v = two_add(v, -o.pres);
         }
     }

@@ -840,3 +840,22 @@ def test_a_bias_of_minus_infinity_bans_a_token():
                                       B.score_controlled(xt, xt, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), h, h).logp_train,
                                       torch.ones(rows, device=DEV), dx)
     assert bool(torch.isfinite(dx).all()) and bool((dx[:, [7, 30, 2]] == 0).all())
+
+
+@pytest.mark.parametrize("name", ["frequency", "presence"])
+def test_an_infinite_penalty_bans_repeats(name):
+    """x1 - inf is -inf for the generated tokens; frequency * 0 is not formed for the prompt's."""
+    rng = np.random.default_rng(53)
+    rows, vocab = 3, 3000
+    xt = tensor(rng.normal(0, 3, (rows, vocab)), "f32")
+    ids = rng.integers(100, vocab, rows).astype(np.int32)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=40, masks=0, bias=0, parts=("repetition", "frequency", "presence"))
+    c["history"][:] = np.arange(41)
+    c["hist_begin"][:], c["hist_split"][:], c["hist_end"][:] = 0, 20, 40
+    c[name][:] = np.inf
+    c["bias_ids"], c["bias"] = np.full((rows, 1), 25, np.int32), np.full((rows, 1), 3.0, np.float32)
+    h = to_device(c)
+    out = B.controls_apply(xt, h)
+    check_apply(c, xt, "f32", out)
+    assert bool(torch.isneginf(out[:, 20:40]).all()) and int(torch.isinf(out).sum()) == 20 * rows
+    check_float64(c, c, xt, xt, ids, score_sides(c, c, xt, xt, ids))
