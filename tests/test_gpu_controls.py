@@ -859,3 +859,73 @@ def test_an_infinite_penalty_bans_repeats(name):
     check_apply(c, xt, "f32", out)
     assert bool(torch.isneginf(out[:, 20:40]).all()) and int(torch.isinf(out).sum()) == 20 * rows
     check_float64(c, c, xt, xt, ids, score_sides(c, c, xt, xt, ids))
+
+
+@pytest.mark.parametrize("rows,vocab,kind", [(1, 129025, "bf16"), (1, 129031, "f32"), (2, 172033, "bf16"), (2, 172001, "f32"),
+                                             (160, 172033, "bf16"), (160, 172040, "bf16"), (160, 172001, "f32")])
+def test_elementwise_forms_at_the_seams_of_their_units(rows, vocab, kind):
+    """Last units of a few columns, and rows longer than a unit where rows are many: on 16-byte boundaries and off
+    them, in place too."""
+    rng = np.random.default_rng(vocab)
+    x = rng.normal(0, 1, (rows, vocab)).astype(np.float32)
+    xt = tensor(x, kind)
+    ids = np.full(rows, vocab - 1, np.int32)
+    ids[rows // 2:] = rng.integers(0, vocab, rows - rows // 2)
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=300, masks=2, bias=4)
+    c["history"][:30] = np.arange(vocab - 30, vocab)
+    c["hist_begin"][:], c["hist_split"][:], c["hist_end"][:] = 0, 10, 280
+    h = to_device(c)
+    out = B.controls_apply(xt, h)
+    some = sorted({0, rows // 2, rows - 1})
+    sub = lambda v: v[some] if len(v) == rows else v  # noqa: E731
+    cs = {k: (v if k in ("history", "mask") else sub(v)) for k, v in c.items()}
+    check_apply(cs, xt[some], kind, out[some])
+    again = xt.clone()
+    B.lpd_controls_apply(again, h, again)
+    assert torch.equal(again, out)
+    lp = np.zeros(rows, np.float32)
+    lp[some] = [ref.logp(ref.row(cs, host(xt[r:r + 1])[0], i)[0], ids[r]) for i, r in enumerate(some)]
+    g = rng.normal(0, 1, rows).astype(np.float32)
+    act = np.ones(rows, np.uint8)
+    dx = torch.empty(rows, vocab, device=DEV)
+    B.lpd_logprob_backward_controlled(xt, h, *(torch.from_numpy(v).to(DEV) for v in (ids, act, lp, g)), dx)
+    for i, r in enumerate(some):
+        z, slope = ref.row(cs, host(xt[r:r + 1])[0], i)
+        p = np.exp(z - z[ids[r]] + np.float64(lp[r]))
+        hot = np.arange(vocab) == ids[r]
+        want = g[r] * slope * (hot - p)
+        tol = np.abs(g[r] * slope) * (1e-5 * p + 2.0 ** -24 * hot + 2.0 ** -126) + 2.0 ** -21 * np.abs(want)
+        assert np.all(np.abs(host(dx[r:r + 1])[0] - want) <= tol), r
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_score_of_rows_longer_than_a_unit(kind):
+    """More than 172032 columns with many rows, two units each, under controls that reach into both."""
+    rng = np.random.default_rng(51)
+    rows, vocab = 320, 200003
+    x = torch.randn(rows, vocab, device=DEV, generator=torch.Generator(DEV).manual_seed(51)).to(KINDS[kind])
+    y = (x.float() + 1e-3).to(KINDS[kind])
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    ids[::3] = rng.integers(172032, vocab, len(ids[::3]))
+    c = ref.random_controls(rng, rows, vocab, keep=ids, history=3000, masks=3, bias=5)
+    h = to_device(c)
+    act = np.ones(rows, np.uint8)
+    res = B.score_controlled(x, y, torch.from_numpy(ids).to(DEV), torch.from_numpy(act).to(DEV), h, h)
+    assert res.metrics["status"] == 0
+    for r in (0, 3, 151, 152, 319):
+        for v, got in ((x, res.logp_train), (y, res.logp_rollout)):
+            want = ref.logp(ref.row(c, host(v[r:r + 1])[0], r)[0], ids[r])
+            assert abs(float(got[r]) - want) <= 1e-5 + 2.0 ** -23 * abs(want), r
+    at = np.array([3, 152, 319])
+    few = to_device({k: (v if k in ("history", "mask") else v[at]) for k, v in c.items()})
+    part = B.score_controlled(x[at], y[at], torch.from_numpy(ids[at]).to(DEV), torch.ones(3, dtype=torch.uint8, device=DEV), few, few)
+    for k in ("logp_train", "logp_rollout", "dlogp"):
+        assert torch.equal(getattr(res, k)[at], getattr(part, k)), k
+
+
+def test_zero_rows():
+    x = torch.empty(0, 300, device=DEV)
+    none = lambda t: torch.empty(0, dtype=t, device=DEV)  # noqa: E731
+    s = B.score_controlled(x, x, none(torch.int32), none(torch.uint8), B.Controls(scale=none(torch.float32)))
+    assert s.metrics["n_active"] == 0 and s.metrics["flags"] & B.LPD_FLAG_NO_ACTIVE
+    B.lpd_logprob_backward_controlled(x, None, none(torch.int32), none(torch.uint8), none(torch.float32), none(torch.float32), x.clone())
