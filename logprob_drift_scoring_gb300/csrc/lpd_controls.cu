@@ -282,6 +282,8 @@ __device__ __forceinline__ float exponent_factor(float scale) {
     return l > FLT_MAX ? FLT_MAX : l;
 }
 
+constexpr float kLargestLow = 8.f;  // octaves
+
 // expm1(u) / u up to u^5 / 720: the next term is u^6 / 5040 = 5e-8 at 1/4
 __device__ __forceinline__ float expm1_ratio(float u) {
     float p = __fmaf_rn(u, 1.f / 720.f, 1.f / 120.f);
@@ -413,8 +415,15 @@ __device__ __forceinline__ void accumulate_far(const f2_t *vt, const f2_t *vr, A
     a.dd = add2(a.dd, sd);
 }
 
-// One pair of controlled logits (h + l of each side) into the state; an -inf
-// adds nothing.
+// A value whose lower part cannot lift its term far above one whose reference
+// is the upper part: at scales or logits so large that it would, the value is
+// the float.
+__device__ __forceinline__ Two beside(Two v, float l) {
+    return Two{v.h, fabsf(__fmul_rn(v.l, l)) <= kLargestLow ? v.l : 0.f};
+}
+
+// One pair of controlled logits (h + l of each side, see `beside`) into the
+// state; an -inf adds nothing.
 __device__ __forceinline__ void accumulate_pair(Two xt, Two xr, Acc2 &a, float lt, float lr, float s, bool same_scale) {
     if (xt.h > a.mt || xr.h > a.mr) raise_to(a, xt.h, xr.h, lt, lr);
     const float er = ex2(__fmaf_rn(xr.l, lr, __fmul_rn(__fsub_rn(xr.h, a.mr), lr)));
@@ -872,8 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_kernel(const __grid_consta
                                 const bool in1 = sm.row[0].mask == sm.row[1].mask && sm.row[0].none == sm.row[1].none
                                                      ? in0
                                                      : ctl_allows(sm.row[1], col[v]);
-                                const Two y0 = ctl_value(x0, t0, sm.row[0], bias[0], nullptr);
-                                const Two y1 = ctl_value(x1, t1, sm.row[1], bias[1], nullptr);
+                                const Two y0 = beside(ctl_value(x0, t0, sm.row[0], bias[0], nullptr), lt);
+                                const Two y1 = beside(ctl_value(x1, t1, sm.row[1], bias[1], nullptr), lr);
                                 if (in0) vt[v] = y0;
                                 if (in1) vr[v] = y1;
                             }

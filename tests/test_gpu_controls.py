@@ -929,3 +929,49 @@ def test_zero_rows():
     s = B.score_controlled(x, x, none(torch.int32), none(torch.uint8), B.Controls(scale=none(torch.float32)))
     assert s.metrics["n_active"] == 0 and s.metrics["flags"] & B.LPD_FLAG_NO_ACTIVE
     B.lpd_logprob_backward_controlled(x, None, none(torch.int32), none(torch.uint8), none(torch.float32), none(torch.float32), x.clone())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("low", [-3e38, -1e35])
+def test_touched_tokens_of_the_lowest_logits(kind, low):
+    """A penalised token far below the others has a rounding error, the two floats' lower part, of 1e28 and more:
+    it may not count beside the reference."""
+    rng = np.random.default_rng(61)
+    rows, vocab = 6, 1200
+    x = rng.normal(0, 1, (rows, vocab))
+    where = rng.random(x.shape) < 0.9
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    where[np.arange(rows), ids] = False
+    y = x + 1e-3
+    x[where], y[where] = low, -np.inf
+    c = ref.random_controls(rng, rows, vocab, history=300, masks=0, bias=3)
+    c["repetition"][:] = [0.77, 0.9, 0.99, 1.01, 1.1, 0.7]
+    for a, b in ((x, y), (y, x), (x, x)):
+        xt, yt = tensor(a, kind), tensor(b, kind)
+        for ct, cr in ((c, c), (c, {}), ({}, c)):
+            with np.errstate(invalid="ignore"):
+                check_float64(ct, cr, xt, yt, ids, score_sides(ct, cr, xt, yt, ids))
+
+
+@pytest.mark.parametrize("scale", [1e8, 1e12, 1e30])
+def test_touched_tokens_at_huge_scales(scale):
+    """A touched token that is the largest has a logprob of 0, and far below it the scaled gap, to float32's
+    rounding of the logits."""
+    rng = np.random.default_rng(62)
+    rows, vocab = 5, 3000
+    x = rng.normal(0, 1, (rows, vocab)).astype(np.float32)
+    ids = np.array([17, 18, 19, 20, 21], np.int32)
+    x[np.arange(rows), ids] = 9.1 + rng.random(rows)
+    c = {"scale": np.full(rows, scale, np.float32), "history": ids, "hist_begin": np.arange(rows), "hist_split": np.arange(rows),
+         "hist_end": np.arange(rows) + 1, "repetition": np.full(rows, 1.3, np.float32), "presence": np.full(rows, 0.1, np.float32)}
+    c = {k: v.astype(np.int64) if k.startswith("hist_") else v for k, v in c.items()}
+    t = tensor(x, "f32")
+    s = score_sides(c, c, t, t, ids)
+    assert s.metrics["status"] == 0 and bool((s.logp_train.abs() <= 1e-5).all()) and bool((s.dlogp == 0).all())
+    other = np.array([40, 41, 42, 43, 44], np.int32)
+    s = score_sides(c, c, t, t, other)
+    for r in range(rows):
+        z, _ = ref.row(c, host(t)[r], r)
+        want = ref.logp(z, other[r])
+        # the largest logit, rounded to float32 where the scale leaves no room for its lower part
+        assert abs(float(s.logp_train[r]) - want) <= 2.0 ** -23 * abs(want) + 2.0 ** -24 * abs(z.max())
