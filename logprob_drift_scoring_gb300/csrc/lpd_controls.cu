@@ -1201,7 +1201,12 @@ __global__ void __launch_bounds__(256) score_finalize_kernel(const __grid_consta
         const double xt = s_t * (x.x - acc.mt), xr = s_r * (x.y - acc.mr);
         const double st = acc.st, sr = acc.sr, dd = acc.dd;
         const double lse_t = log(st), lse_r = log(sr);  // above the scaled maxima
-        const double ratio = fabs(dd) < 0.5 * st ? log1p(-dd / st) : log(sr / st);
+        // dd is st - sr with an error relative to itself where the sides move
+        // together.  Where they do not (thousands on one side before its
+        // dominant token is met, a few on the other) it may have lost more than
+        // the sums, and has to fit them to their roundings: some 50 a side, 2^-17.
+        const bool near = fabs(dd) < 0.5 * st && fabs(dd - (st - sr)) <= 7.6e-6 * st;
+        const double ratio = near ? log1p(-dd / st) : log(sr / st);
         d = (xt - xr) + ratio;
         pt = xt - lse_t;
         pr = xr - lse_r;

@@ -975,3 +975,18 @@ def test_touched_tokens_at_huge_scales(scale):
         want = ref.logp(z, other[r])
         # the largest logit, rounded to float32 where the scale leaves no room for its lower part
         assert abs(float(s.logp_train[r]) - want) <= 2.0 ** -23 * abs(want) + 2.0 ** -24 * abs(z.max())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [20.0, 50.0, 300.0])
+def test_score_of_a_sharp_side_beside_a_flat_one(kind, scale):
+    """One side's sum is a few terms from the start. The other's is thousands until its dominant token, a biased
+    one, is met: the rounding of those may not stay in the difference of the logprobs."""
+    rng = np.random.default_rng(63)
+    rows, vocab = 20, 30000
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    t = tensor(rng.normal(0, 1, (rows, vocab)), kind)
+    sharp = {"scale": np.full(rows, scale, np.float32)}
+    flat = {"bias_ids": ids[:, None], "bias": np.full((rows, 1), 40.0, np.float32)}
+    check_float64(sharp, flat, t, t, ids, score_sides(sharp, flat, t, t, ids))
+    check_float64(flat, sharp, t, t, ids, score_sides(flat, sharp, t, t, ids))
