@@ -990,3 +990,45 @@ def test_score_of_a_sharp_side_beside_a_flat_one(kind, scale):
     flat = {"bias_ids": ids[:, None], "bias": np.full((rows, 1), 40.0, np.float32)}
     check_float64(sharp, flat, t, t, ids, score_sides(sharp, flat, t, t, ids))
     check_float64(flat, sharp, t, t, ids, score_sides(flat, sharp, t, t, ids))
+
+
+@pytest.mark.parametrize("xk,yk", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("vocab", [600, 9003, 57346])
+def test_column_slices(xk, yk, vocab):
+    """Rows that start anywhere in a wider tensor, the sides and the output at different places: the same bits as
+    dense ones, nothing written around them."""
+    rng = np.random.default_rng(71)
+    rows = 5
+    ids = rng.integers(0, vocab, rows).astype(np.int32)
+    h = to_device(ref.random_controls(rng, rows, vocab, keep=ids, history=300))
+    x = tensor(rng.normal(0, 3, (rows, vocab)), xk)
+    y = (x.float() + 2e-3).to(KINDS[yk])
+
+    def sliced(t, lead, behind):
+        wide = torch.full((rows + 2, lead + vocab + behind), 7.0, dtype=t.dtype, device=DEV)
+        wide[1:-1, lead:lead + vocab] = t
+        return wide, wide[1:-1, lead:lead + vocab]
+
+    idt, act = torch.from_numpy(ids).to(DEV), torch.ones(rows, dtype=torch.uint8, device=DEV)
+    dense = B.score_controlled(x, y, idt, act, h, h)
+    want = B.controls_apply(x, h)
+    g = torch.randn(rows, device=DEV)
+    grad = torch.empty(rows, vocab, device=DEV)
+    B.lpd_logprob_backward_controlled(x, h, idt, act, dense.logp_train, g, grad)
+    for a, b, o in ((3, 6, 1), (1, 0, 5), (8, 5, 0)):
+        (_, xs), (_, ys) = sliced(x, a, 2), sliced(y, b, 3)
+        s = B.score_controlled(xs, ys, idt, act, h, h)
+        for k in ("logp_train", "logp_rollout", "dlogp"):
+            assert torch.equal(getattr(s, k), getattr(dense, k)), (k, a, b)
+        for wide, out in (sliced(torch.zeros_like(x), o, a), sliced(torch.zeros_like(grad), o, b)):
+            guard = wide.clone()
+            if out.dtype == torch.float32:
+                B.lpd_logprob_backward_controlled(xs, h, idt, act, dense.logp_train, g, out)
+                # A column at a unit's edge is a scout's or the stream's by its place; exponents to -126 carry
+                # three roundings of 2^-24 in each, 126 * 3 * 2^-24 * ln 2 = 1.6e-5 of p.
+                assert bool(((out - grad).abs() <= 4e-5 * (grad.abs() + 2.0 ** -126)).all())
+            if out.dtype == x.dtype:
+                B.lpd_controls_apply(xs, h, out)
+                assert torch.equal(out, want)
+            out.zero_()
+            assert torch.equal(wide, guard)
