@@ -512,6 +512,11 @@ int lpd_score_fused_transformed(const void *hidden_train, const void *hidden_rol
  *     x3 = x2 + (the sum of bias[r, e] over the entries e with bias_ids[r, e] == j)
  *     z  = (bit j of the row's mask is 0) ? -inf : scale[r] * x3
  *
+ * The order is fixed: an engine that adds its biases in front of the repetition
+ * penalty, or masks behind the temperature with a finite value, samples from
+ * another distribution.  An infinite bias, frequency or presence bans a token
+ * (-inf).  Intermediate values are sums of two floats; where one passes float32's
+ * range the value is infinite.
  * A NULL array leaves its step out (scale: 1).  Every array is in device memory
  * and dense but the mask, and holds one entry a row where a row count is given;
  * the struct itself is a host struct, read during the call.
@@ -553,14 +558,14 @@ typedef struct {
 } lpd_controls;
 
 /* The controlled logits z of every row, for the sampler: out [n_rows,
- * out_row_stride] of out_dtype, columns [0, vocab) written, each value rounded
- * once.  Logits in masked places are not looked at: they may be NaN or
- * infinite.  A row whose mask allows nothing is -inf throughout.  `out` may be
- * the logits themselves (same pointer, type and stride, else
- * LPD_ERR_UNSUPPORTED); it may not overlap them otherwise, nor the controls.  If
- * an internal wait gives up (after 4 s, never expected), what was not begun by
- * then is NaN and the rows in hand, up to two a multiprocessor, are incomplete.
- * controls NULL copies (and converts). */
+ * out_row_stride] of out_dtype, columns [0, vocab) written, each value within two
+ * roundings of float32 (2^-23) and then rounded to out_dtype.  Logits in masked
+ * places are not looked at: they may be NaN or infinite.  A row whose mask allows
+ * nothing is -inf throughout.  `out` may be the logits themselves (same pointer,
+ * type and stride, else LPD_ERR_UNSUPPORTED); it may not overlap them otherwise,
+ * nor the controls.  If an internal wait gives up (after 4 s, never expected),
+ * what was not begun by then is NaN and the rows in hand, up to two a
+ * multiprocessor, are incomplete.  controls NULL copies (and converts). */
 int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, int64_t n_rows, int64_t vocab,
                        void *out, int32_t out_dtype, int64_t out_row_stride, void *stream);
 
@@ -570,7 +575,10 @@ int lpd_controls_apply(const lpd_logits *logits, const lpd_controls *controls, i
  * allow, a row whose mask allows nothing and a scale that is not finite and > 0
  * set LPD_STATUS_NONFINITE, as a non-finite selected logit or log-sum-exp does.
  * The scale is not rounded into the logits: it enters the exponents and the
- * final arithmetic in double.
+ * final arithmetic in double.  Exponents are formed from differences to each
+ * side's running maximum, so the error does not grow with an offset of a row or
+ * of a side.  (Only where scale times a touched logit passes 1e8 is that logit
+ * rounded to float32 first.)
  * workspace   lpd_workspace_size(LPD_KIND_CONTROLLED, n_rows, vocab, 0) bytes. */
 int lpd_score_controlled(const lpd_logits *train, const lpd_logits *rollout, const lpd_controls *train_controls,
                          const lpd_controls *rollout_controls, int64_t n_rows, int64_t vocab,

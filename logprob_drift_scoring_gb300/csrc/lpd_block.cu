@@ -36,8 +36,10 @@ constexpr int kBlk = 128;  // values along k that share one scale
 // at a time kept the shared memory 96 % busy: 1085 us for 151936 x 4096).
 // Bound: HBM (input bytes + one byte a value): 151936 x 4096 bf16 in 276 us
 // transposed and 272 us as it lies with 128 x 128 blocks (6.8 TB/s, the measured
-// copy rate), 297 and 285 us with 1 x 128 blocks; 1024 x 4096 in 11 us is a launch
-// and one block's load, reduction and store in turn.
+// copy rate), 297 and 285 us with 1 x 128 blocks; 75968 x 4096 f32 in 238 us (6.6
+// TB/s).  Rows off 16-byte boundaries are read an element at a time: 263 us for
+// 75968 x 4096 bf16 instead of 145.  1024 x 4096 takes 4 us replayed from a graph,
+// 11 us called from Python, most of it the host's.
 constexpr int kQThreads = 256;
 constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a scale is made for
 
@@ -301,7 +303,10 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 4 : 2) quantize_kernel(cons
 // (4.2 ms: its registers spill), packed multiply-adds (a move each after a read
 // of tensor memory), calling B into L2 ahead (no change; few rows 5 to 30 %
 // slower).  A product of few rows (16 x 151936 x 4096: 136 us, 4.6 TB/s) waits
-// for its 128-byte pieces of B's rows from HBM.
+// for its 128-byte pieces of B's rows from HBM.  Output rows off 16-byte boundaries
+// leave by stores of single elements: 4096 x 50257 x 4096 in 956 us dense, 822 us
+// with a row stride of 50264.  A data gradient of split k (64 x 4096 x 151936: 115
+// us, 93 of them HBM; 512 x 4096 x 151936: 348 us) is joined by a second kernel.
 constexpr int kTM = 128, kTN = 256;
 constexpr int kStages = 3;
 constexpr int kABytes = kTM * kBlk, kBBytes = kTN * kBlk;

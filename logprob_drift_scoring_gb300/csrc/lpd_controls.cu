@@ -22,13 +22,14 @@
 //             leaves them out; else they keep the values and store them once
 //             the stream has passed over the unit;
 //   stream    the other warps, 16 columns of each side a thread and tile.
-// What bounds it now: scoring issues instructions (one exponential, two
-// conversions and the near-reference series a column of both sides): 4096 x
-// 151936 bf16 pairs in 620 us with nothing to control and 830 us with a thousand
-// touched tokens a row (331 us of HBM time), the rest being the scouts' reads
-// of single logits, which a row's stream has to wait for.  The elementwise forms
-// are nearer to HBM: the gradient of 2048 such rows, a tenth of them inactive,
-// 254 us of 175.
+// What bounds it now: waiting, in scoring, not one unit of the SM.  4096 x 151936
+// bf16 pairs take 690 us with nothing to control and 840 us with a thousand
+// touched tokens a row (331 us of HBM time).  In a capture of 1024 rows with
+// nothing to control 53 % of the issue slots are used, the fma pipe 45 % and DRAM
+// 44 %: sixteen warps, each with a chain of dependent steps a tile.  The rest is the
+// scouts' reads of single logits, which a row's stream has to wait for.  The
+// elementwise forms are nearer to HBM: the gradient of 2048 such rows, a tenth of
+// them inactive, 252 us of 175.
 // A first version gave every block a chunk, then scan, list and stream in turn
 // with barriers between: 24 warps on an SM that mostly waited (39 % of issue
 // slots), 1373 us for the same scoring.
