@@ -241,9 +241,9 @@ def _stream(stream) -> int | None:
 
 def _row_stride(t) -> int:
     """Elements between the rows of a 2-D tensor.  A single row's stride has no
-    meaning in torch, so its width serves; rows that overlap or repeat keep
-    theirs, which the library refuses (LPD_ERR_BAD_STRIDE)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    meaning in torch, so where it is too small its width serves; rows that overlap
+    or repeat keep theirs, which the library refuses (LPD_ERR_BAD_STRIDE)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def logits_struct(t) -> LpdLogits:
