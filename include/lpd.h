@@ -600,6 +600,70 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
                                     const float *logp, const float *grad_logp, void *out_dlogits,
                                     int32_t out_dtype, int64_t out_row_stride, void *stream);
 
+/* ---- sampling ------------------------------------------------------------------ */
+
+/* What a sampler leaves of a row before it draws, and the draw.  With z = scale[r] *
+ * x (the logits behind lpd_controls_apply, or raw ones), in this order:
+ *     min-p   the tokens with exp(z - max z) >= min_p[r]
+ *     top-k   of these the top_k[r] largest
+ *     top-p   of these, in descending order, the shortest prefix whose softmax mass
+ *             (of these) is at least top_p[r]; at least one token
+ * Equal logits (+0 and -0 are equal) are ordered by token, the lowest first.  A
+ * token whose logit is -inf is never kept.  The filters are decided on sums that
+ * are exact to about 2^-31 of each weight (2^-41 for the heaviest), so a set is the
+ * mathematical one unless a border lies nearer to a sum than that.
+ * A NULL array leaves its step out; so does min_p <= 0, top_k <= 0 or >= vocab, and
+ * top_p >= 1.  (min_p >= 1 keeps the largest logits, top_p <= 0 and top_k = 1 the
+ * first of them.)  The arrays are device float / int32 [n_rows]; the struct is a
+ * host struct, read during the call.
+ * A row has no distribution if it holds a NaN or +inf or nothing above -inf, or if
+ * scale is not finite and > 0, or min_p or top_p is NaN. */
+typedef struct {
+    const float *scale;
+    const float *min_p;
+    const int32_t *top_k;
+    const float *top_p;
+} lpd_filter;
+
+/* Largest vocabulary of the two calls below. */
+#define LPD_SAMPLE_MAX_VOCAB 393216
+
+/* Draws a token from each row's kept set: the first kept token j, in token order,
+ * with sum_{i <= j, kept} exp(z_i) > uniform[r] * W, W the sum over all kept.
+ * filter (NULL: none) as above.
+ * uniform    device float [n_rows], in [0, 1); 1 and more draw the last kept token,
+ *            0 and less the first, NaN none.
+ * out_ids    device int32 [n_rows]: the token, -1 where the row has no distribution
+ *            or uniform is NaN.
+ * out_logp   device float [n_rows] or NULL: z_j - log W, the token's logprob under
+ *            the distribution that it was drawn from; NaN where the id is -1.
+ * out_kept   device int32 [n_rows] or NULL: the kept tokens (0: no distribution).
+ * No workspace; nothing is allocated.  vocab > LPD_SAMPLE_MAX_VOCAB:
+ * LPD_ERR_UNSUPPORTED. */
+int lpd_sample(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab,
+               const float *uniform, int32_t *out_ids, float *out_logp, int32_t *out_kept, void *stream);
+
+/* The kept sets themselves, as masks that lpd_controls takes (mask_row NULL): with
+ * them and the same scale, lpd_score_controlled measures drift under, and
+ * lpd_logprob_backward_controlled differentiates, the distribution that a filtered
+ * rollout was drawn from.
+ * token_ids  device int32 [n_rows] or NULL: a token of each row (its next one) that
+ *            is kept whatever the filter says, so that its logprob is finite; ids
+ *            outside [0, vocab) and tokens at -inf stay out.
+ * action_mask  device uint8 [n_rows] or NULL (all active).  Inactive rows are not
+ *            read; their masks, kept and lse are 0.
+ * out_mask   device uint32 [n_rows, mask_stride], token j at bit j % 32 of word j /
+ *            32; mask_stride >= ceil(vocab / 32) words, the words behind those stay
+ *            as they were, bits behind the last token are 0.  A row without a
+ *            distribution gets an empty mask.
+ * out_lse    device float [n_rows] or NULL: log of the kept tokens' sum of exp(z)
+ *            (NaN: no distribution).
+ * out_kept   device int32 [n_rows] or NULL: the mask's tokens.
+ * Limits as lpd_sample. */
+int lpd_filter_mask(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab,
+                    const int32_t *token_ids, const uint8_t *action_mask, uint32_t *out_mask,
+                    int64_t mask_stride, float *out_lse, int32_t *out_kept, void *stream);
+
 /* ---- block-scaled 8-bit products ---------------------------------------------- */
 
 /* An operand of the 8-bit matrix product: [rows, k] of 8-bit floats, k innermost,

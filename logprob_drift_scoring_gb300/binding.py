@@ -74,6 +74,11 @@ class LpdControls(ctypes.Structure):
                 ("mask_row", ctypes.c_void_p)]
 
 
+class LpdFilter(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_void_p), ("min_p", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p)]
+
+
 class LpdBlockScaled(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("block", ctypes.c_int32),
                 ("row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64)]
@@ -131,8 +136,10 @@ EXPORTED = ("lpd_workspace_size", "lpd_backend_info", "lpd_strerror", "lpd_score
             "lpd_score_entropy", "lpd_logprob_backward", "lpd_attn_merge", "lpd_attn_merge_order_drift",
             "lpd_topology_workspace_size", "lpd_score_sharded_topology", "lpd_drift_metrics_from_dlogp",
             "lpd_logp_drift_summary", "lpd_merge_rank_metrics", "lpd_controls_apply", "lpd_score_controlled",
-            "lpd_logprob_backward_controlled", "lpd_block_quantize", "lpd_block_workspace_size", "lpd_block_matmul")
+            "lpd_logprob_backward_controlled", "lpd_sample", "lpd_filter_mask", "lpd_block_quantize",
+            "lpd_block_workspace_size", "lpd_block_matmul")
 LPD_MAX_BIAS = 1024
+LPD_SAMPLE_MAX_VOCAB = 393216
 LPD_NOALLOC_MAX_ROWS = 32768
 LPD_ATTN_MAX_PARTS = 64
 
@@ -205,6 +212,10 @@ def lib() -> ctypes.CDLL:
         L.lpd_block_workspace_size.argtypes = [I64, I64, I64]
         L.lpd_block_matmul.restype = ctypes.c_int
         L.lpd_block_matmul.argtypes = [P, P, I64, I64, I64, P, I32, I64, P, SZ, P]
+        L.lpd_sample.restype = ctypes.c_int
+        L.lpd_sample.argtypes = [P, P, I64, I64, P, P, P, P, P]
+        L.lpd_filter_mask.restype = ctypes.c_int
+        L.lpd_filter_mask.argtypes = [P, P, I64, I64, P, P, P, I64, P, P, P]
         L.lpd_controls_apply.restype = ctypes.c_int
         L.lpd_controls_apply.argtypes = [P, P, I64, I64, P, I32, I64, P]
         L.lpd_score_controlled.restype = ctypes.c_int
@@ -688,6 +699,89 @@ def lpd_logprob_backward_controlled(logits, controls, token_ids, action_mask, lo
 
 
 @dataclass(frozen=True)
+class Filter:
+    """A sampler's filters as device tensors of one entry a row (lpd_filter; None
+    leaves a step out): scale (1 / temperature), min_p and top_p float32, top_k
+    int32.  The tensors must live as long as this object."""
+    scale: object = None
+    min_p: object = None
+    top_k: object = None
+    top_p: object = None
+
+    def __post_init__(self):
+        import torch
+
+        rows, device = None, None
+        for name in ("scale", "min_p", "top_k", "top_p"):
+            t = getattr(self, name)
+            if t is None:
+                continue
+            kind = torch.int32 if name == "top_k" else torch.float32
+            if t.dtype != kind or t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a dense {kind} vector, got {t.dtype} {list(t.shape)}")
+            if rows is not None and t.shape[0] != rows:
+                raise ValueError(f"{name} has {t.shape[0]} rows, the other filters {rows}")
+            if device is not None and t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the other filters on {device}")
+            rows, device = t.shape[0], t.device
+        object.__setattr__(self, "_struct", LpdFilter(_ptr(self.scale), _ptr(self.min_p), _ptr(self.top_k),
+                                                      _ptr(self.top_p)))
+        object.__setattr__(self, "_rows", rows)
+        object.__setattr__(self, "_device", device)
+
+
+def _filter(f, logits):
+    """Pointer to the lpd_filter (None: no filter) after the checks that only the tensors allow."""
+    if f is None:
+        return None
+    if f._rows is not None and f._rows != logits.shape[0]:
+        raise ValueError(f"filters of {f._rows} rows for {logits.shape[0]} logits rows")
+    if f._device is not None and f._device != logits.device:
+        raise ValueError(f"filters on {f._device}, logits on {logits.device}")
+    return ctypes.byref(f._struct)
+
+
+def lpd_sample(logits, filter, uniform, out_ids, out_logp=None, out_kept=None, stream=None) -> None:
+    """A token of each row's kept set, drawn with uniform [rows] float32, into out_ids
+    (int32), its logprob into out_logp (float32) and the sets' sizes into out_kept (int32)."""
+    import torch
+
+    x = logits_struct(logits)
+    x.row_stride = _row_stride(logits)
+    _same_rows(logits.shape[0], logits.device, uniform=(uniform, torch.float32), out_ids=(out_ids, torch.int32),
+               out_logp=(out_logp, torch.float32), out_kept=(out_kept, torch.int32))
+    f = _filter(filter, logits)
+    with _on(logits):
+        rc = lib().lpd_sample(ctypes.byref(x), f, logits.shape[0], logits.shape[1], _ptr(uniform), _ptr(out_ids),
+                              _ptr(out_logp), _ptr(out_kept), _stream(stream))
+    _check(rc, "lpd_sample")
+
+
+def lpd_filter_mask(logits, filter, token_ids, action_mask, out_mask, out_lse=None, out_kept=None,
+                    stream=None) -> None:
+    """The rows' kept sets as bits, into out_mask int32 [rows, words] (Controls.mask's form)."""
+    import torch
+
+    x = logits_struct(logits)
+    x.row_stride = _row_stride(logits)
+    words = -(-logits.shape[1] // 32)
+    if out_mask.dtype != torch.int32 or out_mask.dim() != 2 or out_mask.shape[0] != logits.shape[0] \
+            or out_mask.shape[1] < words or (out_mask.shape[1] > 1 and out_mask.stride(1) != 1):
+        raise ValueError(f"out_mask must be int32 [{logits.shape[0]}, {words} or more] with contiguous words")
+    if out_mask.device != logits.device:
+        raise ValueError(f"out_mask on {out_mask.device}, logits on {logits.device}")
+    _same_rows(logits.shape[0], logits.device, token_ids=(token_ids, torch.int32),
+               action_mask=(action_mask, torch.uint8), out_lse=(out_lse, torch.float32),
+               out_kept=(out_kept, torch.int32))
+    f = _filter(filter, logits)
+    with _on(logits):
+        rc = lib().lpd_filter_mask(ctypes.byref(x), f, logits.shape[0], logits.shape[1], _ptr(token_ids),
+                                   _ptr(action_mask), _ptr(out_mask), _row_stride(out_mask), _ptr(out_lse),
+                                   _ptr(out_kept), _stream(stream))
+    _check(rc, "lpd_filter_mask")
+
+
+@dataclass(frozen=True)
 class BlockScaled:
     """An 8-bit operand (lpd_block_scaled): values float8_e4m3fn or float8_e5m2
     [rows, k] with contiguous rows, scales float32 [rows, ceil(k / 128)], or
@@ -923,6 +1017,29 @@ def score_controlled(train, rollout, token_ids, action_mask, train_controls=None
     lpd_score_controlled(train, rollout, train_controls, rollout_controls, token_ids, action_mask, clip[0], clip[1],
                          *outs, met, ws, stream)
     return ScoreResult(*outs, read_metrics(met))
+
+
+def sample(logits, uniform, filter=None, stream=None):
+    """(ids int32, logprobs float32, kept int32) of a draw from each row, in new tensors."""
+    import torch
+
+    n, dev = logits.shape[0], logits.device
+    ids, kept = (torch.empty(n, dtype=torch.int32, device=dev) for _ in range(2))
+    logp = torch.empty(n, dtype=torch.float32, device=dev)
+    lpd_sample(logits, filter, uniform, ids, logp, kept, stream)
+    return ids, logp, kept
+
+
+def filter_mask(logits, filter, token_ids=None, action_mask=None, stream=None):
+    """(mask int32 [rows, words], lse float32, kept int32) of the rows' kept sets, in new tensors."""
+    import torch
+
+    n, dev = logits.shape[0], logits.device
+    mask = torch.empty((n, -(-logits.shape[1] // 32)), dtype=torch.int32, device=dev)
+    lse = torch.empty(n, dtype=torch.float32, device=dev)
+    kept = torch.empty(n, dtype=torch.int32, device=dev)
+    lpd_filter_mask(logits, filter, token_ids, action_mask, mask, lse, kept, stream)
+    return mask, lse, kept
 
 
 def block_quantize(x, dtype=None, block=False, transpose=False, pow2=False, stream=None) -> BlockScaled:

@@ -443,6 +443,26 @@ int to_controls(const lpd_controls *c, int64_t n_rows, int64_t vocab, CtlSide *o
     return LPD_OK;
 }
 
+// What lpd_sample and lpd_filter_mask share.
+int to_sample(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab, SampleCall *out) {
+    int rc = check_rows_vocab(n_rows, vocab);
+    if (rc) return rc;
+    if (vocab > LPD_SAMPLE_MAX_VOCAB || n_rows > kMaxRows / 8) return LPD_ERR_UNSUPPORTED;
+    if ((rc = check_logits(logits, n_rows, vocab))) return rc;
+    if (filter) {
+        for (const void *p : {static_cast<const void *>(filter->scale), static_cast<const void *>(filter->min_p),
+                              static_cast<const void *>(filter->top_k), static_cast<const void *>(filter->top_p)})
+            if (!ptr_aligned(p, 4)) return LPD_ERR_ALIGNMENT;
+        out->f = FilterParams{filter->scale, filter->min_p, filter->top_p, filter->top_k};
+    }
+    out->x = logits->ptr;
+    out->dtype = logits->dtype;
+    out->x_stride_elems = logits->row_stride;
+    out->n_rows = n_rows;
+    out->vocab = vocab;
+    return LPD_OK;
+}
+
 // A block-scaled operand of `rows` rows and k columns as the kernels' copy.
 int to_operand(const lpd_block_scaled *x, int64_t rows, int64_t k, bool product, BlockOperand *out) {
     if (!x) return LPD_ERR_NULL_POINTER;
@@ -1075,6 +1095,42 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
     return cuda_status(launch_controls_gradient(c, logits->ptr, logits->dtype, logits->row_stride, out_dlogits,
                                                 out_dtype, out_row_stride, n_rows, vocab, token_ids, action_mask, logp,
                                                 grad_logp, static_cast<cudaStream_t>(stream)));
+}
+
+int lpd_sample(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab,
+               const float *uniform, int32_t *out_ids, float *out_logp, int32_t *out_kept, void *stream) {
+    SampleCall c{};
+    int rc = to_sample(logits, filter, n_rows, vocab, &c);
+    if (rc) return rc;
+    if (n_rows > 0 && (!uniform || !out_ids)) return LPD_ERR_NULL_POINTER;
+    for (const void *p : {static_cast<const void *>(uniform), static_cast<const void *>(out_ids),
+                          static_cast<const void *>(out_logp), static_cast<const void *>(out_kept)})
+        if (!ptr_aligned(p, 4)) return LPD_ERR_ALIGNMENT;
+    c.uniform = uniform;
+    c.ids = out_ids;
+    c.logp = out_logp;
+    c.kept = out_kept;
+    return cuda_status(launch_sample(c, static_cast<cudaStream_t>(stream)));
+}
+
+int lpd_filter_mask(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab,
+                    const int32_t *token_ids, const uint8_t *action_mask, uint32_t *out_mask, int64_t mask_stride,
+                    float *out_lse, int32_t *out_kept, void *stream) {
+    SampleCall c{};
+    int rc = to_sample(logits, filter, n_rows, vocab, &c);
+    if (rc) return rc;
+    if (n_rows > 0 && !out_mask) return LPD_ERR_NULL_POINTER;
+    if (mask_stride < (vocab + 31) / 32) return LPD_ERR_BAD_STRIDE;
+    for (const void *p : {static_cast<const void *>(token_ids), static_cast<const void *>(out_mask),
+                          static_cast<const void *>(out_lse), static_cast<const void *>(out_kept)})
+        if (!ptr_aligned(p, 4)) return LPD_ERR_ALIGNMENT;
+    c.keep = token_ids;
+    c.active = action_mask;
+    c.mask = out_mask;
+    c.mask_stride = mask_stride;
+    c.lse = out_lse;
+    c.kept = out_kept;
+    return cuda_status(launch_sample(c, static_cast<cudaStream_t>(stream)));
 }
 
 int lpd_block_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols,

@@ -1,4 +1,4 @@
-// What the C entry points hand to the sampling-control and block-scaled kernels.
+// What the C entry points hand to the sampling-control, sampling, block-scaled and microscaled kernels.
 #pragma once
 
 #include "lpd_internal.cuh"
@@ -48,6 +48,31 @@ cudaError_t launch_controls_gradient(const CtlSide &c, const void *x, int x_dtyp
                                      const int32_t *ids, const uint8_t *mask, const float *logp, const float *grad,
                                      cudaStream_t stream);
 cudaError_t launch_controls_score(const CtlScoreCall &c, cudaStream_t stream);
+
+// ---------------------------------------------------------------- sampling
+// One row's filters (include/lpd.h, lpd_filter); a null array leaves its step out.
+struct FilterParams {
+    const float *scale, *min_p, *top_p;
+    const int32_t *top_k;
+};
+
+// One call of lpd_sample (mask null) or lpd_filter_mask.
+struct SampleCall {
+    const void *x;
+    int dtype;
+    int64_t x_stride_elems, n_rows, vocab;
+    FilterParams f;
+    const float *uniform;
+    int32_t *ids;
+    float *logp;
+    const int32_t *keep;
+    const uint8_t *active;
+    uint32_t *mask;
+    int64_t mask_stride;
+    float *lse;
+    int32_t *kept;
+};
+cudaError_t launch_sample(const SampleCall &c, cudaStream_t stream);
 
 // ---------------------------------------------------------------- block-scaled 8-bit operands
 struct BlockOperand {

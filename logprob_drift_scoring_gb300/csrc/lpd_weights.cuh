@@ -1,0 +1,135 @@
+// Softmax weights as whole numbers: exp(scale (x - top)) in steps of 2^-44.
+//
+// A filter's border (the smallest prefix whose mass reaches top_p) and a draw
+// (the first token whose running mass passes u W) compare sums that may lie
+// arbitrarily near each other, so the sums of a row are integers: any order of
+// addition gives the same bits, and one row's answer does not depend on how its
+// columns were spread over threads.  A weight is formed to 2^-31 of itself
+// (weight_rough) and for the row's heaviest tokens to 2^-44 (weight_precise):
+// the errors of many small weights average out, those of a few large ones would
+// not.  (A plain exponential in float32 is off by 2^-22 with the rounding of its
+// argument: it moves the border of a nucleus by a token in one row of a thousand.)
+//
+// x scale log2(e) is cut in units of 1/256 octave, x c = J + a with whole J and
+// |a| <= 1/2; 2^(J / 256) comes from a table and shifts, 2^(a / 256) - 1 from
+// three terms of its series (the fourth is below 2^-41).  The product x c is
+// formed exactly with a multiply-add, so nothing is lost to the size of x.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#ifndef __CUDACC__
+#define __host__
+#define __device__
+#define __forceinline__ inline
+#endif
+
+namespace lpd {
+
+constexpr int kWeightOne = 44;          // weights are multiples of 2^-44 of the top's (about)
+constexpr int kUnits = 256;             // steps an octave
+constexpr float kMagic = 12582912.f;    // 1.5 * 2^23: adding it rounds to a whole number
+constexpr uint32_t kMagicBits = 0x4b400000u;
+
+struct WeightEntry {
+    uint32_t whole;  // 2^(i / 256) in units of 2^-30
+    float part;      // the same as a float
+};
+
+// One row's exponent factor and origin.
+struct WeightScale {
+    double c;        // units for 1.0 of x
+    float ch, cl;    // c in two floats
+    int origin;      // whole units of the top
+    float cut;       // x at or below this weigh nothing
+    int wide;        // the top lies beyond 2^20 units: products by float lose whole units, doubles do not
+};
+
+__host__ __device__ __forceinline__ uint32_t bits_of(float x) {
+#ifdef __CUDA_ARCH__
+    return __float_as_uint(x);
+#else
+    uint32_t u;
+    memcpy(&u, &x, 4);
+    return u;
+#endif
+}
+__host__ __device__ __forceinline__ float mul_rn(float a, float b) {
+#ifdef __CUDA_ARCH__
+    return __fmul_rn(a, b);
+#else
+    return a * b;
+#endif
+}
+__host__ __device__ __forceinline__ float add_rn(float a, float b) {
+#ifdef __CUDA_ARCH__
+    return __fadd_rn(a, b);
+#else
+    return a + b;
+#endif
+}
+__host__ __device__ __forceinline__ float fma_rn(float a, float b, float c) {
+#ifdef __CUDA_ARCH__
+    return __fmaf_rn(a, b, c);
+#else
+    return std::fmaf(a, b, c);
+#endif
+}
+
+// scale: finite and > 0; top: the row's largest logit, finite.
+__host__ __device__ __forceinline__ WeightScale weight_scale(float scale, float top) {
+    WeightScale w;
+    w.c = static_cast<double>(scale) * (1.4426950408889634073599 * kUnits);
+    w.ch = static_cast<float>(w.c);
+    w.cl = static_cast<float>(w.c - static_cast<double>(w.ch));
+    const double at = static_cast<double>(top) * w.c;
+    w.wide = !(fabs(at) < 1048576.0) || !(w.ch < 1e30f) || !(w.ch > 1e-30f);
+    // (beyond 2^20 the origin is taken relative to the top: weight_precise)
+    w.origin = w.wide ? 0 : static_cast<int>(bits_of(add_rn(mul_rn(top, w.ch), kMagic)) - kMagicBits);
+    w.cut = static_cast<float>(static_cast<double>(top) - (kWeightOne + 2) * static_cast<double>(kUnits) / w.c);
+    return w;
+}
+
+constexpr double kLn2Unit = 0.69314718055994530942 / kUnits;
+
+// Units between x and the row's origin, in double.
+__host__ __device__ __forceinline__ double weight_units(float x, const WeightScale &w, float top) {
+    return w.wide ? (static_cast<double>(x) - static_cast<double>(top)) * w.c : static_cast<double>(x) * w.c - w.origin;
+}
+
+// For x > w.cut and x <= top, not wide.
+__host__ __device__ __forceinline__ uint64_t weight_rough(float x, const WeightScale &w, const WeightEntry *table) {
+    const float p = mul_rn(x, w.ch);
+    const float q = fma_rn(x, w.cl, fma_rn(x, w.ch, -p));
+    const float b = add_rn(p, kMagic);
+    const float a = add_rn(add_rn(p, -add_rn(b, -kMagic)), q);
+    const int j = static_cast<int>(bits_of(b) - kMagicBits) - w.origin;
+    constexpr float k1 = static_cast<float>(kLn2Unit), k2 = static_cast<float>(kLn2Unit * kLn2Unit / 2),
+                    k3 = static_cast<float>(kLn2Unit * kLn2Unit * kLn2Unit / 6);
+    const float y = mul_rn(a, fma_rn(a, fma_rn(a, k3, k2), k1));
+    const WeightEntry e = table[j & (kUnits - 1)];
+    const uint32_t m = e.whole + (bits_of(fma_rn(e.part, y, kMagic)) - kMagicBits);
+    const int s = -(j >> 8);  // octaves below the top's
+    return (static_cast<uint64_t>(m) << (kWeightOne - 30)) >> (s & 63);
+}
+
+// For any finite x <= top.
+__host__ __device__ __forceinline__ uint64_t weight_precise(float x, const WeightScale &w, float top, const double *table) {
+    const double u = weight_units(x, w, top);
+    if (!(u > -(kWeightOne + 2.0) * kUnits)) return 0;
+    const double jf = rint(u);
+    const double v = (u - jf) * kLn2Unit;
+    const int j = static_cast<int>(jf);
+    const double t = table[j & (kUnits - 1)];
+    const double m = t + t * (v * (1 + v * (0.5 + v * (1.0 / 6 + v * (1.0 / 24)))));
+    const int s = -(j >> 8);
+#ifdef __CUDA_ARCH__
+    return __double2ull_rn(m * __hiloint2double((1023 + kWeightOne - s) << 20, 0));
+#else
+    return static_cast<uint64_t>(std::nearbyint(std::ldexp(m, kWeightOne - s)));
+#endif
+}
+
+}  // namespace lpd
