@@ -81,14 +81,16 @@ __host__ __device__ __forceinline__ float fma_rn(float a, float b, float c) {
 // scale: finite and > 0; top: the row's largest logit, finite.
 __host__ __device__ __forceinline__ WeightScale weight_scale(float scale, float top) {
     WeightScale w;
-    w.c = static_cast<double>(scale) * (1.4426950408889634073599 * kUnits);
-    w.ch = static_cast<float>(w.c);
-    w.cl = static_cast<float>(w.c - static_cast<double>(w.ch));
-    const double at = static_cast<double>(top) * w.c;
-    w.wide = !(fabs(at) < 1048576.0) || !(w.ch < 1e30f) || !(w.ch > 1e-30f);
-    // (beyond 2^20 the origin is taken relative to the top: weight_precise)
+    // (log2(e) 256 in two floats; c is what the two parts say)
+    constexpr double kC = 1.4426950408889634073599 * kUnits;
+    constexpr float kHi = static_cast<float>(kC), kLo = static_cast<float>(kC - static_cast<double>(kHi));
+    w.ch = mul_rn(scale, kHi);
+    w.cl = fma_rn(scale, kHi, -w.ch) + scale * kLo;
+    w.wide = !(fabsf(top * w.ch) < 1048576.f) || !(w.ch < 1e30f) || !(w.ch > 1e-30f);
+    w.c = w.wide ? static_cast<double>(scale) * kC : static_cast<double>(w.ch) + static_cast<double>(w.cl);
+    // (a wide row's origin is the top itself: weight_precise)
     w.origin = w.wide ? 0 : static_cast<int>(bits_of(add_rn(mul_rn(top, w.ch), kMagic)) - kMagicBits);
-    w.cut = static_cast<float>(static_cast<double>(top) - (kWeightOne + 2) * static_cast<double>(kUnits) / w.c);
+    w.cut = top - (kWeightOne + 2) * static_cast<float>(kUnits) / w.ch;
     return w;
 }
 
