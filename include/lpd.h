@@ -718,6 +718,73 @@ int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64
                      void *out, int32_t out_dtype, int64_t out_row_stride, void *workspace,
                      size_t workspace_bytes, void *stream);
 
+/* ---- microscaled 4-bit products ------------------------------------------------ */
+
+/* An operand of the 4-bit matrix product: [rows, k] codes of 4 bits, k innermost,
+ * two to a byte (the even k in the low half).  A code is a sign and one of 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 (e2m1, in this order); `block` values along k share one scale
+ * byte and the operand one float:
+ *     value(r, c) * scale(r, c / block) * tensor_scale
+ *   block 16   scales in e4m3
+ *   block 32   scales 2^(byte - 127), 255 is NaN
+ * The scale bytes lie as the tensor cores take them, 512 bytes for 128 rows x 4
+ * blocks: with atoms = ceil(ceil(k / block) / 4), the scale of row r and block b is
+ * at byte
+ *     ((r / 128) * atoms + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.
+ * Bytes of rows and blocks behind the last are there but stand for nothing: 0 (for
+ * blocks behind the last any scale that is not NaN). */
+typedef struct {
+    void *ptr;                 /* device, row 0; 16-byte aligned for the product */
+    int32_t block;             /* 16 or 32 */
+    int32_t reserved;          /* set to 0 */
+    int64_t row_stride;        /* bytes between rows, >= ceil(k / 2); a multiple of 16 for the product */
+    void *scales;              /* device, lpd_micro_scale_bytes() bytes, 16-byte aligned */
+    const float *tensor_scale; /* device, one float, or NULL: 1 */
+} lpd_micro_scaled;
+
+/* Bytes of an operand's scales (0 for invalid arguments). */
+size_t lpd_micro_scale_bytes(int32_t block, int64_t rows, int64_t k);
+
+/* Quantises x [rows, cols] (bf16 or f32) into `out`: the same matrix (transpose 0:
+ * out is [rows, cols]) or its transpose (transpose 1: out is [cols, rows], blocks
+ * along x's rows, as the gradients' products take them).  With t = *tensor_scale
+ * and top the largest |x| of a block, each step rounded in float32:
+ *     block 16:  scale = e4m3(top / (6 t)), to nearest even, at most 448
+ *     block 32:  scale = max(top / t, 2^-64) / 6, up to a power of two
+ *     code = e2m1(x * (1 / (scale t))), to nearest even, at most 6 (0 where that
+ *            reciprocal is infinite)
+ * (t: usually 1 for blocks of 32, and the tensor's largest |x| / 2688 for blocks of
+ * 16.)  A block with a NaN or an infinity reads as NaN throughout, and so does
+ * everything if t is not finite and > 0.  An odd k's last byte has 0 in its upper
+ * half; bytes between out's last code and its row stride are left as they were,
+ * scale bytes behind the last row and block are 0.
+ * out_values  device, out's shape, of values_dtype (LPD_BF16 or LPD_F32), or NULL:
+ *             the values that the codes stand for, rounded once from (code scale) t
+ *             in float32: what a training side sees that simulates the rollout's
+ *             rounding.  It may not overlap x. */
+int lpd_micro_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols,
+                       int32_t transpose, const lpd_micro_scaled *out, void *out_values,
+                       int32_t values_dtype, int64_t values_row_stride, void *stream);
+
+/* Bytes of device workspace that lpd_micro_matmul needs for these sizes on the
+ * current device (0 for invalid arguments). */
+size_t lpd_micro_workspace_size(int64_t m, int64_t n, int64_t k);
+
+/* out[m, n] = sum_k A[m, k] B[n, k] over the values that the operands stand for,
+ * accumulated in float32 on the tensor cores, times the two tensor scales, rounded
+ * once to out_dtype (LPD_BF16 or LPD_F32).  Both operands have one block size (else
+ * LPD_ERR_UNSUPPORTED).  Forward product and gradients as for lpd_block_matmul.
+ * k = 0 gives zeros.
+ * workspace   lpd_micro_workspace_size(m, n, k) bytes, 256-byte aligned; its first
+ *             word as in lpd_block_matmul.
+ * Where the output has more than half as many tiles of 128 x 256 as there are
+ * multiprocessors, a row's bits do not depend on the other rows; with fewer the k
+ * axis may be split by a rule on (m, n, k), and the parts are added in order.  The
+ * same call gives the same bits. */
+int lpd_micro_matmul(const lpd_micro_scaled *a, const lpd_micro_scaled *b, int64_t m, int64_t n, int64_t k,
+                     void *out, int32_t out_dtype, int64_t out_row_stride, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 /* ---- attention (out, lse) merge --------------------------------------------- */
 
 /* Split-KV / context-parallel attention partials are merged with the same

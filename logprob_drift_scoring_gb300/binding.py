@@ -84,6 +84,11 @@ class LpdBlockScaled(ctypes.Structure):
                 ("row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64)]
 
 
+class LpdMicroScaled(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("block", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p)]
+
+
 class LpdMetrics(ctypes.Structure):
     _fields_ = [("n_active", ctypes.c_int64), ("argmax_row", ctypes.c_int64), ("flags", ctypes.c_uint32),
                 ("status", ctypes.c_uint32), ("ratio0_mean", ctypes.c_double), ("clipfrac0", ctypes.c_double),
@@ -137,7 +142,8 @@ EXPORTED = ("lpd_workspace_size", "lpd_backend_info", "lpd_strerror", "lpd_score
             "lpd_topology_workspace_size", "lpd_score_sharded_topology", "lpd_drift_metrics_from_dlogp",
             "lpd_logp_drift_summary", "lpd_merge_rank_metrics", "lpd_controls_apply", "lpd_score_controlled",
             "lpd_logprob_backward_controlled", "lpd_sample", "lpd_filter_mask", "lpd_block_quantize",
-            "lpd_block_workspace_size", "lpd_block_matmul")
+            "lpd_block_workspace_size", "lpd_block_matmul", "lpd_micro_scale_bytes", "lpd_micro_quantize",
+            "lpd_micro_workspace_size", "lpd_micro_matmul")
 LPD_MAX_BIAS = 1024
 LPD_SAMPLE_MAX_VOCAB = 393216
 LPD_NOALLOC_MAX_ROWS = 32768
@@ -212,6 +218,14 @@ def lib() -> ctypes.CDLL:
         L.lpd_block_workspace_size.argtypes = [I64, I64, I64]
         L.lpd_block_matmul.restype = ctypes.c_int
         L.lpd_block_matmul.argtypes = [P, P, I64, I64, I64, P, I32, I64, P, SZ, P]
+        L.lpd_micro_scale_bytes.restype = SZ
+        L.lpd_micro_scale_bytes.argtypes = [I32, I64, I64]
+        L.lpd_micro_quantize.restype = ctypes.c_int
+        L.lpd_micro_quantize.argtypes = [P, I32, I64, I64, I64, I32, P, P, I32, I64, P]
+        L.lpd_micro_workspace_size.restype = SZ
+        L.lpd_micro_workspace_size.argtypes = [I64, I64, I64]
+        L.lpd_micro_matmul.restype = ctypes.c_int
+        L.lpd_micro_matmul.argtypes = [P, P, I64, I64, I64, P, I32, I64, P, SZ, P]
         L.lpd_sample.restype = ctypes.c_int
         L.lpd_sample.argtypes = [P, P, I64, I64, P, P, P, P, P]
         L.lpd_filter_mask.restype = ctypes.c_int
@@ -858,6 +872,96 @@ def lpd_block_matmul(a, b, out, workspace, stream=None) -> None:
     _check(rc, "lpd_block_matmul")
 
 
+def lpd_micro_scale_bytes(block: int, rows: int, k: int) -> int:
+    return int(lib().lpd_micro_scale_bytes(block, rows, k))
+
+
+@dataclass(frozen=True)
+class MicroScaled:
+    """A 4-bit operand (lpd_micro_scaled) of k columns: codes uint8 [rows, ceil(k / 2)
+    or more] with contiguous rows, scales uint8, dense, in the tiled order of the
+    header, block 16 or 32, tensor_scale a float32 tensor of one value or None (1).
+    The tensors must live as long as this object."""
+    codes: object
+    scales: object
+    k: int
+    block: int = 16
+    tensor_scale: object = None
+
+    def __post_init__(self):
+        import torch
+
+        c, s, t = self.codes, self.scales, self.tensor_scale
+        if self.block not in (16, 32):
+            raise ValueError(f"block must be 16 or 32, got {self.block}")
+        if self.k < 0 or c.dtype != torch.uint8 or c.dim() != 2 or c.shape[1] < -(-self.k // 2) \
+                or (c.numel() and c.shape[1] > 1 and c.stride(1) != 1):
+            raise ValueError(f"codes must be uint8 [rows, {-(-self.k // 2)} or more] with contiguous columns")
+        want = -(-c.shape[0] // 128) * -(-self.k // (4 * self.block)) * 512
+        if s.dtype != torch.uint8 or not s.is_contiguous() or s.numel() != want:
+            raise ValueError(f"scales must be {want} dense uint8 values, got {s.dtype} {list(s.shape)}")
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise ValueError("tensor_scale must be one float32 value")
+        for name, o in (("scales", s), ("tensor_scale", t)):
+            if o is not None and o.device != c.device:
+                raise ValueError(f"codes on {c.device}, {name} on {o.device}")
+        # the stride of a single row has no meaning in torch: any legal one serves
+        stride = c.stride(0) if c.shape[0] > 1 else -(-c.shape[1] // 16) * 16
+        object.__setattr__(self, "_struct", LpdMicroScaled(c.data_ptr(), self.block, 0, stride, s.data_ptr(), _ptr(t)))
+
+
+def micro_empty(rows: int, k: int, block: int = 16, tensor_scale=None, device="cuda") -> MicroScaled:
+    """An operand of these sizes to quantise into, its rows on 16-byte boundaries
+    as the product needs them."""
+    import torch
+
+    room = torch.empty((rows, -(-k // 32) * 16), dtype=torch.uint8, device=device)
+    scales = torch.empty(lpd_micro_scale_bytes(block, rows, k), dtype=torch.uint8, device=device)
+    return MicroScaled(room[:, :-(-k // 2)], scales, k, block, tensor_scale)
+
+
+def lpd_micro_quantize(x, out, transpose=False, out_values=None, stream=None) -> None:
+    """x (bf16 or f32, 2-D) into the operand `out`, or its transpose; the values that
+    it stands for into out_values (bf16 or f32), if given."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be 2-D with contiguous columns")
+    shape = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
+    if (out.codes.shape[0], out.k) != shape:
+        raise ValueError("out has another shape")
+    if out.codes.device != x.device:
+        raise ValueError(f"x on {x.device}, out on {out.codes.device}")
+    v = out_values
+    if v is not None and (tuple(v.shape) != shape or v.device != x.device or (v.shape[1] > 1 and v.stride(1) != 1)):
+        raise ValueError("out_values must have out's shape and device and contiguous columns")
+    with _on(x):
+        rc = lib().lpd_micro_quantize(_ptr(x), _dtype_code(x), _row_stride(x), x.shape[0], x.shape[1],
+                                      int(bool(transpose)), ctypes.byref(out._struct), _ptr(v),
+                                      _dtype_code(v) if v is not None else 0, _row_stride(v) if v is not None else 0,
+                                      _stream(stream))
+    _check(rc, "lpd_micro_quantize")
+
+
+def lpd_micro_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().lpd_micro_workspace_size(m, n, k))
+
+
+def lpd_micro_matmul(a, b, out, workspace, stream=None) -> None:
+    """out [m, n] (bf16 or f32) = A [m, k] times B [n, k] transposed."""
+    m, n = a.codes.shape[0], b.codes.shape[0]
+    if b.k != a.k or tuple(out.shape) != (m, n):
+        raise ValueError(f"A {[m, a.k]}, B {[n, b.k]} and out {list(out.shape)} do not fit")
+    if out.dim() != 2 or (n > 1 and out.stride(1) != 1):
+        raise ValueError("out must have contiguous columns")
+    if not a.codes.device == b.codes.device == out.device:
+        raise ValueError("the operands and out must be on one device")
+    _buffer("workspace", workspace, out.device)
+    with _on(out):
+        rc = lib().lpd_micro_matmul(ctypes.byref(a._struct), ctypes.byref(b._struct), m, n, a.k, _ptr(out),
+                                    _dtype_code(out), _row_stride(out), _ptr(workspace), _bytes(workspace),
+                                    _stream(stream))
+    _check(rc, "lpd_micro_matmul")
+
+
 # ---- convenience: allocate with torch, call, read back ------------------------
 
 def read_merge_drift(buf) -> dict:
@@ -1061,4 +1165,24 @@ def block_matmul(a, b, out_dtype=None, stream=None):
     out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
     ws = torch.empty(lpd_block_workspace_size(m, n, a.values.shape[1]), dtype=torch.uint8, device=dev)
     lpd_block_matmul(a, b, out, ws, stream)
+    return out
+
+
+def micro_quantize(x, block=16, tensor_scale=None, transpose=False, stream=None) -> MicroScaled:
+    """x as a new 4-bit operand."""
+    rows, k = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
+    out = micro_empty(rows, k, block, tensor_scale, x.device)
+    lpd_micro_quantize(x, out, transpose, None, stream)
+    return out
+
+
+def micro_matmul(a, b, out_dtype=None, stream=None):
+    """The product of two 4-bit operands in a new tensor (bf16 unless given)."""
+    import torch
+
+    m, n = a.codes.shape[0], b.codes.shape[0]
+    dev = a.codes.device
+    out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+    ws = torch.empty(lpd_micro_workspace_size(m, n, a.k), dtype=torch.uint8, device=dev)
+    lpd_micro_matmul(a, b, out, ws, stream)
     return out

@@ -476,6 +476,20 @@ int to_operand(const lpd_block_scaled *x, int64_t rows, int64_t k, bool product,
     return LPD_OK;
 }
 
+// A microscaled operand of `rows` rows and k columns as the kernels' copy.
+int to_micro(const lpd_micro_scaled *x, int64_t rows, int64_t k, bool product, MicroOperand *out) {
+    if (!x) return LPD_ERR_NULL_POINTER;
+    if (x->block != 16 && x->block != 32) return LPD_ERR_BAD_SIZE;
+    if (rows > 0 && k > 0 && (!x->ptr || !x->scales)) return LPD_ERR_NULL_POINTER;
+    if (x->row_stride < (k + 1) / 2) return LPD_ERR_BAD_STRIDE;
+    if (!aligned16(x->scales) || !ptr_aligned(x->tensor_scale, 4)) return LPD_ERR_ALIGNMENT;
+    if (product && rows > 0 && k > 0 && (!aligned16(x->ptr) || x->row_stride % 16 != 0)) return LPD_ERR_ALIGNMENT;
+    const int64_t blocks = (k + x->block - 1) / x->block;
+    *out = MicroOperand{x->ptr, x->row_stride, x->block == 16, static_cast<const uint8_t *>(x->scales), (blocks + 3) / 4,
+                        x->tensor_scale};
+    return LPD_OK;
+}
+
 int check_product_sizes(int64_t m, int64_t n, int64_t k) {
     if (m < 0 || n < 0 || k < 0) return LPD_ERR_BAD_SIZE;
     // TMA coordinates are 32-bit
@@ -1169,6 +1183,57 @@ int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64
     if (!elt_aligned(out, out_dtype)) return LPD_ERR_ALIGNMENT;
     if ((rc = check_workspace(workspace, workspace_bytes, block_plan(m, n, k).bytes))) return rc;
     return cuda_status(launch_block_matmul(x, y, m, n, k, out, out_dtype, out_row_stride, workspace,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+size_t lpd_micro_scale_bytes(int32_t block, int64_t rows, int64_t k) {
+    if ((block != 16 && block != 32) || rows < 0 || k < 0 || rows > kMaxRows || k > kMaxRows) return 0;
+    const int64_t blocks = (k + block - 1) / block;
+    return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((blocks + 3) / 4) * 512;
+}
+
+int lpd_micro_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int64_t rows, int64_t cols,
+                       int32_t transpose, const lpd_micro_scaled *out, void *out_values, int32_t values_dtype,
+                       int64_t values_row_stride, void *stream) {
+    if (rows < 0 || cols < 0 || (transpose != 0 && transpose != 1)) return LPD_ERR_BAD_SIZE;
+    if (rows > kMaxRows || cols > kMaxRows || (rows + 127) / 128 * ((cols + 127) / 128) > INT32_MAX)
+        return LPD_ERR_UNSUPPORTED;
+    if (!x && rows > 0 && cols > 0) return LPD_ERR_NULL_POINTER;
+    if (!valid_dtype(x_dtype)) return LPD_ERR_BAD_DTYPE;
+    if (x_row_stride < cols) return LPD_ERR_BAD_STRIDE;
+    if (!elt_aligned(x, x_dtype)) return LPD_ERR_ALIGNMENT;
+    MicroOperand o;
+    const int rc = transpose ? to_micro(out, cols, rows, false, &o) : to_micro(out, rows, cols, false, &o);
+    if (rc) return rc;
+    if (out_values) {
+        if (!valid_dtype(values_dtype)) return LPD_ERR_BAD_DTYPE;
+        if (values_row_stride < (transpose ? rows : cols)) return LPD_ERR_BAD_STRIDE;
+        if (!elt_aligned(out_values, values_dtype)) return LPD_ERR_ALIGNMENT;
+        if (out_values == x) return LPD_ERR_UNSUPPORTED;
+    }
+    return cuda_status(launch_micro_quantize(x, x_dtype, x_row_stride, rows, cols, transpose == 1, o, out_values,
+                                             values_dtype, values_row_stride, static_cast<cudaStream_t>(stream)));
+}
+
+size_t lpd_micro_workspace_size(int64_t m, int64_t n, int64_t k) {
+    return check_product_sizes(m, n, k) ? 0 : micro_plan(m, n, k).bytes;
+}
+
+int lpd_micro_matmul(const lpd_micro_scaled *a, const lpd_micro_scaled *b, int64_t m, int64_t n, int64_t k,
+                     void *out, int32_t out_dtype, int64_t out_row_stride, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    int rc = check_product_sizes(m, n, k);
+    if (rc) return rc;
+    MicroOperand x, y;
+    if ((rc = to_micro(a, m, k, true, &x))) return rc;
+    if ((rc = to_micro(b, n, k, true, &y))) return rc;
+    if (x.b16 != y.b16) return LPD_ERR_UNSUPPORTED;
+    if (!out && m > 0 && n > 0) return LPD_ERR_NULL_POINTER;
+    if (!valid_dtype(out_dtype)) return LPD_ERR_BAD_DTYPE;
+    if (out_row_stride < n) return LPD_ERR_BAD_STRIDE;
+    if (!elt_aligned(out, out_dtype)) return LPD_ERR_ALIGNMENT;
+    if ((rc = check_workspace(workspace, workspace_bytes, micro_plan(m, n, k).bytes))) return rc;
+    return cuda_status(launch_micro_matmul(x, y, m, n, k, out, out_dtype, out_row_stride, workspace,
                                            static_cast<cudaStream_t>(stream)));
 }
 

@@ -18,6 +18,7 @@
 #include "lpd_acc.cuh"
 #include "lpd_internal.cuh"
 #include "lpd_operators.cuh"
+#include "lpd_tc.cuh"
 
 namespace lpd {
 namespace {
@@ -333,76 +334,10 @@ constexpr int kScaleBytes = 2 * kScaleFloats * 4;
 constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kOutBytes + kScaleBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kRaster = 16;                     // row tiles that share a B tile in L2
-constexpr unsigned long long kWaitLimitNs = 4000000000ull;
-constexpr uint32_t kWaitLimitIters = 1u << 30;
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ unsigned long long globaltimer_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-__device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait of a whole warp, the same answer in every lane (so that no lane
-// goes its own way); when it gives up it raises the CTA's abort flag and sets
-// LPD_STATUS_TIMEOUT in the workspace's first word.  The clock is read only
-// once a wait has been polled for long: a read costs more than a block's MMAs.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
-                                          bool honour_abort = true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    unsigned long long t0 = 0;
-#pragma unroll 1
-    for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((n & 255u) == 0) {
-            const unsigned long long now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (__any_sync(0xffffffffu, (honour_abort && *abort_flag) || now - t0 > kWaitLimitNs)) break;
-        }
-    }
-    if ((threadIdx.x & 31) == 0) {
-        *abort_flag = 1;
-        atomicOr(status, LPD_STATUS_TIMEOUT);
-    }
-    return false;
-}
 __device__ __forceinline__ void copy_async_4(float *dst, const float *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-// Descriptor of a K-major tile of 128-byte rows under the 128-byte swizzle
-// (8-row groups of 1024 bytes): the lower word is the address / 16 (and the
-// unused leading offset), the upper word is the same for every tile.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_low(const void *tile) { return ((smem_u32(tile) & 0x3FFFFu) >> 4) | (1u << 16); }
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc,
                                         uint32_t accumulate) {
     asm volatile(
@@ -414,22 +349,6 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint32_t a_low, uint32_
         "r"(a_low), "r"(b_low), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
         : "memory");
 }
-// One lane of a warp, the same each time.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // 16 lanes x 32 columns: registers 4 i + j hold row lane / 4 + 8 (j / 2), column 8 i + 2 (lane % 4) + j % 2.
 __device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -449,15 +368,6 @@ __device__ __forceinline__ void tmem_ld_issue(uint32_t taddr, uint32_t (&r)[32])
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
-                 "r"(y), "r"(z), "r"(smem_u32(src))
-                 : "memory");
-}
-__device__ __forceinline__ void tma_store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Until the stores so far have read their shared memory.
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 struct MmMaps {
     CUtensorMap a, b;
     CUtensorMap out;  // (column, row, split); only where vec_out
@@ -814,58 +724,6 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t pa
         if (kOutF32) *reinterpret_cast<float *>(out + r * out_stride + 4 * c) = s;
         else *reinterpret_cast<__nv_bfloat16 *>(out + r * out_stride + 2 * c) = __float2bfloat16_rn(s);
     }
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static std::atomic<EncodeTiledFn> cached{nullptr};
-    EncodeTiledFn fn = cached.load(std::memory_order_acquire);
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn = reinterpret_cast<EncodeTiledFn>(p);
-        cached.store(fn, std::memory_order_release);
-    }
-    return fn;
-}
-
-// [rows, k] bytes, boxes of 128 x box_rows, 128-byte swizzle; what lies
-// outside [rows, k] reads as 0.
-bool make_map(CUtensorMap *map, const void *ptr, int64_t rows, int64_t k, int64_t stride, int box_rows) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    // (a single row's stride may be any: it is not used)
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? stride : (k + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kBlk), static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t elem[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, elem,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The output (or its partial results) [splits, m, n] in boxes of 32 rows x 128
-// bytes, 128-byte swizzle.
-bool make_out_map(CUtensorMap *map, void *ptr, int64_t m, int64_t n, int64_t splits, int64_t row_bytes,
-                  int64_t split_bytes, bool f32) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m), static_cast<cuuint64_t>(splits)};
-    if (m == 1) row_bytes = (n * (f32 ? 4 : 2) + 15) / 16 * 16;  // neither stride is used where there is one row, one split
-    if (splits == 1) split_bytes = row_bytes;
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(split_bytes)};
-    const cuuint32_t box[3] = {f32 ? 32u : 64u, 32u, 1u};
-    const cuuint32_t elem[3] = {1, 1, 1};
-    return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, box,
-              elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool kBf16, bool kE5>

@@ -1,0 +1,811 @@
+// Microscaled 4-bit floating point: quantisation and the matrix product.
+//
+// A value of an operand is q * s * t with q in e2m1 (0, 1/2, 1, 3/2, 2, 3, 4, 6 and
+// their negatives), one scale s for 16 (e4m3) or 32 (a power of two) values along k
+// and one float t for the operand: a rollout engine's 4-bit head ("[WS2] Framework
+// for ablation experiment", LogProb knobs table, rows 9-10: the head GEMM and its
+// rounding as a drift source).  The tensor cores take the block scales themselves
+// (tcgen05.mma kind::mxf4nvf4 and kind::mxf4, block_scale), so a product is a plain
+// chain of MMAs over k into one accumulator; t enters once at the end.
+#include <algorithm>
+#include <cfloat>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+#include <math_constants.h>
+
+#include "lpd_internal.cuh"
+#include "lpd_operators.cuh"
+#include "lpd_tc.cuh"
+
+namespace lpd {
+namespace {
+
+constexpr int kAtom = 512;  // bytes of scales of 128 rows x 4 blocks: (row % 32) * 16 + (row / 32 % 4) * 4 + block % 4
+
+// =============================================================== quantisation
+// A block takes a tile of 128 x 128 input values: 16 lanes a row with 8 values
+// each, two rows a warp and pass, eight passes, all held in registers, so the
+// input is read once.  A scale's values lie in two (16) or four (32) neighbouring
+// lanes.  For transposed output a thread takes 8 neighbouring rows: it then has
+// four bytes of codes of each of its 8 output rows, which turn through shared
+// memory (word g of output row c lies at g ^ (c / 8 % 16)).  The tile's scales are
+// gathered in shared memory in their final order and leave as one piece.
+constexpr int kQTile = 128;
+constexpr int kQThreads = 256;
+constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a power-of-two scale is made for
+
+struct QuantArgs {
+    const char *x;
+    int64_t x_stride;  // bytes
+    int64_t rows, cols;
+    uint8_t *out;
+    int64_t out_stride;
+    uint8_t *scales;
+    int64_t atoms;     // of scales along the output's k
+    const float *tensor_scale;
+    char *values;      // null: not wanted
+    int64_t values_stride;
+    int values_f32;
+    int n_tiles_c;
+    int vec_in, vec_out, vec_values;
+};
+
+// The scale byte of a block, the factor onto the codes' range, and what a code's
+// unit is worth before t.  `top`: the largest magnitude's bits (NaN above infinity
+// above numbers).
+template <bool kB16>
+__device__ __forceinline__ uint32_t scale_of(uint32_t top_bits, float t, float *inv, float *unit) {
+    const float top = __uint_as_float(top_bits);
+    uint32_t byte;
+    if constexpr (kB16) {
+        byte = __nv_cvt_float_to_fp8(__fdiv_rn(top, __fmul_rn(6.f, t)), __NV_SATFINITE, __NV_E4M3);
+        *unit = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
+    } else {
+        const uint32_t b = __float_as_uint(__fdiv_rn(fminf(fmaxf(__fdiv_rn(top, t), kFloor), FLT_MAX), 6.f));
+        byte = (b + 0x7fffffu) >> 23;  // up to the next power of two
+        *unit = __uint_as_float(byte << 23);
+    }
+    const float back = __fdiv_rn(1.f, __fmul_rn(*unit, t));
+    *inv = back <= FLT_MAX ? back : 0.f;
+    // a non-finite value, or a tensor scale that is none: the block reads as NaN
+    if (!(top <= FLT_MAX) || !(t > 0.f && t <= FLT_MAX)) {
+        byte = kB16 ? 0x7f : 0xff;
+        *unit = CUDART_NAN_F;
+    }
+    return byte;
+}
+
+__device__ __forceinline__ uint32_t codes_of(float a, float b, float inv) {
+    return __nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv)), __NV_E2M1, cudaRoundNearest);
+}
+// Eight codes in a word to the values that they stand for.
+__device__ __forceinline__ void values_of(uint32_t word, float unit, float t, float *v) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(word >> (8 * q)), __NV_E2M1));
+        const float2 f = __half22float2(h);
+        v[2 * q] = __fmul_rn(__fmul_rn(f.x, unit), t);
+        v[2 * q + 1] = __fmul_rn(__fmul_rn(f.y, unit), t);
+    }
+}
+// Eight neighbouring values, `n` of them inside the row.
+__device__ __forceinline__ void store_values(const QuantArgs &a, int64_t r, int64_t c, int64_t n, const float *v) {
+    char *dst = a.values + r * a.values_stride + c * (a.values_f32 ? 4 : 2);
+    if (a.vec_values && n >= 8) {
+        if (a.values_f32) {
+            __stcs(reinterpret_cast<float4 *>(dst), make_float4(v[0], v[1], v[2], v[3]));
+            __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+                w[q] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < n) {
+            if (a.values_f32) reinterpret_cast<float *>(dst)[q] = v[q];
+            else reinterpret_cast<__nv_bfloat16 *>(dst)[q] = __float2bfloat16_rn(v[q]);
+        }
+}
+
+template <bool kBf16, bool kB16, bool kTranspose>
+__global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+    __shared__ __align__(16) uint8_t atoms[kB16 ? 2 * kAtom : kAtom];
+    __shared__ __align__(16) uint32_t tops[kTranspose && !kB16 ? 8 * kQTile : 4];
+    __shared__ __align__(16) uint32_t turned[kTranspose ? kQTile * 16 : 4];
+    constexpr int kElt = kBf16 ? 2 : 4, kBlk = kB16 ? 16 : 32, kBlocks = kQTile / kBlk;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int64_t tile_r = blockIdx.x / a.n_tiles_c, tile_c = blockIdx.x % a.n_tiles_c;
+    const int64_t r0 = tile_r * kQTile, c0 = tile_c * kQTile;
+    const int col = (lane & 15) * 8;
+    const int row_group = warp * 2 + (lane >> 4);
+    const auto row_of = [&](int p) { return kTranspose ? row_group * 8 + p : p * 16 + row_group; };
+    const float ts = a.tensor_scale ? *a.tensor_scale : 1.f;
+    // raw words of the thread's 8 passes: 8 values each, outside the tensor 0
+    uint4 raw[8][kBf16 ? 1 : 2];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const int64_t r = r0 + row_of(p), c = c0 + col;
+        const char *src = a.x + r * a.x_stride + c * kElt;
+#pragma unroll
+        for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = make_uint4(0, 0, 0, 0);
+        if (r < a.rows && c < a.cols) {
+            if (a.vec_in && c + 8 <= a.cols) {
+#pragma unroll
+                for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = __ldcs(reinterpret_cast<const uint4 *>(src) + h);
+            } else {
+                uint32_t w[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const bool in = c + q < a.cols;
+                    if constexpr (kBf16) {
+                        const uint32_t b = in ? reinterpret_cast<const unsigned short *>(src)[q] : 0u;
+                        if (q & 1) w[q >> 1] |= b << 16;
+                        else w[q >> 1] = b;
+                    } else {
+                        w[q] = in ? reinterpret_cast<const uint32_t *>(src)[q] : 0u;
+                    }
+                }
+                raw[p][0] = make_uint4(w[0], w[1], w[2], w[3]);
+                if constexpr (!kBf16) raw[p][1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+    }
+    const auto values = [&](int p, float *v) {
+        if constexpr (kBf16) {
+            const uint32_t ws[4] = {raw[p][0].x, raw[p][0].y, raw[p][0].z, raw[p][0].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v[2 * q] = __uint_as_float(ws[q] << 16);
+                v[2 * q + 1] = __uint_as_float(ws[q] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < (kBf16 ? 1 : 2); ++h) {
+                v[4 * h] = __uint_as_float(raw[p][h].x);
+                v[4 * h + 1] = __uint_as_float(raw[p][h].y);
+                v[4 * h + 2] = __uint_as_float(raw[p][h].z);
+                v[4 * h + 3] = __uint_as_float(raw[p][h].w);
+            }
+        }
+    };
+    const auto bits = [](float x) { return __float_as_uint(x) & 0x7fffffffu; };
+    // the tile's scale byte of output row r, block b of the tile
+    const auto put = [&](int r, int b, uint32_t byte) {
+        atoms[(b >> 2) * kAtom + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = static_cast<uint8_t>(byte);
+    };
+    if constexpr (!kTranspose) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float v[8];
+            values(p, v);
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            if constexpr (!kB16) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            float inv, unit;
+            const uint32_t byte = scale_of<kB16>(m, ts, &inv, &unit);
+            const int64_t r = r0 + row_of(p), c = c0 + col;
+            const bool in = r < a.rows && c < a.cols;
+            // (a block that starts behind the last value has no scale: 0)
+            if ((lane & (kB16 ? 1 : 3)) == 0) put(row_of(p), col / kBlk, in ? byte : 0u);
+            if (!in) continue;
+            uint32_t word = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) word |= codes_of(v[2 * q], v[2 * q + 1], inv) << (8 * q);
+            uint8_t *dst = a.out + r * a.out_stride + c / 2;
+            const int64_t n = a.cols - c;
+            if (a.vec_out && n >= 8) {
+                __stcs(reinterpret_cast<uint32_t *>(dst), word);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (2 * q < n) dst[q] = static_cast<uint8_t>(word >> (8 * q));
+            }
+            if (a.values) {
+                values_of(word, unit, ts, v);
+                store_values(a, r, c, n, v);
+            }
+        }
+    } else {
+        uint32_t m[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m[q] = 0;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float v[8];
+            values(p, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m[q] = max(m[q], bits(v[q]));
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m[q] = max(m[q], __shfl_xor_sync(0xffffffffu, m[q], 16));
+        if constexpr (!kB16) {  // a block of 32 rows is two warps'
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (lane < 16) tops[warp * kQTile + col + q] = m[q];
+            __syncthreads();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m[q] = max(m[q], tops[(warp ^ 1) * kQTile + col + q]);
+        }
+        const int b = warp / (kB16 ? 1 : 2);  // the tile's block
+        const bool block_in = r0 + b * kBlk < a.rows;
+        // the two halves of a warp have the same columns: four divisions' work each
+        float inv[8], unit[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool upper = lane >= 16;
+            float iv, un;
+            const uint32_t byte = scale_of<kB16>(upper ? m[q + 4] : m[q], ts, &iv, &un);
+            const int c = col + q + (upper ? 4 : 0);
+            if (kB16 || (warp & 1) == 0) put(c, b, block_in && c0 + c < a.cols ? byte : 0u);
+            const float oi = __shfl_xor_sync(0xffffffffu, iv, 16), ou = __shfl_xor_sync(0xffffffffu, un, 16);
+            inv[q] = upper ? oi : iv;
+            inv[q + 4] = upper ? iv : oi;
+            unit[q] = upper ? ou : un;
+            unit[q + 4] = upper ? un : ou;
+        }
+        uint32_t words[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) words[q] = 0;
+#pragma unroll
+        for (int p = 0; p < 8; p += 2) {
+            float v[2][8];
+            values(p, v[0]);
+            values(p + 1, v[1]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) words[q] |= codes_of(v[0][q], v[1][q], inv[q]) << (4 * p);
+        }
+        const int64_t oc = r0 + row_group * 8;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            turned[(col + q) * 16 + (row_group ^ (col >> 3))] = words[q];
+            if (a.values && c0 + col + q < a.cols && oc < a.rows) {
+                float v[8];
+                values_of(words[q], unit[q], ts, v);
+                store_values(a, c0 + col + q, oc, a.rows - oc, v);
+            }
+        }
+        __syncthreads();
+        // 128 output rows (input columns) of 64 bytes: 4 lanes a row with 16 bytes each
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int row = p * 64 + (t >> 2), at = t & 3, key = row >> 3;
+            const int64_t orow = c0 + row, ov = r0 + at * 32;  // (the first of 32 values)
+            if (orow >= a.cols || ov >= a.rows) continue;
+            const uint4 w = *reinterpret_cast<const uint4 *>(&turned[row * 16 + ((at ^ (key >> 2)) << 2)]);
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t ws[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {  // word j lies at j ^ key % 4
+                const uint32_t lo = (key & 1) ? in[j ^ 1] : in[j], hi = (key & 1) ? in[j ^ 3] : in[j ^ 2];
+                ws[j] = (key & 2) ? hi : lo;
+            }
+            uint8_t *dst = a.out + orow * a.out_stride + ov / 2;
+            const int64_t n = a.rows - ov;
+            if (a.vec_out && n >= 32) {
+                __stcs(reinterpret_cast<uint4 *>(dst), make_uint4(ws[0], ws[1], ws[2], ws[3]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (2 * j < n) dst[j] = static_cast<uint8_t>(ws[j >> 2] >> (8 * (j & 3)));
+            }
+        }
+    }
+    __syncthreads();
+    // the tile's scales: the atoms of one group of 128 output rows, neighbours along k
+    const int64_t group = kTranspose ? tile_c : tile_r, atom0 = (kTranspose ? tile_r : tile_c) * (kBlocks / 4);
+    if (t < (kBlocks / 4) * (kAtom / 4) && atom0 + t / (kAtom / 4) < a.atoms)
+        reinterpret_cast<uint32_t *>(a.scales + (group * a.atoms + atom0) * kAtom)[t] = reinterpret_cast<const uint32_t *>(atoms)[t];
+}
+
+// ==================================================================== product
+// One persistent CTA per SM.  Warp 0 streams 256 values of k of A (128 rows), of
+// B (256 rows) and of their scales through a three-stage ring (TMA, 128-byte
+// swizzle; the scales by bulk copies).  Warp 1 copies a stage's scales into tensor
+// memory (tcgen05.cp, each to all four lane quadrants) and issues its four M=128
+// N=256 K=64 MMAs into the one accumulator.  A stage's scales have columns of their
+// own, so they are written only after the MMAs that read the last ones have freed
+// the stage.  Two warpgroups read the accumulator into registers, 128 columns a
+// thread, and free it at once; rounding and stores (TMA) run under the next tile.
+constexpr int kTM = 128, kTN = 256, kTK = 256;
+constexpr int kStages = 3;
+constexpr int kABytes = kTM * kTK / 2, kBBytes = kTN * kTK / 2;
+constexpr int kSaBytes = 4 * kAtom, kSbBytes = 8 * kAtom;  // blocks of 16 (those of 32 need half)
+constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;  // 54 KB
+static_assert(kStageBytes % 1024 == 0, "the swizzle's 1024-byte groups");
+constexpr int kEpiWarps = 8;
+constexpr int kEpiCols = kTN / (kEpiWarps / 4);  // columns a warp
+constexpr int kMmThreads = (4 + kEpiWarps) * 32;
+// registers a thread after the split (three warps a sub-partition, launched at
+// 168 each: 40 + 2 * 232 = 3 * 168)
+constexpr int kRegsFront = 40, kRegsEpi = 232;
+constexpr int kOutWarp = 32 * 128;               // staging of a warp: a box of 32 rows x 128 bytes
+constexpr int kOutPitch = 80;                    // or rows of 64 bytes and 16 against bank conflicts
+constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpiWarps * kOutWarp;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleCol = kTN;              // a stage's scales: 16 columns of A's, 32 of B's
+constexpr uint32_t kScaleCols = 48;
+static_assert(kScaleCol + kStages * kScaleCols <= kTmemCols, "tensor memory");
+constexpr int kRaster = 16;                      // row tiles that share a B tile in L2
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// 32 rows x 16 bytes of scales (an atom) to four columns of all lane quadrants.
+constexpr uint32_t kAtomDescHigh = (128u >> 4) | (1u << 14);  // 8-row groups of 128 bytes, no swizzle
+__device__ __forceinline__ void scales_to_tmem(uint32_t col, uint32_t low) {
+    asm volatile(
+        "{\n\t.reg .b64 d;\n\t"
+        "mov.b64 d, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(col),
+        "r"(low), "r"(kAtomDescHigh)
+        : "memory");
+}
+template <bool kB16>
+__device__ __forceinline__ void umma_f4(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sa,
+                                        uint32_t sb, uint32_t accumulate) {
+    if constexpr (kB16)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %7};\n\t"
+            "mov.b64 db, {%2, %7};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(kDescHigh)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %7};\n\t"
+            "mov.b64 db, {%2, %7};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(kDescHigh)
+            : "memory");
+}
+// 32 lanes x 32 columns, a row a lane.
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+struct MmMaps {
+    CUtensorMap a, b;
+    CUtensorMap out;  // (column, row, split); only where vec_out
+};
+
+struct MmArgs {
+    const uint8_t *sa, *sb;
+    const float *ta, *tb;
+    int64_t m, n, k;
+    int64_t atoms;             // of scales along k
+    int groups_n;              // groups of 128 rows of B
+    int kb_total, kb_per_split, n_splits;
+    int n_tm, n_tn;
+    uint32_t idesc;
+    char *out;
+    int64_t out_stride;        // bytes
+    int64_t split_stride;      // bytes between the partial results of two splits
+    int vec_out;               // 16-byte aligned output rows
+    int whole_out;             // ... of whole 16-byte pieces
+    uint32_t *status;
+};
+
+// Work items in raster order: groups of kRaster row tiles over all column
+// tiles, row tiles innermost, then the splits.
+__device__ __forceinline__ void item_coords(int64_t w, const MmArgs &a, int &tm, int &tn, int &split) {
+    const int64_t tiles = static_cast<int64_t>(a.n_tm) * a.n_tn;
+    split = static_cast<int>(w / tiles);
+    const int64_t i = w - split * tiles;
+    const int64_t per_group = static_cast<int64_t>(kRaster) * a.n_tn;
+    const int g = static_cast<int>(i / per_group);
+    const int64_t local = i - g * per_group;
+    const int gm = min(kRaster, a.n_tm - g * kRaster);
+    tn = static_cast<int>(local / gm);
+    tm = g * kRaster + static_cast<int>(local - static_cast<int64_t>(tn) * gm);
+}
+
+template <bool kOutF32, bool kB16>
+__global__ void __launch_bounds__(kMmThreads, 1)
+    product_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
+    extern __shared__ __align__(1024) char smem_raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full, acc_empty, done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    char *const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset keeps the loads shared ones)
+    char *const staged = smem + static_cast<size_t>(kStages) * kStageBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits;
+    constexpr int kAtomsPer = kB16 ? 4 : 2;  // atoms of scales along a stage's k
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, kEpiWarps);
+        mbar_init(&done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFront));
+        const bool leader = elect_one();  // (whole warps run the loops, so that their values are uniform)
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            uint32_t s = 0, phase = 1, issued = 0;  // the first turn finds every stage empty
+            bool ok = true;
+            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                int tm, tn, split;
+                item_coords(w, a, tm, tn, split);
+                const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
+                const int groups = min(2, a.groups_n - 2 * tn);
+#pragma unroll 1
+                for (int kb = split * a.kb_per_split; kb < kb1; ++kb) {
+                    ok = wait_warp(&empty[s], phase, &abort_flag, a.status);
+                    if (!ok) break;
+                    if (leader) {
+                        char *st = smem + s * kStageBytes;
+                        const int64_t atom = static_cast<int64_t>(kb) * kAtomsPer;
+                        const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kAtomsPer), a.atoms - atom)) * kAtom;
+                        mbar_arrive_expect_tx(&full[s], kABytes + kBBytes + bytes * (1 + groups));
+                        tma_load_2d(st, &maps.a, kb * (kTK / 2), tm * kTM, &full[s]);
+                        tma_load_2d(st + kABytes, &maps.b, kb * (kTK / 2), tn * kTN, &full[s]);
+                        bulk_load(st + kABytes + kBBytes, a.sa + (tm * a.atoms + atom) * kAtom, bytes, &full[s]);
+                        for (int g = 0; g < groups; ++g)
+                            bulk_load(st + kABytes + kBBytes + kSaBytes + g * (kSbBytes / 2),
+                                      a.sb + ((2 * static_cast<int64_t>(tn) + g) * a.atoms + atom) * kAtom, bytes, &full[s]);
+                    }
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // every copy issued must land before the CTA exits: the last turn's
+            // stages, each in the phase of its last use
+            for (uint32_t j = 0; j < issued; ++j) {
+                if (s == 0) {
+                    s = kStages;
+                    phase ^= 1;
+                }
+                --s;
+                wait_warp(&full[s], phase ^ 1, &abort_flag, a.status, false);
+            }
+        } else if (warp == 1) {
+            // ----------------------------------------------------------------- MMA
+            uint32_t s = 0, phase = 0, turn = 1;  // `turn`: the parity that the emptied accumulator shows
+            bool ok = true, issued = false;
+            const uint32_t base = desc_low(smem), plain = (smem_u32(smem) & 0x3FFFFu) >> 4;
+            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+                int tm, tn, split;
+                item_coords(w, a, tm, tn, split);
+                const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
+                ok = wait_warp(&acc_empty, turn, &abort_flag, a.status);
+                turn ^= 1;
+#pragma unroll 1
+                for (int kb = kb0; ok && kb < kb1; ++kb) {
+                    ok = wait_warp(&full[s], phase, &abort_flag, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t da = base + s * (kStageBytes >> 4), db = da + (kABytes >> 4);
+                        const uint32_t sa = plain + s * (kStageBytes >> 4) + ((kABytes + kBBytes) >> 4), sb = sa + (kSaBytes >> 4);
+                        const uint32_t ca = tmem + kScaleCol + s * kScaleCols, cb = ca + 16;
+                        const int mmas = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(kb) * kTK + 63) / 64));
+#pragma unroll
+                        for (int j = 0; j < kAtomsPer; ++j) {
+                            if (j * (4 / kAtomsPer) >= mmas) break;
+                            scales_to_tmem(ca + 4 * j, sa + j * (kAtom >> 4));
+                            scales_to_tmem(cb + 8 * j, sb + j * (kAtom >> 4));
+                            scales_to_tmem(cb + 8 * j + 4, sb + (4 + j) * (kAtom >> 4));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {  // K = 32 bytes inside the swizzle row
+                            if (j >= mmas) break;
+                            // (of a word of four scales of 32 an MMA takes the first or the last two)
+                            const uint32_t idesc = kB16 ? a.idesc : a.idesc | (j & 1) << 5 | (j & 1) << 30;
+                            const int at = kB16 ? j : j / 2;
+                            umma_f4<kB16>(tmem, da + 2 * j, db + 2 * j, idesc, ca + 4 * at, cb + 8 * at, kb > kb0 || j > 0 ? 1u : 0u);
+                        }
+                        umma_commit(&empty[s]);
+                        if (kb + 1 == kb1) umma_commit(&acc_full);
+                    }
+                    issued = true;
+                    if (++s == kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (issued) {
+                if (leader) umma_commit(&done);
+                wait_warp(&done, 0, &abort_flag, a.status, false);
+            }
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+        // ------------------------------------------------------------ epilogue
+        const int quad = warp & 3, part = (warp - 4) >> 2;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kEpiCols;
+        char *const mine = staged + (warp - 4) * kOutWarp;
+        const float scale = __fmul_rn(a.ta ? *a.ta : 1.f, a.tb ? *a.tb : 1.f);
+        uint32_t turn = 0;
+        bool ok = true;
+        for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+            int tm, tn, split;
+            item_coords(w, a, tm, tn, split);
+            const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
+            float acc[kEpiCols];
+            ok = ok && wait_warp(&acc_full, turn, &abort_flag, a.status);
+            turn ^= 1;
+            if (ok) {
+                tc_fence_after();
+                uint32_t *const r = reinterpret_cast<uint32_t *>(acc);
+#pragma unroll
+                for (int c = 0; c < kEpiCols; c += 32) tmem_ld_32(lane_addr + c, r + c);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty);
+#pragma unroll
+                for (int j = 0; j < kEpiCols; ++j) acc[j] = __fmul_rn(acc[j], scale);
+            } else {  // a wait gave up: this tile reads as NaN
+#pragma unroll
+                for (int j = 0; j < kEpiCols; ++j) acc[j] = CUDART_NAN_F;
+            }
+            char *const out = a.out + split * a.split_stride;
+            const int64_t row0 = static_cast<int64_t>(tm) * kTM + quad * 32;
+            if (row0 >= a.m) continue;
+            // (a TMA store writes whole 16-byte pieces: columns behind an n
+            // between two of them are not the product's to write)
+            if (a.vec_out && (a.whole_out || col0 + kEpiCols <= a.n)) {
+                // boxes of 32 rows x 128 bytes under the 128-byte swizzle: chunk
+                // q of row l lies at q ^ (l % 8)
+                constexpr int kBoxCols = kOutF32 ? 32 : 64;
+#pragma unroll
+                for (int box = 0; box < kEpiCols / kBoxCols; ++box) {
+                    if (lane == 0) tma_store_wait_read();  // the last box has been read
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float *v = &acc[box * kBoxCols + q * (kBoxCols / 8)];
+                        uint4 u;
+                        if constexpr (kOutF32) {
+                            u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                        } else {
+                            uint32_t h[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                                h[e] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            u = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                        *reinterpret_cast<uint4 *>(mine + lane * 128 + ((q ^ (lane & 7)) << 4)) = u;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    const int64_t c = col0 + box * kBoxCols;
+                    if (lane == 0) {
+                        if (c < a.n) tma_store_3d(&maps.out, mine, static_cast<int>(c), static_cast<int>(row0), split);
+                        tma_store_commit();
+                    }
+                }
+                continue;
+            }
+            // 64-byte pieces of 32 rows through shared memory
+            if (lane == 0) tma_store_wait_read();  // the last tile's box lay there
+            constexpr int kCols = kOutF32 ? 16 : 32;  // columns of a piece
+#pragma unroll
+            for (int p = 0; p < kEpiCols / kCols; ++p) {
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < kCols; q += 2) {
+                    const float *v = &acc[p * kCols + q];
+                    if (kOutF32) *reinterpret_cast<float2 *>(mine + lane * kOutPitch + 4 * q) = make_float2(v[0], v[1]);
+                    else *reinterpret_cast<__nv_bfloat162 *>(mine + lane * kOutPitch + 2 * q) = __floats2bfloat162_rn(v[0], v[1]);
+                }
+                __syncwarp();
+                const int64_t c = col0 + p * kCols;
+                if (c >= a.n) break;
+                constexpr int kRowsAtOnce = 32 / kCols;
+                for (int q = 0; q < 32 / kRowsAtOnce; ++q) {
+                    const int rr = q * kRowsAtOnce + lane / kCols, cc = lane % kCols;
+                    if (row0 + rr < a.m && c + cc < a.n) {
+                        char *dst = out + (row0 + rr) * a.out_stride + (c + cc) * (kOutF32 ? 4 : 2);
+                        if (kOutF32) *reinterpret_cast<uint32_t *>(dst) = *reinterpret_cast<const uint32_t *>(mine + rr * kOutPitch + 4 * cc);
+                        else *reinterpret_cast<unsigned short *>(dst) = *reinterpret_cast<const unsigned short *>(mine + rr * kOutPitch + 2 * cc);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    if (warp >= 4 && lane == 0) tma_store_wait_read();  // shared memory outlives the last stores' reads
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// C = the partial results added in split order, rounded once.
+template <bool kOutF32>
+__global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t part_stride, int64_t split_stride,
+                                                   int n_splits, int64_t m, int64_t n, char *out, int64_t out_stride) {
+    const int64_t cells = m * n;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < cells; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = i / n, c = i - r * n;
+        const float *p = part + r * part_stride + c;
+        float s = p[0];
+        for (int k = 1; k < n_splits; ++k) s = __fadd_rn(s, p[k * split_stride]);
+        if (kOutF32) *reinterpret_cast<float *>(out + r * out_stride + 4 * c) = s;
+        else *reinterpret_cast<__nv_bfloat16 *>(out + r * out_stride + 2 * c) = __float2bfloat16_rn(s);
+    }
+}
+
+template <bool kBf16>
+cudaError_t quantize_typed(const QuantArgs &a, bool b16, bool transpose, unsigned grid, cudaStream_t s) {
+    if (b16) {
+        if (transpose) quantize_kernel<kBf16, true, true><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, true, false><<<grid, kQThreads, 0, s>>>(a);
+    } else {
+        if (transpose) quantize_kernel<kBf16, false, true><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, false, false><<<grid, kQThreads, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+template <bool kOutF32, bool kB16>
+cudaError_t product_typed(const MmMaps &maps, const MmArgs &a, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    const cudaError_t e = set_smem_once(product_kernel<kOutF32, kB16>, kMmSmem, configured);
+    if (e != cudaSuccess) return e;
+    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits, sms = device_sm_count();
+    product_kernel<kOutF32, kB16><<<static_cast<unsigned>(items < sms ? items : sms), kMmThreads, kMmSmem, stream>>>(maps, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// The k axis is split where the output's tiles would leave half of the
+// multiprocessors idle, into parts of at least four stages (1024 values).
+BlockPlan micro_plan(int64_t m, int64_t n, int64_t k) {
+    BlockPlan p{};
+    p.n_tm = (m + kTM - 1) / kTM;
+    p.n_tn = (n + kTN - 1) / kTN;
+    p.kb_total = (k + kTK - 1) / kTK;
+    const int64_t tiles = p.n_tm * p.n_tn;
+    const int64_t sms = device_sm_count();
+    int64_t want = tiles > 0 ? sms / tiles : 1;
+    want = std::min(want, p.kb_total / 4);
+    p.n_splits = std::max<int64_t>(want, 1);
+    p.kb_per_split = p.n_splits > 1 ? (p.kb_total + p.n_splits - 1) / p.n_splits : p.kb_total;
+    if (p.n_splits > 1) p.n_splits = (p.kb_total + p.kb_per_split - 1) / p.kb_per_split;
+    p.part_stride = (n + 3) / 4 * 4;
+    p.bytes = 256;
+    if (p.n_splits > 1) p.bytes += align256(static_cast<size_t>(p.n_splits) * m * p.part_stride * 4);
+    return p;
+}
+
+cudaError_t launch_micro_quantize(const void *x, int x_dtype, int64_t x_stride_elems, int64_t rows, int64_t cols,
+                                  bool transpose, const MicroOperand &o, void *values, int values_dtype,
+                                  int64_t values_stride_elems, cudaStream_t stream) {
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    QuantArgs a{};
+    const bool bf16 = x_dtype == LPD_BF16;
+    a.x = static_cast<const char *>(x);
+    a.x_stride = x_stride_elems * (bf16 ? 2 : 4);
+    a.rows = rows;
+    a.cols = cols;
+    a.out = static_cast<uint8_t *>(const_cast<void *>(o.ptr));
+    a.out_stride = o.row_stride;
+    a.scales = const_cast<uint8_t *>(o.scales);
+    a.atoms = o.atoms;
+    a.tensor_scale = o.tensor_scale;
+    a.values = static_cast<char *>(values);
+    a.values_f32 = values_dtype == LPD_F32 ? 1 : 0;
+    a.values_stride = values_stride_elems * (a.values_f32 ? 4 : 2);
+    a.n_tiles_c = static_cast<int>((cols + kQTile - 1) / kQTile);
+    const uintptr_t unit = transpose ? 16 : 4;
+    a.vec_in = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.x_stride % 16 == 0;
+    a.vec_out = reinterpret_cast<uintptr_t>(o.ptr) % unit == 0 && static_cast<uintptr_t>(o.row_stride) % unit == 0;
+    a.vec_values = reinterpret_cast<uintptr_t>(values) % 16 == 0 && a.values_stride % 16 == 0;
+    const unsigned grid = static_cast<unsigned>((rows + kQTile - 1) / kQTile * a.n_tiles_c);
+    return bf16 ? quantize_typed<true>(a, o.b16, transpose, grid, stream) : quantize_typed<false>(a, o.b16, transpose, grid, stream);
+}
+
+cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, int64_t m, int64_t n, int64_t k,
+                                void *out, int out_dtype, int64_t out_stride_elems, void *workspace,
+                                cudaStream_t stream) {
+    const bool f32 = out_dtype == LPD_F32;
+    const int64_t out_stride = out_stride_elems * (f32 ? 4 : 2);
+    if (m == 0 || n == 0) return cudaSuccess;
+    if (k == 0) return cudaMemset2DAsync(out, out_stride, 0, n * (f32 ? 4 : 2), m, stream);
+    const BlockPlan p = micro_plan(m, n, k);
+    MmMaps maps;
+    if (!make_map(&maps.a, x.ptr, m, (k + 1) / 2, x.row_stride, kTM) || !make_map(&maps.b, y.ptr, n, (k + 1) / 2, y.row_stride, kTN))
+        return cudaErrorInvalidValue;
+    MmArgs a{};
+    a.sa = x.scales;
+    a.sb = y.scales;
+    a.ta = x.tensor_scale;
+    a.tb = y.tensor_scale;
+    a.m = m;
+    a.n = n;
+    a.k = k;
+    a.atoms = x.atoms;
+    a.groups_n = static_cast<int>((n + 127) / 128);
+    a.kb_total = static_cast<int>(p.kb_total);
+    a.kb_per_split = static_cast<int>(p.kb_per_split);
+    a.n_splits = static_cast<int>(p.n_splits);
+    a.n_tm = static_cast<int>(p.n_tm);
+    a.n_tn = static_cast<int>(p.n_tn);
+    // block scaling: A's and B's format e2m1 (1 at bits 7 and 10), N / 8 at bit 17, scales e4m3 or
+    // powers of two (bit 23), M / 16 at bit 24; both K-major
+    a.idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTN >> 3) << 17) | (x.b16 ? 0u : 1u << 23) |
+              (static_cast<uint32_t>(kTM >> 4) << 24);
+    a.status = static_cast<uint32_t *>(workspace);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    const bool split = p.n_splits > 1;
+    a.out = split ? reinterpret_cast<char *>(part) : static_cast<char *>(out);
+    a.out_stride = split ? p.part_stride * 4 : out_stride;
+    a.split_stride = split ? m * p.part_stride * 4 : 0;
+    a.vec_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 16 == 0;
+    const bool to_f32 = split || f32;
+    // (partial results have room up to their row stride)
+    const int64_t n_written = split ? p.part_stride : n;
+    a.whole_out = n_written % (to_f32 ? 4 : 8) == 0;
+    if (a.vec_out && !make_out_map(&maps.out, a.out, m, n_written, p.n_splits, a.out_stride, a.split_stride, to_f32))
+        return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (to_f32) e = x.b16 ? product_typed<true, true>(maps, a, stream) : product_typed<true, false>(maps, a, stream);
+    else e = x.b16 ? product_typed<false, true>(maps, a, stream) : product_typed<false, false>(maps, a, stream);
+    if (e != cudaSuccess || !split) return e;
+    const int64_t blocks = std::min<int64_t>((m * n + 255) / 256, static_cast<int64_t>(device_sm_count()) * 16);
+    if (f32)
+        join_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
+                                                                          static_cast<char *>(out), out_stride);
+    else
+        join_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
+                                                                           static_cast<char *>(out), out_stride);
+    return cudaGetLastError();
+}
+
+}  // namespace lpd

@@ -97,4 +97,21 @@ cudaError_t launch_block_matmul(const BlockOperand &x, const BlockOperand &y, in
                                 void *out, int out_dtype, int64_t out_stride_elems, void *workspace,
                                 cudaStream_t stream);
 
+// ---------------------------------------------------------------- microscaled 4-bit operands
+struct MicroOperand {
+    const void *ptr;
+    int64_t row_stride;    // bytes
+    bool b16;              // blocks of 16 under e4m3 scales, else of 32 under powers of two
+    const uint8_t *scales;
+    int64_t atoms;         // 512-byte pieces of scales along k
+    const float *tensor_scale;
+};
+BlockPlan micro_plan(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_micro_quantize(const void *x, int x_dtype, int64_t x_stride_elems, int64_t rows, int64_t cols,
+                                  bool transpose, const MicroOperand &out, void *values, int values_dtype,
+                                  int64_t values_stride_elems, cudaStream_t stream);
+cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, int64_t m, int64_t n, int64_t k,
+                                void *out, int out_dtype, int64_t out_stride_elems, void *workspace,
+                                cudaStream_t stream);
+
 }  // namespace lpd
