@@ -5,7 +5,7 @@
 // arbitrarily near each other, so the sums of a row are integers: any order of
 // addition gives the same bits, and one row's answer does not depend on how its
 // columns were spread over threads.  A weight is formed to 2^-31 of itself
-// (weight_rough) and for the row's heaviest tokens to 2^-44 (weight_precise):
+// (weight_rough) and for the row's heaviest tokens to 2^-41 (weight_precise):
 // the errors of many small weights average out, those of a few large ones would
 // not.  (A plain exponential in float32 is off by 2^-22 with the rounding of its
 // argument: it moves the border of a nucleus by a token in one row of a thousand.)
@@ -96,11 +96,6 @@ __host__ __device__ __forceinline__ WeightScale weight_scale(float scale, float 
 
 constexpr double kLn2Unit = 0.69314718055994530942 / kUnits;
 
-// Units between x and the row's origin, in double.
-__host__ __device__ __forceinline__ double weight_units(float x, const WeightScale &w, float top) {
-    return w.wide ? (static_cast<double>(x) - static_cast<double>(top)) * w.c : static_cast<double>(x) * w.c - w.origin;
-}
-
 // For x > w.cut and x <= top, not wide.
 __host__ __device__ __forceinline__ uint64_t weight_rough(float x, const WeightScale &w, const WeightEntry *table) {
     const float p = mul_rn(x, w.ch);
@@ -117,21 +112,50 @@ __host__ __device__ __forceinline__ uint64_t weight_rough(float x, const WeightS
     return (static_cast<uint64_t>(m) << (kWeightOne - 30)) >> (s & 63);
 }
 
-// For any finite x <= top.
-__host__ __device__ __forceinline__ uint64_t weight_precise(float x, const WeightScale &w, float top, const double *table) {
-    const double u = weight_units(x, w, top);
-    if (!(u > -(kWeightOne + 2.0) * kUnits)) return 0;
-    const double jf = rint(u);
-    const double v = (u - jf) * kLn2Unit;
-    const int j = static_cast<int>(jf);
-    const double t = table[j & (kUnits - 1)];
-    const double m = t + t * (v * (1 + v * (0.5 + v * (1.0 / 6 + v * (1.0 / 24)))));
-    const int s = -(j >> 8);
+// 2^44 times a float below 2^19 in magnitude, rounded to a whole number.
+__host__ __device__ __forceinline__ int64_t steps_of(float x) {
 #ifdef __CUDA_ARCH__
-    return __double2ull_rn(m * __hiloint2double((1023 + kWeightOne - s) << 20, 0));
+    return __float2ll_rn(x * 17592186044416.f);
 #else
-    return static_cast<uint64_t>(std::nearbyint(std::ldexp(m, kWeightOne - s)));
+    return static_cast<int64_t>(std::nearbyint(static_cast<double>(x) * 17592186044416.0));
 #endif
+}
+
+// For finite x <= top.  The argument and the terms of the series are carried in
+// two floats, the table's entries in 2^-62: 2^-41 of the weight in all (and 2^-55 for each
+// unit that x itself lies from 0).
+__host__ __device__ __forceinline__ uint64_t weight_precise(float x, const WeightScale &w, float top, const uint64_t *table) {
+    float h, q;  // the argument's fraction of a unit
+    int j;
+    if (w.wide) {
+        const double u = (static_cast<double>(x) - static_cast<double>(top)) * w.c;
+        if (!(u > -(kWeightOne + 2.0) * kUnits)) return 0;
+        const double whole = rint(u);
+        j = static_cast<int>(whole);
+        h = static_cast<float>(u - whole);
+        q = static_cast<float>(u - whole - static_cast<double>(h));
+    } else {
+        if (!(x > w.cut)) return 0;
+        const float p = mul_rn(x, w.ch);
+        const float b = add_rn(p, kMagic);
+        j = static_cast<int>(bits_of(b) - kMagicBits) - w.origin;
+        h = add_rn(p, -add_rn(b, -kMagic));
+        q = fma_rn(x, w.cl, fma_rn(x, w.ch, -p));
+    }
+    const float a = add_rn(h, q), al = add_rn(q, -add_rn(a, -h));
+    constexpr float k1 = static_cast<float>(kLn2Unit), k1l = static_cast<float>(kLn2Unit - static_cast<double>(k1)),
+                    k2 = static_cast<float>(kLn2Unit * kLn2Unit / 2), k3 = static_cast<float>(kLn2Unit * kLn2Unit * kLn2Unit / 6),
+                    k4 = static_cast<float>(kLn2Unit * kLn2Unit * kLn2Unit * kLn2Unit / 24);
+    const float y = mul_rn(a, k1);
+    const float yl = fma_rn(mul_rn(a, a), fma_rn(a, fma_rn(a, k4, k3), k2), fma_rn(al, k1, fma_rn(a, k1l, fma_rn(a, k1, -y))));
+    const uint64_t t = table[j & (kUnits - 1)];  // 2^(i / 256) in units of 2^-62
+    const float th = static_cast<float>(static_cast<uint32_t>(t >> 40)) * 2.384185791015625e-7f;  // its first 23 bits: 2^-22 each
+    const float tl = static_cast<float>(static_cast<uint32_t>(t >> 8)) * 5.551115123125783e-17f;
+    const float m = mul_rn(th, y);
+    const float ml = fma_rn(tl, y, fma_rn(th, yl, fma_rn(th, y, -m)));
+    const int s = -(j >> 8);
+    const uint64_t v = ((t + (1u << (61 - kWeightOne))) >> (62 - kWeightOne)) + static_cast<uint64_t>(steps_of(m) + steps_of(ml));
+    return v >> (s & 63);
 }
 
 }  // namespace lpd

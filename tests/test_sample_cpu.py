@@ -115,9 +115,11 @@ def test_definition_by_hand():
 def test_weights_compiled_for_the_host(tmp_path):
     """The weights against long double: a rough one is off by the table's rounding,
     its correction's and one of the argument's (2^-31 each at the mantissa's lower
-    end, 2^-32 of the argument times ln 2), so below 2^-29.5, plus half a step of
-    2^-44; a precise one by 2^-45 (its argument in double is 2^23 units at most, 2^-30 of
-    one) and that half step."""
+    end, 2^-32 of the argument times ln 2), so below 2^-29.5, plus a step of 2^-44
+    (shifts cut off).  A precise one: three roundings of terms below 2^-20 (2^-44
+    each), those of two parts to steps of 2^-44, so below 2^-41 of a weight that is
+    1/2 at least, that step, and the argument's lower part, at most 2^-23 of the
+    units that x lies from 0, rounded by 2^-24 of itself (times ln 2 / 256: 2^-55)."""
     if not shutil.which("g++"):
         pytest.skip("g++ not found")
     (tmp_path / "w.cpp").write_text(r'''
@@ -127,12 +129,12 @@ def test_weights_compiled_for_the_host(tmp_path):
 using namespace lpd;
 int main() {
     WeightEntry rough[kUnits];
-    double precise[kUnits];
+    uint64_t precise[kUnits];
     for (int i = 0; i < kUnits; ++i) {
         const long double v = exp2l((long double)i / kUnits);
         rough[i].whole = (uint32_t)llroundl(v * 1073741824.0L);
         rough[i].part = (float)(v * 1073741824.0L);
-        precise[i] = (double)v;
+        precise[i] = (uint64_t)llroundl(v * 4611686018427387904.0L);
     }
     std::mt19937_64 g(1);
     std::uniform_real_distribution<double> u(0, 1);
@@ -148,10 +150,11 @@ int main() {
                 const long double at = w.wide ? ((long double)x - top) * w.c : (long double)x * w.c - w.origin;
                 const long double want = at < -48 * kUnits ? 0 : ldexpl(exp2l(at / kUnits), kWeightOne);
                 const long double p = weight_precise(x, w, top, precise);
-                if (fabsl(p - want) > want * ldexpl(1, -45) + 1) ++bad;
+                const long double far = w.wide ? 0 : fabsl((long double)x * w.c);
+                if (fabsl(p - want) > want * (ldexpl(1, -41) + far * ldexpl(1, -55)) + 1.01L) ++bad;
                 if (w.wide || !(x > w.cut)) continue;
                 const long double r = weight_rough(x, w, rough);
-                if (fabsl(r - want) > want * ldexpl(1, -29) * 0.71L + 1) ++bad;
+                if (fabsl(r - want) > want * ldexpl(1, -29) * 0.71L + 1.01L) ++bad;
             }
         }
     printf("%d\n", bad);
