@@ -309,20 +309,34 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
 }
 
 // ==================================================================== product
-// One persistent CTA per SM.  Warp 0 streams 256 values of k of A (128 rows), of
-// B (256 rows) and of their scales through a three-stage ring (TMA, 128-byte
-// swizzle; the scales by bulk copies).  Warp 1 copies a stage's scales into tensor
-// memory (tcgen05.cp, each to all four lane quadrants) and issues its four M=128
-// N=256 K=64 MMAs into the one accumulator.  A stage's scales have columns of their
-// own, so they are written only after the MMAs that read the last ones have freed
-// the stage.  Two warpgroups read the accumulator into registers, 128 columns a
-// thread, and free it at once; rounding and stores (TMA) run under the next tile.
+// One persistent CTA per SM, two of them a pair where the output has more than one
+// row tile.  A tile is 128 rows a CTA x 256 columns; a pair's CTAs take row tiles
+// next to each other, each loads its rows of A and half of B's 256, and the leader's
+// MMAs (cta_group::2, M=256 N=256 K=64) work on both CTAs' shared and tensor memory.
+// Warp 0 streams 256 values of k a stage and their scales through a ring (TMA,
+// 128-byte swizzle for the values).  Warp 1 copies a stage's scales into tensor memory
+// (tcgen05.cp, each to all four lane quadrants) and issues its four MMAs into the one
+// accumulator.  A stage's scales have columns of their own, so they are written only
+// after the MMAs that read the last ones have freed the stage.  Two warpgroups read the
+// accumulator into registers, 128 columns a thread, and free it at once; rounding and
+// stores (TMA) run under the next tile.
+//
+// Bound: an MMA takes 128 cycles, 512 a stage; what a stage's 54 KB (without pairs)
+// take to come from L2 is more, and with three stages in flight a stage took 1000
+// cycles (4096 x 128256 x 4096: 896 us, 4.8 PFLOP/s).  Bringing half of B to both CTAs
+// by multicast left the bytes in flight as they were (847 us); a pair's stage is 38 KB
+// a CTA and five are in flight.
 constexpr int kTM = 128, kTN = 256, kTK = 256;
-constexpr int kStages = 3;
-constexpr int kABytes = kTM * kTK / 2, kBBytes = kTN * kTK / 2;
-constexpr int kSaBytes = 4 * kAtom, kSbBytes = 8 * kAtom;  // blocks of 16 (those of 32 need half)
-constexpr int kStageBytes = kABytes + kBBytes + kSaBytes + kSbBytes;  // 54 KB
-static_assert(kStageBytes % 1024 == 0, "the swizzle's 1024-byte groups");
+template <bool kPair>
+struct Ring {
+    static constexpr int kStages = kPair ? 5 : 3;
+    static constexpr int kBRows = kPair ? kTN / 2 : kTN;  // of B that a CTA holds
+    static constexpr int kA = kTM * kTK / 2, kB = kBRows * kTK / 2;
+    static constexpr int kSa = 4 * kAtom, kSb = 8 * kAtom;  // scales, all 256 columns' (blocks of 32 need half)
+    static constexpr int kStage = kA + kB + kSa + kSb;      // 38 or 54 KB
+    static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + 8 * 32 * 128;
+    static_assert(kStage % 1024 == 0, "the swizzle's 1024-byte groups");
+};
 constexpr int kEpiWarps = 8;
 constexpr int kEpiCols = kTN / (kEpiWarps / 4);  // columns a warp
 constexpr int kMmThreads = (4 + kEpiWarps) * 32;
@@ -331,38 +345,98 @@ constexpr int kMmThreads = (4 + kEpiWarps) * 32;
 constexpr int kRegsFront = 40, kRegsEpi = 232;
 constexpr int kOutWarp = 32 * 128;               // staging of a warp: a box of 32 rows x 128 bytes
 constexpr int kOutPitch = 80;                    // or rows of 64 bytes and 16 against bank conflicts
-constexpr size_t kMmSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpiWarps * kOutWarp;
+static_assert(kEpiWarps * kOutWarp == 8 * 32 * 128, "the ring's room for staging");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = kTN;              // a stage's scales: 16 columns of A's, 32 of B's
 constexpr uint32_t kScaleCols = 48;
-static_assert(kScaleCol + kStages * kScaleCols <= kTmemCols, "tensor memory");
-constexpr int kRaster = 16;                      // row tiles that share a B tile in L2
+static_assert(kScaleCol + 5 * kScaleCols <= kTmemCols, "tensor memory");
+constexpr int kRaster = 16;                      // row tiles (or pairs) that share a B tile in L2
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ uint32_t of_leader(const void *p) {  // the address of a pair's first CTA's own
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+// A box into this CTA's memory; its bytes count at the barrier `bar` (a cluster address).
+template <bool kPair>
+__device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    if constexpr (kPair)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+// Arrive on `bar`, of both CTAs of a pair, once every MMA issued so far completes.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (kPair)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        umma_commit(bar);
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {  // a cluster address
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 32 rows x 16 bytes of scales (an atom) to four columns of all lane quadrants.
 constexpr uint32_t kAtomDescHigh = (128u >> 4) | (1u << 14);  // 8-row groups of 128 bytes, no swizzle
+template <bool kPair>
 __device__ __forceinline__ void scales_to_tmem(uint32_t col, uint32_t low) {
-    asm volatile(
-        "{\n\t.reg .b64 d;\n\t"
-        "mov.b64 d, {%1, %2};\n\t"
-        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(col),
-        "r"(low), "r"(kAtomDescHigh)
-        : "memory");
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\t"
+            "mov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(col),
+            "r"(low), "r"(kAtomDescHigh)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .b64 d;\n\t"
+            "mov.b64 d, {%1, %2};\n\t"
+            "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(col),
+            "r"(low), "r"(kAtomDescHigh)
+            : "memory");
 }
-template <bool kB16>
+template <bool kB16, bool kPair>
 __device__ __forceinline__ void umma_f4(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, uint32_t sa,
                                         uint32_t sb, uint32_t accumulate) {
-    if constexpr (kB16)
+    if constexpr (kB16 && kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %7};\n\t"
+            "mov.b64 db, {%2, %7};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(kDescHigh)
+            : "memory");
+    else if constexpr (kB16)
         asm volatile(
             "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
             "mov.b64 da, {%1, %7};\n\t"
             "mov.b64 db, {%2, %7};\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
             "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+            "r"(a_low), "r"(b_low), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(kDescHigh)
+            : "memory");
+    else if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %7};\n\t"
+            "mov.b64 db, {%2, %7};\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
             "r"(a_low), "r"(b_low), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate), "r"(kDescHigh)
             : "memory");
     else
@@ -389,15 +463,15 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t *r) {
 
 struct MmMaps {
     CUtensorMap a, b;
-    CUtensorMap out;  // (column, row, split); only where vec_out
+    CUtensorMap sa, sb;  // scales: (word of an atom, atom)
+    CUtensorMap out;     // (column, row, split); only where vec_out
 };
 
 struct MmArgs {
-    const uint8_t *sa, *sb;
     const float *ta, *tb;
     int64_t m, n, k;
-    int64_t atoms;             // of scales along k
-    int groups_n;              // groups of 128 rows of B
+    int atoms;                 // of scales along k
+    int groups_m, groups_n;    // groups of 128 rows of A and of B
     int kb_total, kb_per_split, n_splits;
     int n_tm, n_tn;
     uint32_t idesc;
@@ -423,18 +497,23 @@ __device__ __forceinline__ void item_coords(int64_t w, const MmArgs &a, int &tm,
     tm = g * kRaster + static_cast<int>(local - static_cast<int64_t>(tn) * gm);
 }
 
-template <bool kOutF32, bool kB16>
+template <bool kOutF32, bool kB16, bool kPair>
 __global__ void __launch_bounds__(kMmThreads, 1)
     product_kernel(const __grid_constant__ MmMaps maps, const __grid_constant__ MmArgs a) {
     extern __shared__ __align__(1024) char smem_raw[];
+    using R = Ring<kPair>;
+    constexpr int kStages = R::kStages;
     __shared__ uint64_t full[kStages], empty[kStages], acc_full, acc_empty, done;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     char *const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset keeps the loads shared ones)
-    char *const staged = smem + static_cast<size_t>(kStages) * kStageBytes;
+    char *const staged = smem + static_cast<size_t>(kStages) * R::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits;
     constexpr int kAtomsPer = kB16 ? 4 : 2;  // atoms of scales along a stage's k
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int rank = kPair ? blockIdx.x & 1 : 0;
+    const int64_t item0 = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -443,19 +522,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(&acc_full, 1);
-        mbar_init(&acc_empty, kEpiWarps);
+        mbar_init(&acc_empty, kEpiWarps * kCtas);
         mbar_init(&done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) pair_sync();  // (the other's barriers stand before anything arrives at them)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -466,26 +549,28 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             // ------------------------------------------------------------ producer
             uint32_t s = 0, phase = 1, issued = 0;  // the first turn finds every stage empty
             bool ok = true;
-            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+            for (int64_t w = item0; ok && w < items; w += step) {
                 int tm, tn, split;
                 item_coords(w, a, tm, tn, split);
+                tm = tm * kCtas + rank;
                 const int kb1 = min(a.kb_total, (split + 1) * a.kb_per_split);
-                const int groups = min(2, a.groups_n - 2 * tn);
+                // (behind the last group of 128 rows any scales do)
+                const int ga = min(tm, a.groups_m - 1), gb = 2 * tn, gb1 = min(gb + 1, a.groups_n - 1);
 #pragma unroll 1
                 for (int kb = split * a.kb_per_split; kb < kb1; ++kb) {
                     ok = wait_warp(&empty[s], phase, &abort_flag, a.status);
                     if (!ok) break;
                     if (leader) {
-                        char *st = smem + s * kStageBytes;
-                        const int64_t atom = static_cast<int64_t>(kb) * kAtomsPer;
-                        const uint32_t bytes = static_cast<uint32_t>(min(static_cast<int64_t>(kAtomsPer), a.atoms - atom)) * kAtom;
-                        mbar_arrive_expect_tx(&full[s], kABytes + kBBytes + bytes * (1 + groups));
-                        tma_load_2d(st, &maps.a, kb * (kTK / 2), tm * kTM, &full[s]);
-                        tma_load_2d(st + kABytes, &maps.b, kb * (kTK / 2), tn * kTN, &full[s]);
-                        bulk_load(st + kABytes + kBBytes, a.sa + (tm * a.atoms + atom) * kAtom, bytes, &full[s]);
-                        for (int g = 0; g < groups; ++g)
-                            bulk_load(st + kABytes + kBBytes + kSaBytes + g * (kSbBytes / 2),
-                                      a.sb + ((2 * static_cast<int64_t>(tn) + g) * a.atoms + atom) * kAtom, bytes, &full[s]);
+                        char *st = smem + s * R::kStage;
+                        constexpr uint32_t kScaleBytes = 3 * kAtomsPer * kAtom;
+                        const uint32_t bar = kPair ? of_leader(&full[s]) : smem_u32(&full[s]);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], kCtas * (R::kA + R::kB + kScaleBytes));
+                        load_box<kPair>(st, &maps.a, kb * (kTK / 2), tm * kTM, bar);
+                        load_box<kPair>(st + R::kA, &maps.b, kb * (kTK / 2), tn * kTN + rank * R::kBRows, bar);
+                        char *sc = st + R::kA + R::kB;
+                        load_box<kPair>(sc, &maps.sa, 0, ga * a.atoms + kb * kAtomsPer, bar);
+                        load_box<kPair>(sc + R::kSa, &maps.sb, 0, gb * a.atoms + kb * kAtomsPer, bar);
+                        load_box<kPair>(sc + R::kSa + R::kSb / 2, &maps.sb, 0, gb1 * a.atoms + kb * kAtomsPer, bar);
                     }
                     issued = issued < kStages ? issued + 1 : kStages;
                     if (++s == kStages) {
@@ -502,16 +587,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     phase ^= 1;
                 }
                 --s;
-                wait_warp(&full[s], phase ^ 1, &abort_flag, a.status, false);
+                // (a pair's barriers are the leader's; the other CTA waits for it at the end)
+                if (rank == 0) wait_warp(&full[s], phase ^ 1, &abort_flag, a.status, false);
             }
-        } else if (warp == 1) {
+        } else if (warp == 1 && rank == 0) {
             // ----------------------------------------------------------------- MMA
             uint32_t s = 0, phase = 0, turn = 1;  // `turn`: the parity that the emptied accumulator shows
             bool ok = true, issued = false;
             const uint32_t base = desc_low(smem), plain = (smem_u32(smem) & 0x3FFFFu) >> 4;
-            for (int64_t w = blockIdx.x; ok && w < items; w += gridDim.x) {
+            for (int64_t w = item0; ok && w < items; w += step) {
                 int tm, tn, split;
                 item_coords(w, a, tm, tn, split);
+                tm = tm * kCtas + rank;
                 const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
                 ok = wait_warp(&acc_empty, turn, &abort_flag, a.status);
                 turn ^= 1;
@@ -521,16 +608,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {
-                        const uint32_t da = base + s * (kStageBytes >> 4), db = da + (kABytes >> 4);
-                        const uint32_t sa = plain + s * (kStageBytes >> 4) + ((kABytes + kBBytes) >> 4), sb = sa + (kSaBytes >> 4);
+                        const uint32_t da = base + s * (R::kStage >> 4), db = da + (R::kA >> 4);
+                        const uint32_t sa = plain + s * (R::kStage >> 4) + ((R::kA + R::kB) >> 4), sb = sa + (R::kSa >> 4);
                         const uint32_t ca = tmem + kScaleCol + s * kScaleCols, cb = ca + 16;
                         const int mmas = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(kb) * kTK + 63) / 64));
 #pragma unroll
                         for (int j = 0; j < kAtomsPer; ++j) {
                             if (j * (4 / kAtomsPer) >= mmas) break;
-                            scales_to_tmem(ca + 4 * j, sa + j * (kAtom >> 4));
-                            scales_to_tmem(cb + 8 * j, sb + j * (kAtom >> 4));
-                            scales_to_tmem(cb + 8 * j + 4, sb + (4 + j) * (kAtom >> 4));
+                            scales_to_tmem<kPair>(ca + 4 * j, sa + j * (kAtom >> 4));
+                            scales_to_tmem<kPair>(cb + 8 * j, sb + j * (kAtom >> 4));
+                            scales_to_tmem<kPair>(cb + 8 * j + 4, sb + (4 + j) * (kAtom >> 4));
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {  // K = 32 bytes inside the swizzle row
@@ -538,10 +625,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                             // (of a word of four scales of 32 an MMA takes the first or the last two)
                             const uint32_t idesc = kB16 ? a.idesc : a.idesc | (j & 1) << 5 | (j & 1) << 30;
                             const int at = kB16 ? j : j / 2;
-                            umma_f4<kB16>(tmem, da + 2 * j, db + 2 * j, idesc, ca + 4 * at, cb + 8 * at, kb > kb0 || j > 0 ? 1u : 0u);
+                            umma_f4<kB16, kPair>(tmem, da + 2 * j, db + 2 * j, idesc, ca + 4 * at, cb + 8 * at, kb > kb0 || j > 0 ? 1u : 0u);
                         }
-                        umma_commit(&empty[s]);
-                        if (kb + 1 == kb1) umma_commit(&acc_full);
+                        commit<kPair>(&empty[s]);
+                        if (kb + 1 == kb1) commit<kPair>(&acc_full);
                     }
                     issued = true;
                     if (++s == kStages) {
@@ -551,7 +638,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
             }
             if (issued) {
-                if (leader) umma_commit(&done);
+                if (leader) {
+                    if constexpr (kPair) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done)) : "memory");
+                    else umma_commit(&done);
+                }
                 wait_warp(&done, 0, &abort_flag, a.status, false);
             }
             __syncwarp();
@@ -565,9 +655,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const float scale = __fmul_rn(a.ta ? *a.ta : 1.f, a.tb ? *a.tb : 1.f);
         uint32_t turn = 0;
         bool ok = true;
-        for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+        for (int64_t w = item0; w < items; w += step) {
             int tm, tn, split;
             item_coords(w, a, tm, tn, split);
+            tm = tm * kCtas + rank;
             const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
             float acc[kEpiCols];
             ok = ok && wait_warp(&acc_full, turn, &abort_flag, a.status);
@@ -580,7 +671,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_empty);
+                if (lane == 0) {
+                    if constexpr (kPair) arrive_at(of_leader(&acc_empty));
+                    else mbar_arrive(&acc_empty);
+                }
 #pragma unroll
                 for (int j = 0; j < kEpiCols; ++j) acc[j] = __fmul_rn(acc[j], scale);
             } else {  // a wait gave up: this tile reads as NaN
@@ -659,9 +753,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     if (warp >= 4 && lane == 0) tma_store_wait_read();  // shared memory outlives the last stores' reads
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) pair_sync();  // nothing of the pair's is under way any more
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
@@ -680,6 +776,19 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t pa
     }
 }
 
+// An operand's scales as atoms of 128 words, boxes of a stage's.
+bool make_scale_map(CUtensorMap *map, const void *ptr, int64_t atoms, bool b16) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {kAtom / 4, static_cast<cuuint64_t>(atoms)};
+    const cuuint64_t strides[1] = {kAtom};
+    const cuuint32_t box[2] = {kAtom / 4, b16 ? 4u : 2u};
+    const cuuint32_t elem[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(ptr), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kBf16>
 cudaError_t quantize_typed(const QuantArgs &a, bool b16, bool transpose, unsigned grid, cudaStream_t s) {
     if (b16) {
@@ -692,14 +801,29 @@ cudaError_t quantize_typed(const QuantArgs &a, bool b16, bool transpose, unsigne
     return cudaGetLastError();
 }
 
-template <bool kOutF32, bool kB16>
-cudaError_t product_typed(const MmMaps &maps, const MmArgs &a, cudaStream_t stream) {
+template <bool kOutF32, bool kB16, bool kPair>
+cudaError_t product_of(const MmMaps &maps, const MmArgs &a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
-    const cudaError_t e = set_smem_once(product_kernel<kOutF32, kB16>, kMmSmem, configured);
+    const cudaError_t e = set_smem_once(product_kernel<kOutF32, kB16, kPair>, Ring<kPair>::kSmem, configured);
     if (e != cudaSuccess) return e;
-    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits, sms = device_sm_count();
-    product_kernel<kOutF32, kB16><<<static_cast<unsigned>(items < sms ? items : sms), kMmThreads, kMmSmem, stream>>>(maps, a);
-    return cudaGetLastError();
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits, room = device_sm_count() / kCtas;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(items, room) * kCtas));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = Ring<kPair>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, product_kernel<kOutF32, kB16, kPair>, maps, a);
+}
+template <bool kOutF32, bool kB16>
+cudaError_t product_typed(const MmMaps &maps, const MmArgs &a, bool pair, cudaStream_t stream) {
+    return pair ? product_of<kOutF32, kB16, true>(maps, a, stream) : product_of<kOutF32, kB16, false>(maps, a, stream);
 }
 
 }  // namespace
@@ -760,27 +884,30 @@ cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, in
     if (k == 0) return cudaMemset2DAsync(out, out_stride, 0, n * (f32 ? 4 : 2), m, stream);
     const BlockPlan p = micro_plan(m, n, k);
     MmMaps maps;
-    if (!make_map(&maps.a, x.ptr, m, (k + 1) / 2, x.row_stride, kTM) || !make_map(&maps.b, y.ptr, n, (k + 1) / 2, y.row_stride, kTN))
+    const bool pair = p.n_tm > 1;
+    if (!make_map(&maps.a, x.ptr, m, (k + 1) / 2, x.row_stride, kTM) ||
+        !make_map(&maps.b, y.ptr, n, (k + 1) / 2, y.row_stride, pair ? kTN / 2 : kTN) ||
+        !make_scale_map(&maps.sa, x.scales, (m + 127) / 128 * x.atoms, x.b16) ||
+        !make_scale_map(&maps.sb, y.scales, (n + 127) / 128 * y.atoms, y.b16))
         return cudaErrorInvalidValue;
     MmArgs a{};
-    a.sa = x.scales;
-    a.sb = y.scales;
     a.ta = x.tensor_scale;
     a.tb = y.tensor_scale;
     a.m = m;
     a.n = n;
     a.k = k;
-    a.atoms = x.atoms;
+    a.atoms = static_cast<int>(x.atoms);
+    a.groups_m = static_cast<int>((m + 127) / 128);
     a.groups_n = static_cast<int>((n + 127) / 128);
     a.kb_total = static_cast<int>(p.kb_total);
     a.kb_per_split = static_cast<int>(p.kb_per_split);
     a.n_splits = static_cast<int>(p.n_splits);
-    a.n_tm = static_cast<int>(p.n_tm);
+    a.n_tm = static_cast<int>(pair ? (p.n_tm + 1) / 2 : p.n_tm);  // (pairs of row tiles)
     a.n_tn = static_cast<int>(p.n_tn);
     // block scaling: A's and B's format e2m1 (1 at bits 7 and 10), N / 8 at bit 17, scales e4m3 or
-    // powers of two (bit 23), M / 16 at bit 24; both K-major
+    // powers of two (bit 23), M / 16 at bit 24 (a pair's is 256); both K-major
     a.idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(kTN >> 3) << 17) | (x.b16 ? 0u : 1u << 23) |
-              (static_cast<uint32_t>(kTM >> 4) << 24);
+              (static_cast<uint32_t>((pair ? 2 * kTM : kTM) >> 4) << 24);
     a.status = static_cast<uint32_t *>(workspace);
     float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
     const bool split = p.n_splits > 1;
@@ -795,8 +922,8 @@ cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, in
     if (a.vec_out && !make_out_map(&maps.out, a.out, m, n_written, p.n_splits, a.out_stride, a.split_stride, to_f32))
         return cudaErrorInvalidValue;
     cudaError_t e;
-    if (to_f32) e = x.b16 ? product_typed<true, true>(maps, a, stream) : product_typed<true, false>(maps, a, stream);
-    else e = x.b16 ? product_typed<false, true>(maps, a, stream) : product_typed<false, false>(maps, a, stream);
+    if (to_f32) e = x.b16 ? product_typed<true, true>(maps, a, pair, stream) : product_typed<true, false>(maps, a, pair, stream);
+    else e = x.b16 ? product_typed<false, true>(maps, a, pair, stream) : product_typed<false, false>(maps, a, pair, stream);
     if (e != cudaSuccess || !split) return e;
     const int64_t blocks = std::min<int64_t>((m * n + 255) / 256, static_cast<int64_t>(device_sm_count()) * 16);
     if (f32)
