@@ -49,51 +49,74 @@ struct QuantArgs {
     int64_t values_stride;
     int values_f32;
     int n_tiles_c;
-    int vec_in, vec_out, vec_values;
+    int vec_out;
 };
 
-// The scale byte of a block, the factor onto the codes' range, and what a code's
-// unit is worth before t.  `top`: the largest magnitude's bits (NaN above infinity
-// above numbers).
+// What a scale byte means under t: the factor onto the codes' range, and what a code's
+// unit is worth before t.
 template <bool kB16>
-__device__ __forceinline__ uint32_t scale_of(uint32_t top_bits, float t, float *inv, float *unit) {
+__device__ __forceinline__ float2 meaning_of(uint32_t byte, float t) {
+    const float unit = kB16 ? __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)))
+                            : __uint_as_float(byte << 23);
+    const float back = __fdiv_rn(1.f, __fmul_rn(unit, t));
+    return make_float2(back <= FLT_MAX ? back : 0.f, unit);
+}
+// Correctly rounded x / d, from the correctly rounded r = 1 / d: one step of Markstein's
+// division, whose residual is exact while nothing leaves the normal range.
+__device__ __forceinline__ float over(float x, float d, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+struct TensorScale {
+    float t, d, r;   // t; what a block's top is divided by first (6 t or t), and its reciprocal
+    bool valid, plain;
+};
+template <bool kB16>
+__device__ __forceinline__ TensorScale tensor_scale_of(const float *p) {
+    TensorScale s;
+    s.t = p ? *p : 1.f;
+    s.d = kB16 ? __fmul_rn(6.f, s.t) : s.t;
+    s.r = __fdiv_rn(1.f, s.d);
+    s.valid = s.t > 0.f && s.t <= FLT_MAX;
+    s.plain = s.t >= 0x1p-60f && s.t <= 0x1p60f;
+    return s;
+}
+// The scale byte of a block.  `top`: the largest magnitude's bits (NaN above infinity
+// above numbers); a non-finite value, or a tensor scale that is none, makes it NaN.
+// (The divisions' general form took half of the kernel's operations.)
+template <bool kB16>
+__device__ __forceinline__ uint32_t scale_of(uint32_t top_bits, const TensorScale &s) {
     const float top = __uint_as_float(top_bits);
-    uint32_t byte;
-    if constexpr (kB16) {
-        byte = __nv_cvt_float_to_fp8(__fdiv_rn(top, __fmul_rn(6.f, t)), __NV_SATFINITE, __NV_E4M3);
-        *unit = __half2float(__half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)));
-    } else {
-        const uint32_t b = __float_as_uint(__fdiv_rn(fminf(fmaxf(__fdiv_rn(top, t), kFloor), FLT_MAX), 6.f));
-        byte = (b + 0x7fffffu) >> 23;  // up to the next power of two
-        *unit = __uint_as_float(byte << 23);
-    }
-    const float back = __fdiv_rn(1.f, __fmul_rn(*unit, t));
-    *inv = back <= FLT_MAX ? back : 0.f;
-    // a non-finite value, or a tensor scale that is none: the block reads as NaN
-    if (!(top <= FLT_MAX) || !(t > 0.f && t <= FLT_MAX)) {
-        byte = kB16 ? 0x7f : 0xff;
-        *unit = CUDART_NAN_F;
-    }
-    return byte;
+    if (!s.valid || !(top <= FLT_MAX)) return kB16 ? 0x7f : 0xff;
+    const bool plain = s.plain && (top == 0.f || (top >= 0x1p-60f && top <= 0x1p60f));
+    float q = plain ? over(top, s.d, s.r) : __fdiv_rn(top, s.d);
+    if constexpr (kB16) return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+    q = fminf(fmaxf(q, kFloor), FLT_MAX);
+    q = plain ? over(q, 6.f, 0x1.555556p-3f) : __fdiv_rn(q, 6.f);
+    return (__float_as_uint(q) + 0x7fffffu) >> 23;  // up to the next power of two
 }
 
 __device__ __forceinline__ uint32_t codes_of(float a, float b, float inv) {
     return __nv_cvt_float2_to_fp4x2(make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv)), __NV_E2M1, cudaRoundNearest);
 }
-// Eight codes in a word to the values that they stand for.
+// Eight codes in a word to the values that they stand for.  (A code times an e4m3 scale
+// has six bits and lies between 2^-10 and 2688: exact in half precision.)
+template <bool kB16>
 __device__ __forceinline__ void values_of(uint32_t word, float unit, float t, float *v) {
+    const __half2 u = __float2half2_rn(unit);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(word >> (8 * q)), __NV_E2M1));
+        __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(word >> (8 * q)), __NV_E2M1));
+        if constexpr (kB16) h = __hmul2(h, u);
         const float2 f = __half22float2(h);
-        v[2 * q] = __fmul_rn(__fmul_rn(f.x, unit), t);
-        v[2 * q + 1] = __fmul_rn(__fmul_rn(f.y, unit), t);
+        v[2 * q] = __fmul_rn(kB16 ? f.x : __fmul_rn(f.x, unit), t);
+        v[2 * q + 1] = __fmul_rn(kB16 ? f.y : __fmul_rn(f.y, unit), t);
     }
 }
 // Eight neighbouring values, `n` of them inside the row.
 __device__ __forceinline__ void store_values(const QuantArgs &a, int64_t r, int64_t c, int64_t n, const float *v) {
     char *dst = a.values + r * a.values_stride + c * (a.values_f32 ? 4 : 2);
-    if (a.vec_values && n >= 8) {
+    if (n >= 8) {
         if (a.values_f32) {
             __stcs(reinterpret_cast<float4 *>(dst), make_float4(v[0], v[1], v[2], v[3]));
             __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
@@ -116,11 +139,35 @@ __device__ __forceinline__ void store_values(const QuantArgs &a, int64_t r, int6
         }
 }
 
-template <bool kBf16, bool kB16, bool kTranspose>
-__global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
+// Two rows of 128 values that lie in shared memory, a warp's work: rows r and r + step,
+// columns c to c + 127, of those that exist.
+__device__ __forceinline__ void store_rows(const QuantArgs &a, int64_t r, int step, int64_t c, int64_t rows, int64_t cols, const float *v, int pitch) {
+    const int lane = threadIdx.x & 31;
+    const int n = static_cast<int>(min(cols - c, static_cast<int64_t>(128))) - lane;  // values from the lane's first on
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (r + h * step >= rows) break;
+        char *dst = a.values + (r + h * step) * a.values_stride + (c + lane) * (a.values_f32 ? 4 : 2);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (q * 32 < n) {
+                const float x = v[h * pitch + q * 32 + lane];
+                if (a.values_f32) __stcs(reinterpret_cast<float *>(dst) + q * 32, x);
+                else reinterpret_cast<__nv_bfloat16 *>(dst)[q * 32] = __float2bfloat16_rn(x);
+            }
+    }
+}
+
+// kVec: rows of x and of the values on 16-byte boundaries.
+template <bool kBf16, bool kB16, bool kTranspose, bool kVec>
+__global__ void __launch_bounds__(kQThreads, kBf16 && kVec ? 3 : 2) quantize_kernel(const __grid_constant__ QuantArgs a) {
     __shared__ __align__(16) uint8_t atoms[kB16 ? 2 * kAtom : kAtom];
     __shared__ __align__(16) uint32_t tops[kTranspose && !kB16 ? 8 * kQTile : 4];
     __shared__ __align__(16) uint32_t turned[kTranspose ? kQTile * 16 : 4];
+    // rows that pass through shared memory, so that a warp touches neighbouring bytes: a
+    // warp's two rows where rows lie off 16-byte boundaries, or 16 columns of transposed values
+    constexpr int kPitch = kQTile + 4;
+    __shared__ __align__(16) float staged[kVec ? 4 : 16 * kPitch];
     constexpr int kElt = kBf16 ? 2 : 4, kBlk = kB16 ? 16 : 32, kBlocks = kQTile / kBlk;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t tile_r = blockIdx.x / a.n_tiles_c, tile_c = blockIdx.x % a.n_tiles_c;
@@ -128,7 +175,15 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
     const int col = (lane & 15) * 8;
     const int row_group = warp * 2 + (lane >> 4);
     const auto row_of = [&](int p) { return kTranspose ? row_group * 8 + p : p * 16 + row_group; };
-    const float ts = a.tensor_scale ? *a.tensor_scale : 1.f;
+    __shared__ float2 meanings[256];
+    const TensorScale tensor = tensor_scale_of<kB16>(a.tensor_scale);
+    const float ts = tensor.t;
+    {
+        const float2 m = meaning_of<kB16>(t, ts);
+        const bool nan = t == (kB16 ? 0x7f : 0xff);
+        meanings[t] = make_float2(m.x, nan ? CUDART_NAN_F : m.y);
+    }
+    __syncthreads();
     // raw words of the thread's 8 passes: 8 values each, outside the tensor 0
     uint4 raw[8][kBf16 ? 1 : 2];
 #pragma unroll
@@ -137,11 +192,11 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
         const char *src = a.x + r * a.x_stride + c * kElt;
 #pragma unroll
         for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = make_uint4(0, 0, 0, 0);
-        if (r < a.rows && c < a.cols) {
-            if (a.vec_in && c + 8 <= a.cols) {
+        if constexpr (kVec) {
+            if (r < a.rows && c + 8 <= a.cols) {
 #pragma unroll
                 for (int h = 0; h < (kBf16 ? 1 : 2); ++h) raw[p][h] = __ldcs(reinterpret_cast<const uint4 *>(src) + h);
-            } else {
+            } else if (r < a.rows && c < a.cols) {
                 uint32_t w[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -157,7 +212,65 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
                 raw[p][0] = make_uint4(w[0], w[1], w[2], w[3]);
                 if constexpr (!kBf16) raw[p][1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
+        } else {
+            // the warp's two rows side by side: values lane, lane + 32, ... of each
+            uint32_t w[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t rr = r0 + (kTranspose ? (warp * 2 + h) * 8 + p : p * 16 + warp * 2 + h);
+                const char *from = a.x + rr * a.x_stride + (c0 + lane) * kElt;
+                const int n = rr < a.rows ? static_cast<int>(min(a.cols - c0, static_cast<int64_t>(kQTile))) - lane : 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // (without branches two bytes a load are twice as fast: 68 us instead of 136 for 12661 x
+                    // 2051; four bytes a load are not: 88 instead of 63)
+                    if constexpr (kBf16) {
+                        const uint32_t v = __ldg(reinterpret_cast<const unsigned short *>(q * 32 < n ? from + q * 64 : a.x));
+                        w[h * 4 + q] = q * 32 < n ? v << 16 : 0;
+                    } else {
+                        w[h * 4 + q] = 0;
+                        if (q * 32 < n) w[h * 4 + q] = __ldcs(reinterpret_cast<const uint32_t *>(from) + q * 32);
+                    }
+                }
+            }
+            raw[p][0] = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (kBf16) {
+                raw[p][0].x |= w[4] >> 16;
+                raw[p][0].y |= w[5] >> 16;
+                raw[p][0].z |= w[6] >> 16;
+                raw[p][0].w |= w[7] >> 16;
+            } else {
+                raw[p][1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
         }
+    }
+    if constexpr (!kVec) {  // each lane gets eight neighbours
+        float *const mine = &staged[warp * 2 * kPitch];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            const uint32_t w[4] = {raw[p][0].x, raw[p][0].y, raw[p][0].z, raw[p][0].w};
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (kBf16) {
+                    mine[q * 32 + lane] = __uint_as_float(w[q] & 0xffff0000u);
+                    mine[kPitch + q * 32 + lane] = __uint_as_float(w[q] << 16);
+                } else {
+                    const uint32_t w1[4] = {raw[p][1].x, raw[p][1].y, raw[p][1].z, raw[p][1].w};
+                    mine[q * 32 + lane] = __uint_as_float(w[q]);
+                    mine[kPitch + q * 32 + lane] = __uint_as_float(w1[q]);
+                }
+            }
+            __syncwarp();
+            const uint4 lo = *reinterpret_cast<const uint4 *>(&mine[(lane >> 4) * kPitch + col]), hi = *reinterpret_cast<const uint4 *>(&mine[(lane >> 4) * kPitch + col + 4]);
+            if constexpr (kBf16) {
+                raw[p][0] = make_uint4(lo.x >> 16 | lo.y, lo.z >> 16 | lo.w, hi.x >> 16 | hi.y, hi.z >> 16 | hi.w);
+            } else {
+                raw[p][0] = lo;
+                raw[p][1] = hi;
+            }
+        }
+        __syncwarp();
     }
     const auto values = [&](int p, float *v) {
         if constexpr (kBf16) {
@@ -188,22 +301,27 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
             float v[8];
             values(p, v);
             uint32_t m = 0;
+            if constexpr (kBf16) {  // two magnitudes at a time
+                const uint32_t two = __vmaxu2(__vmaxu2(raw[p][0].x & 0x7fff7fffu, raw[p][0].y & 0x7fff7fffu),
+                                              __vmaxu2(raw[p][0].z & 0x7fff7fffu, raw[p][0].w & 0x7fff7fffu));
+                m = max(two << 16, two & 0xffff0000u);
+            } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+                for (int q = 0; q < 8; ++q) m = max(m, bits(v[q]));
+            }
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             if constexpr (!kB16) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            float inv, unit;
-            const uint32_t byte = scale_of<kB16>(m, ts, &inv, &unit);
+            const uint32_t byte = scale_of<kB16>(m, tensor);
+            const float inv = meanings[byte].x, unit = meanings[byte].y;
             const int64_t r = r0 + row_of(p), c = c0 + col;
             const bool in = r < a.rows && c < a.cols;
             // (a block that starts behind the last value has no scale: 0)
             if ((lane & (kB16 ? 1 : 3)) == 0) put(row_of(p), col / kBlk, in ? byte : 0u);
-            if (!in) continue;
             uint32_t word = 0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) word |= codes_of(v[2 * q], v[2 * q + 1], inv) << (8 * q);
             uint8_t *dst = a.out + r * a.out_stride + c / 2;
-            const int64_t n = a.cols - c;
+            const int64_t n = in ? a.cols - c : 0;
             if (a.vec_out && n >= 8) {
                 __stcs(reinterpret_cast<uint32_t *>(dst), word);
             } else {
@@ -212,20 +330,44 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
                     if (2 * q < n) dst[q] = static_cast<uint8_t>(word >> (8 * q));
             }
             if (a.values) {
-                values_of(word, unit, ts, v);
-                store_values(a, r, c, n, v);
+                values_of<kB16>(word, unit, ts, v);
+                if constexpr (kVec) {
+                    store_values(a, r, c, n, v);
+                } else {
+                    float *const mine = &staged[warp * 2 * kPitch];
+                    __syncwarp();
+                    *reinterpret_cast<float4 *>(&mine[(lane >> 4) * kPitch + col]) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(&mine[(lane >> 4) * kPitch + col + 4]) = make_float4(v[4], v[5], v[6], v[7]);
+                    __syncwarp();
+                    store_rows(a, r0 + p * 16 + warp * 2, 1, c0, a.rows, a.cols, mine, kPitch);
+                }
             }
         }
     } else {
         uint32_t m[8];
+        if constexpr (kBf16) {  // two magnitudes at a time
+            uint32_t two[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) m[q] = 0;
+            for (int p = 0; p < 8; ++p) {
+                const uint32_t ws[4] = {raw[p][0].x, raw[p][0].y, raw[p][0].z, raw[p][0].w};
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            float v[8];
-            values(p, v);
+                for (int q = 0; q < 4; ++q) two[q] = __vmaxu2(two[q], ws[q] & 0x7fff7fffu);
+            }
 #pragma unroll
-            for (int q = 0; q < 8; ++q) m[q] = max(m[q], bits(v[q]));
+            for (int q = 0; q < 4; ++q) {
+                m[2 * q] = two[q] << 16;
+                m[2 * q + 1] = two[q] & 0xffff0000u;
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m[q] = 0;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                float v[8];
+                values(p, v);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) m[q] = max(m[q], bits(v[q]));
+            }
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) m[q] = max(m[q], __shfl_xor_sync(0xffffffffu, m[q], 16));
@@ -244,8 +386,8 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const bool upper = lane >= 16;
-            float iv, un;
-            const uint32_t byte = scale_of<kB16>(upper ? m[q + 4] : m[q], ts, &iv, &un);
+            const uint32_t byte = scale_of<kB16>(upper ? m[q + 4] : m[q], tensor);
+            const float iv = meanings[byte].x, un = meanings[byte].y;
             const int c = col + q + (upper ? 4 : 0);
             if (kB16 || (warp & 1) == 0) put(c, b, block_in && c0 + c < a.cols ? byte : 0u);
             const float oi = __shfl_xor_sync(0xffffffffu, iv, 16), ou = __shfl_xor_sync(0xffffffffu, un, 16);
@@ -269,10 +411,19 @@ __global__ void __launch_bounds__(kQThreads, kBf16 ? 3 : 2) quantize_kernel(cons
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             turned[(col + q) * 16 + (row_group ^ (col >> 3))] = words[q];
-            if (a.values && c0 + col + q < a.cols && oc < a.rows) {
+            if (a.values) {
                 float v[8];
-                values_of(words[q], unit[q], ts, v);
-                store_values(a, c0 + col + q, oc, a.rows - oc, v);
+                values_of<kB16>(words[q], unit[q], ts, v);
+                if constexpr (kVec) {
+                    if (c0 + col + q < a.cols && oc < a.rows) store_values(a, c0 + col + q, oc, a.rows - oc, v);
+                } else {  // 16 output rows at a time
+                    __syncthreads();
+                    float *const to = &staged[(lane & 15) * kPitch + row_group * 8];
+                    *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+                    *reinterpret_cast<float4 *>(to + 4) = make_float4(v[4], v[5], v[6], v[7]);
+                    __syncthreads();
+                    store_rows(a, c0 + warp * 16 + q, 8, r0, a.cols, a.rows, &staged[warp * 2 * kPitch], kPitch);
+                }
             }
         }
         __syncthreads();
@@ -789,14 +940,14 @@ bool make_scale_map(CUtensorMap *map, const void *ptr, int64_t atoms, bool b16) 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kBf16>
+template <bool kBf16, bool kVec>
 cudaError_t quantize_typed(const QuantArgs &a, bool b16, bool transpose, unsigned grid, cudaStream_t s) {
     if (b16) {
-        if (transpose) quantize_kernel<kBf16, true, true><<<grid, kQThreads, 0, s>>>(a);
-        else quantize_kernel<kBf16, true, false><<<grid, kQThreads, 0, s>>>(a);
+        if (transpose) quantize_kernel<kBf16, true, true, kVec><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, true, false, kVec><<<grid, kQThreads, 0, s>>>(a);
     } else {
-        if (transpose) quantize_kernel<kBf16, false, true><<<grid, kQThreads, 0, s>>>(a);
-        else quantize_kernel<kBf16, false, false><<<grid, kQThreads, 0, s>>>(a);
+        if (transpose) quantize_kernel<kBf16, false, true, kVec><<<grid, kQThreads, 0, s>>>(a);
+        else quantize_kernel<kBf16, false, false, kVec><<<grid, kQThreads, 0, s>>>(a);
     }
     return cudaGetLastError();
 }
@@ -868,11 +1019,12 @@ cudaError_t launch_micro_quantize(const void *x, int x_dtype, int64_t x_stride_e
     a.values_stride = values_stride_elems * (a.values_f32 ? 4 : 2);
     a.n_tiles_c = static_cast<int>((cols + kQTile - 1) / kQTile);
     const uintptr_t unit = transpose ? 16 : 4;
-    a.vec_in = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.x_stride % 16 == 0;
     a.vec_out = reinterpret_cast<uintptr_t>(o.ptr) % unit == 0 && static_cast<uintptr_t>(o.row_stride) % unit == 0;
-    a.vec_values = reinterpret_cast<uintptr_t>(values) % 16 == 0 && a.values_stride % 16 == 0;
+    const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 && a.x_stride % 16 == 0 &&
+                     (!values || (reinterpret_cast<uintptr_t>(values) % 16 == 0 && a.values_stride % 16 == 0));
     const unsigned grid = static_cast<unsigned>((rows + kQTile - 1) / kQTile * a.n_tiles_c);
-    return bf16 ? quantize_typed<true>(a, o.b16, transpose, grid, stream) : quantize_typed<false>(a, o.b16, transpose, grid, stream);
+    if (bf16) return vec ? quantize_typed<true, true>(a, o.b16, transpose, grid, stream) : quantize_typed<true, false>(a, o.b16, transpose, grid, stream);
+    return vec ? quantize_typed<false, true>(a, o.b16, transpose, grid, stream) : quantize_typed<false, false>(a, o.b16, transpose, grid, stream);
 }
 
 cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, int64_t m, int64_t n, int64_t k,
