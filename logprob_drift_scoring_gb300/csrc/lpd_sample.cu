@@ -69,7 +69,7 @@ __device__ constexpr Tables kTables = make_tables();
 constexpr int kTopList = 2048;      // candidates of a row that a CTA has alone
 constexpr int kTopMost = 512;       // the largest top-k that such a CTA takes
 constexpr int kTopRows = 64;        // from so many rows on
-constexpr int kEach = 4;            // rows of a cluster where most may be such a CTA's
+constexpr float kListShare = 48.f;  // the sampled tokens that a list goes down to without a top-k
 
 // What finding a border takes: bins, and the CTA's sums.
 struct Scratch {
@@ -230,10 +230,6 @@ __device__ __forceinline__ RowFilter filter_of(const SampleArgs &a, int64_t row)
     f.use_p = f.top_p < 1.f;
     return f;
 }
-// Whether the row kernel takes a row: every bf16 one, and those of a small top-k.
-template <bool kBf16>
-__device__ __forceinline__ bool is_row_kernels(const RowFilter &f) { return kBf16 || (f.active && f.valid && f.use_k && f.top_k <= kTopMost); }
-
 // A row without an answer.
 template <bool kMask>
 __device__ __forceinline__ void no_answer(const SampleArgs &a, int64_t row, float value) {
@@ -492,6 +488,7 @@ constexpr int kSide = kOctaves * 128;
 constexpr int kTinyUp = kSide, kZero = kSide + 1, kTinyDown = kSide + 2, kDown = kSide + 3, kLow = 2 * kSide + 3;
 constexpr int kValues = 2 * kSide + 4;
 constexpr int kTinyRoom = 1024;
+constexpr int kWide = 1024;        // bins of a row that is not counted by value
 __device__ __forceinline__ float bin_value(int b) {  // of a bin of one value
     const uint32_t up = static_cast<uint32_t>(kSide - 1 - b + (kLowest << 7)) << 16;
     const uint32_t down = static_cast<uint32_t>(b - kDown + (kLowest << 7)) << 16 | 0x80000000u;
@@ -511,6 +508,10 @@ struct RowShared {
             uint32_t key[kTopList], at[kTopList];
         } list;
         uint64_t value_w[kValues];     // the weights of the bins' values, 0 where they are not kept
+        struct {
+            uint64_t beside[2 * kTopList];  // (the list)
+            uint32_t cnt[kWide], mass_lo[kWide], mass_hi[kWide];
+        } wide;
     };
     uint16_t tiny[kTinyRoom];          // the bits of values within 2^-10 of 0
     uint64_t part[kMaxWarps];
@@ -578,14 +579,17 @@ struct RowChunks {
 
 // The first element of the row whose running sum of g(element, value) passes `target`;
 // of_chunk(chunk, its number) is g's sum over a chunk.
+// (`known`: the sums of the warps' parts are in sh.part.)
 template <bool kBf16, class H, class G>
-__device__ int find_in_row(const RowChunks<kBf16> &c, RowShared &sh, H of_chunk, G g, uint64_t target) {
+__device__ int find_in_row(const RowChunks<kBf16> &c, RowShared &sh, H of_chunk, G g, uint64_t target, bool known = false) {
     constexpr int kPer = RowChunks<kBf16>::kPer, kWarps = kRowThreads / 32;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, per_warp = (c.n + kWarps - 1) / kWarps;
     uint64_t s = 0;
-    c.each_of_warp(per_warp, [&](const uint4 &u, int i) { s += of_chunk(u, i); });
-    s = warp_sum(s);
-    if (lane == 0) sh.part[warp] = s;
+    if (!known) {
+        c.each_of_warp(per_warp, [&](const uint4 &u, int i) { s += of_chunk(u, i); });
+        s = warp_sum(s);
+        if (lane == 0) sh.part[warp] = s;
+    }
     if (t == 0) sh.at = -1;
     __syncthreads();
     int w = 0;
@@ -620,12 +624,64 @@ __device__ int find_in_row(const RowChunks<kBf16> &c, RowShared &sh, H of_chunk,
     return e;
 }
 
-// Top-k: the row is read once.  A sample of it (one turn in `every`) gives a value that
-// about top_k and some tokens reach, the pass over the whole row collects those and the
-// top, and the border is found among them.  False where they are fewer than top_k after
-// all, or too many for the list.
+// The weights of a list's tokens (formed as they are found they take a warp's whole way
+// for each: 154 us instead of 95 for 256 rows with 1000 kept tokens).
+template <bool kBf16>
+__device__ __forceinline__ void weigh_list(RowShared &sh, const Weigh &weight, uint32_t top_key, uint32_t total) {
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < min(total, static_cast<uint32_t>(kTopList)); i += kRowThreads)
+        sh.list.w[i] = weight(value_of<kBf16>(top_key - sh.list.key[i]));
+    __syncthreads();
+}
+
+// The answers that a pass over the row gives, is_kept(element, value) being known.
+template <bool kBf16, class K>
+__device__ __forceinline__ void mask_of_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &c, const Weigh &weight,
+                                            K is_kept, uint32_t set_n, uint64_t set_mass) {
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    uint32_t *const words_of = a.mask + row * a.mask_stride;
+    const int64_t id = a.keep ? a.keep[row] : -1;
+    const int forced = id >= 0 && id < a.vocab ? static_cast<int>(id) : -1;
+    for (int w = warp; w < (a.vocab + 31) / 32; w += kRowThreads / 32) {
+        const int j = w * 32 + lane;
+        bool k = false;
+        if (j < a.vocab) {
+            const float x = c.value(c.lead + j);
+            k = is_kept(c.lead + j, x) || (j == forced && x >= -FLT_MAX);
+        }
+        const uint32_t word = __ballot_sync(0xffffffffu, k);
+        if (lane == 0) words_of[w] = word;
+    }
+    if (t == 0) {
+        if (forced >= 0) {
+            const float x = c.value(c.lead + forced);
+            if (x >= -FLT_MAX && !is_kept(c.lead + forced, x)) {
+                set_n += 1;
+                set_mass += weight(x);
+            }
+        }
+        if (a.kept) a.kept[row] = static_cast<int32_t>(set_n);
+        if (a.lse) a.lse[row] = static_cast<float>(weight.lse(set_mass, f.scale));
+    }
+}
+template <bool kBf16>
+__device__ __forceinline__ void draw_of_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &c, const Weigh &weight,
+                                            int e, float u, uint32_t set_n, uint64_t set_mass) {
+    if (threadIdx.x != 0) return;
+    const float x = c.value(e);
+    const bool drawn = u == u;
+    a.ids[row] = drawn ? e - c.lead : -1;
+    if (a.logp) a.logp[row] = drawn ? static_cast<float>(static_cast<double>(x) * f.scale - weight.lse(set_mass, f.scale)) : CUDART_NAN_F;
+    if (a.kept) a.kept[row] = static_cast<int32_t>(set_n);
+}
+
+// A list of the largest tokens.  A sample of the row (one turn in `every`) gives a value
+// that about `share` of the sample's tokens reach and some more, the pass over the whole
+// row collects what reaches it and the top, and the border is found among those: of a
+// top-k, of what min-p leaves, or of a nucleus (whose other tokens are weighed in a second
+// pass).  False where they are too few after all, or too many for the list.
 template <bool kBf16, bool kMask>
-__device__ bool top_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &row_chunks, RowShared &sh) {
+__device__ bool list_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &row_chunks, RowShared &sh) {
     constexpr int kPer = RowChunks<kBf16>::kPer, kThreads = kRowThreads, kWarps = kThreads / 32, kAhead = 4;
     Scratch &sc = sh.scratch;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -646,10 +702,10 @@ __device__ bool top_row(const SampleArgs &a, int64_t row, const RowFilter &f, co
         for (int i = c0 + turns * turn + t; i < c1; i += kThreads) tmax = fmaxf(tmax, chunk_max<kBf16>(__ldg(from + i)));
         if (row_chunks.has_edge()) tmax = fmaxf(tmax, chunk_max<kBf16>(sh.edge[t]));
     }
-    // Each warp's R-th largest thread maximum, R being the warp's part of top_k's share of
-    // the sample and five standard deviations; the median of the warps'.
+    // Each warp's R-th largest thread maximum, R being the warp's part of the share (of a
+    // top-k the sample's, and five standard deviations); the median of the warps'.
     {
-        const float share = static_cast<float>(f.top_k) / every;
+        const float share = f.use_k ? static_cast<float>(f.top_k) / every : kListShare;
         const int reach = min(32, (static_cast<int>(share + 5.f * sqrtf(share) + 8.f) + kWarps - 1) / kWarps);
         const uint32_t key = key_of<kBf16>(tmax), key16 = kBf16 ? key : key >> 16;
         uint32_t prefix = 0;
@@ -731,15 +787,39 @@ __device__ bool top_row(const SampleArgs &a, int64_t row, const RowFilter &f, co
         total = sh.list_n;
     }
     const float cand = fmaxf(floor_x, base);
-    if (total > kTopList || (total < static_cast<uint32_t>(f.top_k) && !(cand <= base))) return false;
+    const bool complete = cand <= base;  // the list is all that min-p leaves
+    if (total > kTopList || (!complete && (f.use_k ? total < static_cast<uint32_t>(f.top_k) : !f.use_p))) return false;
     const Weigh weight(f.scale, top, sh.table);
+    uint64_t mass = 0, rest = 0;
+    uint32_t none = 0;
     for (uint32_t i = t; i < total; i += kThreads) {
         const uint32_t key = sh.list.key[i];
-        sh.list.w[i] = weight(value_of<kBf16>(key));
+        const uint64_t w = weight(value_of<kBf16>(key));
+        sh.list.w[i] = w;
         sh.list.key[i] = top_key - key;
+        mass += w;
+    }
+    if (!f.use_k) {
+        if (!complete) {
+            const float least = fmaxf(weight.ws.cut, nextafterf(base, -CUDART_INF_F));
+            const bool light = cand <= weight.precise_from;  // (mostly)
+            row_chunks.each([&](const uint4 &c, int) {
+                float v[kPer];
+                unpack<kBf16>(c, v);
+                if (light) {
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q) rest += v[q] > least && v[q] < cand ? weight_rough(v[q], weight.ws, sh.table) : 0;
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < kPer; ++q) rest += v[q] >= base && v[q] < cand ? weight(v[q]) : 0;
+                }
+            });
+        }
+        block_sums<kThreads>(sc, mass, rest, none);
+        if (f.use_p && mass < share_of(f.top_p, mass + rest)) return false;
     }
     __syncthreads();
-    finish_list<kBf16, kMask, kThreads>(a, row, f, sc, weight, top_key, cand, total, sh.list.w, sh.list.key, sh.list.at, 0, 0);
+    finish_list<kBf16, kMask, kThreads>(a, row, f, sc, weight, top_key, cand, total, sh.list.w, sh.list.key, sh.list.at, f.use_k ? 0 : mass, mass + rest);
     return true;
 }
 
@@ -753,6 +833,7 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     constexpr int kPer = 8, kThreads = kRowThreads, kWarps = kThreads / 32;
     Scratch &sc = sh.scratch;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    __syncthreads();  // (what another way has left of the row)
     for (int b = t; b < kOwnBins * kThreads; b += kThreads) sh.bins[b] = 0;
     if (t == 0) {
         sh.tiny_n = sh.list_n = 0;
@@ -942,12 +1023,11 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
                         if (at < kTopList) {
                             sh.list.key[at] = top_key - key_of<true>(v[q]);
                             sh.list.at[at] = i * kPer + q - c.lead;
-                            sh.list.w[at] = weight(v[q]);
                         }
                     }
             }
         });
-        __syncthreads();
+        weigh_list<true>(sh, weight, top_key, reach);
         answer_list<true, kMask, kThreads>(a, row, f, sc, weight, top_key, border_x, min(sh.list_n, static_cast<uint32_t>(kTopList)), sh.list.w,
                                            sh.list.key, sh.list.at, border_far, ties, ties_all, set_n, set_mass);
         return true;
@@ -968,30 +1048,7 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     }
     const auto is_kept = [&](int e, float x) { return x > border_x || (x == border_x && e <= tie_last); };
     if constexpr (kMask) {
-        uint32_t *const words_of = a.mask + row * a.mask_stride;
-        const int64_t id = a.keep ? a.keep[row] : -1;
-        const int forced = id >= 0 && id < a.vocab ? static_cast<int>(id) : -1;
-        for (int w = warp; w < (a.vocab + 31) / 32; w += kWarps) {
-            const int j = w * 32 + lane;
-            bool k = false;
-            if (j < a.vocab) {
-                const float x = c.value(c.lead + j);
-                k = is_kept(c.lead + j, x) || (j == forced && x >= -FLT_MAX);
-            }
-            const uint32_t word = __ballot_sync(0xffffffffu, k);
-            if (lane == 0) words_of[w] = word;
-        }
-        if (t == 0) {
-            if (forced >= 0) {
-                const float x = c.value(c.lead + forced);
-                if (x >= -FLT_MAX && !is_kept(c.lead + forced, x)) {
-                    set_n += 1;
-                    set_mass += weight(x);
-                }
-            }
-            if (a.kept) a.kept[row] = static_cast<int32_t>(set_n);
-            if (a.lse) a.lse[row] = static_cast<float>(weight.lse(set_mass, f.scale));
-        }
+        mask_of_row<true>(a, row, f, c, weight, is_kept, set_n, set_mass);
     } else {
         // (a weight looked up: 10 operations a token, formed anew it takes 30)
         for (int b = t; b < kValues; b += kThreads) {
@@ -1022,13 +1079,199 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
             return s;
         };
         const int e = find_in_row<true>(c, sh, of_chunk, mass_of, place_of(u, set_mass));
-        if (t == 0) {
-            const float x = c.value(e);
-            const bool drawn = u == u;
-            a.ids[row] = drawn ? e - c.lead : -1;
-            if (a.logp) a.logp[row] = drawn ? static_cast<float>(static_cast<double>(x) * f.scale - weight.lse(set_mass, f.scale)) : CUDART_NAN_F;
-            if (a.kept) a.kept[row] = static_cast<int32_t>(set_n);
+        draw_of_row<true>(a, row, f, c, weight, e, u, set_n, set_mass);
+    }
+    return true;
+}
+
+// Any filter on any row, with a weight formed for each token: a pass for the top, one for
+// the numbers and masses of 1024 even bins between the top and where weights end, one
+// that collects the border's bin, one that finds the draw's place.  False where that bin
+// is too full (ties).
+template <bool kBf16, bool kMask>
+__device__ bool massed_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &c, RowShared &sh) {
+    constexpr int kPer = RowChunks<kBf16>::kPer, kThreads = kRowThreads, kWarps = kThreads / 32;
+    Scratch &sc = sh.scratch;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    __syncthreads();  // (what another way has left of the row)
+    float tmax = -CUDART_INF_F;
+    c.each([&](const uint4 &u, int) { tmax = max_nan(tmax, chunk_max<kBf16>(u)); });
+    const bool nan = tmax != tmax;
+    const uint32_t wm = __reduce_max_sync(0xffffffffu, nan ? 0u : key_of<kBf16>(tmax));
+    if (lane == 0) sc.red32[1][warp] = wm;
+    const bool bad = __syncthreads_or(nan);
+    uint32_t top_key = 0;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) top_key = max(top_key, sc.red32[1][q]);
+    const float top = value_of<kBf16>(top_key);
+    if (bad || !(fabsf(top) <= FLT_MAX)) {  // NaN, +inf, or nothing above -inf: no distribution
+        if (t == 0) no_answer<kMask>(a, row, CUDART_NAN_F);
+        return true;
+    }
+    const Weigh weight(f.scale, top, sh.table);
+    const float base = base_of<kBf16>(sc, f, top);
+    uint64_t set_mass = 0, none = 0;
+    uint32_t set_n = 0;
+    float border_x = base;
+    uint32_t last_id = 0xffffffffu;
+    const bool plain = !f.use_k && !f.use_p;
+    if (plain) {
+        // nothing to find: the sums of the warps' parts of the row
+        c.each_of_warp((c.n + kWarps - 1) / kWarps, [&](const uint4 &u, int) {
+            if (!(chunk_max<kBf16>(u) >= base)) return;
+            float v[kPer];
+            unpack<kBf16>(u, v);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (v[q] >= base) {
+                    set_mass += weight(v[q]);
+                    ++set_n;
+                }
+        });
+        const uint64_t part = warp_sum(set_mass);
+        if (lane == 0) sh.part[warp] = part;
+        block_sums<kThreads>(sc, set_mass, none, set_n);
+    } else {
+        for (int b = t; b < kWide; b += kThreads) sh.wide.cnt[b] = sh.wide.mass_lo[b] = sh.wide.mass_hi[b] = 0;
+        __syncthreads();
+        const WeightScale &ws = weight.ws;
+        const float last_x = fmaxf(base, ws.wide ? top - __fdiv_rn(46.f, fmaxf(f.scale, FLT_MIN)) : ws.cut);
+        const float per_bin = __fdiv_rn(kWide - 1.f, fmaxf(top - last_x, FLT_MIN));
+        const auto coarse = [&](float x) { return static_cast<uint32_t>(fminf(__fmul_rn(__fsub_rn(top, x), per_bin), kWide - 1.f)); };
+        c.each([&](const uint4 &u, int) {
+            if (!(chunk_max<kBf16>(u) >= base)) return;
+            float v[kPer];
+            unpack<kBf16>(u, v);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (v[q] >= base) {
+                    const uint32_t b = coarse(v[q]);
+                    const uint64_t w = weight(v[q]);
+                    atomicAdd(&sh.wide.cnt[b], 1u);
+                    const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.wide.mass_lo[b], lo);
+                    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
+                    if (hi) atomicAdd(&sh.wide.mass_hi[b], hi);
+                }
+        });
+        __syncthreads();
+        constexpr int kOwn = kWide / kThreads;
+        uint32_t n = 0;
+        uint64_t mass = 0;
+        const auto bin_mass = [&](int b) { return static_cast<uint64_t>(sh.wide.mass_hi[b]) << 32 | sh.wide.mass_lo[b]; };
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            n += sh.wide.cnt[t * kOwn + i];
+            mass += bin_mass(t * kOwn + i);
         }
+        uint32_t up_n = n;
+        uint64_t up_mass = mass;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t pn = __shfl_up_sync(0xffffffffu, up_n, o);
+            const uint64_t pm = __shfl_up_sync(0xffffffffu, up_mass, o);
+            if (lane >= o) {
+                up_n += pn;
+                up_mass += pm;
+            }
+        }
+        if (lane == 31) {
+            sc.red32[0][warp] = up_n;
+            sc.red64[0][warp] = up_mass;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+            if (q == warp) {
+                up_n += set_n;
+                up_mass += set_mass;
+            }
+            set_n += sc.red32[0][q];
+            set_mass += sc.red64[0][q];
+        }
+        uint32_t listed = kWide, border_far = 0, ties = 0, ties_all = 0;
+        const auto at_far = [&](uint32_t i, uint32_t *p) {
+            *p = sh.list.key[i];
+            return true;
+        };
+        // the border at which the number, or the mass, reaches `target`
+        const auto resolve = [&](bool by_mass, uint64_t target) -> bool {
+            const uint64_t upto = by_mass ? up_mass : up_n, under = upto - (by_mass ? mass : n);
+            if (under < target && upto >= target) {
+                uint32_t an = up_n - n;
+                uint64_t am = up_mass - mass;
+                int b = t * kOwn;
+#pragma unroll 1
+                for (; b < t * kOwn + kOwn - 1; ++b) {
+                    const uint64_t x = bin_mass(b);
+                    if (by_mass ? am + x >= target : an + sh.wide.cnt[b] >= target) break;
+                    an += sh.wide.cnt[b];
+                    am += x;
+                }
+                sh.border = b;
+                sh.above_n = an;
+                sh.above_mass = am;
+                sh.ties_all = sh.wide.cnt[b];
+            }
+            __syncthreads();
+            const uint32_t b = sh.border, total = sh.ties_all;
+            const uint64_t above_n = sh.above_n, above_mass = sh.above_mass;
+            if (total > kTopList) return false;
+            if (b != listed) {
+                if (t == 0) sh.list_n = 0;
+                __syncthreads();
+                c.each([&](const uint4 &u, int i) {
+                    if (!(chunk_max<kBf16>(u) >= base)) return;
+                    float v[kPer];
+                    unpack<kBf16>(u, v);
+#pragma unroll
+                    for (int q = 0; q < kPer; ++q)
+                        if (v[q] >= base && coarse(v[q]) == b) {
+                            const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                            sh.list.key[at] = top_key - key_of<kBf16>(v[q]);
+                            sh.list.at[at] = i * kPer + q - c.lead;
+                        }
+                });
+                listed = b;
+                weigh_list<kBf16>(sh, weight, top_key, total);
+            }
+            __syncthreads();
+            const Picked p = pick<kThreads>(sc, sh.list.w, total, at_far, 0, top_key - key_of<kBf16>(base), by_mass, target - (by_mass ? above_mass : above_n));
+            const uint64_t left = target - (by_mass ? above_mass + p.under_mass : above_n + p.under_n), one = p.mass / p.cnt;
+            border_far = p.at;
+            ties = static_cast<uint32_t>(by_mass ? (left + one - 1) / one : left);
+            ties_all = p.cnt;
+            set_n = static_cast<uint32_t>(above_n + p.under_n) + ties;
+            set_mass = above_mass + p.under_mass + ties * one;
+            return true;
+        };
+        if (f.use_k && static_cast<uint32_t>(f.top_k) < set_n && !resolve(false, f.top_k)) return false;
+        if (f.use_p && !resolve(true, share_of(f.top_p, set_mass))) return false;
+        if (ties_all > 0) border_x = value_of<kBf16>(top_key - border_far);
+        if (ties < ties_all) {
+            const auto at_border = [&](uint32_t i, uint32_t *p) {
+                *p = sh.list.at[i];
+                return sh.list.key[i] == border_far;
+            };
+            last_id = pick<kThreads>(sc, sh.list.w, sh.list_n, at_border, 0, a.vocab - 1, false, ties).at;
+        }
+    }
+    const auto is_kept = [&](int e, float x) { return x > border_x || (x == border_x && static_cast<uint32_t>(e - c.lead) <= last_id); };
+    if constexpr (kMask) {
+        mask_of_row<kBf16>(a, row, f, c, weight, is_kept, set_n, set_mass);
+    } else {
+        const float u = a.uniform[row];
+        const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? weight(x) : 0; };
+        const auto of_chunk = [&](const uint4 &c4, int i) -> uint64_t {
+            uint64_t s = 0;
+            if (!(chunk_max<kBf16>(c4) >= border_x)) return s;
+            float v[kPer];
+            unpack<kBf16>(c4, v);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) s += mass_of(i * kPer + q, v[q]);
+            return s;
+        };
+        const int e = find_in_row<kBf16>(c, sh, of_chunk, mass_of, place_of(u, set_mass), plain);
+        draw_of_row<kBf16>(a, row, f, c, weight, e, u, set_n, set_mass);
     }
     return true;
 }
@@ -1040,7 +1283,6 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_kernel(const __grid_consta
     const int64_t row = blockIdx.x;
     const int t = threadIdx.x;
     const RowFilter f = filter_of(a, row);
-    if (!is_row_kernels<kBf16>(f)) return;
     if constexpr (kMask) {
         uint32_t *const words = a.mask + row * a.mask_stride;
         for (int w = t; w < (a.vocab + 31) / 32; w += kRowThreads) words[w] = 0;
@@ -1054,8 +1296,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_kernel(const __grid_consta
     for (int i = t; i < kUnits; i += kRowThreads) sh.table[i] = kTables.rough[i];
     __syncthreads();
     bool done = false;
-    if (f.use_k && f.top_k <= kTopMost) done = top_row<kBf16, kMask>(a, row, f, c, sh);
-    else if constexpr (kBf16) done = counted_row<kMask>(a, row, f, c, sh);
+    const bool few = f.use_k ? f.top_k <= kTopMost : f.min_p >= 0.01f || (!kBf16 && f.use_p);
+    if (few) done = list_row<kBf16, kMask>(a, row, f, c, sh);
+    if constexpr (kBf16)
+        if (!done) done = counted_row<kMask>(a, row, f, c, sh);
+    if (!done) done = massed_row<kBf16, kMask>(a, row, f, c, sh);
     if (!done && t == 0) {
         if constexpr (kMask) a.mask[row * a.mask_stride] = kLeftMask;
         else a.ids[row] = kLeftId;
@@ -1635,8 +1880,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) cluster_kernel(cons
     for (int64_t at = blockIdx.x / cluster.num_blocks(); at < a.n_rows; at += 32 * step) {
         const int64_t mine = at + (threadIdx.x & 31) * step;
         bool todo = mine < a.n_rows;
-        if (todo && a.after_rows && is_row_kernels<kBf16>(filter_of(a, mine)))
-            todo = kMask ? a.mask[mine * a.mask_stride] == kLeftMask : a.ids[mine] == kLeftId;
+        if (todo && a.after_rows) todo = kMask ? a.mask[mine * a.mask_stride] == kLeftMask : a.ids[mine] == kLeftId;
         // (no row of these is answered before every warp of the cluster has its answer here)
         uint32_t rows = __ballot_sync(0xffffffffu, todo);
         cluster.sync();
@@ -1654,7 +1898,7 @@ cudaError_t launch_clusters(const SampleArgs &a, int ranks, size_t smem, cudaStr
     cudaError_t e = set_smem_max_once(cluster_kernel<kBf16, kMask, kThreads>, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    const int64_t each = a.after_rows ? kBf16 ? 32 : kEach : 1;
+    const int64_t each = a.after_rows ? 32 : 1;
     cfg.gridDim = dim3(static_cast<unsigned>((a.n_rows + each - 1) / each * ranks));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
@@ -1714,7 +1958,7 @@ cudaError_t launch_sample(const SampleCall &c, cudaStream_t stream) {
     a.mask_stride = c.mask_stride;
     a.lse = c.lse;
     a.kept = c.kept;
-    a.after_rows = c.n_rows >= kTopRows && (bf16 || c.f.top_k) ? 1 : 0;
+    a.after_rows = c.n_rows >= kTopRows ? 1 : 0;
     if (bf16) return mask ? launch_typed<true, true>(a, ranks, stream) : launch_typed<true, false>(a, ranks, stream);
     return mask ? launch_typed<false, true>(a, ranks, stream) : launch_typed<false, false>(a, ranks, stream);
 }
