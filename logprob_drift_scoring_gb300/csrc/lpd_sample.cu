@@ -66,9 +66,12 @@ constexpr Tables make_tables() {
 }
 __device__ constexpr Tables kTables = make_tables();
 
+// From so many rows on a CTA takes a row alone (and clusters what it leaves).  64 x 151936
+// bf16 under any filters take 83 us so and 97 us with clusters, 32 take 74 and 41; 152
+// of float32 146 and 148 (under a top-k 40 and 112), 64 take 139 and 76.
+constexpr int kAloneBf16 = 64, kAloneF32 = 128;
 constexpr int kTopList = 2048;      // candidates of a row that a CTA has alone
 constexpr int kTopMost = 512;       // the largest top-k that such a CTA takes
-constexpr int kTopRows = 64;        // from so many rows on
 constexpr float kListShare = 48.f;  // the sampled tokens that a list goes down to without a top-k
 
 // What finding a border takes: bins, and the CTA's sums.
@@ -285,6 +288,13 @@ struct Weigh {
         if (x >= precise_from) return weight_precise(x, ws, top, kTables.precise);
         return x > ws.cut ? weight_rough(x, ws, table) : 0;
     }
+    // log of the share that the token x has of the mass.  (Of more than a half it comes
+    // from what the others have: a token alone has 0, and next to 1 nothing cancels.)
+    __device__ __forceinline__ double logp(float x, uint64_t mass, float scale) const {
+        const uint64_t own = (*this)(x);
+        if (own > mass / 2) return -log1p(static_cast<double>(mass - own) / static_cast<double>(own));
+        return static_cast<double>(x) * scale - lse(mass, scale);
+    }
     // log of the sum that the mass stands for
     __device__ __forceinline__ double lse(uint64_t mass, float scale) const {
         const double origin = ws.wide ? static_cast<double>(top) * scale : ws.origin * kLn2Unit;
@@ -429,7 +439,7 @@ __device__ __forceinline__ void answer_list(const SampleArgs &a, int64_t row, co
                 const float x = value_of<kBf16>(top_key - far_of[i]);
                 const bool drawn = u == u;
                 a.ids[row] = drawn ? static_cast<int32_t>(id) : -1;
-                if (a.logp) a.logp[row] = drawn ? static_cast<float>(static_cast<double>(x) * f.scale - weight.lse(kept_mass, f.scale)) : CUDART_NAN_F;
+                if (a.logp) a.logp[row] = drawn ? static_cast<float>(weight.logp(x, kept_mass, f.scale)) : CUDART_NAN_F;
                 if (a.kept) a.kept[row] = static_cast<int32_t>(kept_n);
             }
     }
@@ -488,7 +498,6 @@ constexpr int kSide = kOctaves * 128;
 constexpr int kTinyUp = kSide, kZero = kSide + 1, kTinyDown = kSide + 2, kDown = kSide + 3, kLow = 2 * kSide + 3;
 constexpr int kValues = 2 * kSide + 4;
 constexpr int kTinyRoom = 1024;
-constexpr int kWide = 1024;        // bins of a row that is not counted by value
 __device__ __forceinline__ float bin_value(int b) {  // of a bin of one value
     const uint32_t up = static_cast<uint32_t>(kSide - 1 - b + (kLowest << 7)) << 16;
     const uint32_t down = static_cast<uint32_t>(b - kDown + (kLowest << 7)) << 16 | 0x80000000u;
@@ -508,10 +517,6 @@ struct RowShared {
             uint32_t key[kTopList], at[kTopList];
         } list;
         uint64_t value_w[kValues];     // the weights of the bins' values, 0 where they are not kept
-        struct {
-            uint64_t beside[2 * kTopList];  // (the list)
-            uint32_t cnt[kWide], mass_lo[kWide], mass_hi[kWide];
-        } wide;
     };
     uint16_t tiny[kTinyRoom];          // the bits of values within 2^-10 of 0
     uint64_t part[kMaxWarps];
@@ -671,7 +676,7 @@ __device__ __forceinline__ void draw_of_row(const SampleArgs &a, int64_t row, co
     const float x = c.value(e);
     const bool drawn = u == u;
     a.ids[row] = drawn ? e - c.lead : -1;
-    if (a.logp) a.logp[row] = drawn ? static_cast<float>(static_cast<double>(x) * f.scale - weight.lse(set_mass, f.scale)) : CUDART_NAN_F;
+    if (a.logp) a.logp[row] = drawn ? static_cast<float>(weight.logp(x, set_mass, f.scale)) : CUDART_NAN_F;
     if (a.kept) a.kept[row] = static_cast<int32_t>(set_n);
 }
 
@@ -1084,12 +1089,10 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     return true;
 }
 
-// Any filter on any row, with a weight formed for each token: a pass for the top, one for
-// the numbers and masses of 1024 even bins between the top and where weights end, one
-// that collects the border's bin, one that finds the draw's place.  False where that bin
-// is too full (ties).
+// A float32 row of which all is kept, or what min-p leaves: a pass for the top, one for the
+// masses of the warps' parts, and a look into the part that the draw falls into.
 template <bool kBf16, bool kMask>
-__device__ bool massed_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &c, RowShared &sh) {
+__device__ void plain_row(const SampleArgs &a, int64_t row, const RowFilter &f, const RowChunks<kBf16> &c, RowShared &sh) {
     constexpr int kPer = RowChunks<kBf16>::kPer, kThreads = kRowThreads, kWarps = kThreads / 32;
     Scratch &sc = sh.scratch;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1106,156 +1109,27 @@ __device__ bool massed_row(const SampleArgs &a, int64_t row, const RowFilter &f,
     const float top = value_of<kBf16>(top_key);
     if (bad || !(fabsf(top) <= FLT_MAX)) {  // NaN, +inf, or nothing above -inf: no distribution
         if (t == 0) no_answer<kMask>(a, row, CUDART_NAN_F);
-        return true;
+        return;
     }
     const Weigh weight(f.scale, top, sh.table);
     const float base = base_of<kBf16>(sc, f, top);
     uint64_t set_mass = 0, none = 0;
     uint32_t set_n = 0;
-    float border_x = base;
-    uint32_t last_id = 0xffffffffu;
-    const bool plain = !f.use_k && !f.use_p;
-    if (plain) {
-        // nothing to find: the sums of the warps' parts of the row
-        c.each_of_warp((c.n + kWarps - 1) / kWarps, [&](const uint4 &u, int) {
-            if (!(chunk_max<kBf16>(u) >= base)) return;
-            float v[kPer];
-            unpack<kBf16>(u, v);
+    c.each_of_warp((c.n + kWarps - 1) / kWarps, [&](const uint4 &u, int) {
+        if (!(chunk_max<kBf16>(u) >= base)) return;
+        float v[kPer];
+        unpack<kBf16>(u, v);
 #pragma unroll
-            for (int q = 0; q < kPer; ++q)
-                if (v[q] >= base) {
-                    set_mass += weight(v[q]);
-                    ++set_n;
-                }
-        });
-        const uint64_t part = warp_sum(set_mass);
-        if (lane == 0) sh.part[warp] = part;
-        block_sums<kThreads>(sc, set_mass, none, set_n);
-    } else {
-        for (int b = t; b < kWide; b += kThreads) sh.wide.cnt[b] = sh.wide.mass_lo[b] = sh.wide.mass_hi[b] = 0;
-        __syncthreads();
-        const WeightScale &ws = weight.ws;
-        const float last_x = fmaxf(base, ws.wide ? top - __fdiv_rn(46.f, fmaxf(f.scale, FLT_MIN)) : ws.cut);
-        const float per_bin = __fdiv_rn(kWide - 1.f, fmaxf(top - last_x, FLT_MIN));
-        const auto coarse = [&](float x) { return static_cast<uint32_t>(fminf(__fmul_rn(__fsub_rn(top, x), per_bin), kWide - 1.f)); };
-        c.each([&](const uint4 &u, int) {
-            if (!(chunk_max<kBf16>(u) >= base)) return;
-            float v[kPer];
-            unpack<kBf16>(u, v);
-#pragma unroll
-            for (int q = 0; q < kPer; ++q)
-                if (v[q] >= base) {
-                    const uint32_t b = coarse(v[q]);
-                    const uint64_t w = weight(v[q]);
-                    atomicAdd(&sh.wide.cnt[b], 1u);
-                    const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.wide.mass_lo[b], lo);
-                    const uint32_t hi = static_cast<uint32_t>(w >> 32) + (old + lo < old);
-                    if (hi) atomicAdd(&sh.wide.mass_hi[b], hi);
-                }
-        });
-        __syncthreads();
-        constexpr int kOwn = kWide / kThreads;
-        uint32_t n = 0;
-        uint64_t mass = 0;
-        const auto bin_mass = [&](int b) { return static_cast<uint64_t>(sh.wide.mass_hi[b]) << 32 | sh.wide.mass_lo[b]; };
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-            n += sh.wide.cnt[t * kOwn + i];
-            mass += bin_mass(t * kOwn + i);
-        }
-        uint32_t up_n = n;
-        uint64_t up_mass = mass;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t pn = __shfl_up_sync(0xffffffffu, up_n, o);
-            const uint64_t pm = __shfl_up_sync(0xffffffffu, up_mass, o);
-            if (lane >= o) {
-                up_n += pn;
-                up_mass += pm;
+        for (int q = 0; q < kPer; ++q)
+            if (v[q] >= base) {
+                set_mass += weight(v[q]);
+                ++set_n;
             }
-        }
-        if (lane == 31) {
-            sc.red32[0][warp] = up_n;
-            sc.red64[0][warp] = up_mass;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int q = 0; q < kWarps; ++q) {
-            if (q == warp) {
-                up_n += set_n;
-                up_mass += set_mass;
-            }
-            set_n += sc.red32[0][q];
-            set_mass += sc.red64[0][q];
-        }
-        uint32_t listed = kWide, border_far = 0, ties = 0, ties_all = 0;
-        const auto at_far = [&](uint32_t i, uint32_t *p) {
-            *p = sh.list.key[i];
-            return true;
-        };
-        // the border at which the number, or the mass, reaches `target`
-        const auto resolve = [&](bool by_mass, uint64_t target) -> bool {
-            const uint64_t upto = by_mass ? up_mass : up_n, under = upto - (by_mass ? mass : n);
-            if (under < target && upto >= target) {
-                uint32_t an = up_n - n;
-                uint64_t am = up_mass - mass;
-                int b = t * kOwn;
-#pragma unroll 1
-                for (; b < t * kOwn + kOwn - 1; ++b) {
-                    const uint64_t x = bin_mass(b);
-                    if (by_mass ? am + x >= target : an + sh.wide.cnt[b] >= target) break;
-                    an += sh.wide.cnt[b];
-                    am += x;
-                }
-                sh.border = b;
-                sh.above_n = an;
-                sh.above_mass = am;
-                sh.ties_all = sh.wide.cnt[b];
-            }
-            __syncthreads();
-            const uint32_t b = sh.border, total = sh.ties_all;
-            const uint64_t above_n = sh.above_n, above_mass = sh.above_mass;
-            if (total > kTopList) return false;
-            if (b != listed) {
-                if (t == 0) sh.list_n = 0;
-                __syncthreads();
-                c.each([&](const uint4 &u, int i) {
-                    if (!(chunk_max<kBf16>(u) >= base)) return;
-                    float v[kPer];
-                    unpack<kBf16>(u, v);
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q)
-                        if (v[q] >= base && coarse(v[q]) == b) {
-                            const uint32_t at = atomicAdd(&sh.list_n, 1u);
-                            sh.list.key[at] = top_key - key_of<kBf16>(v[q]);
-                            sh.list.at[at] = i * kPer + q - c.lead;
-                        }
-                });
-                listed = b;
-                weigh_list<kBf16>(sh, weight, top_key, total);
-            }
-            __syncthreads();
-            const Picked p = pick<kThreads>(sc, sh.list.w, total, at_far, 0, top_key - key_of<kBf16>(base), by_mass, target - (by_mass ? above_mass : above_n));
-            const uint64_t left = target - (by_mass ? above_mass + p.under_mass : above_n + p.under_n), one = p.mass / p.cnt;
-            border_far = p.at;
-            ties = static_cast<uint32_t>(by_mass ? (left + one - 1) / one : left);
-            ties_all = p.cnt;
-            set_n = static_cast<uint32_t>(above_n + p.under_n) + ties;
-            set_mass = above_mass + p.under_mass + ties * one;
-            return true;
-        };
-        if (f.use_k && static_cast<uint32_t>(f.top_k) < set_n && !resolve(false, f.top_k)) return false;
-        if (f.use_p && !resolve(true, share_of(f.top_p, set_mass))) return false;
-        if (ties_all > 0) border_x = value_of<kBf16>(top_key - border_far);
-        if (ties < ties_all) {
-            const auto at_border = [&](uint32_t i, uint32_t *p) {
-                *p = sh.list.at[i];
-                return sh.list.key[i] == border_far;
-            };
-            last_id = pick<kThreads>(sc, sh.list.w, sh.list_n, at_border, 0, a.vocab - 1, false, ties).at;
-        }
-    }
-    const auto is_kept = [&](int e, float x) { return x > border_x || (x == border_x && static_cast<uint32_t>(e - c.lead) <= last_id); };
+    });
+    const uint64_t part = warp_sum(set_mass);
+    if (lane == 0) sh.part[warp] = part;
+    block_sums<kThreads>(sc, set_mass, none, set_n);
+    const auto is_kept = [&](int, float x) { return x >= base; };
     if constexpr (kMask) {
         mask_of_row<kBf16>(a, row, f, c, weight, is_kept, set_n, set_mass);
     } else {
@@ -1263,17 +1137,16 @@ __device__ bool massed_row(const SampleArgs &a, int64_t row, const RowFilter &f,
         const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? weight(x) : 0; };
         const auto of_chunk = [&](const uint4 &c4, int i) -> uint64_t {
             uint64_t s = 0;
-            if (!(chunk_max<kBf16>(c4) >= border_x)) return s;
+            if (!(chunk_max<kBf16>(c4) >= base)) return s;
             float v[kPer];
             unpack<kBf16>(c4, v);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) s += mass_of(i * kPer + q, v[q]);
             return s;
         };
-        const int e = find_in_row<kBf16>(c, sh, of_chunk, mass_of, place_of(u, set_mass), plain);
+        const int e = find_in_row<kBf16>(c, sh, of_chunk, mass_of, place_of(u, set_mass), true);
         draw_of_row<kBf16>(a, row, f, c, weight, e, u, set_n, set_mass);
     }
-    return true;
 }
 
 template <bool kBf16, bool kMask>
@@ -1298,9 +1171,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) row_kernel(const __grid_consta
     bool done = false;
     const bool few = f.use_k ? f.top_k <= kTopMost : f.min_p >= 0.01f || (!kBf16 && f.use_p);
     if (few) done = list_row<kBf16, kMask>(a, row, f, c, sh);
-    if constexpr (kBf16)
+    if constexpr (kBf16) {
         if (!done) done = counted_row<kMask>(a, row, f, c, sh);
-    if (!done) done = massed_row<kBf16, kMask>(a, row, f, c, sh);
+    } else if (!done && !f.use_k && !f.use_p) {
+        plain_row<kBf16, kMask>(a, row, f, c, sh);
+        done = true;
+    }
     if (!done && t == 0) {
         if constexpr (kMask) a.mask[row * a.mask_stride] = kLeftMask;
         else a.ids[row] = kLeftId;
@@ -1862,7 +1738,7 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
                 const float x = value_at(e);
                 const bool drawn = u == u;
                 a.ids[row] = drawn ? first + e - lead : -1;
-                if (a.logp) a.logp[row] = drawn ? static_cast<float>(static_cast<double>(x) * scale - weight.lse(kept_mass, scale)) : CUDART_NAN_F;
+                if (a.logp) a.logp[row] = drawn ? static_cast<float>(weight.logp(x, kept_mass, scale)) : CUDART_NAN_F;
                 if (a.kept) a.kept[row] = static_cast<int32_t>(kept_n);
             }
         }
@@ -1898,7 +1774,8 @@ cudaError_t launch_clusters(const SampleArgs &a, int ranks, size_t smem, cudaStr
     cudaError_t e = set_smem_max_once(cluster_kernel<kBf16, kMask, kThreads>, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    const int64_t each = a.after_rows ? 32 : 1;
+    // (bf16 rows are hardly ever left over, float32 nuclei beyond a list are)
+    const int64_t each = !a.after_rows ? 1 : kBf16 ? 32 : a.n_rows <= 512 ? 1 : 2;
     cfg.gridDim = dim3(static_cast<unsigned>((a.n_rows + each - 1) / each * ranks));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
@@ -1958,7 +1835,7 @@ cudaError_t launch_sample(const SampleCall &c, cudaStream_t stream) {
     a.mask_stride = c.mask_stride;
     a.lse = c.lse;
     a.kept = c.kept;
-    a.after_rows = c.n_rows >= kTopRows ? 1 : 0;
+    a.after_rows = c.n_rows >= (bf16 ? kAloneBf16 : kAloneF32) ? 1 : 0;
     if (bf16) return mask ? launch_typed<true, true>(a, ranks, stream) : launch_typed<true, false>(a, ranks, stream);
     return mask ? launch_typed<false, true>(a, ranks, stream) : launch_typed<false, false>(a, ranks, stream);
 }

@@ -202,6 +202,26 @@ def test_uniforms_at_the_ends():
     assert np.isnan(logp[4]) and np.isfinite(logp[[0, 1, 2, 3, 5, 6]]).all() and (kept[[0, 1, 2, 3, 5, 6]] == 5).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 200])
+def test_tokens_that_are_nearly_certain(rows, kind):
+    """A token alone has the logprob 0; next to 1 the others' share keeps its digits:
+    2^-29 of it and the steps of 2^-44 that each of the others may lose."""
+    rng = np.random.default_rng(rows)
+    vocab = 5000
+    x = rng.normal(0, 0.3, (rows, vocab))
+    x[:, 77] = 18.0
+    t = tensor(x, kind)
+    ids, logp, kept = B.sample(t, torch.full((rows,), 0.5, device=DEV), to_filter(dict(top_k=np.ones(rows, np.int32))))
+    assert bool((ids == 77).all()) and bool((logp == 0).all()) and bool((kept == 1).all())
+    ids, logp, kept = B.sample(t, torch.full((rows,), 0.5, device=DEV))
+    xh = host(t)
+    others = np.exp(xh - xh[:, 77:78]).sum(1) - 1
+    got = logp.cpu().numpy().astype(np.float64)
+    assert bool((ids == 77).all())
+    assert np.all(np.abs(got + np.log1p(others)) <= (2.0 ** -23 + 2.0 ** -29) * others + vocab * 2.0 ** -44)
+
+
 def test_no_filter_and_outputs_left_out():
     rng = np.random.default_rng(3)
     x = tensor(logits(rng, 6, 3001), "bf16", 7)
