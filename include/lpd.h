@@ -732,7 +732,8 @@ int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64
  * at byte
  *     ((r / 128) * atoms + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.
  * Bytes of rows and blocks behind the last are there but stand for nothing: 0 (for
- * blocks behind the last any scale that is not NaN). */
+ * blocks behind the last any scale that is not NaN).  An odd k leaves the upper half
+ * of a row's last byte, which has to be 0. */
 typedef struct {
     void *ptr;                 /* device, row 0; 16-byte aligned for the product */
     int32_t block;             /* 16 or 32 */

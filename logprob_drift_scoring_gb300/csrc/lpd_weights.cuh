@@ -85,7 +85,7 @@ __host__ __device__ __forceinline__ WeightScale weight_scale(float scale, float 
     constexpr double kC = 1.4426950408889634073599 * kUnits;
     constexpr float kHi = static_cast<float>(kC), kLo = static_cast<float>(kC - static_cast<double>(kHi));
     w.ch = mul_rn(scale, kHi);
-    w.cl = fma_rn(scale, kHi, -w.ch) + scale * kLo;
+    w.cl = fma_rn(scale, kLo, fma_rn(scale, kHi, -w.ch));
     w.wide = !(fabsf(top * w.ch) < 1048576.f) || !(w.ch < 1e30f) || !(w.ch > 1e-30f);
     w.c = w.wide ? static_cast<double>(scale) * kC : static_cast<double>(w.ch) + static_cast<double>(w.cl);
     // (a wide row's origin is the top itself: weight_precise)

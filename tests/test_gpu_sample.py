@@ -104,12 +104,16 @@ def check(x, f, u, keep=None, active=None):
     return ids, kept
 
 
+# so few that clusters take them, and so many that a CTA takes each
+ROWS = [24, 136]
+
+
+@pytest.mark.parametrize("rows", ROWS)
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab,pad", [(1, 0), (2, 1), (31, 0), (32, 3), (33, 7), (64, 0), (65, 0), (1000, 8), (1024, 0),
                                        (2049, 5), (8193, 7), (20011, 1), (50021, 1), (131077, 3)])
-def test_sizes(vocab, pad, kind):
+def test_sizes(vocab, pad, kind, rows):
     rng = np.random.default_rng(vocab)
-    rows = 24
     check(tensor(logits(rng, rows, vocab), kind, pad), params(rng, rows, vocab), rng.uniform(0, 1, rows),
           keep=rng.integers(-1, vocab + 1, rows), active=rng.uniform(0, 1, rows) < 0.8)
 
@@ -128,31 +132,32 @@ def test_rows(rows, kind):
     check(tensor(logits(rng, rows, 9001), kind), params(rng, rows, 9001), rng.uniform(0, 1, rows))
 
 
+@pytest.mark.parametrize("rows", [32, 136])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("peak", [0.0, 3.0])
-def test_flat_rows(peak, kind):
+def test_flat_rows(peak, kind, rows):
     """Nuclei of most of the vocabulary: the borders lie below every list."""
     rng = np.random.default_rng(11)
-    rows, vocab = 32, 60013
+    vocab = 60013
     f = params(rng, rows, vocab)
-    f["top_k"][::4] = rng.integers(2000, vocab, 8)
-    f["top_p"][1::4] = rng.uniform(0.5, 0.9999, 8)
+    f["top_k"][::4] = rng.integers(2000, vocab, rows // 4)
+    f["top_p"][1::4] = rng.uniform(0.5, 0.9999, rows // 4)
     f["min_p"][2::8] = 1e-4
     check(tensor(rng.normal(0, 0.7, (rows, vocab)) + peak, kind), f, rng.uniform(0, 1, rows))
 
 
+@pytest.mark.parametrize("rows", [30, 135])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab", [7, 700, 30011])
-def test_ties(vocab, kind):
+def test_ties(vocab, kind, rows):
     """Rows of one value, of a few values, and of both zeros: ties go by token."""
     rng = np.random.default_rng(vocab)
-    rows = 30
     x = np.round(rng.normal(0, 1.5, (rows, vocab)))
     x[::5] = 2.5
-    x[1::5] = np.where(rng.uniform(0, 1, (6, vocab)) < 0.5, 0.0, -0.0)
+    x[1::5] = np.where(rng.uniform(0, 1, (rows // 5, vocab)) < 0.5, 0.0, -0.0)
     f = params(rng, rows, vocab)
-    f["top_k"][::3] = rng.integers(1, vocab + 1, 10)
-    f["top_p"][1::3] = rng.uniform(0, 1, 10)
+    f["top_k"][::3] = rng.integers(1, vocab + 1, rows // 3)
+    f["top_p"][1::3] = rng.uniform(0, 1, rows // 3)
     f["scale"][:] = np.where(np.arange(rows) % 2, 1.0, f["scale"])
     # (equal weights: every sum is a whole number of them, so keep the borders between two)
     n_top = (x == x.max(1, keepdims=True)).sum(1)
@@ -160,10 +165,11 @@ def test_ties(vocab, kind):
     check(tensor(x, kind), f, rng.uniform(0, 1, rows))
 
 
+@pytest.mark.parametrize("rows", [40, 136])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-def test_masked_logits_and_rows_without_a_distribution(kind):
+def test_masked_logits_and_rows_without_a_distribution(kind, rows):
     rng = np.random.default_rng(5)
-    rows, vocab = 40, 20011
+    vocab = 20011
     x = logits(rng, rows, vocab)
     x[rng.uniform(0, 1, x.shape) < 0.9] = -np.inf
     x[3] = -np.inf
@@ -180,14 +186,34 @@ def test_masked_logits_and_rows_without_a_distribution(kind):
     check(tensor(x, kind), f, rng.uniform(0, 1, rows), keep=rng.integers(0, vocab, rows))
 
 
+@pytest.mark.parametrize("rows", [16, 136])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("scale", [1e-30, 1e-6, 0.01, 50.0, 3000.0, 1e9, 1e30])
-@pytest.mark.parametrize("offset", [0.0, 1000.0, -300.0])
-def test_extreme_scales_and_offsets(scale, offset):
+@pytest.mark.parametrize("offset", [0.0, 1000.0, -300.0, 30000.0])
+def test_extreme_scales_and_offsets(scale, offset, kind, rows):
     rng = np.random.default_rng(9)
-    rows, vocab = 16, 5003
+    vocab = 5003
     f = params(rng, rows, vocab)
     f["scale"] = np.full(rows, scale, dtype=np.float32)
-    check(tensor(rng.normal(0, 2, (rows, vocab)) + offset, "f32"), f, rng.uniform(0, 1, rows))
+    check(tensor(rng.normal(0, 2, (rows, vocab)) + offset, kind), f, rng.uniform(0, 1, rows))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_values_next_to_zero_and_lowest_masks(kind):
+    """Rows whose border, or top, lies within 2^-10 of 0, rows masked with the type's
+    lowest value, and rows of float32 values that bf16 has."""
+    rng = np.random.default_rng(13)
+    rows, vocab = 140, 9000
+    x = rng.normal(0, 1, (rows, vocab))
+    x[:70] *= 1e-4
+    x[40:70] -= 3.0
+    x[40:70, :50] = rng.normal(0, 1e-5, (30, 50))
+    x[70:100, 1000:] = float(torch.finfo(torch.bfloat16).min)
+    x[100:120, ::2] = -20000.0
+    x = torch.from_numpy(x).to(torch.bfloat16).float().numpy() if kind == "f32" else x
+    f = params(rng, rows, vocab)
+    f["top_k"][70:90:3] = rng.integers(900, vocab, 7)
+    check(tensor(x, kind), f, rng.uniform(0, 1, rows))
 
 
 def test_uniforms_at_the_ends():
