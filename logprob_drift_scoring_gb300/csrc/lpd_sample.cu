@@ -17,8 +17,8 @@
 //   microsecond: latency bounds it.
 // - Many rows: a CTA a row, the row streamed (row_kernel).  Under a small top-k or a
 //   min-p the largest tokens are collected against a value that a sample of the row gave:
-//   4096 rows (3687 of them active) x 151936 bf16 in 332 us, 3.4 TB/s of 6.8; the pass
-//   over the row takes three quarters of that, with 32 warps a multiprocessor and 64 KB
+//   4096 rows (3687 of them active) x 151936 bf16 in 293 us, 4.1 TB/s of 6.8; the pass
+//   over the row takes three quarters of that, with 48 warps a multiprocessor and 96 KB
 //   in flight, the selections behind it the rest.  A bf16 row under any other filter is
 //   counted by value (counted_row): 509 rows under temperature or top-p in 175 us,
 //   bound by shared-memory atomics in the first pass (24 us a row alone, 14 of a full
@@ -858,12 +858,8 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     }
     __syncthreads();
     bool bad = false;
-    const auto count = [&](uint32_t bits) {  // of one value
-        const uint32_t m = (bits & 0x7fffu) - (kLowest << 7);
-        if (m < static_cast<uint32_t>(kSide)) {
-            atomicAdd(&sh.bins[(bits & 0x8000u) ? kDown + m : kSide - 1 - m], 1u);
-        } else if (bits == 0xff80u) {  // -inf
-        } else if ((bits & 0x7fffu) >= 0x7f80u) {
+    const auto count = [&](uint32_t bits) {  // of a value, not -inf, without a bin of its own
+        if ((bits & 0x7fffu) >= 0x7f80u) {
             bad = true;
         } else if ((bits & 0x7fffu) == 0) {
             atomicAdd(&sh.bins[kZero], 1u);
@@ -879,10 +875,18 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     };
     c.each([&](const uint4 &u, int) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t odd = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            count(w[q] & 0xffffu);
-            count(w[q] >> 16);
+        for (int q = 0; q < kPer; ++q) {
+            const uint32_t bits = (q & 1) ? w[q >> 1] >> 16 : w[q >> 1] & 0xffffu, m = (bits & 0x7fffu) - (kLowest << 7);
+            if (m < static_cast<uint32_t>(kSide)) atomicAdd(&sh.bins[(bits & 0x8000u) ? kDown + m : kSide - 1 - m], 1u);
+            else if (bits != 0xff80u) odd |= 1u << q;
+        }
+#pragma unroll 1
+        for (; odd; odd &= odd - 1) {
+            const int q = __ffs(odd) - 1;
+            const uint32_t pair = q < 4 ? (q < 2 ? w[0] : w[1]) : (q < 6 ? w[2] : w[3]);
+            count((q & 1) ? pair >> 16 : pair & 0xffffu);
         }
     });
     if (__syncthreads_or(bad)) {
@@ -1161,8 +1165,11 @@ __device__ void plain_row(const SampleArgs &a, int64_t row, const RowFilter &f, 
     }
 }
 
+// (Two CTAs a multiprocessor; three where the row's bytes are what counts, masks of bf16
+// rows: 4096 rows in 293 us instead of 334.  Registers then spill, which costs draws 5 to
+// 10 %, and float32 masks 8 %.)
 template <bool kBf16, bool kMask>
-__global__ void __launch_bounds__(kRowThreads, 2) row_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kRowThreads, kBf16 && kMask ? 3 : 2) row_kernel(const __grid_constant__ SampleArgs a) {
     extern __shared__ __align__(16) char smem[];
     RowShared &sh = *reinterpret_cast<RowShared *>(smem);
     const int64_t row = blockIdx.x;
