@@ -745,6 +745,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             // ----------------------------------------------------------------- MMA
             uint32_t s = 0, phase = 0, turn = 1;  // `turn`: the parity that the emptied accumulator shows
             bool ok = true, issued = false;
+            const int whole = static_cast<int>(a.k / kTK), tail = (static_cast<int>(a.k % kTK) + 63) / 64;  // stages of four MMAs, the last one's
             const uint32_t base = desc_low(smem), plain = (smem_u32(smem) & 0x3FFFFu) >> 4;
             for (int64_t w = item0; ok && w < items; w += step) {
                 int tm, tn, split;
@@ -762,22 +763,25 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                         const uint32_t da = base + s * (R::kStage >> 4), db = da + (R::kA >> 4);
                         const uint32_t sa = plain + s * (R::kStage >> 4) + ((R::kA + R::kB) >> 4), sb = sa + (R::kSa >> 4);
                         const uint32_t ca = tmem + kScaleCol + s * kScaleCols, cb = ca + 16;
-                        const int mmas = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(kb) * kTK + 63) / 64));
+                        const auto issue = [&](int mmas) {
 #pragma unroll
-                        for (int j = 0; j < kAtomsPer; ++j) {
-                            if (j * (4 / kAtomsPer) >= mmas) break;
-                            scales_to_tmem<kPair>(ca + 4 * j, sa + j * (kAtom >> 4));
-                            scales_to_tmem<kPair>(cb + 8 * j, sb + j * (kAtom >> 4));
-                            scales_to_tmem<kPair>(cb + 8 * j + 4, sb + (4 + j) * (kAtom >> 4));
-                        }
+                            for (int j = 0; j < kAtomsPer; ++j) {
+                                if (j * (4 / kAtomsPer) >= mmas) break;
+                                scales_to_tmem<kPair>(ca + 4 * j, sa + j * (kAtom >> 4));
+                                scales_to_tmem<kPair>(cb + 8 * j, sb + j * (kAtom >> 4));
+                                scales_to_tmem<kPair>(cb + 8 * j + 4, sb + (4 + j) * (kAtom >> 4));
+                            }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {  // K = 32 bytes inside the swizzle row
-                            if (j >= mmas) break;
-                            // (of a word of four scales of 32 an MMA takes the first or the last two)
-                            const uint32_t idesc = kB16 ? a.idesc : a.idesc | (j & 1) << 5 | (j & 1) << 30;
-                            const int at = kB16 ? j : j / 2;
-                            umma_f4<kB16, kPair>(tmem, da + 2 * j, db + 2 * j, idesc, ca + 4 * at, cb + 8 * at, kb > kb0 || j > 0 ? 1u : 0u);
-                        }
+                            for (int j = 0; j < 4; ++j) {  // K = 32 bytes inside the swizzle row
+                                if (j >= mmas) break;
+                                // (of a word of four scales of 32 an MMA takes the first or the last two)
+                                const uint32_t idesc = kB16 ? a.idesc : a.idesc | (j & 1) << 5 | (j & 1) << 30;
+                                const int at = kB16 ? j : j / 2;
+                                umma_f4<kB16, kPair>(tmem, da + 2 * j, db + 2 * j, idesc, ca + 4 * at, cb + 4 * (kTN / kTM) * at, kb > kb0 || j > 0 ? 1u : 0u);
+                            }
+                        };
+                        if (kb < whole) issue(4);
+                        else issue(tail);
                         commit<kPair>(&empty[s]);
                         if (kb + 1 == kb1) commit<kPair>(&acc_full);
                     }
