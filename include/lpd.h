@@ -50,7 +50,9 @@
  * Bounded waits: no kernel waits without a limit.  The streaming row pass
  * gives up a pipeline wait after 2 s (4 s in the fused LM-head kernel), sets
  * LPD_STATUS_TIMEOUT, lets its in-flight copies land and returns; the context
- * stays usable.  For tests of that path, the environment variable
+ * stays usable.  (Barriers of a thread-block cluster, whose CTAs the hardware
+ * starts together, have no limit of their own: every wait in front of one
+ * has.)  For tests of that path, the environment variable
  * LPD_STALL_ROW_PASS=1 (read at each call) makes one CTA of the row pass
  * withhold its first copy: the call then takes about 4 s and returns with
  * LPD_STATUS_TIMEOUT.
@@ -610,7 +612,7 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
  *             (of these) is at least top_p[r]; at least one token
  * Equal logits (+0 and -0 are equal) are ordered by token, the lowest first.  A
  * token whose logit is -inf is never kept.  The filters are decided on sums that
- * are exact to about 2^-31 of each weight (2^-41 for the heaviest), so a set is the
+ * are exact to about 2^-29 of each weight (2^-41 for the heaviest), so a set is the
  * mathematical one unless a border lies nearer to a sum than that.
  * A NULL array leaves its step out; so does min_p <= 0, top_k <= 0 or >= vocab, and
  * top_p >= 1.  (min_p >= 1 keeps the largest logits, top_p <= 0 and top_k = 1 the
@@ -638,7 +640,7 @@ typedef struct {
  * out_logp   device float [n_rows] or NULL: z_j - log W, the token's logprob under
  *            the distribution that it was drawn from; NaN where the id is -1.
  * out_kept   device int32 [n_rows] or NULL: the kept tokens (0: no distribution).
- * No workspace; nothing is allocated.  vocab > LPD_SAMPLE_MAX_VOCAB:
+ * No output may overlap an input.  No workspace; nothing is allocated.  vocab > LPD_SAMPLE_MAX_VOCAB:
  * LPD_ERR_UNSUPPORTED. */
 int lpd_sample(const lpd_logits *logits, const lpd_filter *filter, int64_t n_rows, int64_t vocab,
                const float *uniform, int32_t *out_ids, float *out_logp, int32_t *out_kept, void *stream);

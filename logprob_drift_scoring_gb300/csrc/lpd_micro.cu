@@ -32,6 +32,14 @@ constexpr int kAtom = 512;  // bytes of scales of 128 rows x 4 blocks: (row % 32
 // four bytes of codes of each of its 8 output rows, which turn through shared
 // memory (word g of output row c lies at g ^ (c / 8 % 16)).  The tile's scales are
 // gathered in shared memory in their final order and leave as one piece.
+//
+// Bound: 151936 x 4096 bf16 with the values that the codes stand for take 501 us as they
+// lie (0.84 of the copy rate; 68 % of the issue slots and 62 % of HBM's cycles in use) and
+// 547 transposed, whose words turn through shared memory; float32, 75968 x 4096, 408 us
+// (0.96).  A tile kept in registers and not in shared memory spares a write and a read of
+// it; rows off 16-byte boundaries pass through shared memory all the same, since a warp
+// then reads and writes 32 neighbours at once (12661 x 2051 float32: 63 us, 8 values a
+// lane 71).
 constexpr int kQTile = 128;
 constexpr int kQThreads = 256;
 constexpr float kFloor = 5.421010862427522e-20f;  // 2^-64: the smallest magnitude a power-of-two scale is made for
@@ -472,11 +480,17 @@ __global__ void __launch_bounds__(kQThreads, kBf16 && kVec ? 3 : 2) quantize_ker
 // accumulator into registers, 128 columns a thread, and free it at once; rounding and
 // stores (TMA) run under the next tile.
 //
-// Bound: an MMA takes 128 cycles, 512 a stage; what a stage's 54 KB (without pairs)
-// take to come from L2 is more, and with three stages in flight a stage took 1000
-// cycles (4096 x 128256 x 4096: 896 us, 4.8 PFLOP/s).  Bringing half of B to both CTAs
-// by multicast left the bytes in flight as they were (847 us); a pair's stage is 38 KB
-// a CTA and five are in flight.
+// 4096 x 128256 x 4096: 632 us, 6.8 PFLOP/s; with a k of 16384 (38912 columns) 7.9.  A
+// stage takes 0.30 us, 560 to 600 cycles, its four MMAs 512 of them; the rest is their
+// issue, which is why a whole stage's runs without a test in between (0.34 us with them).
+// A tile's end costs 1.2 us: its last MMAs, the read of the accumulator, the hand-over to
+// the next tile's first.  Tensor memory has no room for a second accumulator of this width;
+// three of half of it, used in turn, hide the hand-over, but an MMA on 128 columns takes as
+// long as one on 256 (1410 us).  Without pairs (54 KB a stage, three in flight: the bytes
+// from L2 bound it) the product took 896 us, with half of B brought to both CTAs by
+// multicast 847.  Float32 output is bound by its boxes, one in flight a warp (37984 x 4096 x
+// 2051: 190 us, 3.4 TB/s); a second one costs a stage of the ring (5 % slower), stores from
+// registers in 32-byte sectors hold up the loads (246 us).
 constexpr int kTM = 128, kTN = 256, kTK = 256;
 template <bool kPair>
 struct Ring {

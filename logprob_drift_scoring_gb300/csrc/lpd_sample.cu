@@ -20,7 +20,7 @@
 //   4096 rows (3687 of them active) x 151936 bf16 in 293 us, 4.1 TB/s of 6.8; the pass
 //   over the row takes three quarters of that, with 48 warps a multiprocessor and 96 KB
 //   in flight, the selections behind it the rest.  A bf16 row under any other filter is
-//   counted by value (counted_row): 509 rows under temperature or top-p in 175 us,
+//   counted by value (counted_row): 509 rows under temperature or top-p in 170 us,
 //   bound by shared-memory atomics in the first pass (24 us a row alone, 14 of a full
 //   multiprocessor) and table look-ups in a draw's second.  A float32 row of which all
 //   is kept is weighed token by token (plain_row), 30 operations each.

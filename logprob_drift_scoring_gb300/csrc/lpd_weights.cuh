@@ -4,7 +4,7 @@
 // (the first token whose running mass passes u W) compare sums that may lie
 // arbitrarily near each other, so the sums of a row are integers: any order of
 // addition gives the same bits, and one row's answer does not depend on how its
-// columns were spread over threads.  A weight is formed to 2^-31 of itself
+// columns were spread over threads.  A weight is formed to 2^-29.5 of itself
 // (weight_rough) and for the row's heaviest tokens to 2^-41 (weight_precise):
 // the errors of many small weights average out, those of a few large ones would
 // not.  (A plain exponential in float32 is off by 2^-22 with the rounding of its

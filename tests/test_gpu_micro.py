@@ -7,6 +7,10 @@ each of the ceil(k / 64) sums off by at most 2^-22 of the terms' absolute sum S 
 truncations of 2^-23), a split's join adds as many float32 additions as there are
 parts (at most 152, 2^-24 each), the tensor scales two roundings and the output its half step.
 """
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -17,6 +21,7 @@ from logprob_drift_scoring_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = Path(__file__).resolve().parent.parent
 KINDS = {"bf16": torch.bfloat16, "f32": torch.float32}
 HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 
@@ -249,6 +254,66 @@ def test_head_of_a_rollout_from_hidden_rows_to_drift():
     z = torch.where(torch.from_numpy(sample_ref.bits(mask.cpu().numpy(), vocab)).to(DEV), train.double() * filt.scale.double()[:, None], -float("inf"))
     want = torch.log_softmax(z, 1).gather(1, ids.long()[:, None])[:, 0]
     assert bool(((res.logp_train.double() - want).abs() <= 1.1e-5 + 2.0 ** -22 * want.abs()).all())
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_a_row_does_not_depend_on_the_other_rows(block):
+    """One row tile, whose CTAs are alone, and several, whose are pairs: the same bits (the k axis
+    is not split where a row of tiles fills half of the multiprocessors)."""
+    rng = np.random.default_rng(21)
+    n, k = 256 * 100, 1000
+    w = B.micro_quantize(rand(rng, n, k, "bf16"), block)
+    x = rand(rng, 300, k, "bf16")
+    whole = B.micro_matmul(B.micro_quantize(x, block), w, torch.float32)
+    for m in (1, 100, 128, 129):
+        assert torch.equal(B.micro_matmul(B.micro_quantize(x[:m].contiguous(), block), w, torch.float32), whole[:m]), m
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_rows_far_apart(transpose):
+    """Offsets beyond 32 bits of what is read, of the values and of the product."""
+    rng = np.random.default_rng(22)
+    rows, k = 3, 70
+    x = rand(rng, rows, k, "bf16")
+    far = 2 ** 30 + 2 ** 20
+    y = torch.empty(2 * far + k, dtype=x.dtype, device=DEV).as_strided((rows, k), (far, 1))
+    y.copy_(x)
+    out_rows = k if transpose else rows
+    far_values = 2 ** 31 // (out_rows - 1) // 8 * 8 + 8
+    cols = rows if transpose else k
+    values = torch.empty(far_values * (out_rows - 1) + cols, dtype=x.dtype, device=DEV).as_strided((out_rows, cols), (far_values, 1))
+    plain = torch.empty(out_rows, cols, dtype=x.dtype, device=DEV)
+    a, b = (B.micro_empty(out_rows, cols, 16) for _ in range(2))
+    B.lpd_micro_quantize(x, a, transpose, plain)
+    B.lpd_micro_quantize(y, b, transpose, values)
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales) and torch.equal(values, plain)
+    del y, values
+    far = 2 ** 31 // (out_rows - 1) // 8 * 8 + 8
+    out = torch.empty(far * (out_rows - 1) + out_rows, dtype=x.dtype, device=DEV).as_strided((out_rows, out_rows), (far, 1))
+    B.lpd_micro_matmul(a, a, out, torch.empty(B.lpd_micro_workspace_size(out_rows, out_rows, cols), dtype=torch.uint8, device=DEV))
+    assert torch.equal(out, B.micro_matmul(a, a))
+
+
+def test_first_call_is_captured():
+    """In a process that has called nothing yet."""
+    code = """
+import torch
+from logprob_drift_scoring_gb300 import binding as B
+x = torch.randn(200, 320, device="cuda").bfloat16()
+q = B.micro_empty(200, 320, 16)
+out = torch.empty(200, 200, device="cuda")
+ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+    B.lpd_micro_quantize(x, q)
+    B.lpd_micro_matmul(q, q, out, ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, B.micro_matmul(q, q, torch.float32))
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_repeated_streams_and_graph():

@@ -7,6 +7,10 @@ within 2^-28 of the whole mass from a sum: such rows are left out of the compari
 of sets and tokens (one in 2^28 times the number of kept tokens).  The logarithm of a sum is off
 by 2^-29 and the result is rounded to float32: 2^-24 of itself.
 """
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -16,6 +20,7 @@ from logprob_drift_scoring_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+ROOT = Path(__file__).resolve().parent.parent
 KINDS = {"bf16": torch.bfloat16, "f32": torch.float32}
 NEAR = 2.0 ** -28
 
@@ -274,6 +279,49 @@ def test_a_row_does_not_depend_on_its_batch():
         one = to_filter({k: v[r:r + 1] for k, v in f.items()})
         for got, want in zip(B.sample(x[r:r + 1], u[r:r + 1], one), (ids, logp, kept)):
             assert torch.equal(got, want[r:r + 1])
+
+
+@pytest.mark.parametrize("rows", [3, 150])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rows_far_apart(kind, rows):
+    """Offsets beyond 32 bits, of logits and of masks: the bits of the same rows side by side."""
+    rng = np.random.default_rng(12)
+    vocab, words = 5003, 157
+    x = tensor(logits(rng, rows, vocab), kind)
+    f = to_filter(params(rng, rows, vocab))
+    u = torch.rand(rows, device=DEV)
+    far = (2 ** 31 + 2 ** 20) // (rows - 1) // 8 * 8 + 8  # (the last row lies behind 2^31 elements)
+    room = torch.empty(far * (rows - 1) + vocab, dtype=x.dtype, device=DEV)
+    y = room.as_strided((rows, vocab), (far, 1))
+    y.copy_(x)
+    bits = torch.empty(far * (rows - 1) + words, dtype=torch.int32, device=DEV)
+    mask = bits.as_strided((rows, words), (far, 1))
+    for got, want in zip(B.sample(y, u, f), B.sample(x, u, f)):
+        assert torch.equal(got, want)
+    B.lpd_filter_mask(y, f, None, None, mask)
+    assert torch.equal(mask, B.filter_mask(x, f)[0])
+
+
+def test_first_call_is_captured():
+    """In a process that has called nothing yet."""
+    code = """
+import torch
+from logprob_drift_scoring_gb300 import binding as B
+x = torch.randn(200, 5003, device="cuda").bfloat16()
+u = torch.rand(200, device="cuda")
+ids = torch.empty(200, dtype=torch.int32, device="cuda")
+mask = torch.empty(200, 157, dtype=torch.int32, device="cuda")
+g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+    B.lpd_sample(x, None, u, ids)
+    B.lpd_filter_mask(x, None, ids, None, mask)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(ids, B.sample(x, u)[0]) and torch.equal(mask, B.filter_mask(x, None)[0])
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_repeated_streams_and_graph():
