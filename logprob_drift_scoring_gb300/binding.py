@@ -260,7 +260,8 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # (the handle alone: making a Stream object of it takes 3 us, a fifth of a small call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -907,7 +908,9 @@ class MicroScaled:
                 raise ValueError(f"codes on {c.device}, {name} on {o.device}")
         # the stride of a single row has no meaning in torch: any legal one serves
         stride = c.stride(0) if c.shape[0] > 1 else -(-c.shape[1] // 16) * 16
-        object.__setattr__(self, "_struct", LpdMicroScaled(c.data_ptr(), self.block, 0, stride, s.data_ptr(), _ptr(t)))
+        struct = LpdMicroScaled(c.data_ptr(), self.block, 0, stride, s.data_ptr(), _ptr(t))
+        for name, value in (("_struct", struct), ("_ref", ctypes.byref(struct)), ("_rows", c.shape[0]), ("_device", c.device)):
+            object.__setattr__(self, name, value)
 
 
 def micro_empty(rows: int, k: int, block: int = 16, tensor_scale=None, device="cuda") -> MicroScaled:
@@ -925,19 +928,21 @@ def lpd_micro_quantize(x, out, transpose=False, out_values=None, stream=None) ->
     it stands for into out_values (bf16 or f32), if given."""
     if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("x must be 2-D with contiguous columns")
-    shape = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
-    if (out.codes.shape[0], out.k) != shape:
+    rows, cols = x.shape
+    shape = (cols, rows) if transpose else (rows, cols)
+    device = x.device
+    if (out._rows, out.k) != shape:
         raise ValueError("out has another shape")
-    if out.codes.device != x.device:
-        raise ValueError(f"x on {x.device}, out on {out.codes.device}")
-    v = out_values
-    if v is not None and (tuple(v.shape) != shape or v.device != x.device or (v.shape[1] > 1 and v.stride(1) != 1)):
-        raise ValueError("out_values must have out's shape and device and contiguous columns")
+    if out._device != device:
+        raise ValueError(f"x on {device}, out on {out._device}")
+    v, v_dtype, v_stride = out_values, 0, 0
+    if v is not None:
+        if v.shape != shape or v.device != device or (shape[1] > 1 and v.stride(1) != 1):
+            raise ValueError("out_values must have out's shape and device and contiguous columns")
+        v_dtype, v_stride = _dtype_code(v), _row_stride(v)
     with _on(x):
-        rc = lib().lpd_micro_quantize(_ptr(x), _dtype_code(x), _row_stride(x), x.shape[0], x.shape[1],
-                                      int(bool(transpose)), ctypes.byref(out._struct), _ptr(v),
-                                      _dtype_code(v) if v is not None else 0, _row_stride(v) if v is not None else 0,
-                                      _stream(stream))
+        rc = lib().lpd_micro_quantize(_ptr(x), _dtype_code(x), _row_stride(x), rows, cols, int(bool(transpose)),
+                                      out._ref, _ptr(v), v_dtype, v_stride, _stream(stream))
     _check(rc, "lpd_micro_quantize")
 
 
@@ -956,7 +961,7 @@ def lpd_micro_matmul(a, b, out, workspace, stream=None) -> None:
         raise ValueError("the operands and out must be on one device")
     _buffer("workspace", workspace, out.device)
     with _on(out):
-        rc = lib().lpd_micro_matmul(ctypes.byref(a._struct), ctypes.byref(b._struct), m, n, a.k, _ptr(out),
+        rc = lib().lpd_micro_matmul(a._ref, b._ref, m, n, a.k, _ptr(out),
                                     _dtype_code(out), _row_stride(out), _ptr(workspace), _bytes(workspace),
                                     _stream(stream))
     _check(rc, "lpd_micro_matmul")
