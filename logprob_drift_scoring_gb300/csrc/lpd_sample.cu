@@ -1444,12 +1444,12 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
     int round = 0;
     // Adds up a round's bins (in buffer `buf`) over the cluster and finds the first, from the
     // last one down, at which the tokens (or their mass) reach `target`.
-    uint64_t over_mass = 0, over_n = 0;
+    uint64_t over_mass = 0, over_n = 0, own_over = 0;  // own_over: this CTA's part of the mass above, a thread's bins
     const auto descend = [&](int buf, bool by_mass, uint64_t target) -> uint32_t {
         if (t == 0) sc.found_bin = kBins;
         cluster.sync();
         uint32_t cnt = 0, before = 0, largest = 0;
-        uint64_t mass = 0;
+        uint64_t mass = 0, own_bin = 0;
         const int bin = kBins - 1 - t;
         if (t < kBins) {
             for (int r = 0; r < ranks; ++r) {
@@ -1458,7 +1458,9 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
                 if (r < rank) before += c;
                 cnt += c;
                 if (c) {
-                    mass += static_cast<uint64_t>(o->scratch.mass_hi[buf][bin]) << 32 | o->scratch.mass_lo[buf][bin];
+                    const uint64_t m = static_cast<uint64_t>(o->scratch.mass_hi[buf][bin]) << 32 | o->scratch.mass_lo[buf][bin];
+                    if (r == rank) own_bin = m;
+                    mass += m;
                     largest = max(largest, o->scratch.far[buf][bin]);
                 }
             }
@@ -1498,6 +1500,7 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
         }
         __syncthreads();
         ++round;  // (others may still read this round's bins: the next takes the other buffer)
+        if (bin > static_cast<int>(sc.found_bin)) own_over += own_bin;
         return sc.found_bin;
     };
     const auto clear = [&](int buf) {
@@ -1511,7 +1514,7 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
     const float per_bin = __fdiv_rn(kBins - 1.f, fmaxf(top - last_x, FLT_MIN));
     const auto coarse = [&](float x) { return kBins - 1 - static_cast<uint32_t>(fminf(__fmul_rn(__fsub_rn(top, x), per_bin), kBins - 1.f)); };
     const auto select = [&](bool by_mass, uint64_t target, uint32_t lo) -> bool {
-        over_mass = over_n = 0;
+        over_mass = over_n = own_over = 0;
         clear(round & 1);
         {
             const int buf = round & 1;
@@ -1737,10 +1740,7 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
         uint64_t own = own_list_mass + own_rest_mass, none = 0;
         if (!whole) {
             uint32_t c = 0;
-            own = 0;
-            each([&](float x) {
-                if (key_of<kBf16>(x) > border) own += weight(x);
-            });
+            own = own_over;
             block_sums<kThreads>(sc, own, none, c);
             own += own_ties * tie_weight;
         }
@@ -1820,8 +1820,9 @@ cudaError_t launch_typed(const SampleArgs &a, int ranks, cudaStream_t stream) {
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     const size_t smem = static_cast<size_t>(a.chunk_room) * 16 + sizeof(Shared);
-    return a.slice * kElt <= 49152 ? launch_clusters<kBf16, kMask, 256>(a, ranks, smem, stream)
-                                   : launch_clusters<kBf16, kMask, 512>(a, ranks, smem, stream);
+    const bool alone = a.n_rows * ranks <= device_sm_count();
+    return a.slice * kElt <= 49152 && !(alone && a.slice >= 8192) ? launch_clusters<kBf16, kMask, 256>(a, ranks, smem, stream)
+                                                                  : launch_clusters<kBf16, kMask, 512>(a, ranks, smem, stream);
 }
 
 }  // namespace
@@ -1830,7 +1831,10 @@ cudaError_t launch_typed(const SampleArgs &a, int ranks, cudaStream_t stream) {
 // whatever else there is goes to clusters.  Slices of at most 40 KB leave four CTAs a
 // multiprocessor, one loading while others count; rows of fewer than that go to one CTA
 // unless rows are so few that the multiprocessors would stand idle.  Larger slices
-// (float32 rows of a large vocabulary) have twice the threads.
+// (float32 rows of a large vocabulary) have twice the threads, and so have those of 8192
+// tokens and more that have a multiprocessor to themselves (8 rows of 151936 bf16, all kinds
+// of filters: 41 us with 256, 33 with 512; of 37984 under top-k and top-p 19 and 21, of 1024
+// 41 and 43).
 cudaError_t launch_sample(const SampleCall &c, cudaStream_t stream) {
     if (c.n_rows == 0) return cudaSuccess;
     const bool bf16 = c.dtype == LPD_BF16, mask = c.mask != nullptr;
