@@ -1594,7 +1594,7 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
                 return true;
             }
             lo += fb << shift;
-            hi = min(hi, lo + ((1u << shift) - 1));
+            hi = lo + min(hi - lo, (1u << shift) - 1);  // (lo and a bin's width may pass 2^32)
             __syncthreads();
         }
     };

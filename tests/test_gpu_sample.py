@@ -203,6 +203,18 @@ def test_extreme_scales_and_offsets(scale, offset, kind, rows):
     check(tensor(rng.normal(0, 2, (rows, vocab)) + offset, kind), f, rng.uniform(0, 1, rows))
 
 
+@pytest.mark.parametrize("rows", [16, 136])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,spread", [(1.5e-45, 2.0), (3.4e38, 2.0), (1.0, 8e37), (3.4e38, 8e37), (1.5e-45, 8e37)])
+def test_ends_of_the_range(scale, spread, kind, rows):
+    """The smallest and largest scales, and logits whose differences leave float32."""
+    rng = np.random.default_rng(10)
+    vocab = 3001
+    f = params(rng, rows, vocab)
+    f["scale"] = np.full(rows, scale, dtype=np.float32)
+    check(tensor(np.clip(rng.normal(0, spread, (rows, vocab)), -3.3e38, 3.3e38), kind), f, rng.uniform(0, 1, rows))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_values_next_to_zero_and_lowest_masks(kind):
     """Rows whose border, or top, lies within 2^-10 of 0, rows masked with the type's
