@@ -503,7 +503,7 @@ __device__ void finish_list(const SampleArgs &a, int64_t row, const RowFilter &f
 // ------------------------------------------------------------------ many rows, a CTA each
 // Bins of a bf16 row, one for each value of 24 octaves and both signs, in descending
 // order: +2^14 down to +2^-10, what lies between 2^-10 and 0 (a bin of several values),
-// 0 itself, the same below 0, and the finite values under -2^14 (another).
+// 0 itself, the same below 0, and the finite values from -2^14 down (another).
 constexpr int kOctaves = 24, kLowest = 117;             // octaves, and the first one's exponent field
 constexpr int kSide = kOctaves * 128;
 constexpr int kTinyUp = kSide, kZero = kSide + 1, kTinyDown = kSide + 2, kDown = kSide + 3, kLow = 2 * kSide + 3;
@@ -914,12 +914,13 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
     const uint32_t top_key = key_of<true>(top);
     const Weigh weight(f.scale, top, sh.table);
     const float base = base_of<true>(sc, f, top);
-    // (the finite values under -2^14 have to weigh nothing, and a bin of several values lies on one side of min-p)
+    // (the finite values from -2^14 down have to weigh nothing, and a bin of several values lies on one side of min-p:
+    // that one wholly below it, or min-p leaves the lowest of all)
     constexpr float kTiny = 9.765625e-4f;  // 2^-10
     constexpr float kLeast = -3.3895313892515355e38f;  // of bf16's finite values
-    if (sh.bins[kLow] && (weight.ws.wide || weight.ws.cut < -16384.f || (base > kLeast && base < -16384.f))) return false;
+    if (sh.bins[kLow] && (weight.ws.wide || weight.ws.cut < -16384.f || (base > kLeast && base <= -16384.f))) return false;
     if (sh.tiny_n && base > -kTiny && base < kTiny && base != 0.f) return false;
-    const bool low_in = base <= -16384.f, up_in = base <= 0.f, down_in = base <= -kTiny;
+    const bool low_in = base <= kLeast, up_in = base <= 0.f, down_in = base <= -kTiny;
     // ---- numbers and masses of the thread's bins
     uint64_t tiny_up = 0, tiny_down = 0;
     uint32_t none = 0;

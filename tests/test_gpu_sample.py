@@ -406,3 +406,31 @@ def test_filtered_rollout_scored_under_its_own_sets():
         want = -s * p
         want[int(ids[r])] += s
         assert np.all(np.abs(got[r] - want) <= s * (2e-5 * p + 2.0 ** -22)), r
+
+
+@pytest.mark.parametrize("rows", [16, 136])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,log_min_p", [
+    (0.004, -65.81875),  # the bound lies at -16454.7: -16384 is the next bf16 value that it leaves
+    (0.004, -65.536),    # at -16384 itself, or by the logarithm's rounding a little beside it
+    (0.002, -33.0),      # at -16500
+    (0.002, -32.8),      # at -16400
+    (0.004, -66.1),      # at -16525: -16512 is left too
+])
+def test_min_p_next_to_the_lowest_values_that_are_counted(scale, log_min_p, kind, rows):
+    """Bounds at and around -2^14, with tokens on both sides: how many are kept."""
+    rng = np.random.default_rng(17)
+    vocab = 5003
+    x = rng.normal(-3000, 700, (rows, vocab))
+    x[:, ::3] = rng.choice([-16256.0, -16320.0, -16384.0, -16512.0, -16640.0, -20000.0, -3e38], (rows, len(range(0, vocab, 3))))
+    x[:, 7] = 0.0
+    x[1::4] = np.where(x[1::4] <= -16384, -np.inf, x[1::4])  # (and rows without any)
+    x[2::4, ::3] = -20000.0
+    f = dict(scale=np.full(rows, scale, np.float32), min_p=np.full(rows, np.exp(log_min_p), np.float32))
+    u = rng.uniform(0, 1, rows)
+    t = tensor(x, kind)
+    ids, kept = check(t, f, u)
+    xh = host(t)
+    for r in range(rows):  # (every row, none left out)
+        want = ref.row(xh[r], float(f["scale"][r]), float(f["min_p"][r]))[1].sum()
+        assert kept[r] == want, (r, kept[r], want)
