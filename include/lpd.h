@@ -774,8 +774,9 @@ int lpd_micro_quantize(const void *x, int32_t x_dtype, int64_t x_row_stride, int
 size_t lpd_micro_workspace_size(int64_t m, int64_t n, int64_t k);
 
 /* out[m, n] = sum_k A[m, k] B[n, k] over the values that the operands stand for,
- * accumulated in float32 on the tensor cores, times the two tensor scales, rounded
- * once to out_dtype (LPD_BF16 or LPD_F32).  Both operands have one block size (else
+ * accumulated in float32 on the tensor cores without the tensor scales, times those
+ * two (whose product may lie outside float32's range), rounded once to out_dtype
+ * (LPD_BF16 or LPD_F32).  Both operands have one block size (else
  * LPD_ERR_UNSUPPORTED).  Forward product and gradients as for lpd_block_matmul.
  * k = 0 gives zeros.
  * workspace   lpd_micro_workspace_size(m, n, k) bytes, 256-byte aligned; its first

@@ -6,7 +6,7 @@
 // for ablation experiment", LogProb knobs table, rows 9-10: the head GEMM and its
 // rounding as a drift source).  The tensor cores take the block scales themselves
 // (tcgen05.mma kind::mxf4nvf4 and kind::mxf4, block_scale), so a product is a plain
-// chain of MMAs over k into one accumulator; t enters once at the end.
+// chain of MMAs over k into one accumulator; the two t enter once at the end.
 #include <algorithm>
 #include <cfloat>
 #include <cuda.h>
@@ -628,6 +628,29 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t *r) {
         : "r"(taddr));
 }
 
+// The two tensor scales as factors of the sums: f1 alone, their product, where float32 has
+// that among its normal numbers; else f1 is its significand, and f2, f2 and f3 are powers of
+// two, a third of its exponent each.  (Either scale may lie anywhere in float32's range, so
+// their product may leave it where the scaled sums do not.  The three go in one direction:
+// a step overflows only if the result does, and loses bits only where the result is denormal.)
+struct SumScale {
+    float f1, f2, f3;
+    bool one;
+    __device__ __forceinline__ SumScale(const float *ta, const float *tb) : f2(1.f), f3(1.f), one(true) {
+        const float a = ta ? *ta : 1.f, b = tb ? *tb : 1.f;
+        f1 = __fmul_rn(a, b);
+        if (f1 == 0.f ? a == 0.f || b == 0.f : fabsf(f1) >= FLT_MIN && fabsf(f1) <= FLT_MAX) return;
+        if (!(fabsf(a) <= FLT_MAX && fabsf(b) <= FLT_MAX)) return;
+        int ea, eb;
+        f1 = __fmul_rn(frexpf(a, &ea), frexpf(b, &eb));  // in [1/4, 1)
+        const int third = (ea + eb) / 3;
+        f2 = ldexpf(1.f, third);
+        f3 = ldexpf(1.f, ea + eb - 2 * third);
+        one = false;
+    }
+    __device__ __forceinline__ float rest(float x) const { return __fmul_rn(__fmul_rn(__fmul_rn(x, f2), f2), f3); }
+};
+
 struct MmMaps {
     CUtensorMap a, b;
     CUtensorMap sa, sb;  // scales: (word of an atom, atom)
@@ -823,7 +846,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         const int quad = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * kEpiCols;
         char *const mine = staged + (warp - 4) * kOutWarp;
-        const float scale = __fmul_rn(a.ta ? *a.ta : 1.f, a.tb ? *a.tb : 1.f);
+        const SumScale scale(a.ta, a.tb);
         uint32_t turn = 0;
         bool ok = true;
         for (int64_t w = item0; w < items; w += step) {
@@ -847,7 +870,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     else mbar_arrive(&acc_empty);
                 }
 #pragma unroll
-                for (int j = 0; j < kEpiCols; ++j) acc[j] = __fmul_rn(acc[j], scale);
+                for (int j = 0; j < kEpiCols; ++j) acc[j] = __fmul_rn(acc[j], scale.f1);
+                if (!scale.one) {
+#pragma unroll
+                    for (int j = 0; j < kEpiCols; ++j) acc[j] = scale.rest(acc[j]);
+                }
             } else {  // a wait gave up: this tile reads as NaN
 #pragma unroll
                 for (int j = 0; j < kEpiCols; ++j) acc[j] = CUDART_NAN_F;
@@ -932,16 +959,20 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     }
 }
 
-// C = the partial results added in split order, rounded once.
+// C = the partial results added in split order, scaled, rounded once.
 template <bool kOutF32>
 __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t part_stride, int64_t split_stride,
-                                                   int n_splits, int64_t m, int64_t n, char *out, int64_t out_stride) {
+                                                   int n_splits, int64_t m, int64_t n, const float *ta, const float *tb,
+                                                   char *out, int64_t out_stride) {
     const int64_t cells = m * n;
+    const SumScale scale(ta, tb);
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < cells; i += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r = i / n, c = i - r * n;
         const float *p = part + r * part_stride + c;
         float s = p[0];
         for (int k = 1; k < n_splits; ++k) s = __fadd_rn(s, p[k * split_stride]);
+        s = __fmul_rn(s, scale.f1);
+        if (!scale.one) s = scale.rest(s);
         if (kOutF32) *reinterpret_cast<float *>(out + r * out_stride + 4 * c) = s;
         else *reinterpret_cast<__nv_bfloat16 *>(out + r * out_stride + 2 * c) = __float2bfloat16_rn(s);
     }
@@ -1063,8 +1094,9 @@ cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, in
         !make_scale_map(&maps.sb, y.scales, (n + 127) / 128 * y.atoms, y.b16))
         return cudaErrorInvalidValue;
     MmArgs a{};
-    a.ta = x.tensor_scale;
-    a.tb = y.tensor_scale;
+    const bool split = p.n_splits > 1;
+    a.ta = split ? nullptr : x.tensor_scale;  // (partial results are scaled once they are one)
+    a.tb = split ? nullptr : y.tensor_scale;
     a.m = m;
     a.n = n;
     a.k = k;
@@ -1082,7 +1114,6 @@ cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, in
               (static_cast<uint32_t>((pair ? 2 * kTM : kTM) >> 4) << 24);
     a.status = static_cast<uint32_t *>(workspace);
     float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
-    const bool split = p.n_splits > 1;
     a.out = split ? reinterpret_cast<char *>(part) : static_cast<char *>(out);
     a.out_stride = split ? p.part_stride * 4 : out_stride;
     a.split_stride = split ? m * p.part_stride * 4 : 0;
@@ -1100,10 +1131,10 @@ cudaError_t launch_micro_matmul(const MicroOperand &x, const MicroOperand &y, in
     const int64_t blocks = std::min<int64_t>((m * n + 255) / 256, static_cast<int64_t>(device_sm_count()) * 16);
     if (f32)
         join_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
-                                                                          static_cast<char *>(out), out_stride);
+                                                                          x.tensor_scale, y.tensor_scale, static_cast<char *>(out), out_stride);
     else
         join_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(part, p.part_stride, m * p.part_stride, a.n_splits, m, n,
-                                                                           static_cast<char *>(out), out_stride);
+                                                                           x.tensor_scale, y.tensor_scale, static_cast<char *>(out), out_stride);
     return cudaGetLastError();
 }
 

@@ -343,3 +343,35 @@ def test_repeated_streams_and_graph():
             again = B.micro_matmul(B.micro_quantize(x, 32), qw, torch.float32)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(out, again)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("block", [16, 32])
+@pytest.mark.parametrize("m,n,k", [(5, 300, 320), (200, 300, 320), (3, 40, 9000)])  # a tile, a pair, a split k axis
+@pytest.mark.parametrize("ta,tb", [(1e-20, 1e-20), (1e-23, 1e-23), (1e20, 1e-20), (1e20, 1e20), (3e38, 2e-38), (1e-44, 1e30), (3e38, 3e38),
+                                   (1e-45, 1e-45), (0.0, 3e38), (1e-30, 1e-8)])
+def test_tensor_scales_whose_product_leaves_float32(ta, tb, m, n, k, block, kind):
+    """The scaled sums count, not the scales' product: a row of zeros stays zero, and what
+    float32 (or bf16) holds has its digits.  The bound of check_product, whose sums are those
+    without the scales, and a step of float32's denormal numbers for each of two roundings; a
+    result past the type's range may be infinite from half a step (and the sums' error) below."""
+    rng = np.random.default_rng(30)
+    a, va = operand(rng, m, k, block)
+    b, vb = operand(rng, n, k, block)
+    a.codes[1] = 0
+    va[1] = 0.0
+    t = np.float32([ta, tb]).astype(np.float64)
+    a, b = (B.MicroScaled(o.codes, o.scales, k, block, one(s)) for o, s in ((a, ta), (b, tb)))
+    out = B.micro_matmul(a, b, KINDS[kind])
+    torch.cuda.synchronize()
+    got = out.double().cpu().numpy()
+    assert (got[1] == 0).all()
+    sums, size = va @ vb.T, np.abs(va) @ np.abs(vb).T
+    want = sums * (t[0] * t[1])
+    bound = (-(-k // 64) * 2.0 ** -22 + 156 * 2.0 ** -24) * size * (t[0] * t[1]) + (2.0 ** -23 + HALF[kind]) * np.abs(want) + 2 * 2.0 ** -149
+    if kind == "bf16":
+        bound += 2.0 ** -134  # (half a step of bf16's denormal numbers)
+    most = float(torch.finfo(KINDS[kind]).max)
+    inside = np.abs(want) + bound <= most
+    assert (np.abs(got - want)[inside] <= bound[inside]).all()
+    assert np.isinf(got[np.abs(want) - bound > most * (1 + HALF[kind])]).all() and not np.isnan(got).any()
