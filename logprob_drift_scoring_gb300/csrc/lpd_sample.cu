@@ -317,6 +317,10 @@ __device__ __forceinline__ uint64_t share_of(float top_p, uint64_t whole) {
     const double want = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(whole));
     return min(max(static_cast<uint64_t>(want), static_cast<uint64_t>(1)), whole);
 }
+// Whether the draw is the first or the last kept token.  That goes by their number: a kept token
+// may weigh less than half a step and so nothing.
+__device__ __forceinline__ bool at_an_end(float u) { return !(u > 0.f) || u >= 1.f; }
+__device__ __forceinline__ uint64_t end_of(float u, uint64_t kept_n) { return u > 0.f ? kept_n - 1 : 0; }
 // The draw's place in the running mass: the first token that passes it.
 __device__ __forceinline__ uint64_t place_of(float u, uint64_t mass) {
     const uint64_t at = u > 0.f ? static_cast<uint64_t>(static_cast<double>(fminf(u, 1.f)) * static_cast<double>(mass)) : 0;
@@ -444,7 +448,8 @@ __device__ __forceinline__ void answer_list(const SampleArgs &a, int64_t row, co
             *p = id_of[i];
             return is_kept(far_of[i], id_of[i]);
         };
-        const uint32_t id = pick<kThreads>(sh, w_of, total, at_kept, 0, a.vocab - 1, true, place_of(u, kept_mass) + 1).at;
+        const bool end = at_an_end(u);
+        const uint32_t id = pick<kThreads>(sh, w_of, total, at_kept, 0, a.vocab - 1, !end, (end ? end_of(u, kept_n) : place_of(u, kept_mass)) + 1).at;
         for (uint32_t i = t; i < total; i += kThreads)
             if (id_of[i] == id) {
                 const float x = value_of<kBf16>(top_key - far_of[i]);
@@ -1073,13 +1078,14 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
         mask_of_row<true>(a, row, f, c, weight, is_kept, set_n, set_mass);
     } else {
         // (a weight looked up: 10 operations a token, formed anew it takes 30)
+        const float u = a.uniform[row];
+        const bool end = at_an_end(u);
         for (int b = t; b < kValues; b += kThreads) {
             const float x = bin_value(b);
-            sh.value_w[b] = b != kTinyUp && b != kTinyDown && b != kLow && x >= border_x && x <= top ? weight(x) : 0;
+            sh.value_w[b] = b != kTinyUp && b != kTinyDown && b != kLow && x >= border_x && x <= top ? end ? 1 : weight(x) : 0;
         }
         __syncthreads();
-        const float u = a.uniform[row];
-        const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? weight(x) : 0; };
+        const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? end ? 1 : weight(x) : 0; };
         const uint32_t border_bits = __float_as_uint(border_x) >> 16;
         const auto of_chunk = [&](const uint4 &c4, int i) -> uint64_t {
             const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
@@ -1100,7 +1106,7 @@ __device__ bool counted_row(const SampleArgs &a, int64_t row, const RowFilter &f
             }
             return s;
         };
-        const int e = find_in_row<true>(c, sh, of_chunk, mass_of, place_of(u, set_mass));
+        const int e = find_in_row<true>(c, sh, of_chunk, mass_of, end ? end_of(u, set_n) : place_of(u, set_mass));
         draw_of_row<true>(a, row, f, c, weight, e, u, set_n, set_mass);
     }
     return true;
@@ -1151,7 +1157,8 @@ __device__ void plain_row(const SampleArgs &a, int64_t row, const RowFilter &f, 
         mask_of_row<kBf16>(a, row, f, c, weight, is_kept, set_n, set_mass);
     } else {
         const float u = a.uniform[row];
-        const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? weight(x) : 0; };
+        const bool end = at_an_end(u);
+        const auto mass_of = [&](int i, float x) -> uint64_t { return is_kept(i, x) ? end ? 1 : weight(x) : 0; };
         const auto of_chunk = [&](const uint4 &c4, int i) -> uint64_t {
             uint64_t s = 0;
             if (!(chunk_max<kBf16>(c4) >= base)) return s;
@@ -1161,7 +1168,7 @@ __device__ void plain_row(const SampleArgs &a, int64_t row, const RowFilter &f, 
             for (int q = 0; q < kPer; ++q) s += mass_of(i * kPer + q, v[q]);
             return s;
         };
-        const int e = find_in_row<kBf16>(c, sh, of_chunk, mass_of, place_of(u, set_mass), true);
+        const int e = find_in_row<kBf16>(c, sh, of_chunk, mass_of, end ? end_of(u, set_n) : place_of(u, set_mass), !end);
         draw_of_row<kBf16>(a, row, f, c, weight, e, u, set_n, set_mass);
     }
 }
@@ -1745,15 +1752,27 @@ __device__ void cluster_row(const SampleArgs &a, int64_t row, const RowFilter &f
             block_sums<kThreads>(sc, own, none, c);
             own += own_ties * tie_weight;
         }
+        const float u = a.uniform[row];
+        const bool end = at_an_end(u);
+        if (end) {
+            uint32_t c = 0;
+            own = none = 0;
+            each_chunk([&](const uint4 &c4, int i) {
+                float v[kPer];
+                unpack<kBf16>(c4, v);
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) own += is_kept(i * kPer + q, v[q]);
+            });
+            block_sums<kThreads>(sc, own, none, c);
+        }
         if (t == 0) sh.kept_mass = own;
         cluster.sync();
-        const float u = a.uniform[row];
-        const uint64_t target = place_of(u, kept_mass);
+        const uint64_t target = end ? end_of(u, kept_n) : place_of(u, kept_mass);
         uint64_t in_front = 0;
         for (int r = 0; r < rank; ++r) in_front += peer_of(r)->kept_mass;
         cluster.barrier_arrive();
         if (target >= in_front && target - in_front < own) {
-            const int e = find([&](int e, float x) -> uint64_t { return is_kept(e, x) ? weight(x) : 0; }, target - in_front);
+            const int e = find([&](int e, float x) -> uint64_t { return is_kept(e, x) ? end ? 1 : weight(x) : 0; }, target - in_front);
             if (t == 0 && e < 0) no_answer<false>(a, row, CUDART_NAN_F);  // (the logits changed under the call)
             if (t == 0 && e >= 0) {
                 const float x = value_at(e);

@@ -434,3 +434,31 @@ def test_min_p_next_to_the_lowest_values_that_are_counted(scale, log_min_p, kind
     for r in range(rows):  # (every row, none left out)
         want = ref.row(xh[r], float(f["scale"][r]), float(f["min_p"][r]))[1].sum()
         assert kept[r] == want, (r, kept[r], want)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [40, 5003, 60013])
+@pytest.mark.parametrize("form", ["none", "top-k", "min-p", "all", "nucleus"])
+def test_uniforms_at_the_ends_of_sets_with_unlikely_tokens(form, vocab, kind, rows):
+    """0 and less draw the first kept token and 1 and more the last, however little they weigh."""
+    rng = np.random.default_rng(19)
+    x = rng.normal(0, 0.3, (rows, vocab))
+    x[:, :3], x[:, -2:] = -np.inf, -np.inf
+    x[:, 3], x[:, 4], x[:, -3], x[:, -4] = -70.0, -50.0, -60.0, -34.0
+    x[::2, 3], x[::2, -3] = -40.0, -33.0
+    f = dict(none={}, **{"top-k": dict(top_k=np.full(rows, min(vocab - 6, 400), np.int32)),
+                         "min-p": dict(min_p=np.full(rows, 1e-25, np.float32)),
+                         "all": dict(min_p=np.full(rows, 1e-30, np.float32), top_k=np.full(rows, vocab - 7, np.int32)),
+                         "nucleus": dict(top_p=np.full(rows, 0.99, np.float32))})[form]
+    u = np.array([0.0, -1.0, 1.0, 2.0, -0.0, np.inf], dtype=np.float32)[np.arange(rows) % 6]
+    t = tensor(x, kind)
+    ids, logp, kept = (v.cpu().numpy() for v in B.sample(t, torch.from_numpy(u).to(DEV), to_filter(f) if f else None))
+    xh = host(t)
+    for r in range(rows):
+        z, k, margin = ref.row(xh[r], **{name: v[r].item() for name, v in f.items()})
+        assert margin >= NEAR and kept[r] == k.sum(), r
+        want = np.nonzero(k)[0][0 if u[r] <= 0 else -1]
+        assert ids[r] == want, (r, u[r], ids[r], want)
+        lp = z[want] - ref.lse(z, k)
+        assert abs(logp[r] - lp) <= 2.0 ** -24 * abs(lp) + 2.0 ** -28 + 2.0 ** -52 * 70, (r, logp[r], lp)
