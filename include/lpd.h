@@ -611,9 +611,11 @@ int lpd_logprob_backward_controlled(const lpd_logits *logits, const lpd_controls
  *     top-p   of these, in descending order, the shortest prefix whose softmax mass
  *             (of these) is at least top_p[r]; at least one token
  * Equal logits (+0 and -0 are equal) are ordered by token, the lowest first.  A
- * token whose logit is -inf is never kept.  The filters are decided on sums that
- * are exact to about 2^-29 of each weight (2^-41 for the heaviest), so a set is the
- * mathematical one unless a border lies nearer to a sum than that.
+ * token whose logit is -inf is never kept.  The filters and the draw are decided on
+ * sums of weights exp(z - max z), each exact to about 2^-29 of itself (2^-41 for the
+ * heaviest) and cut to a whole number of steps of 2^-45: a sum is off by at most
+ * 2^-29 of itself and vocab 2^-45, and a set or a token is the mathematical one unless
+ * its border lies nearer to a sum than that.
  * A NULL array leaves its step out; so does min_p <= 0, top_k <= 0 or >= vocab, and
  * top_p >= 1.  (min_p >= 1 keeps the largest logits, top_p <= 0 and top_k = 1 the
  * first of them.)  The arrays are device float / int32 [n_rows]; the struct is a

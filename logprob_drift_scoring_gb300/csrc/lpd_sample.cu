@@ -318,7 +318,7 @@ __device__ __forceinline__ uint64_t share_of(float top_p, uint64_t whole) {
     return min(max(static_cast<uint64_t>(want), static_cast<uint64_t>(1)), whole);
 }
 // Whether the draw is the first or the last kept token.  That goes by their number: a kept token
-// may weigh less than half a step and so nothing.
+// may weigh less than a step and so nothing.
 __device__ __forceinline__ bool at_an_end(float u) { return !(u > 0.f) || u >= 1.f; }
 __device__ __forceinline__ uint64_t end_of(float u, uint64_t kept_n) { return u > 0.f ? kept_n - 1 : 0; }
 // The draw's place in the running mass: the first token that passes it.

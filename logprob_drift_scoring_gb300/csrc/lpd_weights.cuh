@@ -1,4 +1,4 @@
-// Softmax weights as whole numbers: exp(scale (x - top)) in steps of 2^-44.
+// Softmax weights as whole numbers: exp(scale (x - top)) in steps of 2^-45.
 //
 // A filter's border (the smallest prefix whose mass reaches top_p) and a draw
 // (the first token whose running mass passes u W) compare sums that may lie
@@ -8,7 +8,11 @@
 // (weight_rough) and for the row's heaviest tokens to 2^-41 (weight_precise):
 // the errors of many small weights average out, those of a few large ones would
 // not.  (A plain exponential in float32 is off by 2^-22 with the rounding of its
-// argument: it moves the border of a nucleus by a token in one row of a thousand.)
+// argument: it moves the border of a nucleus by a token in one row of a thousand.)  What a
+// weight has below a step is cut off: V light tokens take at most V 2^-45 of the top's weight
+// from a sum, 2^-27.8 for 151936 of them.  (Rounded to the nearest step they are off by half of
+// it, and float32 nuclei take 5 to 7 % longer; more bits have no room, 393216 weights of the
+// top's size being 2^63.6.)
 //
 // x scale log2(e) is cut in units of 1/256 octave, x c = J + a with whole J and
 // |a| <= 1/2; 2^(J / 256) comes from a table and shifts, 2^(a / 256) - 1 from
@@ -28,7 +32,7 @@
 
 namespace lpd {
 
-constexpr int kWeightOne = 44;          // weights are multiples of 2^-44 of the top's (about)
+constexpr int kWeightOne = 45;          // weights are multiples of 2^-45 of the top's (about)
 constexpr int kUnits = 256;             // steps an octave
 constexpr float kMagic = 12582912.f;    // 1.5 * 2^23: adding it rounds to a whole number
 constexpr uint32_t kMagicBits = 0x4b400000u;
@@ -112,12 +116,12 @@ __host__ __device__ __forceinline__ uint64_t weight_rough(float x, const WeightS
     return (static_cast<uint64_t>(m) << (kWeightOne - 30)) >> (s & 63);
 }
 
-// 2^44 times a float below 2^19 in magnitude, rounded to a whole number.
+// 2^45 times a float below 2^18 in magnitude, rounded to a whole number.
 __host__ __device__ __forceinline__ int64_t steps_of(float x) {
 #ifdef __CUDA_ARCH__
-    return __float2ll_rn(x * 17592186044416.f);
+    return __float2ll_rn(x * static_cast<float>(uint64_t{1} << kWeightOne));
 #else
-    return static_cast<int64_t>(std::nearbyint(static_cast<double>(x) * 17592186044416.0));
+    return static_cast<int64_t>(std::nearbyint(static_cast<double>(x) * static_cast<double>(uint64_t{1} << kWeightOne)));
 #endif
 }
 

@@ -462,3 +462,22 @@ def test_uniforms_at_the_ends_of_sets_with_unlikely_tokens(form, vocab, kind, ro
         assert ids[r] == want, (r, u[r], ids[r], want)
         lp = z[want] - ref.lse(z, k)
         assert abs(logp[r] - lp) <= 2.0 ** -24 * abs(lp) + 2.0 ** -28 + 2.0 ** -52 * 70, (r, logp[r], lp)
+
+
+@pytest.mark.parametrize("rows", [2, 136])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("tail", [-27.75, -29.875, -30.625, -31.0, -31.25])
+def test_flat_tails_far_below_a_dominant_token(tail, kind, rows):
+    """What many light tokens weigh together: a step of 2^-45 each, 2^-29 of their sum, and
+    the result's rounding."""
+    vocab = 151936
+    x = torch.full((rows, vocab), tail, device=DEV).to(KINDS[kind])
+    x[:, 5] = 0.0
+    others = (vocab - 1) * np.exp(tail)
+    ids, logp, kept = B.sample(x, torch.full((rows,), 0.5, device=DEV))
+    mask, lse, mkept = B.filter_mask(x, None)
+    assert bool((ids == 5).all()) and bool((kept == vocab).all()) and bool((mkept == vocab).all())
+    bound = vocab * 2.0 ** -45 + 2.0 ** -29 * others
+    for got, want in ((logp, -np.log1p(others)), (lse, np.log1p(others))):
+        err = np.abs(got.cpu().numpy().astype(np.float64) - want)
+        assert (err <= bound + 2.0 ** -24 * abs(want)).all(), (err.max(), bound)

@@ -164,3 +164,47 @@ int main() {
     subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", f"-I{csrc}", "-o", str(tmp_path / "w"),
                     str(tmp_path / "w.cpp")], check=True)
     assert subprocess.run([str(tmp_path / "w")], check=True, capture_output=True, text=True).stdout.strip() == "0"
+
+
+def test_light_weights_lose_less_than_2_45_of_the_top(tmp_path):
+    """Weights of the lowest 16 octaves against long double: a step of 2^-45 of the top's
+    beside the errors of a rough and of a precise weight (the bounds above).  The steps are
+    taken in the units of the weights' origin, 2^(1 / 512) off the top at most."""
+    if not shutil.which("g++"):
+        pytest.skip("g++ not found")
+    (tmp_path / "w.cpp").write_text(r'''
+#include "lpd_weights.cuh"
+#include <cstdio>
+#include <random>
+using namespace lpd;
+int main() {
+    WeightEntry rough[kUnits];
+    uint64_t precise[kUnits];
+    for (int i = 0; i < kUnits; ++i) {
+        const long double v = exp2l((long double)i / kUnits);
+        rough[i].whole = (uint32_t)llroundl(v * 1073741824.0L);
+        rough[i].part = (float)(v * 1073741824.0L);
+        precise[i] = (uint64_t)llroundl(v * 4611686018427387904.0L);
+    }
+    std::mt19937_64 g(1);
+    std::uniform_real_distribution<double> u(0, 1);
+    int bad = 0;
+    for (float scale : {0.01f, 0.7f, 1.f, 30.f})
+        for (float top : {13.5f, -3.1f, 0.f}) {
+            const WeightScale w = weight_scale(scale, top);
+            for (int k = 0; k < 200000; ++k) {
+                const float x = (float)(top - (19.5 + u(g) * 12.5) / scale);
+                const long double want = exp2l(((long double)x * w.c - w.origin) / kUnits);
+                const long double p = ldexpl(weight_precise(x, w, top, precise), -kWeightOne) - want;
+                const long double r = (x > w.cut ? ldexpl(weight_rough(x, w, rough), -kWeightOne) : 0) - want;
+                const long double most = want * ldexpl(1, -29) + ldexpl(1.01L, -45);
+                if (fabsl(p) > most || fabsl(r) > most) ++bad;
+            }
+        }
+    printf("%d\n", bad);
+}
+''')
+    csrc = ROOT / "logprob_drift_scoring_gb300" / "csrc"
+    subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", f"-I{csrc}", "-o", str(tmp_path / "w"),
+                    str(tmp_path / "w.cpp")], check=True)
+    assert subprocess.run([str(tmp_path / "w")], check=True, capture_output=True, text=True).stdout.strip() == "0"
