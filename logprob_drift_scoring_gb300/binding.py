@@ -8,6 +8,8 @@ built), importing the binding fails.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 from dataclasses import dataclass
 
 from . import _build
@@ -265,6 +267,30 @@ def _stream(stream) -> int | None:
     return getattr(stream, "cuda_stream", stream)
 
 
+def _with_its_stream(form):
+    """A form that allocates: on a stream of the caller's, what it allocates belongs to that
+    stream, and what it reads back is read there.  (Memory of torch's current stream may still be
+    in use there, and is given out again there as soon as the form lets go of it.)"""
+    at = list(inspect.signature(form).parameters).index("stream")
+
+    @functools.wraps(form)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return form(*args, **kwargs)
+        import torch
+
+        if not isinstance(stream, torch.cuda.Stream):  # a handle
+            first = args[0] if args else next(iter(kwargs.values()))
+            first = first[0] if isinstance(first, (list, tuple)) else first
+            tensors = [t for t in (first, getattr(first, "codes", None), getattr(first, "values", None)) if isinstance(t, torch.Tensor)]
+            stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
+        with torch.cuda.stream(stream):
+            return form(*args, **kwargs)
+
+    return call
+
+
 def _row_stride(t) -> int:
     """Elements between the rows of a 2-D tensor.  A single row's stride has no
     meaning in torch, so where it is too small its width serves; rows that overlap
@@ -421,6 +447,7 @@ def lpd_drift_metrics_from_dlogp(dlogp, action_mask, clip_lo, clip_hi, out_metri
     _check(rc, "lpd_drift_metrics_from_dlogp")
 
 
+@_with_its_stream
 def drift_metrics_from_dlogp(dlogp, action_mask, clip=(0.8, 1.2), stream=None) -> dict:
     """The metrics record of given per-token dlogp (float32, device) over the active rows."""
     import torch
@@ -975,6 +1002,7 @@ def read_merge_drift(buf) -> dict:
     return LpdMergeDrift.from_buffer_copy(host).as_dict()
 
 
+@_with_its_stream
 def attn_merge(out_parts, lse_parts, order=None, lse_base2=False, stream=None):
     """Merged (out [n, d] f32, lse [n] f32) of K partials, allocated with torch."""
     import torch
@@ -986,6 +1014,7 @@ def attn_merge(out_parts, lse_parts, order=None, lse_base2=False, stream=None):
     return out, lse
 
 
+@_with_its_stream
 def attn_merge_order_drift(out_parts, lse_parts, order_a=None, order_b=None, lse_base2=False, stream=None):
     """(out, lse, row_dout, row_dlse, summary dict) of the order_a vs order_b merge."""
     import torch
@@ -1007,6 +1036,7 @@ def read_logp_drift(buf) -> dict:
     return LpdLogpDrift.from_buffer_copy(host).as_dict()
 
 
+@_with_its_stream
 def logp_drift_summary(logp_train_a, logp_rollout_a, logp_train_b, logp_rollout_b, action_mask, stream=None) -> dict:
     """lpd_logp_drift_summary with a torch-allocated record, read back as a dict."""
     import torch
@@ -1038,6 +1068,7 @@ def read_metrics(buf) -> dict:
     return LpdMetrics.from_buffer_copy(host).as_dict()
 
 
+@_with_its_stream
 def score_fused(hidden_train, hidden_rollout, W, token_ids, action_mask, clip=(0.8, 1.2), stream=None,
                 train_ops=None, rollout_ops=None):
     """Allocate outputs and workspace with torch, run lpd_score_fused (or
@@ -1066,6 +1097,7 @@ class ScoreResult:
     metrics: dict
 
 
+@_with_its_stream
 def score(train, rollout, token_ids, action_mask, clip=(0.8, 1.2), stream=None, train_ops=None,
           rollout_ops=None) -> ScoreResult:
     """Allocate outputs and workspace with torch on the logits' device, run
@@ -1086,6 +1118,7 @@ def score(train, rollout, token_ids, action_mask, clip=(0.8, 1.2), stream=None, 
     return ScoreResult(outs[0], outs[1], outs[2], read_metrics(met))
 
 
+@_with_its_stream
 def score_sharded_topology(train_shards, rollout_shards, v_ranges, token_ids, action_mask, topology,
                            reduce_order=None, clip=(0.8, 1.2), stream=None) -> ScoreResult:
     """lpd_score_sharded_topology with torch-allocated outputs and workspace."""
@@ -1104,6 +1137,7 @@ def score_sharded_topology(train_shards, rollout_shards, v_ranges, token_ids, ac
     return ScoreResult(*outs, read_metrics(met))
 
 
+@_with_its_stream
 def controls_apply(logits, controls, out_dtype=None, stream=None):
     """The controlled logits in a new tensor (the logits' type unless given)."""
     import torch
@@ -1113,6 +1147,7 @@ def controls_apply(logits, controls, out_dtype=None, stream=None):
     return out
 
 
+@_with_its_stream
 def score_controlled(train, rollout, token_ids, action_mask, train_controls=None, rollout_controls=None,
                      clip=(0.8, 1.2), stream=None) -> ScoreResult:
     """lpd_score_controlled with torch-allocated outputs and workspace."""
@@ -1128,6 +1163,7 @@ def score_controlled(train, rollout, token_ids, action_mask, train_controls=None
     return ScoreResult(*outs, read_metrics(met))
 
 
+@_with_its_stream
 def sample(logits, uniform, filter=None, stream=None):
     """(ids int32, logprobs float32, kept int32) of a draw from each row, in new tensors."""
     import torch
@@ -1139,6 +1175,7 @@ def sample(logits, uniform, filter=None, stream=None):
     return ids, logp, kept
 
 
+@_with_its_stream
 def filter_mask(logits, filter, token_ids=None, action_mask=None, stream=None):
     """(mask int32 [rows, words], lse float32, kept int32) of the rows' kept sets, in new tensors."""
     import torch
@@ -1151,6 +1188,7 @@ def filter_mask(logits, filter, token_ids=None, action_mask=None, stream=None):
     return mask, lse, kept
 
 
+@_with_its_stream
 def block_quantize(x, dtype=None, block=False, transpose=False, pow2=False, stream=None) -> BlockScaled:
     """x as a new 8-bit operand (e4m3 unless given)."""
     import torch
@@ -1161,6 +1199,7 @@ def block_quantize(x, dtype=None, block=False, transpose=False, pow2=False, stre
     return out
 
 
+@_with_its_stream
 def block_matmul(a, b, out_dtype=None, stream=None):
     """The product of two operands in a new tensor (bf16 unless given)."""
     import torch
@@ -1173,6 +1212,7 @@ def block_matmul(a, b, out_dtype=None, stream=None):
     return out
 
 
+@_with_its_stream
 def micro_quantize(x, block=16, tensor_scale=None, transpose=False, stream=None) -> MicroScaled:
     """x as a new 4-bit operand."""
     rows, k = tuple(x.shape)[::-1] if transpose else tuple(x.shape)
@@ -1181,6 +1221,7 @@ def micro_quantize(x, block=16, tensor_scale=None, transpose=False, stream=None)
     return out
 
 
+@_with_its_stream
 def micro_matmul(a, b, out_dtype=None, stream=None):
     """The product of two 4-bit operands in a new tensor (bf16 unless given)."""
     import torch
