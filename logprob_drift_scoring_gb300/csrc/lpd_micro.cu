@@ -9,6 +9,7 @@
 // chain of MMAs over k into one accumulator; the two t enter once at the end.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
@@ -549,11 +550,28 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
     else
         umma_commit(bar);
 }
-// At a cluster address, after reads of tensor memory that have completed.  (A release would
-// also wait for the stores under way, half a microsecond a tile: 684 us instead of 632.)
+// The accumulator's hand-over, from an epilogue warp to the leader's MMAs.  It orders reads of
+// tensor memory and nothing else, for which PTX asks no more of a barrier than to be observed:
+// tcgen05.ld, wait::ld, fence::before_thread_sync and a relaxed arrival on this side, the wait
+// and fence::after_thread_sync before the MMA on the other.  (A release would also wait for the
+// stores under way, half a microsecond a tile: 684 us instead of 632.)
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// A pair's waits are at the cluster's scope: what they wait for may be the other CTA's.
+struct ClusterScope {
+    static __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+    }
+};
 __device__ __forceinline__ void pair_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -702,6 +720,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     const int64_t items = static_cast<int64_t>(a.n_tm) * a.n_tn * a.n_splits;
     constexpr int kAtomsPer = kB16 ? 4 : 2;  // atoms of scales along a stage's k
     constexpr int kCtas = kPair ? 2 : 1;
+    using Scope = std::conditional_t<kPair, ClusterScope, CtaScope>;
     const int rank = kPair ? blockIdx.x & 1 : 0;
     const int64_t item0 = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
@@ -748,7 +767,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 const int ga = min(tm, a.groups_m - 1), gb = 2 * tn, gb1 = min(gb + 1, a.groups_n - 1);
 #pragma unroll 1
                 for (int kb = split * a.kb_per_split; kb < kb1; ++kb) {
-                    ok = wait_warp(&empty[s], phase, &abort_flag, a.status);
+                    ok = wait_warp<Scope>(&empty[s], phase, &abort_flag, a.status);
                     if (!ok) break;
                     if (leader) {
                         char *st = smem + s * R::kStage;
@@ -778,7 +797,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
                 --s;
                 // (a pair's barriers are the leader's; the other CTA waits for it at the end)
-                if (rank == 0) wait_warp(&full[s], phase ^ 1, &abort_flag, a.status, false);
+                if (rank == 0) wait_warp<Scope>(&full[s], phase ^ 1, &abort_flag, a.status, false);
             }
         } else if (warp == 1 && rank == 0) {
             // ----------------------------------------------------------------- MMA
@@ -791,11 +810,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 item_coords(w, a, tm, tn, split);
                 tm = tm * kCtas + rank;
                 const int kb0 = split * a.kb_per_split, kb1 = min(a.kb_total, kb0 + a.kb_per_split);
-                ok = wait_warp(&acc_empty, turn, &abort_flag, a.status);
+                ok = wait_warp<Scope>(&acc_empty, turn, &abort_flag, a.status);
                 turn ^= 1;
 #pragma unroll 1
                 for (int kb = kb0; ok && kb < kb1; ++kb) {
-                    ok = wait_warp(&full[s], phase, &abort_flag, a.status);
+                    ok = wait_warp<Scope>(&full[s], phase, &abort_flag, a.status);
                     if (!ok) break;
                     tc_fence_after();
                     if (leader) {
@@ -836,7 +855,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     if constexpr (kPair) asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&done)) : "memory");
                     else umma_commit(&done);
                 }
-                wait_warp(&done, 0, &abort_flag, a.status, false);
+                wait_warp<Scope>(&done, 0, &abort_flag, a.status, false);
             }
             __syncwarp();
         }
@@ -855,7 +874,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             tm = tm * kCtas + rank;
             const int64_t col0 = static_cast<int64_t>(tn) * kTN + part * kEpiCols;
             float acc[kEpiCols];
-            ok = ok && wait_warp(&acc_full, turn, &abort_flag, a.status);
+            ok = ok && wait_warp<Scope>(&acc_full, turn, &abort_flag, a.status);
             turn ^= 1;
             if (ok) {
                 tc_fence_after();

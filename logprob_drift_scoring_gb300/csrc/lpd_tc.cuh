@@ -48,13 +48,17 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 // goes its own way); when it gives up it raises the CTA's abort flag and sets
 // LPD_STATUS_TIMEOUT in the workspace's first word.  The clock is read only
 // once a wait has been polled for long: a read costs more than a block's MMAs.
+struct CtaScope {
+    static __device__ __forceinline__ bool try_wait(uint64_t *bar, uint32_t parity) { return mbar_try_wait(bar, parity); }
+};
+template <class Scope = CtaScope>
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint32_t *status,
                                           bool honour_abort = true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, Scope::try_wait(bar, parity))) return true;
     unsigned long long t0 = 0;
 #pragma unroll 1
     for (uint32_t n = 1; n < kWaitLimitIters; ++n) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__all_sync(0xffffffffu, Scope::try_wait(bar, parity))) return true;
         if ((n & 255u) == 0) {
             const unsigned long long now = globaltimer_ns();
             if (t0 == 0) t0 = now;
