@@ -262,8 +262,10 @@ def _stream(stream) -> int | None:
     if stream is None:
         import torch
 
-        # (the handle alone: making a Stream object of it takes 3 us, a fifth of a small call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        # (The handle alone, where this torch gives it: making a Stream object of it takes 3 us, a
+        # fifth of a small call.  The name is not a public one.)
+        handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return handle(torch.cuda.current_device()) if handle else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 

@@ -459,3 +459,18 @@ def test_header_is_plain_c_and_links(tmp_path):
     name, msg, size = out.stdout.strip().split("|")
     assert name == "selected_logprob_drift" and msg == B.lib().lpd_strerror(B.LPD_ERR_BAD_STRIDE).decode()
     assert int(size) == ctypes.sizeof(B.LpdMetrics)
+
+
+def test_stream_of_a_torch_without_the_short_way(monkeypatch):
+    """The current stream's handle comes from the public call where the private one is missing."""
+    import types
+
+    import torch
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=0x1234))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x5000 + device, raising=False)
+    assert B._stream(None) == 0x5003
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    assert B._stream(None) == 0x1234
+    assert B._stream(7) == 7 and B._stream(types.SimpleNamespace(cuda_stream=9)) == 9
