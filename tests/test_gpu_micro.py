@@ -375,3 +375,25 @@ def test_tensor_scales_whose_product_leaves_float32(ta, tb, m, n, k, block, kind
     inside = np.abs(want) + bound <= most
     assert (np.abs(got - want)[inside] <= bound[inside]).all()
     assert np.isinf(got[np.abs(want) - bound > most * (1 + HALF[kind])]).all() and not np.isnan(got).any()
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_every_scale_byte(block):
+    """Each scale that a byte can say, on one value: the denormal e4m3 scales and the powers of
+    two down to 2^-127 among them, against a partner that keeps the product in float32's range."""
+    bytes_ = np.arange(1, 0x7F) if block == 16 else np.arange(0, 255)
+    m, n = len(bytes_), 8
+    codes = np.zeros((m, block), dtype=np.uint8)
+    codes[:, 3] = 1 + np.arange(m) % 7
+    scales = bytes_.astype(np.uint8)[:, None]
+    for other in ((0x38,) if block == 16 else (127, 200, 60)):
+        vb = np.zeros((n, block), dtype=np.uint8)
+        vb[:, 3] = np.arange(n)
+        sb = np.full((n, 1), other, dtype=np.uint8)
+        a, b = (B.MicroScaled(torch.from_numpy(np.pad(ref.packed(c), ((0, 0), (0, 16 - block // 2)))).to(DEV), torch.from_numpy(ref.tiled(s)).to(DEV), block, block)
+                for c, s in ((codes, scales), (vb, sb)))
+        out = B.micro_matmul(a, b, torch.float32).cpu().numpy()
+        with np.errstate(over="ignore"):
+            want = (ref.stands_for(codes, scales, block) @ ref.stands_for(vb, sb, block).T)
+        fits = (np.abs(want) >= 2.0 ** -126) & (np.abs(want) < 2.0 ** 127) | (want == 0)
+        assert np.array_equal(out[fits], want[fits].astype(np.float32))

@@ -481,3 +481,65 @@ def test_flat_tails_far_below_a_dominant_token(tail, kind, rows):
     for got, want in ((logp, -np.log1p(others)), (lse, np.log1p(others))):
         err = np.abs(got.cpu().numpy().astype(np.float64) - want)
         assert (err <= bound + 2.0 ** -24 * abs(want)).all(), (err.max(), bound)
+
+
+def settled(rng, x, scale, min_p, top_k, nucleus):
+    """(top_p, u) of a row whose borders lie in the middle of tokens that weigh 2^-21 of the whole
+    and more: no sum's error (2^-29 and vocab 2^-45 of it) and no rounding of top_p or u to
+    float32 (2^-25) reaches a neighbour."""
+    top_p = 1.0
+    if nucleus:
+        z, kept, _ = ref.row(x, scale, min_p, top_k)
+        order = np.argsort(-x, kind="stable")
+        order = order[kept[order]]
+        mass = np.exp(z[order] - z[order[0]])
+        upto = np.cumsum(mass)
+        i = int(np.searchsorted(upto, rng.uniform(0.3, 0.95) * upto[-1]))
+        while mass[i] < 2.0 ** -21 * upto[-1]:
+            i -= 1
+        top_p = np.float32((upto[i] - mass[i] / 2) / upto[-1])
+    z, kept, _ = ref.row(x, scale, min_p, top_k, float(top_p))
+    mass = np.where(kept, np.exp(np.where(kept, z, -np.inf) - z[kept].max()), 0.0)
+    upto = np.cumsum(mass)
+    j = rng.choice(np.nonzero(mass >= 2.0 ** -21 * upto[-1])[0])
+    return top_p, np.float32((upto[j] - mass[j] / 2) / upto[-1])
+
+
+@pytest.mark.parametrize("copies", [1, 8])
+@pytest.mark.parametrize("kind,vocab", [("bf16", B.LPD_SAMPLE_MAX_VOCAB), ("f32", B.LPD_SAMPLE_MAX_VOCAB), ("f32", 262147)])
+def test_largest_vocabularies_at_few_and_many_rows(kind, vocab, copies):
+    """Peaked, flat, constant rows and rows next to zero under every kind of filter, none left
+    out of the comparison; few rows go to clusters, many to a CTA each and what that leaves to
+    clusters.  (A constant row's masses add up to the most that there is.)"""
+    rng = np.random.default_rng(23)
+    n = 17
+    x = logits(rng, n, vocab)
+    x[1::4] = rng.normal(0, 0.7, x[1::4].shape)
+    x[2::4] = 1.5
+    x[3::4] = rng.normal(0, 0.02, x[3::4].shape)
+    x = np.where(x > 12.0, 12.0 + rng.uniform(0, 1, x.shape), x)
+    t = tensor(x, kind)
+    xh = host(t)
+    scale = rng.uniform(0.5, 1.5, n).astype(np.float32)
+    form = np.arange(n) % 5  # 0: none, 1: top-p, 2: a large top-k, 3: a small one and top-p, 4: min-p and top-p
+    top_k = np.where(form == 2, rng.integers(3000, vocab // 2, n), np.where(form == 3, rng.integers(20, 400, n), 0)).astype(np.int32)
+    min_p = np.where(form == 4, rng.uniform(0.005, 0.2, n), 0).astype(np.float32)
+    pairs = [settled(rng, xh[r], float(scale[r]), float(min_p[r]), int(top_k[r]), form[r] in (1, 3, 4)) for r in range(n)]
+    f = dict(scale=scale, min_p=min_p, top_k=top_k, top_p=np.array([p for p, _ in pairs], np.float32))
+    u = np.array([v for _, v in pairs], np.float32)
+    many = to_filter({k: np.tile(v, copies) for k, v in f.items()})
+    t = t.repeat(copies, 1)
+    ids, logp, kept = (v.cpu().numpy() for v in B.sample(t, torch.from_numpy(np.tile(u, copies)).to(DEV), many))
+    mask, lse, mkept = B.filter_mask(t, many)
+    for r in range(n):
+        z, k, margin = ref.row(xh[r], **{name: v[r].item() for name, v in f.items()})
+        j, lp, near = ref.draw(z, k, float(u[r]))
+        assert margin >= 2.0 ** -23 and near >= 2.0 ** -23, r
+        words = torch.from_numpy(np.packbits(np.pad(k, (0, -vocab % 32)), bitorder="little").view(np.int32)).to(DEV)
+        sums = 2.0 ** -29 + vocab * 2.0 ** -45
+        want_lse = ref.lse(z, k)
+        for c in range(r, n * copies, n):
+            assert ids[c] == j and kept[c] == k.sum() == mkept[c], (c, ids[c], j, kept[c], k.sum())
+            assert torch.equal(mask[c], words), c
+            assert abs(logp[c] - lp) <= 2.0 ** -24 * abs(lp) + sums, (c, logp[c], lp)
+            assert abs(float(lse[c]) - want_lse) <= 2.0 ** -24 * abs(want_lse) + sums, (c, lse[c], want_lse)
