@@ -729,7 +729,7 @@ int lpd_block_matmul(const lpd_block_scaled *a, const lpd_block_scaled *b, int64
  * 1, 1.5, 2, 3, 4, 6 (e2m1, in this order); `block` values along k share one scale
  * byte and the operand one float:
  *     value(r, c) * scale(r, c / block) * tensor_scale
- *   block 16   scales in e4m3
+ *   block 16   scales in e4m3, without a sign (the byte's upper bit is 0)
  *   block 32   scales 2^(byte - 127), 255 is NaN
  * The scale bytes lie as the tensor cores take them, 512 bytes for 128 rows x 4
  * blocks: with atoms = ceil(ceil(k / block) / 4), the scale of row r and block b is

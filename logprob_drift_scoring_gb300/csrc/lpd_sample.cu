@@ -12,18 +12,23 @@
 // number of CTAs that share a row changes a bit of the answer; three ways to it exist:
 //
 // - Few rows: a cluster of CTAs a row, each holding a slice in shared memory, so that the
-//   row is read once and all of its tokens are at hand (cluster_row).  One row of 128256
-//   float32 takes 14 us (20 us a call), each of some dozen steps of exchange a
-//   microsecond: latency bounds it.
+//   row is read once and all of its tokens are at hand (cluster_row).  A row whose border is
+//   in the list takes five barriers of the cluster, and then one CTA's selections (pick: one
+//   for a top-k, one for a top-p, one for the draw, each up to four turns of five barriers
+//   for some hundred entries), a row alone all of them one after the other: one row of
+//   128256 float32 takes 13.5 us for the mask of a top-k, 17 for a draw under it, 18.5 under
+//   a top-p too.
 // - Many rows: a CTA a row, the row streamed (row_kernel).  Under a small top-k or a
 //   min-p the largest tokens are collected against a value that a sample of the row gave:
 //   4096 rows (3687 of them active) x 151936 bf16 in 293 us, 4.1 TB/s of 6.8; the pass
 //   over the row takes three quarters of that, with 48 warps a multiprocessor and 96 KB
 //   in flight, the selections behind it the rest.  A bf16 row under any other filter is
-//   counted by value (counted_row): 509 rows under temperature or top-p in 170 us,
-//   bound by shared-memory atomics in the first pass (24 us a row alone, 14 of a full
-//   multiprocessor) and table look-ups in a draw's second.  A float32 row of which all
-//   is kept is weighed token by token (plain_row), 30 operations each.
+//   counted by value (counted_row).  Rows of 151936 go in rounds of 304, two a
+//   multiprocessor: 304 take 92 us under a temperature and 57 under a top-p, 305 take 135
+//   and 81, a row alone 61 and 41.  A row's passes follow one another: the counting (24 us
+//   alone, an atomic in shared memory a token), the bins, and the list's or, for a draw from
+//   many tokens, a table look-up a token.  A float32 row of which all is kept is weighed
+//   token by token (plain_row), 30 operations each.
 // - What is left of many rows (a nucleus beyond the list in float32, ties without end)
 //   goes to clusters behind them.
 //
@@ -79,7 +84,10 @@ __device__ constexpr Tables kTables = make_tables();
 
 // From so many rows on a CTA takes a row alone (and clusters what it leaves).  64 x 151936
 // bf16 under any filters take 83 us so and 97 us with clusters, 32 take 74 and 41; 152
-// of float32 146 and 148 (under a top-k 40 and 112), 64 take 139 and 76.
+// of float32 146 and 148 (under a top-k 40 and 112), 64 take 139 and 76.  On the two sides
+// of the rule, under a temperature / a top-k of 50: 63 and 64 rows of 1024 bf16 19 and 21 /
+// 26 and 17 us, of 37984 31 and 32 / 17 and 18; 127 and 128 of 1024 float32 15 and 13 / 13
+// and 16, of 37984 38 and 29 / 21 and 18, of 151936 133 and 73 / 78 and 28.
 constexpr int kAloneBf16 = 64, kAloneF32 = 128;
 constexpr int kTopList = 2048;      // candidates of a row that a CTA has alone
 constexpr int kTopMost = 512;       // the largest top-k that such a CTA takes
@@ -1814,7 +1822,10 @@ cudaError_t launch_clusters(const SampleArgs &a, int ranks, size_t smem, cudaStr
     cudaError_t e = set_smem_max_once(cluster_kernel<kBf16, kMask, kThreads>, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    // (bf16 rows are hardly ever left over, float32 nuclei beyond a list are)
+    // (Float32 nuclei beyond a list are left over.  Of bf16 rows few are, and clusters that find
+    // nothing cost time, so a cluster has 32 rows; a row with more than kTinyRoom values within
+    // 2^-10 of 0 is one, and where all are, as with flat logits of a deviation below 0.1, those 32
+    // follow one another: 64 rows of 151936 take 1.9 ms then, 0.07 otherwise.)
     const int64_t each = !a.after_rows ? 1 : kBf16 ? 32 : a.n_rows <= 512 ? 1 : 2;
     cfg.gridDim = dim3(static_cast<unsigned>((a.n_rows + each - 1) / each * ranks));
     cfg.blockDim = dim3(kThreads);
@@ -1847,14 +1858,13 @@ cudaError_t launch_typed(const SampleArgs &a, int ranks, cudaStream_t stream) {
 
 }  // namespace
 
-// Many rows with a top-k are read by one CTA each (read once, at the memory's rate);
-// whatever else there is goes to clusters.  Slices of at most 40 KB leave four CTAs a
-// multiprocessor, one loading while others count; rows of fewer than that go to one CTA
-// unless rows are so few that the multiprocessors would stand idle.  Larger slices
-// (float32 rows of a large vocabulary) have twice the threads, and so have those of 8192
-// tokens and more that have a multiprocessor to themselves (8 rows of 151936 bf16, all kinds
-// of filters: 41 us with 256, 33 with 512; of 37984 under top-k and top-p 19 and 21, of 1024
-// 41 and 43).
+// A cluster's slices have at most 40 KB where 8 CTAs can hold the row so: three CTAs of 256
+// threads a multiprocessor (a slice and 18.5 KB beside it each; four up to 37 KB), of which one
+// loads while others count.  Shorter rows go to fewer CTAs, one at last, unless rows are so few
+// that multiprocessors would stand idle.  Slices beyond 48 KB (float32 rows of a large
+// vocabulary) have twice the threads, and so have those of 8192 tokens and more that have a
+// multiprocessor to themselves (8 rows of 151936 bf16, all kinds of filters: 41 us with 256,
+// 33 with 512; of 37984 under top-k and top-p 19 and 21, of 1024 41 and 43).
 cudaError_t launch_sample(const SampleCall &c, cudaStream_t stream) {
     if (c.n_rows == 0) return cudaSuccess;
     const bool bf16 = c.dtype == LPD_BF16, mask = c.mask != nullptr;
