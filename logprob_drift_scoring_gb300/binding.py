@@ -282,11 +282,12 @@ def _with_its_stream(form):
             return form(*args, **kwargs)
         import torch
 
-        if not isinstance(stream, torch.cuda.Stream):  # a handle
-            first = args[0] if args else next(iter(kwargs.values()))
-            first = first[0] if isinstance(first, (list, tuple)) else first
-            tensors = [t for t in (first, getattr(first, "codes", None), getattr(first, "values", None)) if isinstance(t, torch.Tensor)]
-            stream = torch.cuda.ExternalStream(stream, device=tensors[0].device)
+        if not isinstance(stream, torch.cuda.Stream):  # a handle, of the device of the call's tensors
+            given = [*args, *kwargs.values()]
+            given = sum(([*v] if isinstance(v, (list, tuple)) else [v] for v in given), [])
+            given = [getattr(v, name, None) for v in given for name in ("codes", "values")] + given
+            device = next(t.device for t in given if isinstance(t, torch.Tensor))
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device)
         with torch.cuda.stream(stream):
             return form(*args, **kwargs)
 

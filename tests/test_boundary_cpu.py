@@ -474,3 +474,26 @@ def test_stream_of_a_torch_without_the_short_way(monkeypatch):
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     assert B._stream(None) == 0x1234
     assert B._stream(7) == 7 and B._stream(types.SimpleNamespace(cuda_stream=9)) == 9
+
+
+def test_handles_of_streams_in_the_forms_that_allocate(monkeypatch):
+    """A number or an object with one, wherever it stands among the arguments."""
+    import contextlib
+    import types
+
+    import torch
+
+    made = []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device: made.append((handle, device)) or (handle, device))
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+
+    @B._with_its_stream
+    def form(x, ranges=None, stream=None):
+        return stream
+
+    x = torch.zeros(3)
+    thing = types.SimpleNamespace(cuda_stream=9)
+    assert form(x) is None and not made
+    assert form(x, stream=7) == 7 and form(x, None, 7) == 7 and form(stream=7, ranges=[(0, 3)], x=[x, x]) == 7
+    assert form(types.SimpleNamespace(codes=x), stream=thing) is thing and form(types.SimpleNamespace(values=x), stream=0) == 0
+    assert made == [(7, x.device)] * 3 + [(9, x.device), (0, x.device)]
